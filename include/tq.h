@@ -328,6 +328,7 @@ typedef struct {
 #define TQ_DEVERR_SMEM_PLAN 2     /* the shared-memory plan did not fit the launch             */
 #define TQ_DEVERR_BAD_PAGE 3      /* a block-table entry or position outside the pool/table    */
 #define TQ_DEVERR_BAD_LENGTH 4    /* a device sequence length outside [0, 16 * max_blocks]     */
+#define TQ_DEVERR_NONFINITE 5     /* a byte-cache append met an infinity or a NaN              */
 
 /* Layout of a pool of num_pages pages (plus the one redirect page): total_bytes and the block
  * offsets/sizes of the K and V arrays, each [(num_pages + 1) * H_kv] blocks. */
@@ -349,6 +350,127 @@ tq_status tq_quantize_append_paged(const tq_context* ctx, void* dev_pool, const 
 tq_status tq_decode_attention_paged(const tq_context* ctx, const void* dev_pool, const tq_page_table* pages,
                                     const float* q, int32_t nq, const int32_t* dev_seq_len, float* out,
                                     void* ws, size_t ws_bytes, tq_stream stream);
+
+/* ---- Head norms and position rotation -----------------------------------------------------
+ * What a model does to queries and keys before they meet a cache, in one pass over each row of
+ * head_dim coordinates: the RMS norm y = x / sqrt(mean(x^2) + eps) * w (where a weight is given),
+ * then the position rotation.  Rotary pair i of rotary_dim / 2 turns by the angle
+ * position * freq(i); its two members (a, b) become (a cos - b sin, a sin + b cos).
+ * interleaved = 0: the members are coordinates i and i + rotary_dim / 2; 1: 2 i and 2 i + 1.
+ * Coordinates from rotary_dim on are not turned.  Each pair follows the position on one of
+ * num_axes axes (one axis for text; time, height and width for images and video).  An angle is
+ * held as a 64-bit fraction of a turn and multiplied by the position modulo one turn, so it is
+ * as exact at position 2^31 as at 1.  Arithmetic is fp32, rounded once to the output's type. */
+typedef struct {
+  const uint64_t* table;  /* device [rotary_dim / 2], from tq_rotary_table; NULL: no rotation  */
+  int32_t rotary_dim;     /* a multiple of 16, at most head_dim                                */
+  int32_t interleaved;
+  int32_t num_axes;       /* 1..4                                                              */
+} tq_rotary;
+
+/* A device tensor of rows of head_dim contiguous elements: the row of head h, token j of batch
+ * entry b starts at data + b * batch_stride + j * token_stride + h * head_stride (elements).
+ * Rows start on 16-byte boundaries: data is 16-byte aligned and every stride a multiple of 16
+ * bytes (a stride along an axis of one entry is not looked at). */
+typedef struct {
+  const void* data;
+  int64_t batch_stride, token_stride, head_stride;
+  int32_t heads;
+} tq_heads;
+
+/* The device table of a rotation, built on the host: freqs[i] is pair i's angle per position in
+ * radians (rotary_dim / 2 finite entries), axes[i] in [0, num_axes) its axis (NULL: axis 0).
+ * out[i] holds the frequency as a fraction of a turn in 2^-64ths, rounded to a multiple of 4,
+ * plus the axis in the two low bits.  No CUDA call. */
+tq_status tq_rotary_table(int32_t rotary_dim, const double* freqs, const int32_t* axes, int32_t num_axes,
+                          uint64_t* out);
+
+/* Norm and rotation of n tokens of each of batch entries.  q, k: device rows of dtype (either may
+ * be NULL); q_weight, k_weight: device [head_dim] of dtype, or NULL (no norm).  q_out is
+ * contiguous [batch][n][q heads][head_dim] (as the attention calls read queries), k_out
+ * contiguous [batch][k heads][n][head_dim] (as the appends read keys), both of out_dtype: dtype
+ * or TQ_F32.  An output may be its own input's buffer when the layouts and types are the same.
+ * dev_positions: device int32 [num_axes][batch][n]; NULL: token j of entry b is at dev_start[b] + j
+ * on every axis (device int32 [batch]; NULL: 0).  head_dim 64, 128, 256 or 512. */
+tq_status tq_norm_rotate(int32_t head_dim, tq_dtype dtype, tq_dtype out_dtype, int32_t batch, int32_t n,
+                         const tq_heads* q, const void* q_weight, void* q_out, const tq_heads* k,
+                         const void* k_weight, void* k_out, float eps, const tq_rotary* rotary,
+                         const int32_t* dev_positions, const int32_t* dev_start, tq_stream stream);
+
+/* ---- Byte cache: a paged pool of one e4m3 code per coordinate -------------------------------
+ * The 8-bit format beside the packed schemes: no rotation of coordinates, no norm split; each
+ * block of 16 tokens of one KV head has one power-of-two scale per side.  scale = 2^e with e the
+ * smallest integer in [-30, 30] such that the block's largest magnitude is at most 448 * 2^e, and
+ * a code is e4m3(x / scale), rounded to nearest even.  Powers of two change only a code's
+ * exponent, so an append that raises the scale of a block (its new tokens are larger than those
+ * it holds) leaves the held codes' significands alone, except where they become subnormal.
+ * Codes are always finite: an infinity becomes +-448, a NaN 0, neither counts for the scale, and
+ * TQ_DEVERR_NONFINITE is recorded.
+ *
+ * The pool: (num_pages + 1) * num_kv_heads blocks of 32 * head_dim + 32 bytes, block (page, head)
+ * at page * num_kv_heads + head; the last page takes redirected accesses (tq_page_table).  A block
+ * holds, with d = head_dim:
+ *   K codes, 16 d bytes: 16-byte chunk c of token t's row at
+ *     (c / 8) * 2048 + t * 128 + ((c % 8) ^ (t % 8)) * 16   (d = 128, 256),
+ *     t * 64 + (c ^ ((t / 2) % 4)) * 16                     (d = 64);
+ *   V codes, 16 d bytes: coordinate x of token t at
+ *     16 d + x * 16 + ((t % 8) / 2) * 4 + (t / 8) * 2 + t % 2;
+ *   the K scale and the V scale (fp32) at 32 d and 32 d + 4, and 24 unused bytes. */
+typedef struct {
+  int32_t head_dim;       /* 64, 128 or 256                                                    */
+  int32_t num_q_heads;    /* any multiple of num_kv_heads                                      */
+  int32_t num_kv_heads;
+} tq_byte_config;
+
+/* Bytes of a pool of num_pages pages (0: bad configuration). */
+size_t tq_byte_pool_bytes(const tq_byte_config* cfg, int32_t num_pages);
+
+/* Append with the norm and the rotation of the keys on the way: token j of batch entry b goes to
+ * position dev_start[b] + j.  k, v: device rows of dtype, num_kv_heads heads; k_weight, eps,
+ * rotary (NULL: no rotation) and dev_positions as for tq_norm_rotate, with dev_start for the
+ * positions when dev_positions is NULL.  Keys are rounded once, from fp32 to their codes.
+ * dev_count: device int32 [batch], entry b appends only its first min(dev_count[b], n) tokens
+ * (none when negative); NULL: all n.  q (NULL: none): n tokens of queries per entry, normed
+ * (q_weight) and rotated with the same positions in the same launch into q_out, contiguous
+ * [batch][n][num_q_heads][head_dim] of dtype; all n rows of q are written whatever dev_count says.
+ * A block's held tokens are those before dev_start[b]; bytes of positions behind the appended
+ * tokens stay as they are.  A page that receives tokens must belong to one sequence.  Bad pages
+ * and positions: see tq_page_table.  dev_error: device int32 or NULL; receives a TQ_DEVERR_* code
+ * (the caller zeroes it beforehand).  n = 0 is a no-op. */
+tq_status tq_byte_append_paged(const tq_byte_config* cfg, void* dev_pool, const tq_page_table* pages,
+                               int32_t batch, int32_t n, tq_dtype dtype, const tq_heads* k, const tq_heads* v,
+                               const int32_t* dev_start, const int32_t* dev_count, const void* k_weight,
+                               float eps, const tq_rotary* rotary, const int32_t* dev_positions,
+                               const tq_heads* q, const void* q_weight, void* q_out, int32_t* dev_error,
+                               tq_stream stream);
+
+/* Attention over the pool.  q: device rows of dtype, nq tokens of num_q_heads heads per batch
+ * entry; out: contiguous [batch][nq][num_q_heads][head_dim] of dtype.  dev_seq_len: device int32
+ * [batch], the tokens of each sequence, the step's own included (already appended); a length
+ * outside [0, 16 * max_blocks_per_seq] is clamped and recorded.  dev_count: device int32 [batch]
+ * or NULL (nq): entry b has c = min(dev_count[b], nq) queries, its last c positions.  Query i < c
+ * attends to the first dev_seq_len[b] - c + 1 + i tokens (none when that is <= 0: output zeros);
+ * rows i >= c are written as zeros.  scale multiplies the scores (1 / sqrt(head_dim) in most
+ * models).  What the pool holds behind a sequence's last token is never used.  Scores, softmax
+ * statistics and accumulators are fp32; queries and probabilities enter the matrix products as
+ * fp16 (bf16 and fp16 queries exactly, under a power-of-two scale per row; fp32 queries and their
+ * probabilities as fp16 hi + lo terms).  ws: device workspace of at least
+ * tq_byte_attention_workspace_bytes, 256-byte aligned, uninitialized, owned by the call until it
+ * completes on stream.  dev_error as for the append.  Results do not depend on the other entries
+ * of the batch beyond the order of the sums over a sequence's parts, which the lengths decide;
+ * equal calls give equal bits. */
+size_t tq_byte_attention_workspace_bytes(const tq_byte_config* cfg, const tq_page_table* pages, int32_t batch,
+                                         int32_t nq, tq_dtype dtype);
+tq_status tq_byte_attention_paged(const tq_byte_config* cfg, const void* dev_pool, const tq_page_table* pages,
+                                  int32_t batch, int32_t nq, tq_dtype dtype, const tq_heads* q,
+                                  const int32_t* dev_seq_len, const int32_t* dev_count, float scale, void* out,
+                                  void* ws, size_t ws_bytes, int32_t* dev_error, tq_stream stream);
+
+/* Reconstruct tokens [t0, t1) of KV head kvh of batch entry b as fp32 [t1 - t0][head_dim] (device):
+ * code * scale, exact.  For tests and debugging. */
+tq_status tq_byte_dequantize(const tq_byte_config* cfg, const void* dev_pool, const tq_page_table* pages,
+                             int32_t batch, int32_t b, int32_t kvh, int32_t t0, int32_t t1, float* k_out,
+                             float* v_out, tq_stream stream);
 
 /* Wait for stream, then read the device error word of a decode workspace: 0 = none, else a
  * TQ_DEVERR_* code. */

@@ -12,7 +12,7 @@ import numpy as np
 from . import binding as _b
 from .binding import TQError, check  # noqa: F401
 
-__all__ = ["QuantizedKVCache", "PagedKVCache", "TQError", "binding"]
+__all__ = ["QuantizedKVCache", "PagedKVCache", "PagedByteCache", "Rotary", "norm_rotate", "TQError", "binding"]
 
 _DTYPES = None
 
@@ -270,3 +270,11 @@ class PagedKVCache(_Codec):
 def _torch():
     import torch
     return torch
+
+
+def __getattr__(name):
+    # (torch is imported with the first use, as for the classes above)
+    if name in ("PagedByteCache", "Rotary", "norm_rotate"):
+        from . import byte_cache
+        return getattr(byte_cache, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

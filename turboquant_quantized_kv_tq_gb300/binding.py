@@ -65,6 +65,20 @@ TQ_DEVERR_WAIT_TIMEOUT = 1
 TQ_DEVERR_SMEM_PLAN = 2
 TQ_DEVERR_BAD_PAGE = 3
 TQ_DEVERR_BAD_LENGTH = 4
+TQ_DEVERR_NONFINITE = 5
+
+
+class tq_rotary(ctypes.Structure):
+    _fields_ = [("table", c_void_p), ("rotary_dim", c_int32), ("interleaved", c_int32), ("num_axes", c_int32)]
+
+
+class tq_heads(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("heads", c_int32)]
+
+
+class tq_byte_config(ctypes.Structure):
+    _fields_ = [("head_dim", c_int32), ("num_q_heads", c_int32), ("num_kv_heads", c_int32)]
 
 
 class TQError(RuntimeError):
@@ -119,6 +133,23 @@ DECLARATIONS = [
                                            c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p]),
     ("tq_decode_attention_paged", c_int32, [c_void_p, c_void_p, ctypes.POINTER(tq_page_table), c_void_p,
                                             c_int32, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    ("tq_rotary_table", c_int32, [c_int32, c_void_p, c_void_p, c_int32, c_void_p]),
+    ("tq_norm_rotate", c_int32, [c_int32, c_int32, c_int32, c_int32, c_int32, ctypes.POINTER(tq_heads), c_void_p,
+                                 c_void_p, ctypes.POINTER(tq_heads), c_void_p, c_void_p, ctypes.c_float,
+                                 ctypes.POINTER(tq_rotary), c_void_p, c_void_p, c_void_p]),
+    ("tq_byte_pool_bytes", c_size_t, [ctypes.POINTER(tq_byte_config), c_int32]),
+    ("tq_byte_append_paged", c_int32, [ctypes.POINTER(tq_byte_config), c_void_p, ctypes.POINTER(tq_page_table),
+                                       c_int32, c_int32, c_int32, ctypes.POINTER(tq_heads),
+                                       ctypes.POINTER(tq_heads), c_void_p, c_void_p, c_void_p, ctypes.c_float,
+                                       ctypes.POINTER(tq_rotary), c_void_p, ctypes.POINTER(tq_heads), c_void_p,
+                                       c_void_p, c_void_p, c_void_p]),
+    ("tq_byte_attention_workspace_bytes", c_size_t, [ctypes.POINTER(tq_byte_config), ctypes.POINTER(tq_page_table),
+                                                     c_int32, c_int32, c_int32]),
+    ("tq_byte_attention_paged", c_int32, [ctypes.POINTER(tq_byte_config), c_void_p, ctypes.POINTER(tq_page_table),
+                                          c_int32, c_int32, c_int32, ctypes.POINTER(tq_heads), c_void_p, c_void_p,
+                                          ctypes.c_float, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
+    ("tq_byte_dequantize", c_int32, [ctypes.POINTER(tq_byte_config), c_void_p, ctypes.POINTER(tq_page_table),
+                                     c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p, c_void_p, c_void_p]),
     ("tq_get_device_error", c_int32, [c_void_p, ctypes.POINTER(c_int32), c_void_p]),
     ("tq_get_static_device_error", c_int32, [ctypes.POINTER(c_int32), c_void_p]),
     ("tq_status_string", ctypes.c_char_p, [c_int32]),

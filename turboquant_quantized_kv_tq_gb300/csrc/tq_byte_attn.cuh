@@ -1,0 +1,253 @@
+// The tile step shared by the byte cache's mma.sync attention kernels: 16 tokens of one KV head
+// against 8 NR query rows held by one warp.
+//
+// Mathematics, per row: o = sum_j p_j 2^(e_j) c_j / sum_j p_j, with c_j token j's V codes, 2^(e_j) its
+// block's V scale and p_j = 2^(s_j), s_j = log2(e) scale q . k_j.  The running reference is
+//   M = max_j (s_j + e_j) - 14,   P_j = 2^(s_j + e_j - M) in (0, 2^14],
+// so that the matrix product sum_j P_j c_j takes P as fp16 whatever the scales are: its largest
+// contribution sits at the top of fp16's range, and what underflows is 2^-38 of it.  The softmax
+// sum l = sum_j P_j 2^(-e_j) stays in fp32 (|e_j| <= 30 keeps it in range).  The scale of a block
+// costs nothing this way: e_j is added to the exponent's constant.
+//
+// Products are mma.sync m16n8k16 on fp16 (codes are exact in fp16) with the tokens (scores) or the
+// coordinates (readout) as M and the query rows as N, so 8 rows fill an instruction:
+//   S^T[16 tok x 8 rows] += K[16 x 16 d] Q^T[16 d x 8],  O^T[16 d x 8 rows] += V^T[16 d x 16 tok] P^T.
+// Thread (g, u) of the warp (g = lane / 4, u = lane % 4) holds tokens g, g + 8 and rows 2u, 2u + 1 of
+// the scores; coordinates within a 16-product are permuted so that its K operand is 16 contiguous
+// codes per shared-memory load, and V's stored token order is that of the P operand.
+#pragma once
+
+#include "tq_byte.cuh"
+
+namespace tqb {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kShift = 14.f;            // M is this far below the largest s + e
+constexpr uint32_t kWaitLimit = 1u << 20; // polls of an mbarrier before giving up
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int D, int NR, int TERMS>
+struct QFrag {
+  uint32_t v[TERMS][NR][D / 16][2];  // B operand of k-step s: coordinates 4 s' .. of the thread's chunks
+  float f[NR][2];                    // rows 2u, 2u + 1: log2(e) * scale * the row's power-of-two scale
+};
+
+template <int D, int NR>
+struct State {
+  float o[NR][D / 16][4];  // O^T: coordinates 16 m + g, + 8; rows 2u, 2u + 1
+  float m[NR][2], l[NR][2];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[r][i][k] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        m[r][k] = -INFINITY;
+        l[r][k] = 0.f;
+      }
+    }
+  }
+};
+
+// First coordinate of the 16 codes of load i (0 .. D/64 - 1) of thread u of a quad, and its chunk.
+template <int D>
+__device__ __forceinline__ int frag_chunk(int u, int i) {
+  if constexpr (D == 64) return u;
+  return (i >> 1) * 8 + 2 * u + (i & 1);
+}
+
+template <typename T>
+__device__ __forceinline__ float to_float(T x);
+template <> __device__ __forceinline__ float to_float(float x) { return x; }
+template <> __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+template <> __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// Query rows row0 + 8 r + g (head h G + row % G of query row / G) as fp16 operands.  Each row is
+// scaled by the power of two that brings its largest magnitude into [1, 2): bf16 and fp16 values
+// are then exact in fp16 down to 2^-14 of that (below, off by at most 2^-25 of it); fp32 rows take
+// a second fp16 term of what the first leaves (together off by at most 2^-23 or so of a value).
+template <int D, int NR, int TERMS, typename T>
+__device__ __forceinline__ void load_q(QFrag<D, NR, TERMS>& q, const Rows& X, int b, int h, int G, int row0, int rows,
+                                       float score_scale, int lane) {
+  const int g = lane >> 2, u = lane & 3;
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    const int row = row0 + 8 * r + g;
+    const bool live = row < rows;
+    const int i = live ? row / G : 0, hd = h * G + (live ? row - i * G : 0);
+    const T* src = reinterpret_cast<const T*>(X.p) + b * X.sb + i * X.st + hd * X.sh;
+    float amax = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      float x[16];
+      tqd::load_row<16>(src + 16 * frag_chunk<D>(u, c), x);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(x[k]));
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+    // exponent of amax, held where 2^-e is a normal number; 0 for rows of zeros or with infinities
+    int e = log2i(amax);
+    if (e < -120 || e > 120) e = amax > 1.f && e < 128 ? 120 : amax > 0.f && e < 0 ? -120 : 0;
+    const float inv = exp2i(-e);
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      float x[16];
+      tqd::load_row<16>(src + 16 * frag_chunk<D>(u, c), x);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const float a = live ? x[4 * k + 2 * w] * inv : 0.f, bb = live ? x[4 * k + 2 * w + 1] * inv : 0.f;
+          const uint32_t hi = tqd::pack_half2(a, bb);
+          q.v[0][r][4 * c + k][w] = hi;
+          if constexpr (TERMS == 2) {
+            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+            q.v[1][r][4 * c + k][w] = tqd::pack_half2(a - back.x, bb - back.y);
+          }
+        }
+    }
+    const float f = exp2i(e) * score_scale * kLog2e;  // (of row g: the threads that hold rows 2u, 2u + 1 need it)
+    q.f[r][0] = __shfl_sync(kFull, f, 8 * u);
+    q.f[r][1] = __shfl_sync(kFull, f, 8 * u + 4);
+  }
+}
+
+// One tile: `blk` is the block in shared memory, tok0 its first token, lim[r][k] the tokens that row
+// 2u + k of group r attends to, edge: some row of the warp does not attend to all 16 tokens, len:
+// the sequence's length (codes of tokens behind it may be anything).
+template <int D, int NR, int TERMS>
+__device__ __forceinline__ void tile_step(const unsigned char* blk, const QFrag<D, NR, TERMS>& q, State<D, NR>& st,
+                                          int tok0, const int (&lim)[NR][2], bool edge, int len, int lane) {
+  const int g = lane >> 2, u = lane & 3;
+  float s[NR][4];
+#pragma unroll
+  for (int r = 0; r < NR; ++r)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s[r][k] = 0.f;
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) {
+    const int ch = frag_chunk<D>(u, c);
+    const uint4 lo = *reinterpret_cast<const uint4*>(blk + k_chunk<D>(g, ch));
+    const uint4 hi = *reinterpret_cast<const uint4*>(blk + k_chunk<D>(g + 8, ch));
+    const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t a0, a1, a2, a3;
+      codes_half4(wl[k], a0, a2);
+      codes_half4(wh[k], a1, a3);
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) tqd::mma16816(s[r], a0, a1, a2, a3, q.v[t][r][4 * c + k][0], q.v[t][r][4 * c + k][1]);
+    }
+  }
+  const float2 scales = *reinterpret_cast<const float2*>(blk + 32 * D);
+  const int ev = log2i(scales.y);
+  const float e = (float)ev, inv_e = exp2i(max(-126, min(126, -ev)));
+  bool up = false;
+  float fk[NR][2];
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    fk[r][0] = q.f[r][0] * scales.x;
+    fk[r][1] = q.f[r][1] * scales.x;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s[r][k] *= fk[r][k & 1];
+    if (edge) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (tok0 + g + 8 * (k >> 1) >= lim[r][k & 1]) s[r][k] = -INFINITY;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) up |= fmaxf(s[r][k], s[r][k + 2]) + (e - kShift) > st.m[r][k];
+  }
+  if (__any_sync(kFull, up)) {  // some row's reference rises
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float c = fmaxf(s[r][k], s[r][k + 2]) + (e - kShift);
+#pragma unroll
+        for (int m = 4; m <= 16; m <<= 1) c = fmaxf(c, __shfl_xor_sync(kFull, c, m));
+        const float mn = fmaxf(st.m[r][k], c);
+        const float cor = ex2(st.m[r][k] - (mn == -INFINITY ? 0.f : mn));
+        st.m[r][k] = mn;
+        st.l[r][k] *= cor;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          st.o[r][i][k] *= cor;
+          st.o[r][i][k + 2] *= cor;
+        }
+      }
+  }
+  uint32_t p[TERMS][NR][2];
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float m = st.m[r][k & 1];
+      v[k] = ex2(s[r][k] + (e - (m == -INFINITY ? 0.f : m)));
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) st.l[r][k] = fmaf(v[k] + v[k + 2], inv_e, st.l[r][k]);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const uint32_t hi = tqd::pack_half2(v[2 * w], v[2 * w + 1]);
+      p[0][r][w] = tqd::movmatrix_trans(hi);
+      if constexpr (TERMS == 2) {
+        const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+        p[1][r][w] = tqd::movmatrix_trans(tqd::pack_half2(v[2 * w] - back.x, v[2 * w + 1] - back.y));
+      }
+    }
+  }
+  // codes behind the sequence's end may be NaN: zero them (their probabilities are zero already)
+  uint32_t keep = 0xffffffffu;
+  if (edge && tok0 + 16 > len) {
+    const int t = len - tok0;
+    keep = (2 * u < t ? 0xffu : 0u) | (2 * u + 1 < t ? 0xff00u : 0u) | (2 * u + 8 < t ? 0xff0000u : 0u) |
+           (2 * u + 9 < t ? 0xff000000u : 0u);
+  }
+  const unsigned char* vb = blk + 16 * D + 16 * g + 4 * u;
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    const uint32_t w0 = *reinterpret_cast<const uint32_t*>(vb + 256 * i) & keep;
+    const uint32_t w1 = *reinterpret_cast<const uint32_t*>(vb + 256 * i + 128) & keep;
+    uint32_t a0, a1, a2, a3;
+    codes_half4(w0, a0, a2);
+    codes_half4(w1, a1, a3);
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int t = 0; t < TERMS; ++t) tqd::mma16816(st.o[r][i], a0, a1, a2, a3, p[t][r][0], p[t][r][1]);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ T from_float(float x);
+template <> __device__ __forceinline__ float from_float<float>(float x) { return x; }
+template <> __device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// Length and count of sequence b as the kernels use them.
+__device__ __forceinline__ int clamped_len(const int32_t* seq_len, int b, int most, int32_t* err) {
+  const int v = __ldg(seq_len + b);
+  const int c = min(max(v, 0), most);
+  if (c != v && err) atomicExch(err, TQ_DEVERR_BAD_LENGTH);
+  return c;
+}
+__device__ __forceinline__ int clamped_count(const int32_t* count, int b, int nq) {
+  return count ? min(max(__ldg(count + b), 0), nq) : nq;
+}
+// Tokens that a row of query i attends to.
+__device__ __forceinline__ int row_limit(int i, int len, int cnt) { return i < cnt ? max(0, len - cnt + 1 + i) : 0; }
+
+}  // namespace tqb

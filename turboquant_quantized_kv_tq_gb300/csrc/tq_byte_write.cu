@@ -1,0 +1,470 @@
+// Head norms with the position rotation (norm_rotate), and the append of keys and values into the
+// byte cache with that norm and rotation on the way (byte_append).
+//
+// norm_rotate reads every row once and writes it once: bound by HBM for chunks, by the launch and
+// the chain position -> angle -> row for single tokens.  A block of 256 threads takes a few tokens
+// and all their heads, so a token's sines are computed once for its 2 * heads rows.
+//
+// byte_append gives each warp one side of one 16-token block of one KV head: it reads the block's
+// new rows, rotates keys, finds the block's scale with a warp maximum, and writes the codes; held
+// codes are rounded to a raised scale by the same warp, so a block has one writer.  The queries of
+// the step ride along as further blocks of the grid.
+#include <string>
+
+#include "tq_byte.cuh"
+#include "tq_rotate.cuh"
+
+namespace tqb {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Cosines of tokens [0, count) at pos(token, axis) into cs ([token][r / 2] float2, pair_slot order).
+template <typename F>
+__device__ __forceinline__ void fill_angles(float2* cs, const Rotary& R, int count, F pos) {
+  const int half = R.r / 2;
+  for (int i = threadIdx.x; i < count * half; i += blockDim.x) {
+    const int tk = i / half, p = i - tk * half;
+    const uint64_t entry = __ldg(reinterpret_cast<const unsigned long long*>(R.table) + p);
+    cs[tk * half + pair_slot(p, R.r, R.interleaved)] = pair_angle(entry, [&](int axis) { return pos(tk, axis); });
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void load_weight(const void* w, int ca, int cb, float (&wa)[8], float (&wb)[8]) {
+  if (w) {
+    unpack8(load8(reinterpret_cast<const T*>(w) + 8 * ca), wa);
+    unpack8(load8(reinterpret_cast<const T*>(w) + 8 * cb), wb);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) wa[i] = wb[i] = 1.f;
+  }
+}
+
+// Rows of `heads` heads (from h0) of tokens [t0, t0 + nt) of [B][n] (linear token index), cosines
+// already in cs: normed, rotated and stored at out(b, j, h).  Loads of kU rows are in flight per
+// thread; the block's barrier that publishes cs comes between the first loads and their use.
+template <int D, typename T, typename O, int kU, typename F>
+__device__ __forceinline__ void rows_pass(const Rows& X, const void* w, float eps, const Rotary& R, const float4* cs,
+                                          int t0, int nt, int h0, int nh, int n, bool& synced, F out) {
+  constexpr int TPR = D / 16, RPP = kThreads / TPR;
+  const int l = threadIdx.x % TPR, row0 = threadIdx.x / TPR;
+  const int ca = chunk_a(l, R.r), cb = chunk_b(l, R.r);
+  const int total = nt * nh;
+  float wa[8], wb[8];
+  load_weight<T>(w, ca, cb, wa, wb);
+  for (int base = 0; base < total; base += RPP * kU) {
+    Raw8<T> ra[kU], rb[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int row = base + u * RPP + row0;
+      if (row < total) {
+        const int tk = row / nh, h = h0 + row - tk * nh, g = t0 + tk, b = g / n, j = g - b * n;
+        const T* src = reinterpret_cast<const T*>(X.p) + b * X.sb + j * X.st + h * X.sh;
+        ra[u] = load8_rw(src + 8 * ca);
+        rb[u] = load8_rw(src + 8 * cb);
+      }
+    }
+    if (!synced) {
+      __syncthreads();
+      synced = true;
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int row = base + u * RPP + row0;
+      if (base + u * RPP >= total) break;  // (uniform over the block)
+      const int tk = min(row, total - 1) / nh;
+      float a[8], b8[8];
+      if (row < total) {
+        unpack8(ra[u], a);
+        unpack8(rb[u], b8);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] = b8[i] = 0.f;
+      }
+      norm_rotate_row<TPR>(a, b8, l, w != nullptr, wa, wb, D, eps, cs + tk * (R.r / 4), R.r, R.interleaved);
+      if (row < total) {
+        const int h = h0 + row - tk * nh, g = t0 + tk, b = g / n, j = g - b * n;
+        O* dst = reinterpret_cast<O*>(out(b, j, h));
+        store8(dst + 8 * ca, a);
+        store8(dst + 8 * cb, b8);
+      }
+    }
+  }
+}
+
+struct RotateParams {
+  RotateArgs a;
+  int tokens;      // B n
+  int per;         // tokens per block
+  int q_split;     // blocks over the heads: blockIdx.y takes heads [y * q_split, ...) of q then k
+};
+
+template <int D, typename T, typename O>
+__global__ void __launch_bounds__(kThreads) norm_rotate_kernel(const RotateParams p) {
+  extern __shared__ __align__(16) float2 cs[];
+  const RotateArgs& A = p.a;
+  const int t0 = blockIdx.x * p.per, nt = min(p.per, p.tokens - t0);
+  if (A.rot.r)
+    fill_angles(cs, A.rot, nt, [&](int tk, int axis) {
+      const int g = t0 + tk, b = g / A.n;
+      return token_position(A.pos, axis, b, g - b * A.n, A.B, A.n);
+    });
+  // heads of q and k in one range [0, Hq + Hk)
+  const int lo = blockIdx.y * p.q_split, hi = min(lo + p.q_split, A.q.heads + A.k.heads);
+  const int q0 = min(lo, A.q.heads), q1 = min(hi, A.q.heads);
+  const int k0 = max(lo, A.q.heads) - A.q.heads, k1 = max(hi, A.q.heads) - A.q.heads;
+  bool synced = false;
+  constexpr int kU = sizeof(T) == 2 ? 4 : 2;
+  if (q1 > q0)
+    rows_pass<D, T, O, kU>(A.q, A.wq, A.eps, A.rot, reinterpret_cast<const float4*>(cs), t0, nt, q0, q1 - q0, A.n, synced,
+                           [&](int b, int j, int h) {
+                             return reinterpret_cast<O*>(A.q_out) + (((long long)b * A.n + j) * A.q.heads + h) * D;
+                           });
+  if (k1 > k0)
+    rows_pass<D, T, O, kU>(A.k, A.wk, A.eps, A.rot, reinterpret_cast<const float4*>(cs), t0, nt, k0, k1 - k0, A.n, synced,
+                           [&](int b, int j, int h) {
+                             return reinterpret_cast<O*>(A.k_out) + (((long long)b * A.k.heads + h) * A.n + j) * D;
+                           });
+}
+
+struct AppendParams {
+  AppendArgs a;
+  int blocks;      // 16-token blocks a batch entry's tokens can touch
+  int groups;      // head groups of 4
+  int kv_blocks;   // B * blocks * groups; later grid blocks take queries
+  int per, tokens, q_split, q_groups;
+};
+
+template <typename T, int E>
+__device__ __forceinline__ void load_narrow(const T* p, float (&x)[E]);
+template <>
+__device__ __forceinline__ void load_narrow<float, 2>(const float* p, float (&x)[2]) {
+  const float2 v = __ldg(reinterpret_cast<const float2*>(p));
+  x[0] = v.x; x[1] = v.y;
+}
+template <>
+__device__ __forceinline__ void load_narrow<__nv_bfloat16, 2>(const __nv_bfloat16* p, float (&x)[2]) {
+  const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p));
+  x[0] = __uint_as_float(w << 16);
+  x[1] = __uint_as_float(w & 0xffff0000u);
+}
+template <>
+__device__ __forceinline__ void load_narrow<__half, 2>(const __half* p, float (&x)[2]) {
+  const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  x[0] = f.x; x[1] = f.y;
+}
+template <typename T, int E>
+__device__ __forceinline__ void load_some(const T* p, float (&x)[E]) {
+  if constexpr (E == 2) load_narrow<T, 2>(p, x);
+  else tqd::load_row<E>(p, x);
+}
+
+// The block's scale exponent from its new tokens' largest magnitude and, where it holds tokens, its
+// old one; the scale is stored and the old exponent returned in e_old.
+__device__ __forceinline__ int block_scale(float amax, int held, float old_scale, float* scale, int lane, int& e_old) {
+  int e = scale_exponent(tqd::warp_max(amax));
+  e_old = e;
+  if (held > 0) {
+    e_old = min(kEMax, max(kEMin, log2i(old_scale)));
+    e = max(e, e_old);
+  }
+  if (lane == 0) *scale = exp2i(e);
+  return e;
+}
+
+template <int D, typename T>
+__device__ __forceinline__ bool append_keys(const AppendArgs& A, unsigned char* blk, const float4* cs, int b, int h,
+                                            long long j0, int lo, int hi, int held, int lane) {
+  constexpr int TPR = D / 16, RPW = 32 / TPR, NP = 16 / RPW;
+  const int l = lane % TPR, r0 = lane / TPR;
+  const int ca = chunk_a(l, A.rot.r), cb = chunk_b(l, A.rot.r);
+  float* scale = reinterpret_cast<float*>(blk + 32 * D);
+  const float old_scale = held > 0 ? *scale : 1.f;
+  const T* src = reinterpret_cast<const T*>(A.k.p) + b * A.k.sb + h * A.k.sh;
+  float a[NP][8], c[NP][8], wa[8], wb[8];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int s = p * RPW + r0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[p][i] = c[p][i] = 0.f;
+    if (s >= lo && s < hi) {
+      const T* row = src + (j0 + s) * A.k.st;
+      unpack8(load8(row + 8 * ca), a[p]);
+      unpack8(load8(row + 8 * cb), c[p]);
+    }
+  }
+  load_weight<T>(A.wk, ca, cb, wa, wb);
+  __syncthreads();  // cosines
+  float amax = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int s = p * RPW + r0;
+    // (rows without a new token are zeros; their cosines are those of an existing slot)
+    norm_rotate_row<TPR>(a[p], c[p], l, A.wk != nullptr, wa, wb, D, A.eps, cs + (s >= lo && s < hi ? s : lo) * (A.rot.r / 4),
+                         A.rot.r, A.rot.interleaved);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      amax = fmaxf(amax, fmaxf(finite_abs(a[p][i]), finite_abs(c[p][i])));
+      bad |= !(fabsf(a[p][i]) <= 3.402823466e38f) || !(fabsf(c[p][i]) <= 3.402823466e38f);
+    }
+  }
+  int e_old;
+  const int e = block_scale(amax, held, old_scale, scale, lane, e_old);
+  const float inv = exp2i(-e);
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int s = p * RPW + r0;
+    if (s < lo || s >= hi) continue;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      a[p][i] *= inv;
+      c[p][i] *= inv;
+    }
+    *reinterpret_cast<uint2*>(blk + k_chunk<D>(s, ca >> 1) + 8 * (ca & 1)) = make_uint2(encode4(a[p]), encode4(a[p] + 4));
+    *reinterpret_cast<uint2*>(blk + k_chunk<D>(s, cb >> 1) + 8 * (cb & 1)) = make_uint2(encode4(c[p]), encode4(c[p] + 4));
+  }
+  if (e > e_old && held > 0) {  // held rows to the raised scale, 16 codes at a time
+    const float f = exp2i(e_old - e);
+    for (int i = lane; i < held * (D / 16); i += 32) {
+      uint4* at = reinterpret_cast<uint4*>(blk + k_chunk<D>(i / (D / 16), i % (D / 16)));
+      uint4 v = *at;
+      uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float x[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) x[m] = decode1((unsigned char)(w[u] >> (8 * m))) * f;
+        w[u] = encode4(x);
+      }
+      *at = v;
+    }
+  }
+  return bad;
+}
+
+template <int D, typename T>
+__device__ __forceinline__ bool append_values(const AppendArgs& A, unsigned char* blk, int b, int h, long long j0, int lo,
+                                              int hi, int held, int lane) {
+  constexpr int E = D / 32;  // coordinates E * lane .. of all 16 tokens
+  float* scale = reinterpret_cast<float*>(blk + 32 * D + 4);
+  const float old_scale = held > 0 ? *scale : 1.f;
+  const T* src = reinterpret_cast<const T*>(A.v.p) + b * A.v.sb + h * A.v.sh + E * lane;
+  float x[16][E];
+#pragma unroll
+  for (int s = 0; s < 16; ++s) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[s][i] = 0.f;
+    if (s >= lo && s < hi) load_some<T, E>(src + (j0 + s) * A.v.st, x[s]);
+  }
+  __syncthreads();  // (the block's barrier for the key warps' cosines)
+  float amax = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int s = 0; s < 16; ++s)
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      amax = fmaxf(amax, finite_abs(x[s][i]));
+      bad |= !(fabsf(x[s][i]) <= 3.402823466e38f);
+    }
+  int e_old;
+  const int e = block_scale(amax, held, old_scale, scale, lane, e_old);
+  const float inv = exp2i(-e);
+  const bool raise = held > 0 && e > e_old;
+  const float f = exp2i(e_old - e);
+  unsigned char* vb = blk + 16 * D + 16 * E * lane;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {  // tokens 2u, 2u + 1, 2u + 8, 2u + 9
+      const float four[4] = {x[2 * u][i] * inv, x[2 * u + 1][i] * inv, x[2 * u + 8][i] * inv, x[2 * u + 9][i] * inv};
+      w[u] = encode4(four);
+    }
+    if (lo == 0 && hi == 16) {
+      *reinterpret_cast<uint4*>(vb + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int s = 0; s < 16; ++s) {
+        unsigned char* at = vb + 16 * i + v_slot(s);
+        if (s >= lo && s < hi)
+          *at = (unsigned char)(w[v_slot(s) >> 2] >> (8 * (v_slot(s) & 3)));
+        else if (raise && s < held)
+          *at = (unsigned char)encode2(decode1(*at) * f, 0.f);
+      }
+    }
+  }
+  return bad;
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads) byte_append_kernel(const AppendParams p) {
+  extern __shared__ __align__(16) float2 cs[];
+  const AppendArgs& A = p.a;
+  if ((int)blockIdx.x >= p.kv_blocks) {  // queries
+    const int i = blockIdx.x - p.kv_blocks, part = i % p.q_groups, t0 = i / p.q_groups * p.per;
+    const int nt = min(p.per, p.tokens - t0), h0 = part * p.q_split, nh = min(p.q_split, A.Hq - h0);
+    if (A.rot.r)
+      fill_angles(cs, A.rot, nt, [&](int tk, int axis) {
+        const int g = t0 + tk, b = g / A.n;
+        return token_position(A.pos, axis, b, g - b * A.n, A.B, A.n);
+      });
+    bool synced = false;
+    rows_pass<D, T, T, (sizeof(T) == 2 ? 4 : 2)>(A.q, A.wq, A.eps, A.rot, reinterpret_cast<const float4*>(cs), t0, nt, h0,
+                                                 nh, A.n, synced, [&](int b, int j, int h) {
+                                                   return reinterpret_cast<T*>(A.q_out) +
+                                                          (((long long)b * A.n + j) * A.Hq + h) * D;
+                                                 });
+    return;
+  }
+  const int hg = blockIdx.x % p.groups, rest = blockIdx.x / p.groups;
+  const int i = rest % p.blocks, b = rest / p.blocks;
+  const int start = __ldg(A.start + b);
+  const int count = A.count ? min(A.n, __ldg(A.count + b)) : A.n;
+  const int first = start >> 4;                            // (floor, also of a negative start)
+  const long long tile = (long long)first + i;
+  const long long j0 = tile * 16 - start;                  // the token at the block's slot 0
+  const int lo = (int)max(0ll, -j0), hi = (int)min(16ll, (long long)count - j0);
+  if (hi <= lo) return;                                    // (uniform over the block)
+  const int held = i == 0 ? (start & 15) : 0;              // = lo in the first block
+  if (A.rot.r) {
+    const int half = A.rot.r / 2;
+    for (int u = threadIdx.x; u < (hi - lo) * half; u += kThreads) {
+      const int s = lo + u / half, pr = u % half;
+      const uint64_t entry = __ldg(reinterpret_cast<const unsigned long long*>(A.rot.table) + pr);
+      cs[s * half + pair_slot(pr, A.rot.r, A.rot.interleaved)] = pair_angle(entry, [&](int axis) {
+        return token_position(A.pos, axis, b, (int)(j0 + s), A.B, A.n);
+      });
+    }
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = hg * 4 + (warp >> 1);
+  if (h >= A.pool.heads) {
+    __syncthreads();
+    return;
+  }
+  const int page = page_of(A.pool, b, tile);
+  unsigned char* blk = A.pool.base + pool_block(A.pool, page, h) * block_bytes(D);
+  const bool bad = (warp & 1) ? append_values<D, T>(A, blk, b, h, j0, lo, hi, held, lane)
+                              : append_keys<D, T>(A, blk, reinterpret_cast<const float4*>(cs), b, h, j0, lo, hi, held, lane);
+  if (bad && A.pool.err) atomicExch(A.pool.err, TQ_DEVERR_NONFINITE);
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) byte_dequantize_kernel(const Pool P, int b, int h, int t0, int t1, float* k, float* v) {
+  const long long total = (long long)(t1 - t0) * D;
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+    const int t = t0 + (int)(i / D), x = (int)(i % D);
+    const unsigned char* blk = P.base + pool_block(P, page_of(P, b, t >> 4), h) * block_bytes(D);
+    const float* s = reinterpret_cast<const float*>(blk + 32 * D);
+    k[i] = decode1(blk[k_chunk<D>(t & 15, x >> 4) + (x & 15)]) * s[0];
+    v[i] = decode1(blk[16 * D + 16 * x + v_slot(t & 15)]) * s[1];
+  }
+}
+
+// Tokens per block and heads per block of a rows pass: enough rows for a few passes of the block's
+// threads per set of cosines, unless that leaves SMs without a block; single tokens spread their
+// heads over blocks instead, one pass each.
+void rows_split(int d, int tokens, int heads, int* per, int* split) {
+  const int rpp = kThreads / (d / 16);
+  *split = heads;
+  *per = (6 * rpp + heads - 1) / heads;
+  const int fill = tokens / 608;  // four blocks on each of 152 SMs
+  if (*per > fill) *per = fill;
+  if (*per > 16) *per = 16;
+  if (*per < 1) *per = 1;
+  if (tokens <= 304 && heads > rpp) *split = rpp;
+}
+
+template <int D, typename T, typename O>
+cudaError_t rotate_go(const RotateArgs& a, cudaStream_t s) {
+  RotateParams p;
+  p.a = a;
+  p.tokens = a.B * a.n;
+  const int heads = a.q.heads + a.k.heads;
+  rows_split(D, p.tokens, heads, &p.per, &p.q_split);
+  const dim3 grid((p.tokens + p.per - 1) / p.per, (heads + p.q_split - 1) / p.q_split);
+  norm_rotate_kernel<D, T, O><<<grid, kThreads, (size_t)p.per * (a.rot.r / 2) * sizeof(float2), s>>>(p);
+  return cudaGetLastError();
+}
+template <int D, typename T>
+cudaError_t rotate_out(const RotateArgs& a, cudaStream_t s) {
+  return a.out_dtype == TQ_F32 ? rotate_go<D, T, float>(a, s) : rotate_go<D, T, T>(a, s);
+}
+template <int D>
+cudaError_t rotate_type(const RotateArgs& a, cudaStream_t s) {
+  if (a.dtype == TQ_F32) return rotate_go<D, float, float>(a, s);
+  if (a.dtype == TQ_BF16) return rotate_out<D, __nv_bfloat16>(a, s);
+  return rotate_out<D, __half>(a, s);
+}
+
+template <int D, typename T>
+cudaError_t append_go(const AppendArgs& a, cudaStream_t s) {
+  AppendParams p;
+  p.a = a;
+  p.blocks = (15 + a.n + 15) / 16;
+  p.groups = (a.pool.heads + 3) / 4;
+  p.kv_blocks = a.B * p.blocks * p.groups;
+  p.tokens = a.B * a.n;
+  p.per = 1;
+  p.q_split = p.q_groups = 1;
+  int q_blocks = 0;
+  if (a.q.heads) {
+    rows_split(D, p.tokens, a.Hq, &p.per, &p.q_split);
+    p.q_groups = (a.Hq + p.q_split - 1) / p.q_split;
+    q_blocks = (p.tokens + p.per - 1) / p.per * p.q_groups;
+  }
+  const int tk = p.per > 16 ? p.per : 16;
+  byte_append_kernel<D, T><<<p.kv_blocks + q_blocks, kThreads, (size_t)tk * (a.rot.r / 2) * sizeof(float2), s>>>(p);
+  return cudaGetLastError();
+}
+template <int D>
+cudaError_t append_type(const AppendArgs& a, cudaStream_t s) {
+  if (a.dtype == TQ_F32) return append_go<D, float>(a, s);
+  if (a.dtype == TQ_BF16) return append_go<D, __nv_bfloat16>(a, s);
+  return append_go<D, __half>(a, s);
+}
+
+}  // namespace
+
+tq_status cuda_error(const char* what, int e) {
+  if (e == 0) return TQ_OK;
+  tqi::set_error(std::string(what) + ": " + cudaGetErrorString((cudaError_t)e));
+  return TQ_ERR_CUDA;
+}
+
+tq_status launch_norm_rotate(const RotateArgs& a, Stream s) {
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (a.d) {
+    case 64: e = rotate_type<64>(a, (cudaStream_t)s); break;
+    case 128: e = rotate_type<128>(a, (cudaStream_t)s); break;
+    case 256: e = rotate_type<256>(a, (cudaStream_t)s); break;
+    case 512: e = rotate_type<512>(a, (cudaStream_t)s); break;
+  }
+  return cuda_error("norm_rotate", e);
+}
+
+tq_status launch_byte_append(const AppendArgs& a, Stream s) {
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (a.d) {
+    case 64: e = append_type<64>(a, (cudaStream_t)s); break;
+    case 128: e = append_type<128>(a, (cudaStream_t)s); break;
+    case 256: e = append_type<256>(a, (cudaStream_t)s); break;
+  }
+  return cuda_error("byte append", e);
+}
+
+tq_status launch_byte_dequantize(const Pool& pool, int d, int b, int h, int t0, int t1, float* k, float* v, Stream s) {
+  const long long total = (long long)(t1 - t0) * d;
+  const int grid = (int)(total / 256 + 1 < 1216 ? total / 256 + 1 : 1216);
+  switch (d) {
+    case 64: byte_dequantize_kernel<64><<<grid, 256, 0, (cudaStream_t)s>>>(pool, b, h, t0, t1, k, v); break;
+    case 128: byte_dequantize_kernel<128><<<grid, 256, 0, (cudaStream_t)s>>>(pool, b, h, t0, t1, k, v); break;
+    case 256: byte_dequantize_kernel<256><<<grid, 256, 0, (cudaStream_t)s>>>(pool, b, h, t0, t1, k, v); break;
+  }
+  return cuda_error("byte dequantize", cudaGetLastError());
+}
+
+}  // namespace tqb

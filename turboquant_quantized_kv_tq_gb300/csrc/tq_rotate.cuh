@@ -1,0 +1,179 @@
+// One pass over a row of D coordinates: RMS norm and position rotation (fp32).
+//
+// D / 16 threads share a row; thread l holds two chunks of 8 coordinates.  With r = rotary_dim,
+// threads l < r / 16 hold chunks l and l + r / 16 -- with "halves" pairing the two members of
+// eight pairs, with "interleaved" pairing two groups of four whole pairs -- and the other threads
+// the unrotated rest.  So a rotation never needs a neighbour's value, and every load and store is
+// 16 bytes (16-bit types) of a contiguous run.
+//
+// The angle of a pair is position * frequency in turns modulo 1, in 64-bit fixed point: the product
+// of the 64-bit fraction with the position wraps exactly, its top 32 bits are the signed fraction
+// of a turn to 2^-32 (an angle error of 2^-33 turns for any position, plus the frequency's own
+// rounding of 2^-63 turns per position), and sincospi of that fp32 fraction needs no range
+// reduction.  A table of cosines by position would be 64 MB at 131072 positions and d = 128; the
+// cosines of a token are instead computed once per block and shared by all its heads.
+#pragma once
+
+#include <type_traits>
+
+#include "tq_byte.h"
+#include "tq_device.cuh"
+
+namespace tqb {
+
+using tqd::kFull;
+
+template <typename T>
+struct Raw8 {  // 8 elements as loaded
+  uint4 v[sizeof(T) * 8 / 16];
+};
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> load8(const T* p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) * 8 / 16); ++i) r.v[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  return r;
+}
+// (no read-only path: a buffer that the same launch may overwrite, row by row)
+template <typename T>
+__device__ __forceinline__ Raw8<T> load8_rw(const T* p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) * 8 / 16); ++i) r.v[i] = *(reinterpret_cast<const uint4*>(p) + i);
+  return r;
+}
+
+__device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x[4 * i] = __uint_as_float(r.v[i].x);
+    x[4 * i + 1] = __uint_as_float(r.v[i].y);
+    x[4 * i + 2] = __uint_as_float(r.v[i].z);
+    x[4 * i + 3] = __uint_as_float(r.v[i].w);
+  }
+}
+__device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16>& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void unpack8(const Raw8<__half>& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(__half* p, const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = tqd::pack_half2(x[2 * i], x[2 * i + 1]);
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The chunks (of 8 coordinates) that thread l of a row holds.
+__device__ __forceinline__ int chunk_a(int l, int r) { return l < r / 16 ? l : r / 8 + 2 * (l - r / 16); }
+__device__ __forceinline__ int chunk_b(int l, int r) { return l < r / 16 ? l + r / 16 : r / 8 + 2 * (l - r / 16) + 1; }
+
+// Cosines and sines of one token lie in shared memory as [4][r / 16] groups of two pairs
+// (cos, sin, cos, sin): group j of thread l at j * (r / 16) + l, so that the threads of a row read
+// consecutive 16-byte words.  float2 index of pair p:
+__device__ __forceinline__ int pair_slot(int p, int r, int interleaved) {
+  int l, j;
+  if (!interleaved) {
+    l = p >> 3;
+    j = (p & 7) >> 1;
+  } else {
+    const int hi = p >= r / 4;
+    const int u = p - (hi ? r / 4 : 0);
+    l = u >> 2;
+    j = 2 * hi + ((u & 3) >> 1);
+  }
+  return 2 * (j * (r / 16) + l) + (p & 1);
+}
+
+// (cos, sin) of one pair at the token whose positions on axis a are pos(a).
+template <typename F>
+__device__ __forceinline__ float2 pair_angle(uint64_t entry, F pos) {
+  const long long at = pos((int)(entry & 3u));
+  const uint64_t turns = (entry & ~3ull) * (uint64_t)at;              // modulo one turn
+  // signed fraction of a turn in [-1/2, 1/2), as half-turns for sincospi
+  const float x = (float)(int32_t)(uint32_t)((turns + 0x80000000ull) >> 32) * 4.656612873077393e-10f;  // 2^-31
+  float2 cs;
+  sincospif(x, &cs.y, &cs.x);
+  return cs;
+}
+
+// Norm (w non-null: a, b of the row's weight chunks) and rotation of one row's values.
+template <int TPR>
+__device__ __forceinline__ void norm_rotate_row(float (&a)[8], float (&b)[8], int l, bool norm, const float (&wa)[8],
+                                                const float (&wb)[8], int D, float eps, const float4* cs, int r,
+                                                int interleaved) {
+  if (norm) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
+#pragma unroll
+    for (int m = 1; m < TPR; m <<= 1) ss += __shfl_xor_sync(kFull, ss, m);
+    const float rs = rsqrtf(ss / (float)D + eps);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      a[i] = a[i] * rs * wa[i];
+      b[i] = b[i] * rs * wb[i];
+    }
+  }
+  if (l < r / 16) {
+    float c[8], s[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 v = cs[j * (r / 16) + l];
+      c[2 * j] = v.x; s[2 * j] = v.y; c[2 * j + 1] = v.z; s[2 * j + 1] = v.w;
+    }
+    if (!interleaved) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float x = a[i], y = b[i];
+        a[i] = x * c[i] - y * s[i];
+        b[i] = x * s[i] + y * c[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float x = a[2 * i], y = a[2 * i + 1];
+        a[2 * i] = x * c[i] - y * s[i];
+        a[2 * i + 1] = x * s[i] + y * c[i];
+        x = b[2 * i], y = b[2 * i + 1];
+        b[2 * i] = x * c[4 + i] - y * s[4 + i];
+        b[2 * i + 1] = x * s[4 + i] + y * c[4 + i];
+      }
+    }
+  }
+}
+
+// Position of token j of batch entry b on axis a.
+__device__ __forceinline__ long long token_position(const Positions& P, int axis, int b, int j, int B, int n) {
+  if (P.pos) return __ldg(P.pos + ((long long)axis * B + b) * n + j);
+  return (long long)(P.start ? __ldg(P.start + b) : 0) + j;
+}
+
+}  // namespace tqb
