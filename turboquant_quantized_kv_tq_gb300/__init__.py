@@ -276,5 +276,6 @@ def __getattr__(name):
     # (torch is imported with the first use, as for the classes above)
     if name in ("PagedByteCache", "Rotary", "norm_rotate"):
         from . import byte_cache
-        return getattr(byte_cache, name)
+        globals()[name] = value = getattr(byte_cache, name)
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -2,13 +2,15 @@
 // mma.sync kernel for chunks where the tensor-memory kernel is not built.
 //
 // split_kernel: bound by HBM -- every code is read once, 4 d flops per byte and row.  The tiles
-// (16-token blocks) of all slabs (batch entry, KV head, group of 8 NR rows) form one sequence that
-// is cut into equal contiguous ranges, one per resident block, so the load is even whatever the
-// lengths are.  Each warp streams its own tiles through its own ring of bulk copies: a block of the
+// (16-token blocks) of all slabs (batch entry, KV head, group of 8 NR rows), each slab followed by
+// kSlabCost virtual tiles for the work it costs a block beside its tiles (queries, the join of the
+// warps), form one sequence that is cut into equal contiguous ranges, one per resident block, so the
+// load is even whatever the lengths are.  Each warp streams its own tiles through its own ring of bulk copies: a block of the
 // pool is contiguous, codes and scales in one copy.  Warps meet only at the end of a slab's range.
 // Ranges that cover part of a slab leave (M, l, O) in the workspace for merge_kernel, which is
 // launched early and waits for this grid.
 // rows_kernel: 8 warps of 8 NR rows share one ring; each tile is read once per 64 NR rows.
+#include <atomic>
 #include <string>
 
 #include "tq_byte_attn.cuh"
@@ -19,6 +21,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kMaxGrid = 512;  // resident blocks of the split, at most (the workspace is sized for it)
 constexpr int kMinTiles = 8;   // tiles of a range, at least: one per warp
+constexpr int kSlabCost = 8;   // virtual tiles of a slab
 
 struct AttnParams {
   AttnArgs a;
@@ -27,7 +30,8 @@ struct AttnParams {
   int grid;              // blocks of the split
 };
 
-// Tiles before each batch entry, in the order entry, head, row group; the split's range length.
+// Tiles (virtual ones included) before each batch entry, in the order entry, head, row group; the
+// split's range length.
 struct Plan {
   long long total, per;
 };
@@ -41,8 +45,10 @@ __device__ __forceinline__ Plan make_plan(const AttnParams& p, long long* pre) {
     for (int b0 = 0; b0 < p.a.B; b0 += 32) {
       const int b = b0 + lane;
       long long t = 0;
-      if (b < p.a.B && clamped_count(p.a.count, b, p.a.nq) > 0)
-        t = (long long)((clamped_len(p.a.seq_len, b, most, blockIdx.x == 0 ? p.a.pool.err : nullptr) + 15) >> 4) * per_tile;
+      if (b < p.a.B && clamped_count(p.a.count, b, p.a.nq) > 0) {
+        const int len = clamped_len(p.a.seq_len, b, most, blockIdx.x == 0 ? p.a.pool.err : nullptr);
+        if (len > 0) t = (((len + 15) >> 4) + kSlabCost) * per_tile;
+      }
 #pragma unroll
       for (int m = 1; m < 32; m <<= 1) {
         const long long o = __shfl_up_sync(kFull, t, m);
@@ -60,24 +66,26 @@ __device__ __forceinline__ Plan make_plan(const AttnParams& p, long long* pre) {
   return P;
 }
 
-// A stretch of one slab.
+// A stretch of one slab: tiles [t0, t1) of its `tiles`; next: where the following stretch begins.
 struct Seg {
   int b, h, rg;
-  int t0, t1;   // tiles of the slab
-  int tiles;    // the slab's tiles
-  long long slab;
+  int t0, t1, tiles;
+  long long slab, next;
 };
-// The stretch that begins at tile `at` (< end) of the sequence; b: the entry to look from.
+// The stretch that begins at tile `at` (< end) of the sequence, empty where only virtual tiles are
+// left; b: the entry to look from.
 __device__ __forceinline__ Seg seg_at(const AttnParams& p, const long long* pre, long long at, long long end, int b) {
   while (pre[b + 1] <= at) ++b;
   Seg s;
   s.b = b;
   const int slabs = p.a.Hkv * p.groups;
-  s.tiles = (int)((pre[b + 1] - pre[b]) / slabs);
+  const int span = (int)((pre[b + 1] - pre[b]) / slabs);
+  s.tiles = span - kSlabCost;
   const long long off = at - pre[b];
-  const int k = (int)(off / s.tiles);
-  s.t0 = (int)(off - (long long)k * s.tiles);
-  s.t1 = (int)min((long long)s.tiles, s.t0 + (end - at));
+  const int k = (int)(off / span), x = (int)(off - (long long)k * span);
+  s.t0 = min(x, s.tiles);
+  s.t1 = (int)min((long long)s.tiles, x + (end - at));
+  s.next = min(end, at + (span - x));
   s.h = k / p.groups;
   s.rg = k - s.h * p.groups;
   s.slab = (long long)b * slabs + k;
@@ -151,7 +159,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Cfg<D, NR, TERMS>::TWO ? 2 : 1))
   uint32_t issued = 0;
   auto issue = [&]() {  // the warp's next tile into the next stage, if there is one
     while (c_more && c_t >= c.t1) {
-      c_at += c.t1 - c.t0;
+      c_at = c.next;
       if (c_at >= end) {
         c_more = false;
       } else {
@@ -184,6 +192,8 @@ __global__ void __launch_bounds__(kWarps * 32, (Cfg<D, NR, TERMS>::TWO ? 2 : 1))
   while (at < end) {
     const Seg s = seg_at(p, pre, at, end, b_from);
     b_from = s.b;
+    at = s.next;
+    if (s.t0 == s.t1) continue;
     const int len = min(max(__ldg(A.seq_len + s.b), 0), most), cnt = clamped_count(A.count, s.b, A.nq);
     const int row0 = s.rg * 8 * NR;
     QFrag<D, NR, TERMS> q;
@@ -284,7 +294,6 @@ __global__ void __launch_bounds__(kWarps * 32, (Cfg<D, NR, TERMS>::TWO ? 2 : 1))
       }
       __syncthreads();
     }
-    at += s.t1 - s.t0;
   }
   if (!alive)  // copies still in flight must land before the block's shared memory is given up
     for (uint32_t i = landed; i < issued; ++i) tqd::mbar_wait(bar0 + 8 * (i % C::STAGES), (i / C::STAGES) & 1, kWaitLimit);
@@ -303,9 +312,9 @@ __global__ void __launch_bounds__(D) merge_kernel(const AttnParams p) {
   const AttnArgs& A = p.a;
   const int slabs = A.Hkv * p.groups, slab = blockIdx.x, b = slab / slabs, k = slab - b * slabs;
   const int h = k / p.groups, rg = k - h * p.groups, row = blockIdx.y, rr = rg * 8 * NR + row;
-  const long long tiles = (pre[b + 1] - pre[b]) / slabs;
-  if (tiles == 0 || rr >= p.rows) return;
-  const long long g0 = pre[b] + k * tiles, c0 = g0 / P.per, c1 = (g0 + tiles - 1) / P.per;
+  const long long span = (pre[b + 1] - pre[b]) / slabs;
+  if (span == 0 || rr >= p.rows) return;
+  const long long g0 = pre[b] + k * span, c0 = g0 / P.per, c1 = (g0 + span - kSlabCost - 1) / P.per;
   if (c0 == c1) return;
   const float* part = p.part + (c0 + slab) * PART;
   const int n = (int)(c1 - c0 + 1), d = threadIdx.x;
@@ -434,11 +443,26 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) rows_kernel(const AttnPa
   __syncthreads();
 }
 
-int sm_count() {
+// SMs of the current device, and its index (looked up once per device).
+int sm_count(int* device) {
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 152;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 152;
+  if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
+  *device = dev;
+  if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (dev < 0 || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 152;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
+}
+
+// Lets a kernel use `bytes` of shared memory on the device, once per kernel and device (`done`:
+// the kernel's own bit set; `bytes` is then its largest).
+cudaError_t allow_smem(const void* kernel, int bytes, int device, std::atomic<uint64_t>& done) {
+  const uint64_t bit = device >= 0 && device < 64 ? 1ull << device : 0;
+  if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 // Rows per warp: 16 where the registers hold them and there are more than 8.
@@ -450,13 +474,15 @@ cudaError_t split_go(AttnParams p, cudaStream_t s) {
   static_assert(C::STAGES >= 2, "ring");
   p.groups = (p.rows + 8 * NR - 1) / (8 * NR);
   const long long most = (long long)p.a.B * p.a.Hkv * p.groups * p.a.pool.max_blocks;
-  long long grid = (long long)sm_count() * (C::TWO ? 2 : 1);
+  static std::atomic<uint64_t> done{0};
+  int dev;
+  long long grid = (long long)sm_count(&dev) * (C::TWO ? 2 : 1);
   if (grid > kMaxGrid) grid = kMaxGrid;
-  const long long need = (most + kMinTiles - 1) / kMinTiles;
+  const long long need = (most + (long long)p.a.B * p.a.Hkv * p.groups * kSlabCost + kMinTiles - 1) / kMinTiles;
   if (grid > need) grid = need;
   p.grid = (int)grid;
   const int smem = C::smem(p.a.B);
-  cudaError_t e = cudaFuncSetAttribute(split_kernel<D, NR, TERMS, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_smem((const void*)split_kernel<D, NR, TERMS, T>, C::smem(TQ_MAX_BATCH), dev, done);
   if (e != cudaSuccess) return e;
   split_kernel<D, NR, TERMS, T><<<p.grid, kWarps * 32, smem, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -477,7 +503,10 @@ cudaError_t split_go(AttnParams p, cudaStream_t s) {
 template <int D, int NR, int TERMS, typename T>
 cudaError_t rows_go(AttnParams p, cudaStream_t s) {
   using C = RowsCfg<D, NR, TERMS>;
-  cudaError_t e = cudaFuncSetAttribute(rows_kernel<D, NR, TERMS, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static std::atomic<uint64_t> done{0};
+  int dev;
+  sm_count(&dev);
+  cudaError_t e = allow_smem((const void*)rows_kernel<D, NR, TERMS, T>, C::SMEM, dev, done);
   if (e != cudaSuccess) return e;
   const dim3 grid((p.rows + kWarps * 8 * NR - 1) / (kWarps * 8 * NR), p.a.Hkv, p.a.B);
   rows_kernel<D, NR, TERMS, T><<<grid, (kWarps + 1) * 32, C::SMEM, s>>>(p);
