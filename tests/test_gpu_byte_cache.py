@@ -285,6 +285,27 @@ def test_attention_chunks(dtype, d, hq, hkv, nq):
     assert c.device_error() == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("hq,hkv,nq,lens,count", [
+    (8, 2, 32, [32, 1000, 129], None), (8, 2, 33, [33, 4000, 128], [33, 20, 0]), (6, 2, 128, [128, 127, 300], [128, 100, 1]),
+    (4, 4, 300, [300, 2000, 301], None), (16, 1, 50, [777, 64, 50], [50, 7, 50]), (3, 1, 400, [400], None)])
+def test_attention_row_groups(dtype, hq, hkv, nq, lens, count):
+    """Row groups that end inside a block's rows, ranges that end inside a group's tokens."""
+    c, table, pool = _filled(128, hq, hkv, lens, DT[dtype], seed=nq + 1)
+    B = len(lens)
+    q = torch.randn(B, nq, hq, 128, device="cuda").to(DT[dtype])
+    out = c.attention(q, _i32(lens), _i32(table), count=None if count is None else _i32(count))
+    cnt = count or [nq] * B
+    want, spread, reach = ref.attention(_np(q), pool, lens, cnt, table, 128 ** -0.5)
+    _check_attention(out, want, spread, reach, max(lens), 128, DT[dtype])
+    # a negative and a zero scale
+    for scale in (-0.05, 0.0):
+        out = c.attention(q, _i32(lens), _i32(table), count=None if count is None else _i32(count), scale=scale)
+        want, spread, reach = ref.attention(_np(q), pool, lens, cnt, table, scale)
+        _check_attention(out, want, spread, reach, max(lens), 128, DT[dtype])
+    assert c.device_error() == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("nq", [1, 70])
 def test_attention_split_over_long_sequences(dtype, nq):

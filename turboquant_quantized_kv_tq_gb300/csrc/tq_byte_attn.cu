@@ -26,7 +26,7 @@ constexpr int kSlabCost = 8;   // virtual tiles of a slab
 struct AttnParams {
   AttnArgs a;
   int G, rows, groups;   // query heads per KV head, rows per KV head, row groups of 8 NR
-  float* part;           // partials: [slot](M[8 NR], l[8 NR], O[8 NR][D])
+  float* part;           // partials: [block][first stretch, last](M[8 NR], l[8 NR], O[8 NR][D])
   int grid;              // blocks of the split
 };
 
@@ -70,7 +70,7 @@ __device__ __forceinline__ Plan make_plan(const AttnParams& p, long long* pre) {
 struct Seg {
   int b, h, rg;
   int t0, t1, tiles;
-  long long slab, next;
+  long long next;
 };
 // The stretch that begins at tile `at` (< end) of the sequence, empty where only virtual tiles are
 // left; b: the entry to look from.
@@ -88,7 +88,6 @@ __device__ __forceinline__ Seg seg_at(const AttnParams& p, const long long* pre,
   s.next = min(end, at + (span - x));
   s.h = k / p.groups;
   s.rg = k - s.h * p.groups;
-  s.slab = (long long)b * slabs + k;
   return s;
 }
 // Entry that holds tile `at`.
@@ -192,6 +191,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Cfg<D, NR, TERMS>::TWO ? 2 : 1))
   while (at < end) {
     const Seg s = seg_at(p, pre, at, end, b_from);
     b_from = s.b;
+    const int place = at == begin ? 0 : 1;  // (a stretch that is neither the first nor the last covers its slab)
     at = s.next;
     if (s.t0 == s.t1) continue;
     const int len = min(max(__ldg(A.seq_len + s.b), 0), most), cnt = clamped_count(A.count, s.b, A.nq);
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Cfg<D, NR, TERMS>::TWO ? 2 : 1))
         f[r][k] = ex2(st.m[r][k] - (mt == -INFINITY ? 0.f : mt));
       }
     const bool whole = s.t0 == 0 && s.t1 == s.tiles;
-    float* part = p.part + (blockIdx.x + s.slab) * C::PART;
+    float* part = p.part + (2ll * blockIdx.x + place) * C::PART;
     constexpr int QD = D / 4, PITCH = QD + 4;
 #pragma unroll
     for (int qd = 0; qd < 4; ++qd) {
@@ -316,15 +316,17 @@ __global__ void __launch_bounds__(D) merge_kernel(const AttnParams p) {
   if (span == 0 || rr >= p.rows) return;
   const long long g0 = pre[b] + k * span, c0 = g0 / P.per, c1 = (g0 + span - kSlabCost - 1) / P.per;
   if (c0 == c1) return;
-  const float* part = p.part + (c0 + slab) * PART;
+  // the slab's stretch is its range's first one except perhaps in range c0
+  const float* part = p.part + 2 * c0 * PART;
+  const long long head = g0 == c0 * P.per ? 0 : PART;
   const int n = (int)(c1 - c0 + 1), d = threadIdx.x;
   float mt = -INFINITY;
-  for (int i = 0; i < n; ++i) mt = fmaxf(mt, part[(long long)i * PART + row]);
+  for (int i = 0; i < n; ++i) mt = fmaxf(mt, part[i ? 2ll * i * PART + row : head + row]);
   const float mr = mt == -INFINITY ? 0.f : mt;
   float l = 0.f, o = 0.f;
 #pragma unroll 8
   for (int i = 0; i < n; ++i) {
-    const float* x = part + (long long)i * PART;
+    const float* x = part + (i ? 2ll * i * PART : head);
     const float w = ex2(x[row] - mr);
     l = fmaf(x[8 * NR + row], w, l);
     o = fmaf(x[16 * NR + row * D + d], w, o);
@@ -443,28 +445,6 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) rows_kernel(const AttnPa
   __syncthreads();
 }
 
-// SMs of the current device, and its index (looked up once per device).
-int sm_count(int* device) {
-  static std::atomic<int> known[64];
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
-  *device = dev;
-  if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
-  if (dev < 0 || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 152;
-  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
-  return n;
-}
-
-// Lets a kernel use `bytes` of shared memory on the device, once per kernel and device (`done`:
-// the kernel's own bit set; `bytes` is then its largest).
-cudaError_t allow_smem(const void* kernel, int bytes, int device, std::atomic<uint64_t>& done) {
-  const uint64_t bit = device >= 0 && device < 64 ? 1ull << device : 0;
-  if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-  return e;
-}
-
 // Rows per warp: 16 where the registers hold them and there are more than 8.
 int row_groups_of(int d, int terms, int rows) { return rows > 8 && d <= 128 ? 2 : 1; }
 
@@ -536,14 +516,38 @@ cudaError_t attention_type(const AttnParams& p, cudaStream_t s) {
 
 }  // namespace
 
+// SMs of the current device, and its index (looked up once per device).
+int sm_count(int* device) {
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
+  *device = dev;
+  if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (dev < 0 || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 152;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// Lets a kernel use `bytes` of shared memory on the device, once per kernel and device (`done`:
+// the kernel's own bit set; `bytes` is then its largest).
+cudaError_t allow_smem(const void* kernel, int bytes, int device, std::atomic<uint64_t>& done) {
+  const uint64_t bit = device >= 0 && device < 64 ? 1ull << device : 0;
+  if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 size_t byte_attention_workspace(int d, int B, int nq, int Hq, int Hkv, tq_dtype dtype) {
   const int rows = Hq / Hkv * nq, nr = row_groups_of(d, dtype == TQ_F32 ? 2 : 1, rows);
   const int groups = (rows + 8 * nr - 1) / (8 * nr);
-  if (use_rows(groups)) return 256;
-  return ((size_t)kMaxGrid + (size_t)B * Hkv * groups) * 8 * nr * (d + 2) * sizeof(float) + 256;
+  size_t need = use_rows(groups) ? 256 : (size_t)2 * kMaxGrid * 8 * nr * (d + 2) * sizeof(float);
+  if (d == 128 && dtype != TQ_F32 && rows > kTcMinRows && tc_workspace(rows) > need) need = tc_workspace(rows);
+  return need;
 }
 
 tq_status launch_byte_attention(const AttnArgs& a, Stream s) {
+  if (tc_takes(a)) return cuda_error("byte attention", launch_tc(a, (cudaStream_t)s));
   AttnParams p;
   p.a = a;
   p.G = a.Hq / a.Hkv;

@@ -17,6 +17,8 @@
 // codes per shared-memory load, and V's stored token order is that of the P operand.
 #pragma once
 
+#include <atomic>
+
 #include "tq_byte.cuh"
 
 namespace tqb {
@@ -236,6 +238,17 @@ __device__ __forceinline__ T from_float(float x);
 template <> __device__ __forceinline__ float from_float<float>(float x) { return x; }
 template <> __device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// Host side (tq_byte_attn.cu): SMs of the current device and its index; a kernel's permission for its
+// shared memory, once per kernel and device.
+int sm_count(int* device);
+cudaError_t allow_smem(const void* kernel, int bytes, int device, std::atomic<uint64_t>& done);
+// The tensor-memory kernel (tq_byte_tc.cu): whether it takes a call, its workspace, its launch.
+constexpr int kMaxSms = 160;
+constexpr int kTcMinRows = 64;
+bool tc_takes(const AttnArgs& a);
+size_t tc_workspace(int rows);
+cudaError_t launch_tc(const AttnArgs& a, cudaStream_t s);
 
 // Length and count of sequence b as the kernels use them.
 __device__ __forceinline__ int clamped_len(const int32_t* seq_len, int b, int most, int32_t* err) {
