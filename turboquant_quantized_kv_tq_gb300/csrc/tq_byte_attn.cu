@@ -7,7 +7,7 @@
 // warps), form one sequence that is cut into equal contiguous ranges, one per resident block, so the
 // load is even whatever the lengths are.  Each warp streams its own tiles through its own ring of bulk copies: a block of the
 // pool is contiguous, codes and scales in one copy.  Warps meet only at the end of a slab's range.
-// Ranges that cover part of a slab leave (M, l, O) in the workspace for merge_kernel, which is
+// Ranges that cover part of a slab leave (M, l, O) in the workspace for join_kernel, which is
 // launched early and waits for this grid.
 // rows_kernel: 8 warps of 8 NR rows share one ring; each tile is read once per 64 NR rows.
 #include <atomic>
@@ -27,6 +27,7 @@ struct AttnParams {
   AttnArgs a;
   int G, rows, groups;   // query heads per KV head, rows per KV head, row groups of 8 NR
   float* part;           // partials: [block][first stretch, last](M[8 NR], l[8 NR], O[8 NR][D])
+  JoinHead* heads;
   int grid;              // blocks of the split
 };
 
@@ -66,11 +67,12 @@ __device__ __forceinline__ Plan make_plan(const AttnParams& p, long long* pre) {
   return P;
 }
 
-// A stretch of one slab: tiles [t0, t1) of its `tiles`; next: where the following stretch begins.
+// A stretch of one slab: tiles [t0, t1) of its `tiles`; next: where the following stretch begins;
+// start: where the slab does.
 struct Seg {
   int b, h, rg;
   int t0, t1, tiles;
-  long long next;
+  long long start, next;
 };
 // The stretch that begins at tile `at` (< end) of the sequence, empty where only virtual tiles are
 // left; b: the entry to look from.
@@ -85,6 +87,7 @@ __device__ __forceinline__ Seg seg_at(const AttnParams& p, const long long* pre,
   const int k = (int)(off / span), x = (int)(off - (long long)k * span);
   s.t0 = min(x, s.tiles);
   s.t1 = (int)min((long long)s.tiles, x + (end - at));
+  s.start = at - x;
   s.next = min(end, at + (span - x));
   s.h = k / p.groups;
   s.rg = k - s.h * p.groups;
@@ -143,7 +146,11 @@ __global__ void __launch_bounds__(kWarps * 32, (Cfg<D, NR, TERMS>::TWO ? 2 : 1))
           out[(long long)b * A.nq * A.Hq * D + i] = from_float<T>(0.f);
   }
   const long long begin = blockIdx.x * P.per, end = min(P.total, begin + P.per);
-  if (begin >= end) return;
+  bool headed = false;
+  if (begin >= end) {
+    if (threadIdx.x == 0) p.heads[blockIdx.x].last = -1;
+    return;
+  }
 
   // the warp's cursor of copies: runs ahead of the computation, across stretches
   long long c_at = begin;
@@ -294,46 +301,14 @@ __global__ void __launch_bounds__(kWarps * 32, (Cfg<D, NR, TERMS>::TWO ? 2 : 1))
       }
       __syncthreads();
     }
+    if (threadIdx.x == 0 && s.t0 == 0 && s.t1 < s.tiles) {  // this range's last stretch begins a slab that goes on
+      p.heads[blockIdx.x] = JoinHead{(int)((s.start + s.tiles - 1) / P.per), place, s.b, s.h, s.rg};
+      headed = true;
+    }
   }
+  if (threadIdx.x == 0 && !headed) p.heads[blockIdx.x].last = -1;
   if (!alive)  // copies still in flight must land before the block's shared memory is given up
     for (uint32_t i = landed; i < issued; ++i) tqd::mbar_wait(bar0 + 8 * (i % C::STAGES), (i / C::STAGES) & 1, kWaitLimit);
-}
-
-// Joins the partials of one row of one slab: weights 2^(M_i - max M).
-template <int D, int NR, typename T>
-__global__ void __launch_bounds__(D) merge_kernel(const AttnParams p) {
-  extern __shared__ __align__(128) unsigned char sm[];
-  long long* pre = reinterpret_cast<long long*>(sm);
-  constexpr int PART = 8 * NR * (D + 2);
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  AttnParams q = p;
-  q.a.pool.err = nullptr;  // (recorded by the split already)
-  const Plan P = make_plan(q, pre);
-  const AttnArgs& A = p.a;
-  const int slabs = A.Hkv * p.groups, slab = blockIdx.x, b = slab / slabs, k = slab - b * slabs;
-  const int h = k / p.groups, rg = k - h * p.groups, row = blockIdx.y, rr = rg * 8 * NR + row;
-  const long long span = (pre[b + 1] - pre[b]) / slabs;
-  if (span == 0 || rr >= p.rows) return;
-  const long long g0 = pre[b] + k * span, c0 = g0 / P.per, c1 = (g0 + span - kSlabCost - 1) / P.per;
-  if (c0 == c1) return;
-  // the slab's stretch is its range's first one except perhaps in range c0
-  const float* part = p.part + 2 * c0 * PART;
-  const long long head = g0 == c0 * P.per ? 0 : PART;
-  const int n = (int)(c1 - c0 + 1), d = threadIdx.x;
-  float mt = -INFINITY;
-  for (int i = 0; i < n; ++i) mt = fmaxf(mt, part[i ? 2ll * i * PART + row : head + row]);
-  const float mr = mt == -INFINITY ? 0.f : mt;
-  float l = 0.f, o = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < n; ++i) {
-    const float* x = part + (i ? 2ll * i * PART : head);
-    const float w = ex2(x[row] - mr);
-    l = fmaf(x[8 * NR + row], w, l);
-    o = fmaf(x[16 * NR + row * D + d], w, o);
-  }
-  const int qi = rr / p.G, hd = h * p.G + rr - qi * p.G;
-  reinterpret_cast<T*>(A.out)[(((long long)b * A.nq + qi) * A.Hq + hd) * D + d] =
-      from_float<T>(l > 0.f || l != l ? o / l : 0.f);
 }
 
 template <int D, int NR, int TERMS>
@@ -466,18 +441,18 @@ cudaError_t split_go(AttnParams p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   split_kernel<D, NR, TERMS, T><<<p.grid, kWarps * 32, smem, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (p.grid == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   const int rows = p.rows < 8 * NR ? p.rows : 8 * NR;
-  cfg.gridDim = dim3(p.a.B * p.a.Hkv * p.groups, rows);
-  cfg.blockDim = dim3(D);
-  cfg.dynamicSmemBytes = (p.a.B + 1) * 8;
+  cfg.gridDim = dim3(p.grid - 1, (rows + kJoinRows - 1) / kJoinRows);
+  cfg.blockDim = dim3(32 * kJoinRows);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel<D, NR, T>, p);
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, 8 * NR, T>, JoinParams{p.heads, p.part, p.a.out, p.a.nq, p.a.Hq, p.G, p.rows});
 }
 
 template <int D, int NR, int TERMS, typename T>
@@ -541,7 +516,7 @@ cudaError_t allow_smem(const void* kernel, int bytes, int device, std::atomic<ui
 size_t byte_attention_workspace(int d, int B, int nq, int Hq, int Hkv, tq_dtype dtype) {
   const int rows = Hq / Hkv * nq, nr = row_groups_of(d, dtype == TQ_F32 ? 2 : 1, rows);
   const int groups = (rows + 8 * nr - 1) / (8 * nr);
-  size_t need = use_rows(groups) ? 256 : (size_t)2 * kMaxGrid * 8 * nr * (d + 2) * sizeof(float);
+  size_t need = use_rows(groups) ? 256 : kJoinHeadBytes + (size_t)2 * kMaxGrid * 8 * nr * (d + 2) * sizeof(float);
   if (d == 128 && dtype != TQ_F32 && rows > kTcMinRows && tc_workspace(rows) > need) need = tc_workspace(rows);
   return need;
 }
@@ -554,7 +529,8 @@ tq_status launch_byte_attention(const AttnArgs& a, Stream s) {
   p.rows = p.G * a.nq;
   p.groups = 0;
   p.grid = 0;
-  p.part = (float*)a.ws;
+  p.heads = (JoinHead*)a.ws;
+  p.part = (float*)((unsigned char*)a.ws + kJoinHeadBytes);
   cudaError_t e = cudaErrorInvalidValue;
   switch (a.d) {
     case 64: e = attention_type<64>(p, (cudaStream_t)s); break;

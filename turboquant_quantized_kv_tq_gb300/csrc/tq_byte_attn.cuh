@@ -263,4 +263,62 @@ __device__ __forceinline__ int clamped_count(const int32_t* count, int b, int nq
 // Tokens that a row of query i attends to.
 __device__ __forceinline__ int row_limit(int i, int len, int cnt) { return i < cnt ? max(0, len - cnt + 1 + i) : 0; }
 
+// ---- The join of ranges that share a slab's rows.  A range (one block of the main kernel) covers a
+// contiguous stretch of slabs; where a slab goes on past its range's end, that range's head names the
+// slab and the last range that holds a part of it.  In every later range the part is the first
+// stretch (place 0), in the first one at place `place`.
+struct JoinHead {
+  int last;   // -1: no slab goes on past this range's end
+  int place;
+  int b, h, group;
+};
+constexpr int kJoinRows = 8;
+constexpr size_t kJoinHeadBytes = 16384;  // heads of up to 512 ranges, at the workspace's start
+static_assert(kJoinHeadBytes >= 512 * sizeof(JoinHead), "heads");
+
+struct JoinParams {
+  const JoinHead* heads;
+  const float* part;  // [range][2](M[ROWS], l[ROWS], O[ROWS][D])
+  void* out;
+  int nq, Hq, G, rows;
+};
+
+// A warp joins one row of the slab that goes on past range blockIdx.x: weights 2^(M_i - max M).
+template <int D, int ROWS, typename T>
+__global__ void __launch_bounds__(32 * kJoinRows) join_kernel(const JoinParams p) {
+  constexpr long long PART = (long long)ROWS * (D + 2);
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const int lane = threadIdx.x & 31, rr = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+  const JoinHead H = p.heads[blockIdx.x];
+  const int row = H.group * ROWS + rr;
+  if (H.last < 0 || rr >= ROWS || row >= p.rows) return;
+  const int n = H.last - (int)blockIdx.x + 1;
+  const float* first = p.part + (2ll * blockIdx.x + H.place) * PART;
+  const float* rest = p.part + 2ll * blockIdx.x * PART;  // part i >= 1 at rest + 2 i PART
+  auto at = [&](int i) { return i ? rest + 2ll * i * PART : first; };
+  float mt = -INFINITY;
+  for (int i = lane; i < n; i += 32) mt = fmaxf(mt, at(i)[rr]);
+  mt = tqd::warp_max(mt);
+  const float mr = mt == -INFINITY ? 0.f : mt;
+  float l = 0.f, o[D / 32] = {};
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float* x = at(i);
+    const float w = ex2(x[rr] - mr);
+    l = fmaf(x[ROWS + rr], w, l);
+    const float* v = x + 2 * ROWS + rr * D + lane * (D / 32);
+#pragma unroll
+    for (int k = 0; k < D / 32; k += 2) {
+      const float2 f = *reinterpret_cast<const float2*>(v + k);
+      o[k] = fmaf(f.x, w, o[k]);
+      o[k + 1] = fmaf(f.y, w, o[k + 1]);
+    }
+  }
+  const float il = l > 0.f || l != l ? 1.f / l : 0.f;
+  const int qi = row / p.G, hd = H.h * p.G + row - qi * p.G;
+  T* out = reinterpret_cast<T*>(p.out) + (((long long)H.b * p.nq + qi) * p.Hq + hd) * D + lane * (D / 32);
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) out[k] = from_float<T>(o[k] * il);
+}
+
 }  // namespace tqb

@@ -20,7 +20,9 @@
 // The (row group, token tile) pairs of all slabs form one sequence cut into equal ranges, one per
 // SM; ranges that share a row group leave partials that merge_tc_kernel joins.
 //
-// Warps: 0-7 rows, 8-11 V to fp16, 12 copies, 13 MMA issue.
+// Warps: 0-7 rows, 8-11 V to fp16, 12 copies, 13 MMA issue (14, 15 only complete the warpgroup that
+// gives registers to the rows: 192 a thread there, so that a row's 128 scores stay in registers from
+// the maximum to the probabilities, and 64 in the other warps).
 #include <atomic>
 #include <string>
 
@@ -34,7 +36,8 @@ using tqd::mbar_wait;
 
 constexpr int kTok = 128;          // tokens per tile
 constexpr int kD = 128;
-constexpr int kThreads = 448;
+constexpr int kThreads = 512;
+constexpr int kRowRegs = 192, kOtherRegs = 64;  // 256 * 192 + 256 * 64 = 512 * 128, the launch's registers
 constexpr int kGroupCost = 4;      // virtual tiles of a row group: what a range costs beside its tiles
 constexpr float kTop = 7.f;        // M lies this far below the maximum it was set from
 constexpr float kSlack = 15.f;     // M is raised when the maximum passes it by this: P <= 2^15
@@ -43,7 +46,8 @@ constexpr int kBlk = 32 * kD + 32;
 struct TcParams {
   AttnArgs a;
   int G, rows, groups;  // groups: row groups of a slab
-  float* part;
+  JoinHead* heads;  // [grid]
+  float* part;      // [grid][first stretch, last](M[ROWS], l[ROWS], O[ROWS][128])
   int grid;
 };
 
@@ -57,8 +61,9 @@ struct Plan {
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static constexpr int PART = ROWS * (kD + 2);                    // floats of a partial
 };
-enum Bar { K_FULL = 0, K_EMPTY = 2, VR_FULL = 4, VR_EMPTY = 6, V_FULL = 8, V_EMPTY = 10, S_FULL = 12, P_FULL = 14,
-           O_DONE = 16, Q_FULL = 18, SC_FULL = 20, SC_EMPTY = 24, BAR_COUNT = 28 };
+// (P_FULL: half h of row tile i at 2 i + h)
+enum Bar { K_FULL = 0, K_EMPTY = 2, VR_FULL = 4, VR_EMPTY = 6, V_FULL = 8, V_EMPTY = 10, S_FULL = 12, O_DONE = 14,
+           Q_FULL = 16, P_FULL = 18, SC_FULL = 22, SC_EMPTY = 26, BAR_COUNT = 30 };
 
 // 128-byte-swizzled K-major operand: rows of 128 bytes in groups of 8 (1024 bytes).
 __device__ __forceinline__ uint64_t sdesc128(uint32_t addr) {
@@ -167,32 +172,53 @@ __device__ __forceinline__ void store16(__half* dst, const float* x) {
   reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
+// 16 packed values as fp32.
+__device__ __forceinline__ void unpack16(const uint4& lo, const uint4& hi, float (&x)[16], const __nv_bfloat16*) {
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void unpack16(const uint4& lo, const uint4& hi, float (&x)[16], const __half*) {
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
 // One query row as NT e4m3 terms in the swizzled operand tiles at q (term t at q + 16384 t); returns
 // the factor of its scores, log2(e) |scale| 2^e (the sign of `scale` goes into the terms).
 template <typename T, int NT>
 __device__ __forceinline__ float query_row(const T* src, bool live, float scale, unsigned char* q, int r) {
+  uint4 raw[16];
+#pragma unroll
+  for (int c = 0; c < 16; ++c) raw[c] = live ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0u, 0u, 0u, 0u);
   float amax = 0.f;
-  bool odd = false;  // an infinity: the row's result is NaN, as the formula's is
-#pragma unroll 4
+#pragma unroll
   for (int c = 0; c < 8; ++c) {
     float x[16];
-    tqd::load_row<16>(src + 16 * c, x);
+    unpack16(raw[2 * c], raw[2 * c + 1], x, src);
 #pragma unroll
     for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(x[k]));
   }
-  odd = !(amax <= 3.402823466e38f);
+  const bool odd = !(amax <= 3.402823466e38f);  // an infinity: the row's result is NaN, as the formula's is
   const unsigned u = __float_as_uint(amax);
   int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);  // amax <= 448 2^e
   e = min(120, max(-120, e));
   if (amax == 0.f || odd) e = 0;
-  const float inv = live ? (scale < 0.f ? -exp2i(-e) : exp2i(-e)) : 0.f;
-#pragma unroll 2
+  const float inv = scale < 0.f ? -exp2i(-e) : exp2i(-e);
+#pragma unroll
   for (int c = 0; c < 8; ++c) {
     float x[16];
-    tqd::load_row<16>(src + 16 * c, x);
+    unpack16(raw[2 * c], raw[2 * c + 1], x, src);
     const int at = r * 128 + ((c ^ (r & 7)) << 4);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) x[k] = live ? x[k] * inv : 0.f;
+    for (int k = 0; k < 16; ++k) x[k] *= inv;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       uint32_t w[4];
@@ -213,7 +239,54 @@ __device__ __forceinline__ float query_row(const T* src, bool live, float scale,
       *reinterpret_cast<uint4*>(q + 16384 * t + at) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  return odd && live ? __uint_as_float(0x7fc00000u) : fabsf(scale) * kLog2e * exp2i(e);
+  return odd ? __uint_as_float(0x7fc00000u) : fabsf(scale) * kLog2e * exp2i(e);
+}
+
+// Pairs of fp32 values in one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// 32 columns of this thread's lane, without the wait for the load.
+__device__ __forceinline__ void ld32_async(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr));
+}
+// The wait, tied to the values it makes valid.
+__device__ __forceinline__ void ld_wait(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(v[i]));
+}
+// 32 columns stored, without the wait.
+__device__ __forceinline__ void st32_async(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n"
+      :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+         "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]),
+         "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]),
+         "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
 }
 
 template <typename T, int NT, int NQ>
@@ -242,7 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
       tqd::mbar_init(bar(V_FULL, i), 4);
       tqd::mbar_init(bar(V_EMPTY, i), 1);
       tqd::mbar_init(bar(S_FULL, i), 1);
-      tqd::mbar_init(bar(P_FULL, i), 128);
+      tqd::mbar_init(bar(P_FULL, 2 * i), 128);
+      tqd::mbar_init(bar(P_FULL, 2 * i + 1), 128);
       tqd::mbar_init(bar(O_DONE, i), 1);
       tqd::mbar_init(bar(Q_FULL, i), 128);
     }
@@ -266,6 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
     return ok;
   };
 
+  if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRowRegs));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
   if (warp < 4 * NQ) {
     // ---- rows
     const int i = warp >> 2, r = (warp & 3) * 32 + lane;
@@ -287,6 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
       }
     }
     int at = begin;
+    bool headed = false;
     while (at < end) {
       const Seg s = seg_at(p, L::ROWS, pre, at, end);
       const bool first = at == begin;
@@ -310,26 +387,32 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
         const unsigned char* sc = sm + L::SCALES + 128 * ss;
         const bool edge = kTok * (t + 1) > least;
         const int left = lim - kTok * t;  // columns of this tile that the row attends to
+        float v[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ld32_async(t_s + 32 * c, v + 32 * c);
+        float ka[8], kb[8];  // per block: the scores' factor, the value scale's exponent
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          const float2 kv = *reinterpret_cast<const float2*>(sc + 16 * g);
+          ka[g] = f * kv.x;
+          kb[g] = (float)log2i(kv.y);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ld_wait(v + 32 * c);
+        if (edge) {
+#pragma unroll
+          for (int k = 0; k < 128; ++k)
+            if (k >= left) v[k] = -INFINITY;
+        }
         float top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float v[32];
-          tqd::tc_ld32(t_s + 32 * c, v);
-          if (edge) {
+        for (int g = 0; g < 8; ++g) {
+          float m = v[16 * g];
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (32 * c + k >= left) v[k] = -INFINITY;
-          }
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const float2 kv = *reinterpret_cast<const float2*>(sc + 16 * (2 * c + g));
-            float m = v[16 * g];
-#pragma unroll
-            for (int k = 1; k < 16; ++k) m = fmaxf(m, v[16 * g + k]);
-            // (a group without a token of the row stays out: its scale may be anything)
-            const float cand = fmaf(m, f * kv.x, (float)log2i(kv.y));
-            top = m == -INFINITY ? top : fmaxf(top, cand);
-          }
+          for (int k = 1; k < 15; k += 2) m = fmaxf(m, fmaxf(v[16 * g + k], v[16 * g + k + 1]));
+          m = fmaxf(m, v[16 * g + 15]);
+          // (a block without a token of the row stays out: its scale may be anything)
+          top = m == -INFINITY ? top : fmaxf(top, fmaf(m, ka[g], kb[g]));
         }
         const bool raise = top > M + kSlack;
         if (__any_sync(kFull, raise)) {
@@ -340,48 +423,54 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
             l *= cor;
             if (!wait(bar(O_DONE, i), (n - 1) & 1)) break;
             tqd::tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              float o[16];
+              uint32_t w[16];
+              tqd::tc_ld16(t_o + 16 * c, o);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float v[32];
-              tqd::tc_ld32(t_o + 32 * c, v);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] *= cor;
-              tqd::tc_st32(t_o + 32 * c, v);
+              for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(o[k] * cor);
+              tqd::tc_st16(t_o + 16 * c, w);
             }
           }
         }
         const float mr = M == -INFINITY ? 0.f : M;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float v[32];
-          uint32_t w[16];
-          tqd::tc_ld32(t_s + 32 * c, v);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[32];
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const float2 kv = *reinterpret_cast<const float2*>(sc + 16 * (2 * c + g));
-            const int ev = log2i(kv.y);
-            const float a = f * kv.x, b = (float)ev - mr;
-            float x[16], sum = 0.f;
+          for (int g4 = 0; g4 < 4; ++g4) {
+            const int g = 4 * h + g4;
+            const uint64_t a2 = pair(ka[g], ka[g]), b2 = pair(kb[g] - mr, kb[g] - mr);
+            float x[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = ex2(fmaf(v[16 * g + k], a, b));
+            for (int k = 0; k < 8; ++k) {
+              unpair(fma2(pair(v[16 * g + 2 * k], v[16 * g + 2 * k + 1]), a2, b2), x[2 * k], x[2 * k + 1]);
+              x[2 * k] = ex2(x[2 * k]);
+              x[2 * k + 1] = ex2(x[2 * k + 1]);
+            }
             if (edge) {
 #pragma unroll
               for (int k = 0; k < 16; ++k)
-                if (32 * c + 16 * g + k >= left) x[k] = 0.f;
+                if (16 * g + k >= left) x[k] = 0.f;
             }
+            uint64_t sum = pair(x[0], x[1]);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) sum += x[k];
-            l = fmaf(sum, exp2i(max(-126, min(126, -ev))), l);
+            for (int k = 1; k < 8; ++k) sum = add2(sum, pair(x[2 * k], x[2 * k + 1]));
+            float s0, s1;
+            unpair(sum, s0, s1);
+            l = fmaf(s0 + s1, exp2i(max(-126, min(126, -(int)kb[g]))), l);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {  // tokens in V's stored order
-              w[8 * g + 2 * m] = tqd::pack_half2(x[2 * m], x[2 * m + 1]);
-              w[8 * g + 2 * m + 1] = tqd::pack_half2(x[2 * m + 8], x[2 * m + 9]);
+              w[8 * g4 + 2 * m] = tqd::pack_half2(x[2 * m], x[2 * m + 1]);
+              w[8 * g4 + 2 * m + 1] = tqd::pack_half2(x[2 * m + 8], x[2 * m + 9]);
             }
           }
-          tqd::tc_st16(t_s + 16 * c, w);
+          st32_async(t_s + 32 * h, w);
+          asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+          tqd::tc_fence_before();
+          tqd::tc_mbar_arrive(bar(P_FULL, 2 * i + h));
         }
-        tqd::tc_fence_before();
-        tqd::tc_mbar_arrive(bar(P_FULL, i));
         __syncwarp();
         if (lane == 0) tqd::tc_mbar_arrive(bar(SC_EMPTY, ss));
       }
@@ -418,7 +507,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
         }
       }
       tqd::tc_fence_before();  // (the next range's first product overwrites O after its P arrives)
+      if (threadIdx.x == 0 && s.t0 == 0 && s.t1 < s.tiles) {  // this range's last stretch begins a group that goes on
+        p.heads[blockIdx.x] = JoinHead{(s.start + s.tiles - 1) / per, first ? 0 : 1, s.b, s.h, s.rg};
+        headed = true;
+      }
     }
+    if (threadIdx.x == 0 && !headed) p.heads[blockIdx.x].last = -1;
   } else if (warp >= 8 && warp < 12) {
     // ---- V codes to fp16, K-major [coordinate][token], 64 tokens per 128-byte row
     uint32_t n = 0;
@@ -541,18 +635,24 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
           if (i == 0 && !wait(bar(V_FULL, n & 1), (n >> 1) & 1)) break;
-          if (!wait(bar(P_FULL, i), n & 1)) break;
-          tqd::tc_fence_after();
-          if (lane == 0) {
-            const uint64_t vd = v_d + (uint64_t)((n & 1) * (32768 >> 4));
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              tqd::tc_mma_f16_ta(tmem + 256 + 128 * i, tmem + 128 * i + 8 * k,
-                                 vd + (uint64_t)((k >> 2) * (16384 >> 4) + 2 * (k & 3)), idesc, t > s.t0 || k > 0);
-            tqd::tc_commit(bar(O_DONE, i));
-            if (i == NQ - 1) tqd::tc_commit(bar(V_EMPTY, n & 1));
+          for (int h = 0; h < 2; ++h) {
+            if (!wait(bar(P_FULL, 2 * i + h), n & 1)) break;
+            tqd::tc_fence_after();
+            if (lane == 0) {
+              const uint64_t vd = v_d + (uint64_t)((n & 1) * (32768 >> 4) + h * (16384 >> 4));
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tqd::tc_mma_f16_ta(tmem + 256 + 128 * i, tmem + 128 * i + 32 * h + 8 * k, vd + 2 * k, idesc,
+                                   t > s.t0 || h + k > 0);
+              if (h == 1) {
+                tqd::tc_commit(bar(O_DONE, i));
+                if (i == NQ - 1) tqd::tc_commit(bar(V_EMPTY, n & 1));
+              }
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          if (!ok) break;
           if (t + 1 < s.t1) {
             if (i == 0 && !wait(bar(K_FULL, (n + 1) & 1), ((n + 1) >> 1) & 1)) break;
             scores(i, n + 1);
@@ -570,41 +670,6 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
   }
 }
 
-// Joins the partials of the row group that lies across the boundary between ranges blockIdx.x and
-// blockIdx.x + 1, if it is the first boundary inside the group; 8 rows per block.
-template <typename T, int NT, int NQ>
-__global__ void __launch_bounds__(kD) merge_tc_kernel(const TcParams p) {
-  using L = Plan<NT, NQ>;
-  __shared__ int pre[TQ_MAX_BATCH + 1];
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  fill_plan(p, L::ROWS, pre, nullptr);
-  __syncthreads();
-  const int total = pre[p.a.B], per = range_of(total, p.grid), c0 = blockIdx.x, edge = (c0 + 1) * per;
-  if (edge >= total) return;
-  const Seg s = seg_at(p, L::ROWS, pre, edge, total);
-  const int tiles_end = s.start + s.tiles;
-  if (s.start >= edge || s.start < c0 * per || tiles_end <= edge) return;
-  const int c1 = (tiles_end - 1) / per;
-  const int d = threadIdx.x;
-  for (int k = 0; k < 8; ++k) {
-    const int rr = blockIdx.y * 8 + k, row = s.rg * L::ROWS + rr;
-    if (row >= p.rows) return;
-    // the group's stretch is its range's first one except perhaps in range c0
-    const int s0 = s.start == c0 * per ? 0 : 1;
-    float mt = -INFINITY;
-    for (int c = c0; c <= c1; ++c) mt = fmaxf(mt, p.part[(2ll * c + (c == c0 ? s0 : 0)) * L::PART + rr]);
-    const float mr = mt == -INFINITY ? 0.f : mt;
-    float l = 0.f, o = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-      const float* x = p.part + (2ll * c + (c == c0 ? s0 : 0)) * L::PART;
-      const float w = ex2(x[rr] - mr);
-      l = fmaf(x[L::ROWS + rr], w, l);
-      o = fmaf(x[2 * L::ROWS + rr * kD + d], w, o);
-    }
-    out_row<T>(p, s.b, s.h, row)[d] = from_float<T>(l > 0.f || l != l ? o / l : 0.f);
-  }
-}
-
 template <typename T, int NT, int NQ>
 cudaError_t tc_go(TcParams p, int sms, int device, cudaStream_t s) {
   using L = Plan<NT, NQ>;
@@ -618,15 +683,15 @@ cudaError_t tc_go(TcParams p, int sms, int device, cudaStream_t s) {
   if (p.grid == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   const int rows = p.rows < L::ROWS ? p.rows : L::ROWS;
-  cfg.gridDim = dim3(p.grid - 1, (rows + 7) / 8);
-  cfg.blockDim = dim3(kD);
+  cfg.gridDim = dim3(p.grid - 1, (rows + kJoinRows - 1) / kJoinRows);
+  cfg.blockDim = dim3(32 * kJoinRows);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_tc_kernel<T, NT, NQ>, p);
+  return cudaLaunchKernelEx(&cfg, join_kernel<kD, L::ROWS, T>, JoinParams{p.heads, p.part, p.a.out, p.a.nq, p.a.Hq, p.G, p.rows});
 }
 
 }  // namespace
@@ -640,7 +705,7 @@ bool tc_takes(const AttnArgs& a) {
 }
 
 size_t tc_workspace(int rows) {
-  return (size_t)2 * kMaxSms * (rows > 128 ? Plan<2, 2>::PART : Plan<2, 1>::PART) * sizeof(float);
+  return kJoinHeadBytes + (size_t)2 * kMaxSms * (rows > 128 ? Plan<2, 2>::PART : Plan<2, 1>::PART) * sizeof(float);
 }
 
 cudaError_t launch_tc(const AttnArgs& a, cudaStream_t s) {
@@ -649,7 +714,8 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t s) {
   p.G = a.Hq / a.Hkv;
   p.rows = p.G * a.nq;
   p.groups = p.grid = 0;
-  p.part = (float*)a.ws;
+  p.heads = (JoinHead*)a.ws;
+  p.part = (float*)((unsigned char*)a.ws + kJoinHeadBytes);
   int dev, sms = sm_count(&dev);
   if (sms > kMaxSms) sms = kMaxSms;
   if (a.dtype == TQ_BF16)
