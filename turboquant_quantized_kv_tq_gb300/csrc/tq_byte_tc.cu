@@ -69,11 +69,52 @@ enum Bar { K_FULL = 0, K_EMPTY = 2, VR_FULL = 4, VR_EMPTY = 6, V_FULL = 8, V_EMP
 __device__ __forceinline__ uint64_t sdesc128(uint32_t addr) {
   return (uint64_t)((addr & 0x3FFFFu) >> 4) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
+  asm volatile("{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\nselp.u32 %0, 1, 0, e;\n}\n" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
       :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// Products of one elected lane of a converged warp, from constant operands.
+constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);  // M = N = 128, fp32 D
+static_assert(kTok == 128 && kD == 128, "one instruction shape for both products");
+
+// S_i of the tile in K buffer ST.
+template <int NT, int NQ, int ST>
+__device__ __forceinline__ void issue_scores(uint32_t sb, int i) {
+  using L = Plan<NT, NQ>;
+  const uint64_t q = sdesc128(sb + L::Q + i * NT * 16384), k = sdesc128(sb + L::KR + ST * 16384);
+  if (elected()) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mma_f8(128 * i, q + (uint64_t)(t * (16384 >> 4) + 2 * j), k + 2 * j, kIdesc, t + j > 0);
+    tqd::tc_commit(sb + L::BARS + 8 * (S_FULL + i));
+    if (i == NQ - 1) tqd::tc_commit(sb + L::BARS + 8 * (K_EMPTY + ST));
+  }
+  __syncwarp();
+}
+// Half h of O_i += P_i V of the tile in V buffer ST (accumulate: not the range's first tile).
+template <int NT, int NQ, int ST>
+__device__ __forceinline__ void issue_readout(uint32_t sb, int i, int h, bool accumulate) {
+  using L = Plan<NT, NQ>;
+  const uint64_t v = sdesc128(sb + L::V16 + ST * 32768 + h * 16384);
+  if (elected()) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      tqd::tc_mma_f16_ta(256 + 128 * i, 128 * i + 32 * h + 8 * k, v + 2 * k, kIdesc, accumulate || h + k > 0);
+    if (h == 1) {
+      tqd::tc_commit(sb + L::BARS + 8 * (O_DONE + i));
+      if (i == NQ - 1) tqd::tc_commit(sb + L::BARS + 8 * (V_EMPTY + ST));
+    }
+  }
+  __syncwarp();
 }
 
 // Tokens that the rows of group rg of an entry attend to at most, and tiles.
@@ -330,11 +371,13 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
   tqd::tc_fence_before();
   __syncthreads();
   tqd::tc_fence_after();
-  const uint32_t tmem = *slot;
+  // all 512 columns are this block's: they begin at column 0, lane 0
+  const bool whole_tmem = *slot == 0;
+  constexpr uint32_t tmem = 0;
   const int total = pre[A.B], per = range_of(total, p.grid);
   const int begin = min(total, (int)blockIdx.x * per), end = min(total, begin + per);
 
-  bool ok = true;  // cleared by a wait that gave up: the role stops working and ends
+  bool ok = whole_tmem;  // cleared by a wait that gave up: the role stops working and ends
   auto wait = [&](uint32_t b, uint32_t parity) {
     if (ok && !mbar_wait(b, parity, kWaitLimit)) ok = false;
     return ok;
@@ -364,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
     }
     int at = begin;
     bool headed = false;
-    while (at < end) {
+    while (at < end && ok) {
       const Seg s = seg_at(p, L::ROWS, pre, at, end);
       const bool first = at == begin;
       at = s.next;
@@ -600,25 +643,11 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
       mbar_wait(bar(SC_FULL, k % L::SC), (k / L::SC) & 1, kWaitLimit);
     }
   } else if (warp == 13) {
-    // ---- MMA issue
-    constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-    static_assert(kTok == 128 && kD == 128, "one instruction shape for both products");
-    const uint64_t q_d = sdesc128(sb + L::Q), k_d = sdesc128(sb + L::KR), v_d = sdesc128(sb + L::V16);
+    // ---- MMA issue.  Every operand is a constant of the stage (the buffers' parity is a template
+    // argument, the tensor memory begins at column 0), so the descriptors sit in uniform registers;
+    // with operands computed per tile the issue took 60-100 cycles an instruction and bounded the kernel.
     uint32_t n = 0, segs = 0;
     int at = begin;
-    auto scores = [&](int i, uint32_t m) {  // S_i of tile m
-      if (lane == 0) {
-        const uint64_t kd = k_d + (uint64_t)((m & 1) * (16384 >> 4));
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f8(tmem + 128 * i, q_d + (uint64_t)((i * NT + t) * (16384 >> 4) + 2 * k), kd + 2 * k, idesc, t + k > 0);
-        tqd::tc_commit(bar(S_FULL, i));
-        if (i == NQ - 1) tqd::tc_commit(bar(K_EMPTY, m & 1));
-      }
-      __syncwarp();
-    };
     while (at < end && ok) {
       const Seg s = seg_at(p, L::ROWS, pre, at, end);
       at = s.next;
@@ -628,10 +657,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
       for (int i = 0; i < NQ; ++i) {
         if (!wait(bar(Q_FULL, i), segs & 1)) break;
         tqd::tc_fence_after();
-        scores(i, n);
+        if (n & 1) issue_scores<NT, NQ, 1>(sb, i);
+        else issue_scores<NT, NQ, 0>(sb, i);
       }
       ++segs;
       for (int t = s.t0; t < s.t1 && ok; ++t, ++n) {
+        const bool more = t + 1 < s.t1;
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
           if (i == 0 && !wait(bar(V_FULL, n & 1), (n >> 1) & 1)) break;
@@ -639,23 +670,14 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
           for (int h = 0; h < 2; ++h) {
             if (!wait(bar(P_FULL, 2 * i + h), n & 1)) break;
             tqd::tc_fence_after();
-            if (lane == 0) {
-              const uint64_t vd = v_d + (uint64_t)((n & 1) * (32768 >> 4) + h * (16384 >> 4));
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                tqd::tc_mma_f16_ta(tmem + 256 + 128 * i, tmem + 128 * i + 32 * h + 8 * k, vd + 2 * k, idesc,
-                                   t > s.t0 || h + k > 0);
-              if (h == 1) {
-                tqd::tc_commit(bar(O_DONE, i));
-                if (i == NQ - 1) tqd::tc_commit(bar(V_EMPTY, n & 1));
-              }
-            }
-            __syncwarp();
+            if (n & 1) issue_readout<NT, NQ, 1>(sb, i, h, t > s.t0);
+            else issue_readout<NT, NQ, 0>(sb, i, h, t > s.t0);
           }
           if (!ok) break;
-          if (t + 1 < s.t1) {
+          if (more) {
             if (i == 0 && !wait(bar(K_FULL, (n + 1) & 1), ((n + 1) >> 1) & 1)) break;
-            scores(i, n + 1);
+            if (n & 1) issue_scores<NT, NQ, 0>(sb, i);
+            else issue_scores<NT, NQ, 1>(sb, i);
           }
         }
       }
@@ -666,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
   __syncthreads();  // (the rows waited for every readout, so every MMA has completed)
   if (warp == 13) {
     tqd::tc_fence_after();
-    tqd::tc_dealloc(tmem, 512);
+    tqd::tc_dealloc(*slot, 512);
   }
 }
 
