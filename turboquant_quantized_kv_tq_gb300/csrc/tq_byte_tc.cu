@@ -25,6 +25,7 @@
 // the maximum to the probabilities, and 64 in the other warps).
 #include <atomic>
 #include <string>
+#include <type_traits>
 
 #include "tq_byte_attn.cuh"
 #include "tq_tc05.cuh"
@@ -56,14 +57,16 @@ struct Plan {
   static constexpr int ROWS = 128 * NQ;
   static constexpr int SC = 4;                                    // scale stages of 8 x 16 bytes
   static constexpr int Q = 0, KR = Q + NQ * NT * 16384, VR = KR + 2 * 16384, V16 = VR + 2 * 16384;
-  static constexpr int SCALES = V16 + 2 * 32768, BARS = SCALES + SC * 128, PRE = BARS + 256;
+  // [stage][block]: as copied (K scale, V scale, -, -), then in place (K scale, e, 2^-e, -)
+  static constexpr int SCALES = V16 + 2 * 32768, BARS = SCALES + SC * 128, PRE = BARS + 320;
   static constexpr int SMEM = PRE + (TQ_MAX_BATCH + 1) * 4;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static constexpr int PART = ROWS * (kD + 2);                    // floats of a partial
 };
 // (P_FULL: half h of row tile i at 2 i + h)
 enum Bar { K_FULL = 0, K_EMPTY = 2, VR_FULL = 4, VR_EMPTY = 6, V_FULL = 8, V_EMPTY = 10, S_FULL = 12, O_DONE = 14,
-           Q_FULL = 16, P_FULL = 18, SC_FULL = 22, SC_EMPTY = 26, BAR_COUNT = 30 };
+           Q_FULL = 16, P_FULL = 18, SC_FULL = 22, SC_EMPTY = 26, SC_READY = 30, BAR_COUNT = 34 };
+static_assert(8 * BAR_COUNT + 4 <= 320, "barriers and the tensor-memory slot");
 
 // 128-byte-swizzled K-major operand: rows of 128 bytes in groups of 8 (1024 bytes).
 __device__ __forceinline__ uint64_t sdesc128(uint32_t addr) {
@@ -312,22 +315,66 @@ __device__ __forceinline__ void ld32_async(uint32_t taddr, float* v) {
         "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(taddr));
 }
-// The wait, tied to the values it makes valid.
+// The wait for the loads before it, tied to the N values it makes valid.
+template <int N>
 __device__ __forceinline__ void ld_wait(float* v) {
   asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(v[i]));
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
 }
-// 32 columns stored, without the wait.
-__device__ __forceinline__ void st32_async(uint32_t taddr, const uint32_t* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n"
-      :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-         "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]),
-         "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]),
-         "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-      : "memory");
+// 8 columns stored, without the wait.
+__device__ __forceinline__ void st8_async(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n"
+               :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// The largest s + e of one block's 16 scores (left: those the row attends to, when EDGE).
+template <bool EDGE>
+__device__ __forceinline__ float block_top(float* v, int left, float a, float e) {
+  if (EDGE) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (k >= left) v[k] = -INFINITY;
+  }
+  float m = v[0];
+#pragma unroll
+  for (int k = 1; k < 15; k += 2) m = fmaxf(m, fmaxf(v[k], v[k + 1]));
+  m = fmaxf(m, v[15]);
+  const float top = fmaf(m, a, e);
+  // (a block without a token of the row stays out: its scale may be anything)
+  return EDGE && m == -INFINITY ? -INFINITY : top;
+}
+// P of one block as fp16 pairs in V's stored token order; the sum of its 16 values is returned.
+template <bool EDGE>
+__device__ __forceinline__ float block_p(const float* v, int left, float a, float b, uint32_t* w) {
+  const uint64_t a2 = pair(a, a), b2 = pair(b, b);
+  float x[16];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    unpair(fma2(pair(v[2 * k], v[2 * k + 1]), a2, b2), x[2 * k], x[2 * k + 1]);
+    x[2 * k] = ex2(x[2 * k]);
+    x[2 * k + 1] = ex2(x[2 * k + 1]);
+  }
+  if (EDGE) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (k >= left) x[k] = 0.f;
+  }
+  uint64_t s0 = pair(x[0], x[1]), s1 = pair(x[2], x[3]);
+#pragma unroll
+  for (int k = 2; k < 8; k += 2) {
+    s0 = add2(s0, pair(x[2 * k], x[2 * k + 1]));
+    s1 = add2(s1, pair(x[2 * k + 2], x[2 * k + 3]));
+  }
+  float t0, t1;
+  unpair(add2(s0, s1), t0, t1);
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    w[2 * m] = tqd::pack_half2(x[2 * m], x[2 * m + 1]);
+    w[2 * m + 1] = tqd::pack_half2(x[2 * m + 8], x[2 * m + 9]);
+  }
+  return t0 + t1;
 }
 
 template <typename T, int NT, int NQ>
@@ -364,6 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
     for (int i = 0; i < L::SC; ++i) {
       tqd::mbar_init(bar(SC_FULL, i), 1);
       tqd::mbar_init(bar(SC_EMPTY, i), 4 * NQ);
+      tqd::mbar_init(bar(SC_READY, i), 1);
     }
     tqd::fence_mbar_init();
   }
@@ -422,41 +470,34 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
       tqd::tc_fence_smem();
       tqd::tc_mbar_arrive(bar(Q_FULL, i));
       float M = -INFINITY, l = 0.f;
-      for (int t = s.t0; t < s.t1; ++t, ++n) {
-        if (!wait(bar(S_FULL, i), n & 1)) break;
+      // one tile; false: a wait gave up
+      auto tile = [&](auto edge_tag, int t) {
+        constexpr bool EDGE = decltype(edge_tag)::value;
+        if (!wait(bar(S_FULL, i), n & 1)) return false;
         const int ss = n % L::SC;
-        if (!wait(bar(SC_FULL, ss), (n / L::SC) & 1)) break;
+        if (!wait(bar(SC_READY, ss), (n / L::SC) & 1)) return false;
         tqd::tc_fence_after();
-        const unsigned char* sc = sm + L::SCALES + 128 * ss;
-        const bool edge = kTok * (t + 1) > least;
-        const int left = lim - kTok * t;  // columns of this tile that the row attends to
+        const float4* sc = reinterpret_cast<const float4*>(sm + L::SCALES + 128 * ss);
+        const int left = lim - kTok * t;  // tokens of this tile that the row attends to
         float v[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) ld32_async(t_s + 32 * c, v + 32 * c);
-        float ka[8], kb[8];  // per block: the scores' factor, the value scale's exponent
-#pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          const float2 kv = *reinterpret_cast<const float2*>(sc + 16 * g);
-          ka[g] = f * kv.x;
-          kb[g] = (float)log2i(kv.y);
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) ld_wait(v + 32 * c);
-        if (edge) {
-#pragma unroll
-          for (int k = 0; k < 128; ++k)
-            if (k >= left) v[k] = -INFINITY;
-        }
-        float top = -INFINITY;
+        ld32_async(t_s, v);
+        ld32_async(t_s + 32, v + 32);
+        float a[8], e[8];
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
-          float m = v[16 * g];
-#pragma unroll
-          for (int k = 1; k < 15; k += 2) m = fmaxf(m, fmaxf(v[16 * g + k], v[16 * g + k + 1]));
-          m = fmaxf(m, v[16 * g + 15]);
-          // (a block without a token of the row stays out: its scale may be anything)
-          top = m == -INFINITY ? top : fmaxf(top, fmaf(m, ka[g], kb[g]));
+          const float4 x = sc[g];
+          a[g] = f * x.x;
+          e[g] = x.y;
         }
+        ld_wait<64>(v);
+        ld32_async(t_s + 64, v + 64);
+        ld32_async(t_s + 96, v + 96);
+        float top = block_top<EDGE>(v, left, a[0], e[0]);
+#pragma unroll
+        for (int g = 1; g < 4; ++g) top = fmaxf(top, block_top<EDGE>(v + 16 * g, left - 16 * g, a[g], e[g]));
+        ld_wait<64>(v + 64);
+#pragma unroll
+        for (int g = 4; g < 8; ++g) top = fmaxf(top, block_top<EDGE>(v + 16 * g, left - 16 * g, a[g], e[g]));
         const bool raise = top > M + kSlack;
         if (__any_sync(kFull, raise)) {
           const float m_new = raise ? top - kTop : M;
@@ -464,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
           M = m_new;
           if (t > s.t0) {
             l *= cor;
-            if (!wait(bar(O_DONE, i), (n - 1) & 1)) break;
+            if (!wait(bar(O_DONE, i), (n - 1) & 1)) return false;
             tqd::tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < 8; ++c) {
@@ -479,43 +520,24 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
         }
         const float mr = M == -INFINITY ? 0.f : M;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[32];
-#pragma unroll
-          for (int g4 = 0; g4 < 4; ++g4) {
-            const int g = 4 * h + g4;
-            const uint64_t a2 = pair(ka[g], ka[g]), b2 = pair(kb[g] - mr, kb[g] - mr);
-            float x[16];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              unpair(fma2(pair(v[16 * g + 2 * k], v[16 * g + 2 * k + 1]), a2, b2), x[2 * k], x[2 * k + 1]);
-              x[2 * k] = ex2(x[2 * k]);
-              x[2 * k + 1] = ex2(x[2 * k + 1]);
-            }
-            if (edge) {
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                if (16 * g + k >= left) x[k] = 0.f;
-            }
-            uint64_t sum = pair(x[0], x[1]);
-#pragma unroll
-            for (int k = 1; k < 8; ++k) sum = add2(sum, pair(x[2 * k], x[2 * k + 1]));
-            float s0, s1;
-            unpair(sum, s0, s1);
-            l = fmaf(s0 + s1, exp2i(max(-126, min(126, -(int)kb[g]))), l);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {  // tokens in V's stored order
-              w[8 * g4 + 2 * m] = tqd::pack_half2(x[2 * m], x[2 * m + 1]);
-              w[8 * g4 + 2 * m + 1] = tqd::pack_half2(x[2 * m + 8], x[2 * m + 9]);
-            }
+        for (int g = 0; g < 8; ++g) {
+          uint32_t w[8];
+          const float sum = block_p<EDGE>(v + 16 * g, left - 16 * g, a[g], e[g] - mr, w);
+          l = fmaf(sum, sc[g].z, l);
+          st8_async(t_s + 8 * g, w);
+          if (g == 3 || g == 7) {
+            asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+            tqd::tc_fence_before();
+            tqd::tc_mbar_arrive(bar(P_FULL, 2 * i + (g == 7)));
           }
-          st32_async(t_s + 32 * h, w);
-          asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
-          tqd::tc_fence_before();
-          tqd::tc_mbar_arrive(bar(P_FULL, 2 * i + h));
         }
         __syncwarp();
         if (lane == 0) tqd::tc_mbar_arrive(bar(SC_EMPTY, ss));
+        ++n;
+        return true;
+      };
+      for (int t = s.t0; t < s.t1; ++t) {
+        if (kTok * (t + 1) > least ? !tile(std::true_type{}, t) : !tile(std::false_type{}, t)) break;
       }
       if (!ok || !wait(bar(O_DONE, i), (n - 1) & 1)) break;
       tqd::tc_fence_after();
@@ -564,7 +586,18 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
       const Seg s = seg_at(p, L::ROWS, pre, at, end);
       at = s.next;
       for (int t = s.t0; t < s.t1; ++t, ++n) {
-        const int st = n & 1;
+        const int st = n & 1, ss = n % L::SC;
+        if (warp == 8) {
+          if (!wait(bar(SC_FULL, ss), (n / L::SC) & 1)) break;
+          if (lane < 8) {
+            float4* x = reinterpret_cast<float4*>(sm + L::SCALES + 128 * ss + 16 * lane);
+            const int e = log2i(x->y);  // (of a block behind the tokens: any exponent; 2^-e stays finite)
+            x->y = (float)e;
+            x->z = exp2i(max(-126, min(126, -e)));
+          }
+          __syncwarp();
+          if (lane == 0) tqd::tc_mbar_arrive(bar(SC_READY, ss));
+        }
         if (!wait(bar(VR_FULL, st), (n >> 1) & 1)) break;
         if (n >= 2 && !wait(bar(V_EMPTY, st), ((n >> 1) - 1) & 1)) break;
 #pragma unroll
