@@ -30,29 +30,21 @@ __device__ __forceinline__ void fill_angles(float2* cs, const Rotary& R, int cou
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void load_weight(const void* w, int ca, int cb, float (&wa)[8], float (&wb)[8]) {
-  if (w) {
-    unpack8(load8(reinterpret_cast<const T*>(w) + 8 * ca), wa);
-    unpack8(load8(reinterpret_cast<const T*>(w) + 8 * cb), wb);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) wa[i] = wb[i] = 1.f;
-  }
-}
-
-// Rows of `heads` heads (from h0) of tokens [t0, t0 + nt) of [B][n] (linear token index), cosines
-// already in cs: normed, rotated and stored at out(b, j, h).  Loads of kU rows are in flight per
-// thread; the block's barrier that publishes cs comes between the first loads and their use.
-template <int D, typename T, typename O, int kU, typename F>
+// Rows of `nh` heads (from h0) of tokens [t0, t0 + nt) of [B][n] (linear token index): normed, rotated
+// and stored at out(b, j, h).  Loads of kU rows are in flight per thread; `angles` (which writes the
+// tokens' cosines) runs once, behind the first loads.
+template <int D, typename T, typename O, int kU, typename A, typename F>
 __device__ __forceinline__ void rows_pass(const Rows& X, const void* w, float eps, const Rotary& R, const float4* cs,
-                                          int t0, int nt, int h0, int nh, int n, bool& synced, F out) {
+                                          int t0, int nt, int h0, int nh, int n, bool& filled, A angles, F out) {
   constexpr int TPR = D / 16, RPP = kThreads / TPR;
   const int l = threadIdx.x % TPR, row0 = threadIdx.x / TPR;
   const int ca = chunk_a(l, R.r), cb = chunk_b(l, R.r);
   const int total = nt * nh;
-  float wa[8], wb[8];
-  load_weight<T>(w, ca, cb, wa, wb);
+  Raw8<T> wa = {}, wb = {};  // (kept packed: half the registers)
+  if (w) {
+    wa = load8(reinterpret_cast<const T*>(w) + 8 * ca);
+    wb = load8(reinterpret_cast<const T*>(w) + 8 * cb);
+  }
   for (int base = 0; base < total; base += RPP * kU) {
     Raw8<T> ra[kU], rb[kU];
 #pragma unroll
@@ -63,11 +55,15 @@ __device__ __forceinline__ void rows_pass(const Rows& X, const void* w, float ep
         const T* src = reinterpret_cast<const T*>(X.p) + b * X.sb + j * X.st + h * X.sh;
         ra[u] = load8_rw(src + 8 * ca);
         rb[u] = load8_rw(src + 8 * cb);
+      } else {
+        ra[u] = Raw8<T>{};
+        rb[u] = Raw8<T>{};
       }
     }
-    if (!synced) {
+    if (!filled) {
+      angles();
       __syncthreads();
-      synced = true;
+      filled = true;
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
@@ -75,14 +71,9 @@ __device__ __forceinline__ void rows_pass(const Rows& X, const void* w, float ep
       if (base + u * RPP >= total) break;  // (uniform over the block)
       const int tk = min(row, total - 1) / nh;
       float a[8], b8[8];
-      if (row < total) {
-        unpack8(ra[u], a);
-        unpack8(rb[u], b8);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = b8[i] = 0.f;
-      }
-      norm_rotate_row<TPR>(a, b8, l, w != nullptr, wa, wb, D, eps, cs + tk * (R.r / 4), R.r, R.interleaved);
+      unpack8(ra[u], a);
+      unpack8(rb[u], b8);
+      norm_rotate_row<TPR, T>(a, b8, l, w != nullptr, wa, wb, D, eps, cs + tk * (R.r / 4), R.r, R.interleaved);
       if (row < total) {
         const int h = h0 + row - tk * nh, g = t0 + tk, b = g / n, j = g - b * n;
         O* dst = reinterpret_cast<O*>(out(b, j, h));
@@ -101,29 +92,31 @@ struct RotateParams {
 };
 
 template <int D, typename T, typename O>
-__global__ void __launch_bounds__(kThreads) norm_rotate_kernel(const RotateParams p) {
+__global__ void __launch_bounds__(kThreads, 3) norm_rotate_kernel(const RotateParams p) {
   extern __shared__ __align__(16) float2 cs[];
   const RotateArgs& A = p.a;
   const int t0 = blockIdx.x * p.per, nt = min(p.per, p.tokens - t0);
-  if (A.rot.r)
-    fill_angles(cs, A.rot, nt, [&](int tk, int axis) {
-      const int g = t0 + tk, b = g / A.n;
-      return token_position(A.pos, axis, b, g - b * A.n, A.B, A.n);
-    });
+  auto angles = [&] {
+    if (A.rot.r)
+      fill_angles(cs, A.rot, nt, [&](int tk, int axis) {
+        const int g = t0 + tk, b = g / A.n;
+        return token_position(A.pos, axis, b, g - b * A.n, A.B, A.n);
+      });
+  };
   // heads of q and k in one range [0, Hq + Hk)
   const int lo = blockIdx.y * p.q_split, hi = min(lo + p.q_split, A.q.heads + A.k.heads);
   const int q0 = min(lo, A.q.heads), q1 = min(hi, A.q.heads);
   const int k0 = max(lo, A.q.heads) - A.q.heads, k1 = max(hi, A.q.heads) - A.q.heads;
-  bool synced = false;
-  constexpr int kU = sizeof(T) == 2 ? 4 : 2;
+  bool filled = false;
+  constexpr int kU = sizeof(T) == 2 ? 3 : 2;
   if (q1 > q0)
-    rows_pass<D, T, O, kU>(A.q, A.wq, A.eps, A.rot, reinterpret_cast<const float4*>(cs), t0, nt, q0, q1 - q0, A.n, synced,
-                           [&](int b, int j, int h) {
+    rows_pass<D, T, O, kU>(A.q, A.wq, A.eps, A.rot, reinterpret_cast<const float4*>(cs), t0, nt, q0, q1 - q0, A.n, filled,
+                           angles, [&](int b, int j, int h) {
                              return reinterpret_cast<O*>(A.q_out) + (((long long)b * A.n + j) * A.q.heads + h) * D;
                            });
   if (k1 > k0)
-    rows_pass<D, T, O, kU>(A.k, A.wk, A.eps, A.rot, reinterpret_cast<const float4*>(cs), t0, nt, k0, k1 - k0, A.n, synced,
-                           [&](int b, int j, int h) {
+    rows_pass<D, T, O, kU>(A.k, A.wk, A.eps, A.rot, reinterpret_cast<const float4*>(cs), t0, nt, k0, k1 - k0, A.n, filled,
+                           angles, [&](int b, int j, int h) {
                              return reinterpret_cast<O*>(A.k_out) + (((long long)b * A.k.heads + h) * A.n + j) * D;
                            });
 }
@@ -136,29 +129,51 @@ struct AppendParams {
   int per, tokens, q_split, q_groups;
 };
 
+// E = 2, 4 or 8 consecutive elements as loaded, and as fp32.
 template <typename T, int E>
-__device__ __forceinline__ void load_narrow(const T* p, float (&x)[E]);
-template <>
-__device__ __forceinline__ void load_narrow<float, 2>(const float* p, float (&x)[2]) {
-  const float2 v = __ldg(reinterpret_cast<const float2*>(p));
-  x[0] = v.x; x[1] = v.y;
-}
-template <>
-__device__ __forceinline__ void load_narrow<__nv_bfloat16, 2>(const __nv_bfloat16* p, float (&x)[2]) {
-  const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p));
-  x[0] = __uint_as_float(w << 16);
-  x[1] = __uint_as_float(w & 0xffff0000u);
-}
-template <>
-__device__ __forceinline__ void load_narrow<__half, 2>(const __half* p, float (&x)[2]) {
-  const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p));
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-  x[0] = f.x; x[1] = f.y;
-}
+struct RawE {
+  static constexpr int W = E * (int)sizeof(T) / 4;  // 32-bit words
+  uint32_t w[W];
+};
 template <typename T, int E>
-__device__ __forceinline__ void load_some(const T* p, float (&x)[E]) {
-  if constexpr (E == 2) load_narrow<T, 2>(p, x);
-  else tqd::load_row<E>(p, x);
+__device__ __forceinline__ RawE<T, E> load_some(const T* p) {
+  RawE<T, E> r;
+  constexpr int W = RawE<T, E>::W;
+  if constexpr (W == 1) {
+    r.w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+  } else if constexpr (W == 2) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    r.w[0] = v.x; r.w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      r.w[4 * i] = v.x; r.w[4 * i + 1] = v.y; r.w[4 * i + 2] = v.z; r.w[4 * i + 3] = v.w;
+    }
+  }
+  return r;
+}
+template <int E>
+__device__ __forceinline__ void unpack_some(const RawE<float, E>& r, float (&x)[E]) {
+#pragma unroll
+  for (int i = 0; i < E; ++i) x[i] = __uint_as_float(r.w[i]);
+}
+template <int E>
+__device__ __forceinline__ void unpack_some(const RawE<__nv_bfloat16, E>& r, float (&x)[E]) {
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    x[2 * i] = __uint_as_float(r.w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
+  }
+}
+template <int E>
+__device__ __forceinline__ void unpack_some(const RawE<__half, E>& r, float (&x)[E]) {
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r.w[i]));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
 }
 
 // The block's scale exponent from its new tokens' largest magnitude and, where it holds tokens, its
@@ -174,36 +189,45 @@ __device__ __forceinline__ int block_scale(float amax, int held, float old_scale
   return e;
 }
 
-template <int D, typename T>
+template <int D, typename T, typename F>
 __device__ __forceinline__ bool append_keys(const AppendArgs& A, unsigned char* blk, const float4* cs, int b, int h,
-                                            long long j0, int lo, int hi, int held, int lane) {
+                                            long long j0, int lo, int hi, int held, int lane, F angles) {
   constexpr int TPR = D / 16, RPW = 32 / TPR, NP = 16 / RPW;
   const int l = lane % TPR, r0 = lane / TPR;
   const int ca = chunk_a(l, A.rot.r), cb = chunk_b(l, A.rot.r);
   float* scale = reinterpret_cast<float*>(blk + 32 * D);
   const float old_scale = held > 0 ? *scale : 1.f;
   const T* src = reinterpret_cast<const T*>(A.k.p) + b * A.k.sb + h * A.k.sh;
-  float a[NP][8], c[NP][8], wa[8], wb[8];
+  Raw8<T> ra[NP], rc[NP], wa = {}, wb = {};
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
     const int s = p * RPW + r0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[p][i] = c[p][i] = 0.f;
+    ra[p] = rc[p] = Raw8<T>{};
     if (s >= lo && s < hi) {
       const T* row = src + (j0 + s) * A.k.st;
-      unpack8(load8(row + 8 * ca), a[p]);
-      unpack8(load8(row + 8 * cb), c[p]);
+      ra[p] = load8(row + 8 * ca);
+      rc[p] = load8(row + 8 * cb);
     }
   }
-  load_weight<T>(A.wk, ca, cb, wa, wb);
-  __syncthreads();  // cosines
+  if (A.wk) {
+    wa = load8(reinterpret_cast<const T*>(A.wk) + 8 * ca);
+    wb = load8(reinterpret_cast<const T*>(A.wk) + 8 * cb);
+  }
+  angles();
+  __syncthreads();
+  float a[NP][8], c[NP][8];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    unpack8(ra[p], a[p]);
+    unpack8(rc[p], c[p]);
+  }
   float amax = 0.f;
   bool bad = false;
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
     const int s = p * RPW + r0;
     // (rows without a new token are zeros; their cosines are those of an existing slot)
-    norm_rotate_row<TPR>(a[p], c[p], l, A.wk != nullptr, wa, wb, D, A.eps, cs + (s >= lo && s < hi ? s : lo) * (A.rot.r / 4),
+    norm_rotate_row<TPR, T>(a[p], c[p], l, A.wk != nullptr, wa, wb, D, A.eps, cs + (s >= lo && s < hi ? s : lo) * (A.rot.r / 4),
                          A.rot.r, A.rot.interleaved);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -245,21 +269,24 @@ __device__ __forceinline__ bool append_keys(const AppendArgs& A, unsigned char* 
   return bad;
 }
 
-template <int D, typename T>
+template <int D, typename T, typename F>
 __device__ __forceinline__ bool append_values(const AppendArgs& A, unsigned char* blk, int b, int h, long long j0, int lo,
-                                              int hi, int held, int lane) {
+                                              int hi, int held, int lane, F angles) {
   constexpr int E = D / 32;  // coordinates E * lane .. of all 16 tokens
   float* scale = reinterpret_cast<float*>(blk + 32 * D + 4);
   const float old_scale = held > 0 ? *scale : 1.f;
   const T* src = reinterpret_cast<const T*>(A.v.p) + b * A.v.sb + h * A.v.sh + E * lane;
-  float x[16][E];
+  RawE<T, E> raw[16];
 #pragma unroll
   for (int s = 0; s < 16; ++s) {
-#pragma unroll
-    for (int i = 0; i < E; ++i) x[s][i] = 0.f;
-    if (s >= lo && s < hi) load_some<T, E>(src + (j0 + s) * A.v.st, x[s]);
+    raw[s] = RawE<T, E>{};
+    if (s >= lo && s < hi) raw[s] = load_some<T, E>(src + (j0 + s) * A.v.st);
   }
+  angles();
   __syncthreads();  // (the block's barrier for the key warps' cosines)
+  float x[16][E];
+#pragma unroll
+  for (int s = 0; s < 16; ++s) unpack_some<E>(raw[s], x[s]);
   float amax = 0.f;
   bool bad = false;
 #pragma unroll
@@ -306,14 +333,16 @@ __global__ void __launch_bounds__(kThreads) byte_append_kernel(const AppendParam
   if ((int)blockIdx.x >= p.kv_blocks) {  // queries
     const int i = blockIdx.x - p.kv_blocks, part = i % p.q_groups, t0 = i / p.q_groups * p.per;
     const int nt = min(p.per, p.tokens - t0), h0 = part * p.q_split, nh = min(p.q_split, A.Hq - h0);
-    if (A.rot.r)
-      fill_angles(cs, A.rot, nt, [&](int tk, int axis) {
-        const int g = t0 + tk, b = g / A.n;
-        return token_position(A.pos, axis, b, g - b * A.n, A.B, A.n);
-      });
-    bool synced = false;
-    rows_pass<D, T, T, (sizeof(T) == 2 ? 4 : 2)>(A.q, A.wq, A.eps, A.rot, reinterpret_cast<const float4*>(cs), t0, nt, h0,
-                                                 nh, A.n, synced, [&](int b, int j, int h) {
+    bool filled = false;
+    auto angles = [&] {
+      if (A.rot.r)
+        fill_angles(cs, A.rot, nt, [&](int tk, int axis) {
+          const int g = t0 + tk, b = g / A.n;
+          return token_position(A.pos, axis, b, g - b * A.n, A.B, A.n);
+        });
+    };
+    rows_pass<D, T, T, (sizeof(T) == 2 ? 3 : 2)>(A.q, A.wq, A.eps, A.rot, reinterpret_cast<const float4*>(cs), t0, nt, h0,
+                                                 nh, A.n, filled, angles, [&](int b, int j, int h) {
                                                    return reinterpret_cast<T*>(A.q_out) +
                                                           (((long long)b * A.n + j) * A.Hq + h) * D;
                                                  });
@@ -329,26 +358,29 @@ __global__ void __launch_bounds__(kThreads) byte_append_kernel(const AppendParam
   const int lo = (int)max(0ll, -j0), hi = (int)min(16ll, (long long)count - j0);
   if (hi <= lo) return;                                    // (uniform over the block)
   const int held = i == 0 ? (start & 15) : 0;              // = lo in the first block
-  if (A.rot.r) {
-    const int half = A.rot.r / 2;
-    for (int u = threadIdx.x; u < (hi - lo) * half; u += kThreads) {
-      const int s = lo + u / half, pr = u % half;
-      const uint64_t entry = __ldg(reinterpret_cast<const unsigned long long*>(A.rot.table) + pr);
-      cs[s * half + pair_slot(pr, A.rot.r, A.rot.interleaved)] = pair_angle(entry, [&](int axis) {
-        return token_position(A.pos, axis, b, (int)(j0 + s), A.B, A.n);
-      });
+  auto angles = [&] {
+    if (A.rot.r) {
+      const int half = A.rot.r / 2;
+      for (int u = threadIdx.x; u < (hi - lo) * half; u += kThreads) {
+        const int s = lo + u / half, pr = u % half;
+        const uint64_t entry = __ldg(reinterpret_cast<const unsigned long long*>(A.rot.table) + pr);
+        cs[s * half + pair_slot(pr, A.rot.r, A.rot.interleaved)] = pair_angle(entry, [&](int axis) {
+          return token_position(A.pos, axis, b, (int)(j0 + s), A.B, A.n);
+        });
+      }
     }
-  }
+  };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = hg * 4 + (warp >> 1);
   if (h >= A.pool.heads) {
+    angles();
     __syncthreads();
     return;
   }
   const int page = page_of(A.pool, b, tile);
   unsigned char* blk = A.pool.base + pool_block(A.pool, page, h) * block_bytes(D);
-  const bool bad = (warp & 1) ? append_values<D, T>(A, blk, b, h, j0, lo, hi, held, lane)
-                              : append_keys<D, T>(A, blk, reinterpret_cast<const float4*>(cs), b, h, j0, lo, hi, held, lane);
+  const bool bad = (warp & 1) ? append_values<D, T>(A, blk, b, h, j0, lo, hi, held, lane, angles)
+                              : append_keys<D, T>(A, blk, reinterpret_cast<const float4*>(cs), b, h, j0, lo, hi, held, lane, angles);
   if (bad && A.pool.err) atomicExch(A.pool.err, TQ_DEVERR_NONFINITE);
 }
 

@@ -124,10 +124,10 @@ __device__ __forceinline__ float2 pair_angle(uint64_t entry, F pos) {
   return cs;
 }
 
-// Norm (w non-null: a, b of the row's weight chunks) and rotation of one row's values.
-template <int TPR>
-__device__ __forceinline__ void norm_rotate_row(float (&a)[8], float (&b)[8], int l, bool norm, const float (&wa)[8],
-                                                const float (&wb)[8], int D, float eps, const float4* cs, int r,
+// Norm (with wa, wb the row's weight chunks as loaded) and rotation of one row's values.
+template <int TPR, typename T>
+__device__ __forceinline__ void norm_rotate_row(float (&a)[8], float (&b)[8], int l, bool norm, const Raw8<T>& wa,
+                                                const Raw8<T>& wb, int D, float eps, const float4* cs, int r,
                                                 int interleaved) {
   if (norm) {
     float ss = 0.f;
@@ -136,10 +136,13 @@ __device__ __forceinline__ void norm_rotate_row(float (&a)[8], float (&b)[8], in
 #pragma unroll
     for (int m = 1; m < TPR; m <<= 1) ss += __shfl_xor_sync(kFull, ss, m);
     const float rs = rsqrtf(ss / (float)D + eps);
+    float x[8], y[8];
+    unpack8(wa, x);
+    unpack8(wb, y);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      a[i] = a[i] * rs * wa[i];
-      b[i] = b[i] * rs * wb[i];
+      a[i] = a[i] * rs * x[i];
+      b[i] = b[i] * rs * y[i];
     }
   }
   if (l < r / 16) {
