@@ -65,6 +65,12 @@ __device__ __forceinline__ uint32_t encode2(float a, float b) {
 }
 __device__ __forceinline__ uint32_t encode4(const float* x) { return encode2(x[0], x[1]) | (encode2(x[2], x[3]) << 16); }
 
+// The same of finite values.
+__device__ __forceinline__ uint32_t encode4_finite(const float* x) {
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3) |
+         ((uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3) << 16);
+}
+
 // Two codes (low 16 bits) as fp16 pairs: exact, e4m3 values are fp16 values.
 __device__ __forceinline__ uint32_t codes_half2(uint32_t two) {
   uint32_t r;

@@ -11,7 +11,7 @@
 // the step ride along as further blocks of the grid.
 #include <string>
 
-#include "tq_byte.cuh"
+#include "tq_byte_attn.cuh"
 #include "tq_rotate.cuh"
 
 namespace tqb {
@@ -19,45 +19,81 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Cosines of tokens [0, count) at pos(token, axis) into cs ([token][r / 2] float2, pair_slot order).
+// Cosines and sines of tokens [0, count) at pos(token, axis) into cs ([token][r floats], pair_slot order).
 template <typename F>
-__device__ __forceinline__ void fill_angles(float2* cs, const Rotary& R, int count, F pos) {
+__device__ __forceinline__ void fill_angles(float* cs, const Rotary& R, int count, F pos) {
   const int half = R.r / 2;
   for (int i = threadIdx.x; i < count * half; i += blockDim.x) {
     const int tk = i / half, p = i - tk * half;
     const uint64_t entry = __ldg(reinterpret_cast<const unsigned long long*>(R.table) + p);
-    cs[tk * half + pair_slot(p, R.r, R.interleaved)] = pair_angle(entry, [&](int axis) { return pos(tk, axis); });
+    float* at = cs + 2 * tk * half + pair_slot(p, R.r, R.interleaved);
+    const float2 v = pair_angle(entry, [&](int axis) { return pos(tk, axis); });
+    at[0] = v.x;
+    at[2] = v.y;
   }
 }
 
-// Rows of `nh` heads (from h0) of tokens [t0, t0 + nt) of [B][n] (linear token index): normed, rotated
-// and stored at out(b, j, h).  Loads of kU rows are in flight per thread; `angles` (which writes the
-// tokens' cosines) runs once, behind the first loads.
-template <int D, typename T, typename O, int kU, typename A, typename F>
-__device__ __forceinline__ void rows_pass(const Rows& X, const void* w, float eps, const Rotary& R, const float4* cs,
-                                          int t0, int nt, int h0, int nh, int n, bool& filled, A angles, F out) {
+template <typename T>
+__device__ __forceinline__ void load_weight(const void* w, int ca, int cb, float (&wa)[8], float (&wb)[8]) {
+  if (w) {
+    unpack8(load8(reinterpret_cast<const T*>(w) + 8 * ca), wa);
+    unpack8(load8(reinterpret_cast<const T*>(w) + 8 * cb), wb);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) wa[i] = wb[i] = 1.f;
+  }
+}
+
+// Where the rows of a block's tokens begin: source, and destination of keys ([B][heads][n][D]).
+struct TokenAt {
+  long long src, dst;
+};
+constexpr int kMaxTokens = 16;  // of a block
+
+template <bool KEYS>
+__device__ __forceinline__ void fill_tokens(TokenAt* tok, const Rows& X, int t0, int nt, int n, int D) {
+  if ((int)threadIdx.x < nt) {
+    const int g = t0 + threadIdx.x, b = g / n, j = g - b * n;
+    tok[threadIdx.x].src = b * X.sb + j * X.st;
+    tok[threadIdx.x].dst = KEYS ? ((long long)b * X.heads * n + j) * D : (long long)g * X.heads * D;
+  }
+}
+
+// Rows of heads [h0, h0 + nh) of a block's nt tokens: normed, rotated and stored at out + tok.dst +
+// h * out_head.  Loads of kU rows are in flight per thread; `angles` (which writes the tokens' cosines)
+// runs once, behind the first loads.  Rows are walked without divisions: those and the address
+// arithmetic were half of the pass's instructions.
+template <int D, typename T, typename O, int kU, typename A>
+__device__ __forceinline__ void rows_pass(const Rows& X, const TokenAt* tok, const void* w, float eps, const Rotary& R,
+                                          const float4* cs, int nt, int h0, int nh, O* out, long long out_head, bool& filled,
+                                          A angles) {
   constexpr int TPR = D / 16, RPP = kThreads / TPR;
   const int l = threadIdx.x % TPR, row0 = threadIdx.x / TPR;
   const int ca = chunk_a(l, R.r), cb = chunk_b(l, R.r);
-  const int total = nt * nh;
-  Raw8<T> wa = {}, wb = {};  // (kept packed: half the registers)
-  if (w) {
-    wa = load8(reinterpret_cast<const T*>(w) + 8 * ca);
-    wb = load8(reinterpret_cast<const T*>(w) + 8 * cb);
-  }
+  const int total = nt * nh, step_t = RPP / nh, step_h = RPP - step_t * nh;
+  int tk = row0 / nh, h = row0 - tk * nh;  // of the next row to load
+  float wa[8], wb[8];
+  load_weight<T>(w, ca, cb, wa, wb);
   for (int base = 0; base < total; base += RPP * kU) {
     Raw8<T> ra[kU], rb[kU];
+    int tks[kU], hs[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int row = base + u * RPP + row0;
-      if (row < total) {
-        const int tk = row / nh, h = h0 + row - tk * nh, g = t0 + tk, b = g / n, j = g - b * n;
-        const T* src = reinterpret_cast<const T*>(X.p) + b * X.sb + j * X.st + h * X.sh;
+      tks[u] = tk;
+      hs[u] = h0 + h;
+      if (tk < nt) {
+        const T* src = reinterpret_cast<const T*>(X.p) + tok[tk].src + hs[u] * X.sh;
         ra[u] = load8_rw(src + 8 * ca);
         rb[u] = load8_rw(src + 8 * cb);
       } else {
         ra[u] = Raw8<T>{};
         rb[u] = Raw8<T>{};
+      }
+      tk += step_t;
+      h += step_h;
+      if (h >= nh) {
+        h -= nh;
+        ++tk;
       }
     }
     if (!filled) {
@@ -67,18 +103,16 @@ __device__ __forceinline__ void rows_pass(const Rows& X, const void* w, float ep
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int row = base + u * RPP + row0;
       if (base + u * RPP >= total) break;  // (uniform over the block)
-      const int tk = min(row, total - 1) / nh;
-      float a[8], b8[8];
+      float a[8], b[8];
       unpack8(ra[u], a);
-      unpack8(rb[u], b8);
-      norm_rotate_row<TPR, T>(a, b8, l, w != nullptr, wa, wb, D, eps, cs + tk * (R.r / 4), R.r, R.interleaved);
-      if (row < total) {
-        const int h = h0 + row - tk * nh, g = t0 + tk, b = g / n, j = g - b * n;
-        O* dst = reinterpret_cast<O*>(out(b, j, h));
+      unpack8(rb[u], b);
+      const bool live = tks[u] < nt;
+      norm_rotate_row<TPR>(a, b, l, w != nullptr, wa, wb, D, eps, cs + (live ? tks[u] : 0) * (R.r / 4), R.r, R.interleaved);
+      if (live) {
+        O* dst = out + tok[tks[u]].dst + hs[u] * out_head;
         store8(dst + 8 * ca, a);
-        store8(dst + 8 * cb, b8);
+        store8(dst + 8 * cb, b);
       }
     }
   }
@@ -93,7 +127,8 @@ struct RotateParams {
 
 template <int D, typename T, typename O>
 __global__ void __launch_bounds__(kThreads, 3) norm_rotate_kernel(const RotateParams p) {
-  extern __shared__ __align__(16) float2 cs[];
+  extern __shared__ __align__(16) float cs[];
+  __shared__ TokenAt tok[2][kMaxTokens];
   const RotateArgs& A = p.a;
   const int t0 = blockIdx.x * p.per, nt = min(p.per, p.tokens - t0);
   auto angles = [&] {
@@ -107,25 +142,27 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rotate_kernel(const RotatePa
   const int lo = blockIdx.y * p.q_split, hi = min(lo + p.q_split, A.q.heads + A.k.heads);
   const int q0 = min(lo, A.q.heads), q1 = min(hi, A.q.heads);
   const int k0 = max(lo, A.q.heads) - A.q.heads, k1 = max(hi, A.q.heads) - A.q.heads;
+  fill_tokens<false>(tok[0], A.q, t0, nt, A.n, D);
+  fill_tokens<true>(tok[1], A.k, t0, nt, A.n, D);
+  __syncthreads();
   bool filled = false;
   constexpr int kU = sizeof(T) == 2 ? 3 : 2;
+  const float4* c4 = reinterpret_cast<const float4*>(cs);
   if (q1 > q0)
-    rows_pass<D, T, O, kU>(A.q, A.wq, A.eps, A.rot, reinterpret_cast<const float4*>(cs), t0, nt, q0, q1 - q0, A.n, filled,
-                           angles, [&](int b, int j, int h) {
-                             return reinterpret_cast<O*>(A.q_out) + (((long long)b * A.n + j) * A.q.heads + h) * D;
-                           });
+    rows_pass<D, T, O, kU>(A.q, tok[0], A.wq, A.eps, A.rot, c4, nt, q0, q1 - q0, reinterpret_cast<O*>(A.q_out), D, filled, angles);
   if (k1 > k0)
-    rows_pass<D, T, O, kU>(A.k, A.wk, A.eps, A.rot, reinterpret_cast<const float4*>(cs), t0, nt, k0, k1 - k0, A.n, filled,
-                           angles, [&](int b, int j, int h) {
-                             return reinterpret_cast<O*>(A.k_out) + (((long long)b * A.k.heads + h) * A.n + j) * D;
-                           });
+    rows_pass<D, T, O, kU>(A.k, tok[1], A.wk, A.eps, A.rot, c4, nt, k0, k1 - k0, reinterpret_cast<O*>(A.k_out),
+                           (long long)A.n * D, filled, angles);
 }
 
 struct AppendParams {
   AppendArgs a;
   int blocks;      // 16-token blocks a batch entry's tokens can touch
   int groups;      // head groups of 4
-  int kv_blocks;   // B * blocks * groups; later grid blocks take queries
+  int kv_blocks;   // B * blocks * groups; the other grid blocks take queries
+  int every;       // grid block i * every is kv block i: the append's blocks wait on memory in long
+                   // chains, so they are spread among the queries' (together first: 43 us instead
+                   // of 32 for 4096 tokens of 64 + 8 heads)
   int per, tokens, q_split, q_groups;
 };
 
@@ -176,6 +213,18 @@ __device__ __forceinline__ void unpack_some(const RawE<__half, E>& r, float (&x)
   }
 }
 
+// Element i of those.
+template <int E>
+__device__ __forceinline__ float element(const RawE<float, E>& r, int i) { return __uint_as_float(r.w[i]); }
+template <int E>
+__device__ __forceinline__ float element(const RawE<__nv_bfloat16, E>& r, int i) {
+  return __uint_as_float(i & 1 ? r.w[i >> 1] & 0xffff0000u : r.w[i >> 1] << 16);
+}
+template <int E>
+__device__ __forceinline__ float element(const RawE<__half, E>& r, int i) {
+  return __half2float(__ushort_as_half((unsigned short)(i & 1 ? r.w[i >> 1] >> 16 : r.w[i >> 1])));
+}
+
 // The block's scale exponent from its new tokens' largest magnitude and, where it holds tokens, its
 // old one; the scale is stored and the old exponent returned in e_old.
 __device__ __forceinline__ int block_scale(float amax, int held, float old_scale, float* scale, int lane, int& e_old) {
@@ -189,16 +238,32 @@ __device__ __forceinline__ int block_scale(float amax, int held, float old_scale
   return e;
 }
 
-template <int D, typename T, typename F>
-__device__ __forceinline__ bool append_keys(const AppendArgs& A, unsigned char* blk, const float4* cs, int b, int h,
+// Running largest magnitude, and 0 * x summed: NaN as soon as one x is infinite or NaN.
+struct Magnitude {
+  float top = 0.f;
+  uint64_t zero = 0;
+  __device__ __forceinline__ void add(float a, float b) {
+    top = fmaxf(top, fmaxf(fabsf(a), fabsf(b)));
+    zero = fma2(pair(a, b), 0, zero);
+  }
+  __device__ __forceinline__ bool odd() const {
+    float x, y;
+    unpair(zero, x, y);
+    return x + y != 0.f;
+  }
+};
+
+// The warp's rows [lo, hi) of one block of keys.  rot: the warp's shared memory for its rotated rows
+// (fp32, 16 D of them): a thread reads back what it wrote, so that it need not hold 64 values (d = 128)
+// from the maximum to the codes, which would cost the occupancy that the loads need.
+template <int D, typename T, typename B, typename F>
+__device__ __forceinline__ bool append_keys(const AppendArgs& A, B block, const float4* cs, float4* rot, int b, int h,
                                             long long j0, int lo, int hi, int held, int lane, F angles) {
   constexpr int TPR = D / 16, RPW = 32 / TPR, NP = 16 / RPW;
   const int l = lane % TPR, r0 = lane / TPR;
   const int ca = chunk_a(l, A.rot.r), cb = chunk_b(l, A.rot.r);
-  float* scale = reinterpret_cast<float*>(blk + 32 * D);
-  const float old_scale = held > 0 ? *scale : 1.f;
   const T* src = reinterpret_cast<const T*>(A.k.p) + b * A.k.sb + h * A.k.sh;
-  Raw8<T> ra[NP], rc[NP], wa = {}, wb = {};
+  Raw8<T> ra[NP], rc[NP];
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
     const int s = p * RPW + r0;
@@ -209,46 +274,60 @@ __device__ __forceinline__ bool append_keys(const AppendArgs& A, unsigned char* 
       rc[p] = load8(row + 8 * cb);
     }
   }
-  if (A.wk) {
-    wa = load8(reinterpret_cast<const T*>(A.wk) + 8 * ca);
-    wb = load8(reinterpret_cast<const T*>(A.wk) + 8 * cb);
-  }
+  float wa[8], wb[8];
+  load_weight<T>(A.wk, ca, cb, wa, wb);
   angles();
   __syncthreads();
-  float a[NP][8], c[NP][8];
+  unsigned char* blk = block();
+  float* scale = reinterpret_cast<float*>(blk + 32 * D);
+  const float old_scale = held > 0 ? *scale : 1.f;
+  rot += lane;
+  Magnitude mag;
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
-    unpack8(ra[p], a[p]);
-    unpack8(rc[p], c[p]);
-  }
-  float amax = 0.f;
-  bool bad = false;
-#pragma unroll
-  for (int p = 0; p < NP; ++p) {
+    if (p * RPW + RPW <= lo || p * RPW >= hi) continue;  // (uniform over the warp)
     const int s = p * RPW + r0;
+    float a[8], c[8];
+    unpack8(ra[p], a);
+    unpack8(rc[p], c);
     // (rows without a new token are zeros; their cosines are those of an existing slot)
-    norm_rotate_row<TPR, T>(a[p], c[p], l, A.wk != nullptr, wa, wb, D, A.eps, cs + (s >= lo && s < hi ? s : lo) * (A.rot.r / 4),
+    norm_rotate_row<TPR>(a, c, l, A.wk != nullptr, wa, wb, D, A.eps, cs + (s >= lo && s < hi ? s : lo) * (A.rot.r / 4),
                          A.rot.r, A.rot.interleaved);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      amax = fmaxf(amax, fmaxf(finite_abs(a[p][i]), finite_abs(c[p][i])));
-      bad |= !(fabsf(a[p][i]) <= 3.402823466e38f) || !(fabsf(c[p][i]) <= 3.402823466e38f);
+    for (int i = 0; i < 8; i += 2) {
+      mag.add(a[i], a[i + 1]);
+      mag.add(c[i], c[i + 1]);
+    }
+    rot[(4 * p + 0) * 32] = make_float4(a[0], a[1], a[2], a[3]);
+    rot[(4 * p + 1) * 32] = make_float4(a[4], a[5], a[6], a[7]);
+    rot[(4 * p + 2) * 32] = make_float4(c[0], c[1], c[2], c[3]);
+    rot[(4 * p + 3) * 32] = make_float4(c[4], c[5], c[6], c[7]);
+  }
+  const bool odd = __any_sync(kFull, mag.odd());
+  if (odd) {  // infinities and NaN do not count for the scale
+    mag.top = 0.f;
+    for (int i = 0; i < 4 * NP; ++i) {
+      const int p = i >> 2;
+      if (p * RPW + RPW <= lo || p * RPW >= hi) continue;
+      const float4 v = rot[i * 32];
+      mag.top = fmaxf(mag.top, fmaxf(fmaxf(finite_abs(v.x), finite_abs(v.y)), fmaxf(finite_abs(v.z), finite_abs(v.w))));
     }
   }
   int e_old;
-  const int e = block_scale(amax, held, old_scale, scale, lane, e_old);
+  const int e = block_scale(mag.top, held, old_scale, scale, lane, e_old);
   const float inv = exp2i(-e);
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
     const int s = p * RPW + r0;
     if (s < lo || s >= hi) continue;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      a[p][i] *= inv;
-      c[p][i] *= inv;
+    for (int k = 0; k < 2; ++k) {
+      const float4 v = rot[(4 * p + 2 * k) * 32], u = rot[(4 * p + 2 * k + 1) * 32];
+      const float x[8] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv, u.x * inv, u.y * inv, u.z * inv, u.w * inv};
+      const uint2 w = odd ? make_uint2(encode4(x), encode4(x + 4)) : make_uint2(encode4_finite(x), encode4_finite(x + 4));
+      const int ch = k ? cb : ca;
+      *reinterpret_cast<uint2*>(blk + k_chunk<D>(s, ch >> 1) + 8 * (ch & 1)) = w;
     }
-    *reinterpret_cast<uint2*>(blk + k_chunk<D>(s, ca >> 1) + 8 * (ca & 1)) = make_uint2(encode4(a[p]), encode4(a[p] + 4));
-    *reinterpret_cast<uint2*>(blk + k_chunk<D>(s, cb >> 1) + 8 * (cb & 1)) = make_uint2(encode4(c[p]), encode4(c[p] + 4));
   }
   if (e > e_old && held > 0) {  // held rows to the raised scale, 16 codes at a time
     const float f = exp2i(e_old - e);
@@ -266,15 +345,13 @@ __device__ __forceinline__ bool append_keys(const AppendArgs& A, unsigned char* 
       *at = v;
     }
   }
-  return bad;
+  return odd;
 }
 
-template <int D, typename T, typename F>
-__device__ __forceinline__ bool append_values(const AppendArgs& A, unsigned char* blk, int b, int h, long long j0, int lo,
-                                              int hi, int held, int lane, F angles) {
+template <int D, typename T, typename B, typename F>
+__device__ __forceinline__ bool append_values(const AppendArgs& A, B block, int b, int h, long long j0, int lo, int hi,
+                                              int held, int lane, F angles) {
   constexpr int E = D / 32;  // coordinates E * lane .. of all 16 tokens
-  float* scale = reinterpret_cast<float*>(blk + 32 * D + 4);
-  const float old_scale = held > 0 ? *scale : 1.f;
   const T* src = reinterpret_cast<const T*>(A.v.p) + b * A.v.sb + h * A.v.sh + E * lane;
   RawE<T, E> raw[16];
 #pragma unroll
@@ -284,20 +361,30 @@ __device__ __forceinline__ bool append_values(const AppendArgs& A, unsigned char
   }
   angles();
   __syncthreads();  // (the block's barrier for the key warps' cosines)
-  float x[16][E];
+  unsigned char* blk = block();
+  float* scale = reinterpret_cast<float*>(blk + 32 * D + 4);
+  const float old_scale = held > 0 ? *scale : 1.f;
+  Magnitude mag;
 #pragma unroll
-  for (int s = 0; s < 16; ++s) unpack_some<E>(raw[s], x[s]);
-  float amax = 0.f;
-  bool bad = false;
+  for (int s = 0; s < 16; ++s) {
+    float x[E];
+    unpack_some<E>(raw[s], x);
 #pragma unroll
-  for (int s = 0; s < 16; ++s)
+    for (int i = 0; i < E; i += 2) mag.add(x[i], x[i + 1]);
+  }
+  const bool odd = __any_sync(kFull, mag.odd());
+  if (odd) {  // infinities and NaN do not count for the scale
+    mag.top = 0.f;
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      amax = fmaxf(amax, finite_abs(x[s][i]));
-      bad |= !(fabsf(x[s][i]) <= 3.402823466e38f);
+    for (int s = 0; s < 16; ++s) {
+      float x[E];
+      unpack_some<E>(raw[s], x);
+#pragma unroll
+      for (int i = 0; i < E; ++i) mag.top = fmaxf(mag.top, finite_abs(x[i]));
     }
+  }
   int e_old;
-  const int e = block_scale(amax, held, old_scale, scale, lane, e_old);
+  const int e = block_scale(mag.top, held, old_scale, scale, lane, e_old);
   const float inv = exp2i(-e);
   const bool raise = held > 0 && e > e_old;
   const float f = exp2i(e_old - e);
@@ -307,8 +394,9 @@ __device__ __forceinline__ bool append_values(const AppendArgs& A, unsigned char
     uint32_t w[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {  // tokens 2u, 2u + 1, 2u + 8, 2u + 9
-      const float four[4] = {x[2 * u][i] * inv, x[2 * u + 1][i] * inv, x[2 * u + 8][i] * inv, x[2 * u + 9][i] * inv};
-      w[u] = encode4(four);
+      const float four[4] = {element<E>(raw[2 * u], i) * inv, element<E>(raw[2 * u + 1], i) * inv,
+                             element<E>(raw[2 * u + 8], i) * inv, element<E>(raw[2 * u + 9], i) * inv};
+      w[u] = odd ? encode4(four) : encode4_finite(four);
     }
     if (lo == 0 && hi == 16) {
       *reinterpret_cast<uint4*>(vb + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -323,16 +411,20 @@ __device__ __forceinline__ bool append_values(const AppendArgs& A, unsigned char
       }
     }
   }
-  return bad;
+  return odd;
 }
 
 template <int D, typename T>
-__global__ void __launch_bounds__(kThreads) byte_append_kernel(const AppendParams p) {
-  extern __shared__ __align__(16) float2 cs[];
+__global__ void __launch_bounds__(kThreads, (D * sizeof(T) <= 256 ? 3 : 1)) byte_append_kernel(const AppendParams p) {
+  extern __shared__ __align__(16) float cs[];
   const AppendArgs& A = p.a;
-  if ((int)blockIdx.x >= p.kv_blocks) {  // queries
-    const int i = blockIdx.x - p.kv_blocks, part = i % p.q_groups, t0 = i / p.q_groups * p.per;
+  const int turn = (int)blockIdx.x / p.every;
+  if (turn >= p.kv_blocks || (int)blockIdx.x != turn * p.every) {  // queries
+    const int i = blockIdx.x - min(p.kv_blocks, turn + 1), part = i % p.q_groups, t0 = i / p.q_groups * p.per;
     const int nt = min(p.per, p.tokens - t0), h0 = part * p.q_split, nh = min(p.q_split, A.Hq - h0);
+    __shared__ TokenAt tok[kMaxTokens];
+    fill_tokens<false>(tok, A.q, t0, nt, A.n, D);
+    __syncthreads();
     bool filled = false;
     auto angles = [&] {
       if (A.rot.r)
@@ -341,14 +433,11 @@ __global__ void __launch_bounds__(kThreads) byte_append_kernel(const AppendParam
           return token_position(A.pos, axis, b, g - b * A.n, A.B, A.n);
         });
     };
-    rows_pass<D, T, T, (sizeof(T) == 2 ? 3 : 2)>(A.q, A.wq, A.eps, A.rot, reinterpret_cast<const float4*>(cs), t0, nt, h0,
-                                                 nh, A.n, filled, angles, [&](int b, int j, int h) {
-                                                   return reinterpret_cast<T*>(A.q_out) +
-                                                          (((long long)b * A.n + j) * A.Hq + h) * D;
-                                                 });
+    rows_pass<D, T, T, (sizeof(T) == 2 ? 3 : 2)>(A.q, tok, A.wq, A.eps, A.rot, reinterpret_cast<const float4*>(cs), nt, h0, nh,
+                                                 reinterpret_cast<T*>(A.q_out), D, filled, angles);
     return;
   }
-  const int hg = blockIdx.x % p.groups, rest = blockIdx.x / p.groups;
+  const int hg = turn % p.groups, rest = turn / p.groups;
   const int i = rest % p.blocks, b = rest / p.blocks;
   const int start = __ldg(A.start + b);
   const int count = A.count ? min(A.n, __ldg(A.count + b)) : A.n;
@@ -364,9 +453,10 @@ __global__ void __launch_bounds__(kThreads) byte_append_kernel(const AppendParam
       for (int u = threadIdx.x; u < (hi - lo) * half; u += kThreads) {
         const int s = lo + u / half, pr = u % half;
         const uint64_t entry = __ldg(reinterpret_cast<const unsigned long long*>(A.rot.table) + pr);
-        cs[s * half + pair_slot(pr, A.rot.r, A.rot.interleaved)] = pair_angle(entry, [&](int axis) {
-          return token_position(A.pos, axis, b, (int)(j0 + s), A.B, A.n);
-        });
+        float* at = cs + 2 * s * half + pair_slot(pr, A.rot.r, A.rot.interleaved);
+        const float2 v = pair_angle(entry, [&](int axis) { return token_position(A.pos, axis, b, (int)(j0 + s), A.B, A.n); });
+        at[0] = v.x;
+        at[2] = v.y;
       }
     }
   };
@@ -377,10 +467,19 @@ __global__ void __launch_bounds__(kThreads) byte_append_kernel(const AppendParam
     __syncthreads();
     return;
   }
-  const int page = page_of(A.pool, b, tile);
-  unsigned char* blk = A.pool.base + pool_block(A.pool, page, h) * block_bytes(D);
-  const bool bad = (warp & 1) ? append_values<D, T>(A, blk, b, h, j0, lo, hi, held, lane, angles)
-                              : append_keys<D, T>(A, blk, reinterpret_cast<const float4*>(cs), b, h, j0, lo, hi, held, lane, angles);
+  // the table's entry is requested here and looked at behind the rows' loads
+  const int entry = tile >= 0 && tile < A.pool.max_blocks ? __ldg(A.pool.table + (long long)b * A.pool.max_blocks + tile) : -1;
+  auto block = [&] {
+    int page = entry;
+    if ((unsigned)page >= (unsigned)A.pool.num_pages) {
+      if (A.pool.err) atomicExch(A.pool.err, TQ_DEVERR_BAD_PAGE);
+      page = A.pool.num_pages;
+    }
+    return A.pool.base + pool_block(A.pool, page, h) * block_bytes(D);
+  };
+  const bool bad = (warp & 1) ? append_values<D, T>(A, block, b, h, j0, lo, hi, held, lane, angles)
+                              : append_keys<D, T>(A, block, reinterpret_cast<const float4*>(cs),
+                                                    reinterpret_cast<float4*>(cs + 16 * A.rot.r) + (warp >> 1) * 4 * D, b, h, j0, lo, hi, held, lane, angles);
   if (bad && A.pool.err) atomicExch(A.pool.err, TQ_DEVERR_NONFINITE);
 }
 
@@ -405,7 +504,7 @@ void rows_split(int d, int tokens, int heads, int* per, int* split) {
   *per = (6 * rpp + heads - 1) / heads;
   const int fill = tokens / 608;  // four blocks on each of 152 SMs
   if (*per > fill) *per = fill;
-  if (*per > 16) *per = 16;
+  if (*per > kMaxTokens) *per = kMaxTokens;
   if (*per < 1) *per = 1;
   if (tokens <= 304 && heads > rpp) *split = rpp;
 }
@@ -418,7 +517,7 @@ cudaError_t rotate_go(const RotateArgs& a, cudaStream_t s) {
   const int heads = a.q.heads + a.k.heads;
   rows_split(D, p.tokens, heads, &p.per, &p.q_split);
   const dim3 grid((p.tokens + p.per - 1) / p.per, (heads + p.q_split - 1) / p.q_split);
-  norm_rotate_kernel<D, T, O><<<grid, kThreads, (size_t)p.per * (a.rot.r / 2) * sizeof(float2), s>>>(p);
+  norm_rotate_kernel<D, T, O><<<grid, kThreads, (size_t)p.per * a.rot.r * sizeof(float), s>>>(p);
   return cudaGetLastError();
 }
 template <int D, typename T>
@@ -448,8 +547,16 @@ cudaError_t append_go(const AppendArgs& a, cudaStream_t s) {
     p.q_groups = (a.Hq + p.q_split - 1) / p.q_split;
     q_blocks = (p.tokens + p.per - 1) / p.per * p.q_groups;
   }
+  p.every = (p.kv_blocks + q_blocks) / p.kv_blocks;
   const int tk = p.per > 16 ? p.per : 16;
-  byte_append_kernel<D, T><<<p.kv_blocks + q_blocks, kThreads, (size_t)tk * (a.rot.r / 2) * sizeof(float2), s>>>(p);
+  // the cosines of a block's tokens, and its four key warps' rotated rows
+  const size_t smem = (size_t)tk * a.rot.r * sizeof(float) + 4 * 16 * D * sizeof(float);
+  static std::atomic<uint64_t> done{0};
+  int dev;
+  sm_count(&dev);
+  const cudaError_t e = allow_smem((const void*)byte_append_kernel<D, T>, 2 * 4 * 16 * D * sizeof(float), dev, done);
+  if (e != cudaSuccess) return e;
+  byte_append_kernel<D, T><<<p.kv_blocks + q_blocks, kThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 template <int D>

@@ -96,8 +96,8 @@ __device__ __forceinline__ int chunk_a(int l, int r) { return l < r / 16 ? l : r
 __device__ __forceinline__ int chunk_b(int l, int r) { return l < r / 16 ? l + r / 16 : r / 8 + 2 * (l - r / 16) + 1; }
 
 // Cosines and sines of one token lie in shared memory as [4][r / 16] groups of two pairs
-// (cos, sin, cos, sin): group j of thread l at j * (r / 16) + l, so that the threads of a row read
-// consecutive 16-byte words.  float2 index of pair p:
+// (cos, cos, sin, sin): group j of thread l at j * (r / 16) + l, so that the threads of a row read
+// consecutive 16-byte words.  Index of pair p's cosine (its sine is 2 floats on):
 __device__ __forceinline__ int pair_slot(int p, int r, int interleaved) {
   int l, j;
   if (!interleaved) {
@@ -109,7 +109,7 @@ __device__ __forceinline__ int pair_slot(int p, int r, int interleaved) {
     l = u >> 2;
     j = 2 * hi + ((u & 3) >> 1);
   }
-  return 2 * (j * (r / 16) + l) + (p & 1);
+  return 4 * (j * (r / 16) + l) + (p & 1);
 }
 
 // (cos, sin) of one pair at the token whose positions on axis a are pos(a).
@@ -124,51 +124,78 @@ __device__ __forceinline__ float2 pair_angle(uint64_t entry, F pos) {
   return cs;
 }
 
-// Norm (with wa, wb the row's weight chunks as loaded) and rotation of one row's values.
-template <int TPR, typename T>
-__device__ __forceinline__ void norm_rotate_row(float (&a)[8], float (&b)[8], int l, bool norm, const Raw8<T>& wa,
-                                                const Raw8<T>& wb, int D, float eps, const float4* cs, int r,
+// Pairs of fp32 values in one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Norm (norm: with wa, wb the row's weights) and rotation of one row's values.
+template <int TPR>
+__device__ __forceinline__ void norm_rotate_row(float (&a)[8], float (&b)[8], int l, bool norm, const float (&wa)[8],
+                                                const float (&wb)[8], int D, float eps, const float4* cs, int r,
                                                 int interleaved) {
-  if (norm) {
-    float ss = 0.f;
+  uint64_t a2[4], b2[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
+  for (int i = 0; i < 4; ++i) {
+    a2[i] = pair(a[2 * i], a[2 * i + 1]);
+    b2[i] = pair(b[2 * i], b[2 * i + 1]);
+  }
+  if (norm) {
+    uint64_t s2 = mul2(a2[0], a2[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) s2 = fma2(a2[i], a2[i], s2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s2 = fma2(b2[i], b2[i], s2);
+    float ss, s1;
+    unpair(s2, ss, s1);
+    ss += s1;
 #pragma unroll
     for (int m = 1; m < TPR; m <<= 1) ss += __shfl_xor_sync(kFull, ss, m);
     const float rs = rsqrtf(ss / (float)D + eps);
-    float x[8], y[8];
-    unpack8(wa, x);
-    unpack8(wb, y);
+    const uint64_t rs2 = pair(rs, rs);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      a[i] = a[i] * rs * x[i];
-      b[i] = b[i] * rs * y[i];
+    for (int i = 0; i < 4; ++i) {
+      a2[i] = mul2(mul2(a2[i], rs2), pair(wa[2 * i], wa[2 * i + 1]));
+      b2[i] = mul2(mul2(b2[i], rs2), pair(wb[2 * i], wb[2 * i + 1]));
     }
   }
-  if (l < r / 16) {
-    float c[8], s[8];
+  if (l < r / 16 && !interleaved) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float4 v = cs[j * (r / 16) + l];
-      c[2 * j] = v.x; s[2 * j] = v.y; c[2 * j + 1] = v.z; s[2 * j + 1] = v.w;
+      const uint64_t c = pair(v.x, v.y), s = pair(v.z, v.w), ns = pair(-v.z, -v.w), x = a2[j];
+      a2[j] = fma2(b2[j], ns, mul2(x, c));
+      b2[j] = fma2(b2[j], c, mul2(x, s));
     }
-    if (!interleaved) {
+  }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float x = a[i], y = b[i];
-        a[i] = x * c[i] - y * s[i];
-        b[i] = x * s[i] + y * c[i];
-      }
-    } else {
+  for (int i = 0; i < 4; ++i) {
+    unpair(a2[i], a[2 * i], a[2 * i + 1]);
+    unpair(b2[i], b[2 * i], b[2 * i + 1]);
+  }
+  if (l < r / 16 && interleaved) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float x = a[2 * i], y = a[2 * i + 1];
-        a[2 * i] = x * c[i] - y * s[i];
-        a[2 * i + 1] = x * s[i] + y * c[i];
-        x = b[2 * i], y = b[2 * i + 1];
-        b[2 * i] = x * c[4 + i] - y * s[4 + i];
-        b[2 * i + 1] = x * s[4 + i] + y * c[4 + i];
-      }
+    for (int j = 0; j < 4; ++j) {
+      const float4 v = cs[j * (r / 16) + l];
+      float* m = j < 2 ? a + 4 * j : b + 4 * (j - 2);
+      const float x = m[0], y = m[1], z = m[2], w = m[3];
+      m[0] = x * v.x - y * v.z;
+      m[1] = x * v.z + y * v.x;
+      m[2] = z * v.y - w * v.w;
+      m[3] = z * v.w + w * v.y;
     }
   }
 }
