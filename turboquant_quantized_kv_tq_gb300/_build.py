@@ -2,7 +2,8 @@
 
 Each translation unit is compiled in parallel with nvcc (CUDA sources) or g++ (host sources),
 then linked into ``turboquant_quantized_kv_tq_gb300/_lib/libtq.so`` with the CUDA runtime linked
-statically.  Objects go to ``_build/`` at the repository root.
+statically.  Beside it goes ``_lib/_tq_torch.so``, the Python extension of ``byte_cache`` (torch
+tensors to the C ABI).  Objects go to ``_build/`` at the repository root.
 """
 
 import os
@@ -17,6 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libtq.so")
+EXT_SRC = os.path.join(CSRC, "python", "tq_torch.cpp")
+EXT_PATH = os.path.join(LIB_DIR, "_tq_torch.so")
 OBJ_DIR = os.path.join(ROOT, "_build", "obj")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -51,20 +54,48 @@ def _compile(src, extra_nvcc=()):
     return src, res.returncode, res.stdout + res.stderr, out
 
 
+def _compile_ext():
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    out = os.path.join(OBJ_DIR, "tq_torch.cpp.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", INCLUDE, "-isystem", inc, "-isystem", os.path.join(_cuda_home(), "include"),
+           "-I", sysconfig.get_paths()["include"], "-c", EXT_SRC, "-o", out]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    return EXT_SRC, res.returncode, res.stdout + res.stderr, out
+
+
+def _link_ext(obj):
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = EXT_PATH + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", LIB_DIR, "-l:libtq.so", "-Wl,-rpath,$ORIGIN", "-L", lib,
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("linking _tq_torch.so failed:\n" + res.stdout + res.stderr)
+    os.replace(tmp, EXT_PATH)
+
+
 def build(verbose=False, extra_nvcc=()):
     """Compile every source and link libtq.so; raise RuntimeError on the first failure."""
     os.makedirs(OBJ_DIR, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
     srcs = sources()
-    with ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        ext = ex.submit(_compile_ext)
         results = list(ex.map(lambda s: _compile(s, extra_nvcc), srcs))
+        ext = ext.result()
     objs = []
-    for src, rc, log, out in results:
+    for src, rc, log, out in results + [ext]:
         if verbose and log.strip():
             print(f"[{src}]\n{log}", file=sys.stderr)
         if rc != 0:
             raise RuntimeError(f"compiling {src} failed:\n{log}")
-        objs.append(out)
+        if out != ext[3]:
+            objs.append(out)
     cuda = _cuda_home()
     tmp = LIB_PATH + ".tmp"
     cmd = [os.path.join(cuda, "bin", "nvcc"), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
@@ -72,6 +103,7 @@ def build(verbose=False, extra_nvcc=()):
     if res.returncode != 0:
         raise RuntimeError("linking libtq.so failed:\n" + res.stdout + res.stderr)
     os.replace(tmp, LIB_PATH)
+    _link_ext(ext[3])
     return LIB_PATH
 
 

@@ -8,64 +8,47 @@ be contiguous, with rows on 16-byte boundaries.  Nothing is copied or converted 
 the kernels do not take is refused.
 """
 
+import importlib.machinery
+import importlib.util
+import os
+
 import numpy as np
 import torch
 
+from . import _build
 from . import binding as _b
 from .binding import check
 
-_CODES = {torch.float32: _b.TQ_F32, torch.bfloat16: _b.TQ_BF16, torch.float16: _b.TQ_F16}
 
-# (the current stream's handle without building a Stream object: a tenth of the cost)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-_heads_c, _pages_c, _empty = _b.tq_heads, _b.tq_page_table, torch.empty
-
-
-def _code(t):
-    try:
-        return _CODES[t.dtype]
-    except KeyError:
-        raise ValueError(f"unsupported dtype {t.dtype}: float32, bfloat16 or float16") from None
+def _load_ext():
+    path = _build.EXT_PATH
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build the library first "
+                          "(python -c 'import __graft_entry__ as g; g.build()')")
+    loader = importlib.machinery.ExtensionFileLoader("_tq_torch", path)
+    mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_tq_torch", loader))
+    loader.exec_module(mod)
+    mod.set_error(_b.TQError)
+    return mod
 
 
-def _heads(t, name, shape, dtype, index, b, n, h):
-    """tq_heads of a 4-d view whose dims b, n, h are batch, token and head."""
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {list(shape)} on cuda:{index}, not {t.dtype} "
-                         f"{list(t.shape)} on {t.device}")
-    s = t.stride()
-    if s[3] != 1:
-        raise ValueError(f"{name}: the head dimension must be contiguous")
-    return _heads_c(t.data_ptr() or None, s[b], s[n], s[h], shape[h])
+# The calls from tensors to the C ABI (csrc/python/tq_torch.cpp): they check the tensors, allocate what
+# is returned and launch on the current stream of the tensors' device.
+_c = _load_ext()
 
 
-def _ints(t, name, shape, index):
-    if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != index or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)} on cuda:{index}")
-    return t.data_ptr()
-
-
-def _dense(t, name, shape, dtype, index):
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on cuda:{index}")
-    return t
-
-
-def _launch(index, device, stream, inputs, go):
-    """go(handle) with the device current and ``stream`` (default: the device's current one) the current
-    stream, so that outputs and workspaces allocated in it belong to the stream that uses them."""
-    if stream is None and torch._C._cuda_getDevice() == index:
-        return go(_raw_stream(index))
-    with torch.cuda.device(device):
-        if stream is None:
-            return go(_raw_stream(index))
-        with torch.cuda.stream(stream):
-            got = go(stream.cuda_stream)
-    for t in inputs:  # (their memory is not handed out again before the stream is done with it)
+def _on_stream(stream, inputs, call, *args):
+    """The call with ``stream`` as the current one, so that what it allocates belongs to that stream;
+    the inputs' memory is not handed out again before the stream is done with it."""
+    for t in inputs:
+        if t is not None and t.get_device() != stream.device_index:
+            raise ValueError("the tensors must be on the stream's device")
+    with torch.cuda.stream(stream):
+        out = call(*args)
+    for t in inputs:
         if t is not None:
             t.record_stream(stream)
-    return got
+    return out
 
 
 def _device(device):
@@ -110,16 +93,8 @@ class Rotary:
         self.rotary_dim, self.interleaved = int(rotary_dim), bool(interleaved)
         self.host_table = host
         self.table = torch.from_numpy(host.view(np.int64)).to(_device(device))
-        self.index = self.table.get_device()
-        self._c = _b.tq_rotary(self.table.data_ptr(), self.rotary_dim, int(self.interleaved), self.num_axes)
-
-
-def _rotary(rotary, index):
-    if rotary is None:
-        return None, 1
-    if rotary.index != index:
-        raise ValueError(f"the rotary table must be on cuda:{index}")
-    return rotary._c, rotary.num_axes
+        self._args = (self.table.data_ptr(), self.rotary_dim, int(self.interleaved), self.num_axes,
+                      self.table.get_device())
 
 
 def norm_rotate(q=None, k=None, rotary=None, positions=None, start=None, q_weight=None, k_weight=None, eps=1e-6,
@@ -132,47 +107,13 @@ def norm_rotate(q=None, k=None, rotary=None, positions=None, start=None, q_weigh
     is at ``start[b] + j`` (``start``: int32 CUDA [batch]; None: 0).  ``out_dtype``: q's dtype (default) or float32, which the packed caches'
     queries need.  Returns (q_out, k_out), contiguous in the shapes of q and k.
     """
-    x = q if q is not None else k
-    if x is None:
-        raise ValueError("neither q nor k given")
-    if x.dim() != 4 or not x.is_cuda:
-        raise ValueError("q and k must be CUDA tensors of 4 dims")
-    code, index, dt, device = _code(x), x.get_device(), x.dtype, x.device
-    shape = x.shape
-    batch, d = shape[0], shape[3]
-    n = shape[1 if q is not None else 2]
-    odt = dt if out_dtype is None else out_dtype
-    if odt is not dt and odt is not torch.float32:
+    if out_dtype is not None and out_dtype is not torch.float32 and out_dtype != (k if q is None else q).dtype:
         raise ValueError("out_dtype must be the inputs' dtype or float32")
-    rc, axes = _rotary(rotary, index)
-    qs = ks = None
-    q_shape = k_shape = None
-    if q is not None:
-        q_shape = (batch, n, shape[2], d)
-        qs = _heads(q, "q", q_shape, dt, index, 0, 1, 2)
-    if k is not None:
-        k_shape = (batch, k.shape[1] if k.dim() == 4 else 0, n, d)
-        ks = _heads(k, "k", k_shape, dt, index, 0, 2, 1)
-    pos = None if positions is None else _ints(positions, "positions", (axes, batch, n), index)
-    st = None if start is None else _ints(start, "start", (batch,), index)
-    wq = None if q_weight is None else _dense(q_weight, "q_weight", (d,), dt, index).data_ptr()
-    wk = None if k_weight is None else _dense(k_weight, "k_weight", (d,), dt, index).data_ptr()
-
-    def go(handle):
-        qo = ko = qp = kp = None
-        if qs is not None:
-            qo = _empty(q_shape, dtype=odt, device=device) if q_out is None else _dense(q_out, "q_out", q_shape, odt, index)
-            qp = qo.data_ptr()
-        if ks is not None:
-            ko = _empty(k_shape, dtype=odt, device=device) if k_out is None else _dense(k_out, "k_out", k_shape, odt, index)
-            kp = ko.data_ptr()
-        if batch and n:
-            status = _b.tq_norm_rotate(d, code, _CODES[odt], batch, n, qs, wq, qp, ks, wk, kp, eps, rc, pos, st, handle)
-            if status:
-                check(status)
-        return qo, ko
-
-    return _launch(index, device, stream, (q, k, positions, start, q_weight, k_weight, q_out, k_out), go)
+    args = (q, k, None if rotary is None else rotary._args, positions, start, q_weight, k_weight, eps,
+            out_dtype is torch.float32, q_out, k_out)
+    if stream is None:
+        return _c.norm_rotate(*args)
+    return _on_stream(stream, (q, k, positions, start, q_weight, k_weight, q_out, k_out), _c.norm_rotate, *args)
 
 
 class PagedByteCache:
@@ -199,16 +140,8 @@ class PagedByteCache:
         self.device = _device(device)
         self.pool = torch.zeros(need, dtype=torch.uint8, device=self.device)
         self.error = torch.zeros(1, dtype=torch.int32, device=self.device)
-        self._index = self.pool.get_device()
-        self._pool, self._error = self.pool.data_ptr(), self.error.data_ptr()
-        self._need = {}  # workspace bytes by (batch, nq, dtype)
-
-    def _pages(self, table):
-        if (table.dtype is not torch.int32 or table.dim() != 2 or table.shape[1] != self.max_blocks_per_seq
-                or table.get_device() != self._index or not table.is_contiguous()):
-            raise ValueError(f"block_table must be a contiguous int32 tensor [batch][{self.max_blocks_per_seq}] "
-                             f"on {self.device}")
-        return _pages_c(table.data_ptr(), self.max_blocks_per_seq, self.num_pages)
+        self._args = (self.head_dim, self.num_q_heads, self.num_kv_heads, self.num_pages, self.max_blocks_per_seq,
+                      self.pool.data_ptr(), self.error.data_ptr(), self.pool.get_device())
 
     def device_error(self):
         """The recorded TQ_DEVERR_* code (0: none), cleared by the call.  Waits for the device."""
@@ -225,38 +158,12 @@ class PagedByteCache:
         ``positions`` ([num_axes][batch][n]) are the rotation's positions; None: ``start[b] + j``.
         ``count[b]``: entry b appends only its first count[b] tokens.  ``q`` ([batch][n][num_q_heads][d]) is
         normed and rotated alike in the same launch: returns q_out (None without q)."""
-        d, dev, index = self.head_dim, self.device, self._index
-        pt = self._pages(block_table)
-        batch, n = block_table.shape[0], k.shape[2] if k.dim() == 4 else 0
-        code, dt = _code(k), k.dtype
-        shape = (batch, self.num_kv_heads, n, d)
-        ks, vs = _heads(k, "k", shape, dt, index, 0, 2, 1), _heads(v, "v", shape, dt, index, 0, 2, 1)
-        rc, axes = _rotary(rotary, index)
-        if start is None:
-            raise ValueError("start must be given")
-        st = _ints(start, "start", (batch,), index)
-        cn = None if count is None else _ints(count, "count", (batch,), index)
-        pos = None if positions is None else _ints(positions, "positions", (axes, batch, n), index)
-        wq = None if q_weight is None else _dense(q_weight, "q_weight", (d,), dt, index).data_ptr()
-        wk = None if k_weight is None else _dense(k_weight, "k_weight", (d,), dt, index).data_ptr()
-        qs = None
-        if q is not None:
-            q_shape = (batch, n, self.num_q_heads, d)
-            qs = _heads(q, "q", q_shape, dt, index, 0, 1, 2)
-
-        def go(handle):
-            qo = qp = None
-            if qs is not None:
-                qo = _empty(q_shape, dtype=dt, device=dev) if q_out is None else _dense(q_out, "q_out", q_shape, dt, index)
-                qp = qo.data_ptr()
-            if batch and n:
-                status = _b.tq_byte_append_paged(self.cfg, self._pool, pt, batch, n, code, ks, vs, st, cn, wk, eps, rc, pos,
-                                                 qs, wq, qp, self._error, handle)
-                if status:
-                    check(status)
-            return qo
-
-        return _launch(index, dev, stream, (k, v, start, block_table, count, positions, k_weight, q, q_weight, q_out), go)
+        args = (self._args, k, v, start, block_table, count, None if rotary is None else rotary._args, positions,
+                k_weight, q, q_weight, eps, q_out)
+        if stream is None:
+            return _c.append(*args)
+        return _on_stream(stream, (k, v, start, block_table, count, positions, k_weight, q, q_weight, q_out), _c.append,
+                          *args)
 
     def attention(self, q, seq_len, block_table, count=None, scale=None, out=None, stream=None):
         """q: CUDA tensor [batch][nq][num_q_heads][d] (or [batch][num_q_heads][d] for one query), any
@@ -264,44 +171,22 @@ class PagedByteCache:
         queries: query i attends to the first ``seq_len[b] - count[b] + 1 + i`` tokens, and rows
         i >= count[b] come out as zeros.  ``scale`` multiplies the scores (default 1 / sqrt(d)).  Returns
         out, contiguous in q's shape and dtype."""
-        dev, index = self.device, self._index
-        pt = self._pages(block_table)
-        q4 = q.unsqueeze(1) if q.dim() == 3 else q
-        batch, nq = block_table.shape[0], q4.shape[1] if q4.dim() == 4 else 0
-        code, dt = _code(q), q.dtype
-        qs = _heads(q4, "q", (batch, nq, self.num_q_heads, self.head_dim), dt, index, 0, 1, 2)
-        if seq_len is None:
-            raise ValueError("seq_len must be given")
-        sl = _ints(seq_len, "seq_len", (batch,), index)
-        cn = None if count is None else _ints(count, "count", (batch,), index)
-        if scale is None:
-            scale = self.head_dim ** -0.5
+        args = (self._args, q, seq_len, block_table, count, self.head_dim ** -0.5 if scale is None else scale, out)
+        if stream is None:
+            return _c.attention(*args)
+        return _on_stream(stream, (q, seq_len, block_table, count, out), _c.attention, *args)
 
-        def go(handle):
-            o = _empty(q.shape, dtype=dt, device=dev) if out is None else _dense(out, "out", q.shape, dt, index)
-            if batch and nq:
-                need = self._need.get((batch, nq, code))
-                if need is None:
-                    need = _b.tq_byte_attention_workspace_bytes(self.cfg, pt, batch, nq, code)
-                    self._need[(batch, nq, code)] = need
-                ws = _empty(need, dtype=torch.uint8, device=dev)
-                status = _b.tq_byte_attention_paged(self.cfg, self._pool, pt, batch, nq, code, qs, sl, cn, scale,
-                                                    o.data_ptr(), ws.data_ptr(), need, self._error, handle)
-                if status:
-                    check(status)
-            return o
-
-        return _launch(index, dev, stream, (q, seq_len, block_table, count, out), go)
-
-    def dequantize(self, b, kvh, t0, t1, block_table, stream=None):
+    def dequantize(self, b, kvh, t0, t1, block_table):
         """Tokens [t0, t1) of KV head kvh of entry b as fp32 (k, v) [t1 - t0][d]."""
-        pt = self._pages(block_table)
-
-        def go(handle):
-            k = _empty((max(t1 - t0, 0), self.head_dim), dtype=torch.float32, device=self.device)
+        if (block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous()
+                or block_table.shape[1] != self.max_blocks_per_seq or block_table.device != self.device):
+            raise ValueError(f"block_table must be a contiguous int32 tensor [batch][{self.max_blocks_per_seq}] "
+                             f"on {self.device}")
+        pt = _b.tq_page_table(block_table.data_ptr(), self.max_blocks_per_seq, self.num_pages)
+        with torch.cuda.device(self.device):
+            k = torch.empty(max(t1 - t0, 0), self.head_dim, dtype=torch.float32, device=self.device)
             v = torch.empty_like(k)
-            check(_b.tq_byte_dequantize(self.cfg, self._pool, pt, block_table.shape[0], b, kvh, t0, t1,
-                                        k.data_ptr() or None, v.data_ptr() or None, handle))
-            return k, v
-
-        return _launch(self._index, self.device, stream, (block_table,), go)
+            check(_b.tq_byte_dequantize(self.cfg, self.pool.data_ptr(), pt, block_table.shape[0], b, kvh, t0, t1,
+                                        k.data_ptr() or None, v.data_ptr() or None,
+                                        torch.cuda.current_stream().cuda_stream))
+        return k, v
