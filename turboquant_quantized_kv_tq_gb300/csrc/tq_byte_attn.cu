@@ -19,7 +19,7 @@ namespace tqb {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kMaxGrid = 512;  // resident blocks of the split, at most (the workspace is sized for it)
+constexpr int kMaxGrid = kMaxRanges;  // resident blocks of the split, at most (the workspace is sized for it)
 constexpr int kMinTiles = 8;   // tiles of a range, at least: one per warp
 constexpr int kSlabCost = 8;   // virtual tiles of a slab
 
@@ -30,6 +30,11 @@ struct AttnParams {
   JoinHead* heads;
   int grid;              // blocks of the split
 };
+
+// a / b, in 32 bits where a fits (a 64-bit division costs hundreds of cycles).
+__device__ __forceinline__ long long div_small(long long a, int b) {
+  return (a >> 31) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
 
 // Tiles (virtual ones included) before each batch entry, in the order entry, head, row group; the
 // split's range length.
@@ -63,7 +68,7 @@ __device__ __forceinline__ Plan make_plan(const AttnParams& p, long long* pre) {
   __syncthreads();
   Plan P;
   P.total = pre[p.a.B];
-  P.per = ((P.total + p.grid - 1) / p.grid + kMinTiles - 1) / kMinTiles * kMinTiles;
+  P.per = (div_small(P.total + p.grid - 1, p.grid) + kMinTiles - 1) / kMinTiles * kMinTiles;
   return P;
 }
 
@@ -81,10 +86,10 @@ __device__ __forceinline__ Seg seg_at(const AttnParams& p, const long long* pre,
   Seg s;
   s.b = b;
   const int slabs = p.a.Hkv * p.groups;
-  const int span = (int)((pre[b + 1] - pre[b]) / slabs);
+  const int span = (int)div_small(pre[b + 1] - pre[b], slabs);
   s.tiles = span - kSlabCost;
   const long long off = at - pre[b];
-  const int k = (int)(off / span), x = (int)(off - (long long)k * span);
+  const int k = (int)div_small(off, span), x = (int)(off - (long long)k * span);
   s.t0 = min(x, s.tiles);
   s.t1 = (int)min((long long)s.tiles, x + (end - at));
   s.start = at - x;
@@ -162,6 +167,9 @@ __global__ void __launch_bounds__(kWarps * 32, (Cfg<D, NR, TERMS>::TWO ? 2 : 1))
     return t < c.t1 ? page_of(A.pool, c.b, t) : 0;
   };
   c_page = pages(c_base);
+  QRaw<D, NR, T> raw;  // of the next stretch
+  request_q<D, NR, T>(raw, A.q, c.b, c.h, p.G, c.rg * 8 * NR, p.rows, lane);
+  int raw_b = c.b, raw_h = c.h, raw_rg = c.rg;
   uint32_t issued = 0;
   auto issue = [&]() {  // the warp's next tile into the next stage, if there is one
     while (c_more && c_t >= c.t1) {
@@ -204,7 +212,8 @@ __global__ void __launch_bounds__(kWarps * 32, (Cfg<D, NR, TERMS>::TWO ? 2 : 1))
     const int len = min(max(__ldg(A.seq_len + s.b), 0), most), cnt = clamped_count(A.count, s.b, A.nq);
     const int row0 = s.rg * 8 * NR;
     QFrag<D, NR, TERMS> q;
-    load_q<D, NR, TERMS, T>(q, A.q, s.b, s.h, p.G, row0, p.rows, A.scale, lane);
+    if (raw_b != s.b || raw_h != s.h || raw_rg != s.rg) request_q<D, NR, T>(raw, A.q, s.b, s.h, p.G, row0, p.rows, lane);
+    convert_q<D, NR, TERMS, T>(q, raw, A.scale, lane);
     int lim[NR][2], least = 0x7fffffff;
 #pragma unroll
     for (int r = 0; r < NR; ++r)
@@ -233,6 +242,11 @@ __global__ void __launch_bounds__(kWarps * 32, (Cfg<D, NR, TERMS>::TWO ? 2 : 1))
         landed = used;
         issue();
       }
+    }
+    if (at < end) {  // the next stretch's queries, while the warps meet
+      const Seg nx = seg_at(p, pre, at, end, b_from);
+      request_q<D, NR, T>(raw, A.q, nx.b, nx.h, p.G, nx.rg * 8 * NR, p.rows, lane);
+      raw_b = nx.b, raw_h = nx.h, raw_rg = nx.rg;
     }
     // the warps' states of this stretch into one
     float* ml = reinterpret_cast<float*>(sm + C::O_ML);
@@ -370,7 +384,9 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) rows_kernel(const AttnPa
   } else {
     const int row0 = first + warp * 8 * NR;
     QFrag<D, NR, TERMS> q;
-    load_q<D, NR, TERMS, T>(q, A.q, b, h, p.G, row0, p.rows, A.scale, lane);
+    QRaw<D, NR, T> raw;
+    request_q<D, NR, T>(raw, A.q, b, h, p.G, row0, p.rows, lane);
+    convert_q<D, NR, TERMS, T>(q, raw, A.scale, lane);
     int lim[NR][2], least = 0x7fffffff;
 #pragma unroll
     for (int r = 0; r < NR; ++r)
@@ -444,15 +460,15 @@ cudaError_t split_go(AttnParams p, cudaStream_t s) {
   if (p.grid == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   const int rows = p.rows < 8 * NR ? p.rows : 8 * NR;
-  cfg.gridDim = dim3(p.grid - 1, (rows + kJoinRows - 1) / kJoinRows);
-  cfg.blockDim = dim3(32 * kJoinRows);
+  cfg.gridDim = dim3(p.grid - 1, rows);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, 8 * NR, T>, JoinParams{p.heads, p.part, p.a.out, p.a.nq, p.a.Hq, p.G, p.rows});
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, 8 * NR, kJoinWarps, T>, JoinParams{p.heads, p.part, p.a.out, p.a.nq, p.a.Hq, p.G, p.rows});
 }
 
 template <int D, int NR, int TERMS, typename T>

@@ -72,13 +72,44 @@ template <> __device__ __forceinline__ float to_float(float x) { return x; }
 template <> __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 template <> __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// Query rows row0 + 8 r + g (head h G + row % G of query row / G) as fp16 operands.  Each row is
-// scaled by the power of two that brings its largest magnitude into [1, 2): bf16 and fp16 values
-// are then exact in fp16 down to 2^-14 of that (below, off by at most 2^-25 of it); fp32 rows take
-// a second fp16 term of what the first leaves (together off by at most 2^-23 or so of a value).
-template <int D, int NR, int TERMS, typename T>
-__device__ __forceinline__ void load_q(QFrag<D, NR, TERMS>& q, const Rows& X, int b, int h, int G, int row0, int rows,
-                                       float score_scale, int lane) {
+// 16 consecutive elements as loaded.
+template <typename T>
+struct Raw16 {
+  uint4 v[sizeof(T)];
+};
+__device__ __forceinline__ void unpack16(const Raw16<float>& r, float (&x)[16], const float*) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[4 * i] = __uint_as_float(r.v[i].x); x[4 * i + 1] = __uint_as_float(r.v[i].y);
+    x[4 * i + 2] = __uint_as_float(r.v[i].z); x[4 * i + 3] = __uint_as_float(r.v[i].w);
+  }
+}
+__device__ __forceinline__ void unpack16(const Raw16<__nv_bfloat16>& r, float (&x)[16], const __nv_bfloat16*) {
+  const uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void unpack16(const Raw16<__half>& r, float (&x)[16], const __half*) {
+  const uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+// The thread's part of query rows row0 + 8 r + g (head h G + row % G of query row / G), as loaded: the
+// load is issued before the copies of the slab's tiles, behind which it would wait for microseconds.
+template <int D, int NR, typename T>
+struct QRaw {
+  Raw16<T> x[NR][D / 64];
+};
+template <int D, int NR, typename T>
+__device__ __forceinline__ void request_q(QRaw<D, NR, T>& q, const Rows& X, int b, int h, int G, int row0, int rows, int lane) {
   const int g = lane >> 2, u = lane & 3;
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
@@ -86,11 +117,30 @@ __device__ __forceinline__ void load_q(QFrag<D, NR, TERMS>& q, const Rows& X, in
     const bool live = row < rows;
     const int i = live ? row / G : 0, hd = h * G + (live ? row - i * G : 0);
     const T* src = reinterpret_cast<const T*>(X.p) + b * X.sb + i * X.st + hd * X.sh;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+      for (int k = 0; k < (int)sizeof(T); ++k) {
+        q.x[r][c].v[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (live) q.x[r][c].v[k] = __ldg(reinterpret_cast<const uint4*>(src + 16 * frag_chunk<D>(u, c)) + k);
+      }
+  }
+}
+
+// Query rows as fp16 operands.  Each row is scaled by the power of two that brings its largest magnitude
+// into [1, 2): bf16 and fp16 values are then exact in fp16 down to 2^-14 of that (below, off by at most
+// 2^-25 of it); fp32 rows take a second fp16 term of what the first leaves (together off by at most
+// 2^-23 or so of a value).
+template <int D, int NR, int TERMS, typename T>
+__device__ __forceinline__ void convert_q(QFrag<D, NR, TERMS>& q, const QRaw<D, NR, T>& raw, float score_scale, int lane) {
+  const int u = lane & 3;
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
     float amax = 0.f;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
       float x[16];
-      tqd::load_row<16>(src + 16 * frag_chunk<D>(u, c), x);
+      unpack16(raw.x[r][c], x, (const T*)nullptr);
 #pragma unroll
       for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(x[k]));
     }
@@ -103,12 +153,12 @@ __device__ __forceinline__ void load_q(QFrag<D, NR, TERMS>& q, const Rows& X, in
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
       float x[16];
-      tqd::load_row<16>(src + 16 * frag_chunk<D>(u, c), x);
+      unpack16(raw.x[r][c], x, (const T*)nullptr);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          const float a = live ? x[4 * k + 2 * w] * inv : 0.f, bb = live ? x[4 * k + 2 * w + 1] * inv : 0.f;
+          const float a = x[4 * k + 2 * w] * inv, bb = x[4 * k + 2 * w + 1] * inv;
           const uint32_t hi = tqd::pack_half2(a, bb);
           q.v[0][r][4 * c + k][w] = hi;
           if constexpr (TERMS == 2) {
@@ -273,8 +323,9 @@ struct JoinHead {
   int b, h, group;
 };
 constexpr int kJoinRows = 8;
-constexpr size_t kJoinHeadBytes = 16384;  // heads of up to 512 ranges, at the workspace's start
-static_assert(kJoinHeadBytes >= 512 * sizeof(JoinHead), "heads");
+constexpr int kMaxRanges = 1024;
+constexpr size_t kJoinHeadBytes = 32768;  // heads of the ranges, at the workspace's start
+static_assert(kJoinHeadBytes >= kMaxRanges * sizeof(JoinHead), "heads");
 
 struct JoinParams {
   const JoinHead* heads;
@@ -283,15 +334,19 @@ struct JoinParams {
   int nq, Hq, G, rows;
 };
 
-// A warp joins one row of the slab that goes on past range blockIdx.x: weights 2^(M_i - max M).
-template <int D, int ROWS, typename T>
-__global__ void __launch_bounds__(32 * kJoinRows) join_kernel(const JoinParams p) {
+// Joins rows of the slab that goes on past range blockIdx.x: weights 2^(M_i - max M).  WARPS = 1: a block
+// of kJoinRows warps takes as many rows; otherwise a block's WARPS warps share one row's parts.
+constexpr int kJoinWarps = 4;
+template <int D, int ROWS, int WARPS, typename T>
+__global__ void __launch_bounds__(32 * (WARPS == 1 ? kJoinRows : WARPS)) join_kernel(const JoinParams p) {
   constexpr long long PART = (long long)ROWS * (D + 2);
+  __shared__ float sum[WARPS][D + 1];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const int lane = threadIdx.x & 31, rr = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rr = WARPS == 1 ? blockIdx.y * kJoinRows + warp : blockIdx.y, part0 = WARPS == 1 ? 0 : warp;
   const JoinHead H = p.heads[blockIdx.x];
   const int row = H.group * ROWS + rr;
-  if (H.last < 0 || rr >= ROWS || row >= p.rows) return;
+  if (H.last < 0 || rr >= ROWS || row >= p.rows) return;  // (uniform over the warps that share a row)
   const int n = H.last - (int)blockIdx.x + 1;
   const float* first = p.part + (2ll * blockIdx.x + H.place) * PART;
   const float* rest = p.part + 2ll * blockIdx.x * PART;  // part i >= 1 at rest + 2 i PART
@@ -301,17 +356,40 @@ __global__ void __launch_bounds__(32 * kJoinRows) join_kernel(const JoinParams p
   mt = tqd::warp_max(mt);
   const float mr = mt == -INFINITY ? 0.f : mt;
   float l = 0.f, o[D / 32] = {};
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float* x = at(i);
-    const float w = ex2(x[rr] - mr);
-    l = fmaf(x[ROWS + rr], w, l);
-    const float* v = x + 2 * ROWS + rr * D + lane * (D / 32);
+  // lane i takes the statistics of the warp's parts i, i + 32, ...; their values are then read eight at a time
+  for (int base = part0; base < n; base += 32 * WARPS) {
+    const int mine = base + WARPS * lane;
+    float w = 0.f;
+    if (mine < n) {
+      const float* x = at(mine);
+      w = ex2(x[rr] - mr);
+      l = fmaf(x[ROWS + rr], w, l);
+    }
+    const int m = min(32, (n - base + WARPS - 1) / WARPS);
+#pragma unroll 8
+    for (int i = 0; i < m; ++i) {
+      const float wi = __shfl_sync(kFull, w, i);
+      const float* v = at(base + WARPS * i) + 2 * ROWS + rr * D + lane * (D / 32);
 #pragma unroll
-    for (int k = 0; k < D / 32; k += 2) {
-      const float2 f = *reinterpret_cast<const float2*>(v + k);
-      o[k] = fmaf(f.x, w, o[k]);
-      o[k + 1] = fmaf(f.y, w, o[k + 1]);
+      for (int k = 0; k < D / 32; k += 2) {
+        const float2 f = *reinterpret_cast<const float2*>(v + k);
+        o[k] = fmaf(f.x, wi, o[k]);
+        o[k + 1] = fmaf(f.y, wi, o[k + 1]);
+      }
+    }
+  }
+  l = tqd::warp_sum(l);
+  if constexpr (WARPS > 1) {
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) sum[warp][lane * (D / 32) + k] = o[k];
+    if (lane == 0) sum[warp][D] = l;
+    __syncthreads();
+    if (warp) return;
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) {
+      l += sum[w][D];
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) o[k] += sum[w][lane * (D / 32) + k];
     }
   }
   const float il = l > 0.f || l != l ? 1.f / l : 0.f;

@@ -216,25 +216,6 @@ __device__ __forceinline__ void store16(__half* dst, const float* x) {
   reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-// 16 packed values as fp32.
-__device__ __forceinline__ void unpack16(const uint4& lo, const uint4& hi, float (&x)[16], const __nv_bfloat16*) {
-  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ void unpack16(const uint4& lo, const uint4& hi, float (&x)[16], const __half*) {
-  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
-}
-
 // One query row as NT e4m3 terms in the swizzled operand tiles at q (term t at q + 16384 t); returns
 // the factor of its scores, log2(e) |scale| 2^e (the sign of `scale` goes into the terms).
 template <typename T, int NT>
@@ -246,7 +227,7 @@ __device__ __forceinline__ float query_row(const T* src, bool live, float scale,
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     float x[16];
-    unpack16(raw[2 * c], raw[2 * c + 1], x, src);
+    unpack16(Raw16<T>{{raw[2 * c], raw[2 * c + 1]}}, x, src);
 #pragma unroll
     for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(x[k]));
   }
@@ -259,7 +240,7 @@ __device__ __forceinline__ float query_row(const T* src, bool live, float scale,
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     float x[16];
-    unpack16(raw[2 * c], raw[2 * c + 1], x, src);
+    unpack16(Raw16<T>{{raw[2 * c], raw[2 * c + 1]}}, x, src);
     const int at = r * 128 + ((c ^ (r & 7)) << 4);
 #pragma unroll
     for (int k = 0; k < 16; ++k) x[k] *= inv;
@@ -746,7 +727,7 @@ cudaError_t tc_go(TcParams p, int sms, int device, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<kD, L::ROWS, T>, JoinParams{p.heads, p.part, p.a.out, p.a.nq, p.a.Hq, p.G, p.rows});
+  return cudaLaunchKernelEx(&cfg, join_kernel<kD, L::ROWS, 1, T>, JoinParams{p.heads, p.part, p.a.out, p.a.nq, p.a.Hq, p.G, p.rows});
 }
 
 }  // namespace
