@@ -21,7 +21,8 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kMaxGrid = kMaxRanges;  // resident blocks of the split, at most (the workspace is sized for it)
 constexpr int kMinTiles = 8;   // tiles of a range, at least: one per warp
-constexpr int kSlabCost = 8;   // virtual tiles of a slab
+constexpr int kSlabCost = 32;  // virtual tiles of a slab (4-5 us of a block; 8 / 16 / 24 / 40: a batch of 64 unlike
+                               // lengths 45 / 32 / 27 / 26 us)
 
 struct AttnParams {
   AttnArgs a;
@@ -112,21 +113,23 @@ __device__ __forceinline__ int find_entry(const long long* pre, int B, long long
 template <int D, int NR, int TERMS>
 struct Cfg {
   static constexpr int BLK = 32 * D + 32;
+  // warps: fp32 at d = 128 12 of 168 registers (8 x 32768 tokens: 100 us, 8 warps 109 us)
+  static constexpr int NW = NR == 1 && D == 128 && TERMS == 2 ? 12 : 8;
   static constexpr bool TWO = NR == 1 && D <= 128 && TERMS * D <= 128;      // two blocks per SM
   static constexpr int ROOM = (TWO ? 115200 : 231424) - 4160 - 512;         // less the plan and barriers
-  static constexpr int RED = kWarps * 8 * NR * (D / 4 + 4) * 4;             // a quarter of O per round
-  static constexpr int ST0 = (ROOM - RED) / (kWarps * BLK);
+  static constexpr int RED = NW * 8 * NR * (D / 4 + 4) * 4;             // a quarter of O per round
+  static constexpr int ST0 = (ROOM - RED) / (NW * BLK);
   static constexpr int STAGES = ST0 > 8 ? 8 : ST0;
-  static constexpr int RING = kWarps * STAGES * BLK;
+  static constexpr int RING = NW * STAGES * BLK;
   // ring, reduction, barriers, (m, l) of the warps, plan
-  static constexpr int O_RED = RING, O_BAR = O_RED + RED, O_ML = O_BAR + kWarps * STAGES * 8;
-  static constexpr int O_PRE = (O_ML + kWarps * 8 * NR * 8 + 15) / 16 * 16;
+  static constexpr int O_RED = RING, O_BAR = O_RED + RED, O_ML = O_BAR + NW * STAGES * 8;
+  static constexpr int O_PRE = (O_ML + NW * 8 * NR * 8 + 15) / 16 * 16;
   static int smem(int B) { return O_PRE + (B + 1) * 8; }
   static constexpr int PART = 8 * NR * (D + 2);                             // floats of a partial
 };
 
 template <int D, int NR, int TERMS, typename T>
-__global__ void __launch_bounds__(kWarps * 32, (Cfg<D, NR, TERMS>::TWO ? 2 : 1)) split_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(Cfg<D, NR, TERMS>::NW * 32, (Cfg<D, NR, TERMS>::TWO ? 2 : 1)) split_kernel(const AttnParams p) {
   using C = Cfg<D, NR, TERMS>;
   extern __shared__ __align__(128) unsigned char sm[];
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -147,7 +150,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Cfg<D, NR, TERMS>::TWO ? 2 : 1))
     T* out = reinterpret_cast<T*>(A.out);
     for (int b = blockIdx.x; b < A.B; b += gridDim.x)
       if (pre[b + 1] == pre[b])
-        for (long long i = threadIdx.x; i < (long long)A.nq * A.Hq * D; i += kWarps * 32)
+        for (long long i = threadIdx.x; i < (long long)A.nq * A.Hq * D; i += C::NW * 32)
           out[(long long)b * A.nq * A.Hq * D + i] = from_float<T>(0.f);
   }
   const long long begin = blockIdx.x * P.per, end = min(P.total, begin + P.per);
@@ -163,7 +166,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Cfg<D, NR, TERMS>::TWO ? 2 : 1))
   int c_t = c.t0 + warp, c_base = c_t, c_page = 0;
   bool c_more = true;
   auto pages = [&](int from) {
-    const int t = from + kWarps * lane;
+    const int t = from + C::NW * lane;
     return t < c.t1 ? page_of(A.pool, c.b, t) : 0;
   };
   c_page = pages(c_base);
@@ -183,18 +186,18 @@ __global__ void __launch_bounds__(kWarps * 32, (Cfg<D, NR, TERMS>::TWO ? 2 : 1))
       }
     }
     if (!c_more) return;
-    if (c_t - c_base >= 32 * kWarps) {
+    if (c_t - c_base >= 32 * C::NW) {
       c_base = c_t;
       c_page = pages(c_base);
     }
-    const int page = __shfl_sync(kFull, c_page, (c_t - c_base) / kWarps);
+    const int page = __shfl_sync(kFull, c_page, (c_t - c_base) / C::NW);
     if (lane == 0) {
       const uint32_t st = issued % C::STAGES;
       tqd::mbar_arrive_expect_tx(bar0 + 8 * st, C::BLK);
       tqd::bulk_g2s(ring_s + st * C::BLK, A.pool.base + pool_block(A.pool, page, c.h) * C::BLK, C::BLK, bar0 + 8 * st);
     }
     ++issued;
-    c_t += kWarps;
+    c_t += C::NW;
   };
 #pragma unroll 1
   for (int i = 0; i < C::STAGES; ++i) issue();
@@ -211,9 +214,9 @@ __global__ void __launch_bounds__(kWarps * 32, (Cfg<D, NR, TERMS>::TWO ? 2 : 1))
     if (s.t0 == s.t1) continue;
     const int len = min(max(__ldg(A.seq_len + s.b), 0), most), cnt = clamped_count(A.count, s.b, A.nq);
     const int row0 = s.rg * 8 * NR;
-    QFrag<D, NR, TERMS> q;
+    QFrag<D, NR, T> q;
     if (raw_b != s.b || raw_h != s.h || raw_rg != s.rg) request_q<D, NR, T>(raw, A.q, s.b, s.h, p.G, row0, p.rows, lane);
-    convert_q<D, NR, TERMS, T>(q, raw, A.scale, lane);
+    convert_q<D, NR, T>(q, raw, A.scale, lane);
     int lim[NR][2], least = 0x7fffffff;
 #pragma unroll
     for (int r = 0; r < NR; ++r)
@@ -228,14 +231,14 @@ __global__ void __launch_bounds__(kWarps * 32, (Cfg<D, NR, TERMS>::TWO ? 2 : 1))
     State<D, NR> st;
     st.clear();
 #pragma unroll 1
-    for (int t = s.t0 + warp; t < s.t1; t += kWarps) {
+    for (int t = s.t0 + warp; t < s.t1; t += C::NW) {
       const uint32_t slot = used % C::STAGES;
       if (alive && !tqd::mbar_wait(bar0 + 8 * slot, (used / C::STAGES) & 1, kWaitLimit)) {
         alive = false;
         if (A.pool.err) atomicExch(A.pool.err, TQ_DEVERR_WAIT_TIMEOUT);
       }
       if (alive)
-        tile_step<D, NR, TERMS>(ring + slot * C::BLK, q, st, 16 * t, lim, 16 * t + 16 > least, len, lane);
+        tile_step<D, NR, T>(ring + slot * C::BLK, q, st, 16 * t, lim, 16 * t + 16 > least, len, lane);
       __syncwarp();
       ++used;
       if (alive) {
@@ -270,7 +273,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Cfg<D, NR, TERMS>::TWO ? 2 : 1))
       for (int k = 0; k < 2; ++k) {
         float mt = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, ml[2 * (w * 8 * NR + 8 * r + 2 * u + k)]);
+        for (int w = 0; w < C::NW; ++w) mt = fmaxf(mt, ml[2 * (w * 8 * NR + 8 * r + 2 * u + k)]);
         f[r][k] = ex2(st.m[r][k] - (mt == -INFINITY ? 0.f : mt));
       }
     const bool whole = s.t0 == 0 && s.t1 == s.tiles;
@@ -287,14 +290,14 @@ __global__ void __launch_bounds__(kWarps * 32, (Cfg<D, NR, TERMS>::TWO ? 2 : 1))
             red[(warp * 8 * NR + 8 * r + 2 * u + (k & 1)) * PITCH + 16 * i + g + 8 * (k >> 1)] =
                 st.o[r][qd * (QD / 16) + i][k] * f[r][k & 1];
       __syncthreads();
-      for (int i = threadIdx.x; i < 8 * NR * QD; i += kWarps * 32) {
+      for (int i = threadIdx.x; i < 8 * NR * QD; i += C::NW * 32) {
         const int row = i / QD, x = i - row * QD;
         float mt = -INFINITY, lt = 0.f, o = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, ml[2 * (w * 8 * NR + row)]);
+        for (int w = 0; w < C::NW; ++w) mt = fmaxf(mt, ml[2 * (w * 8 * NR + row)]);
         const float mr = mt == -INFINITY ? 0.f : mt;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < C::NW; ++w) {
           lt = fmaf(ml[2 * (w * 8 * NR + row) + 1], ex2(ml[2 * (w * 8 * NR + row)] - mr), lt);
           o += red[(w * 8 * NR + row) * PITCH + x];
         }
@@ -383,10 +386,10 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) rows_kernel(const AttnPa
       tqd::mbar_wait(full + 8 * (t % C::STAGES), (t / C::STAGES) & 1, kWaitLimit);
   } else {
     const int row0 = first + warp * 8 * NR;
-    QFrag<D, NR, TERMS> q;
+    QFrag<D, NR, T> q;
     QRaw<D, NR, T> raw;
     request_q<D, NR, T>(raw, A.q, b, h, p.G, row0, p.rows, lane);
-    convert_q<D, NR, TERMS, T>(q, raw, A.scale, lane);
+    convert_q<D, NR, T>(q, raw, A.scale, lane);
     int lim[NR][2], least = 0x7fffffff;
 #pragma unroll
     for (int r = 0; r < NR; ++r)
@@ -409,7 +412,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) rows_kernel(const AttnPa
       }
       if (!alive) break;
       if (t < mine)
-        tile_step<D, NR, TERMS>(sm + slot * C::BLK, q, st, 16 * t, lim, 16 * t + 16 > least, len, lane);
+        tile_step<D, NR, T>(sm + slot * C::BLK, q, st, 16 * t, lim, 16 * t + 16 > least, len, lane);
       __syncwarp();
       if (lane == 0) asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n" ::"r"(empty + 8 * slot) : "memory");
     }
@@ -455,7 +458,7 @@ cudaError_t split_go(AttnParams p, cudaStream_t s) {
   const int smem = C::smem(p.a.B);
   cudaError_t e = allow_smem((const void*)split_kernel<D, NR, TERMS, T>, C::smem(TQ_MAX_BATCH), dev, done);
   if (e != cudaSuccess) return e;
-  split_kernel<D, NR, TERMS, T><<<p.grid, kWarps * 32, smem, s>>>(p);
+  split_kernel<D, NR, TERMS, T><<<p.grid, C::NW * 32, smem, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (p.grid == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};

@@ -9,12 +9,15 @@
 // sum l = sum_j P_j 2^(-e_j) stays in fp32 (|e_j| <= 30 keeps it in range).  The scale of a block
 // costs nothing this way: e_j is added to the exponent's constant.
 //
-// Products are mma.sync m16n8k16 on fp16 (codes are exact in fp16) with the tokens (scores) or the
-// coordinates (readout) as M and the query rows as N, so 8 rows fill an instruction:
-//   S^T[16 tok x 8 rows] += K[16 x 16 d] Q^T[16 d x 8],  O^T[16 d x 8 rows] += V^T[16 d x 16 tok] P^T.
-// Thread (g, u) of the warp (g = lane / 4, u = lane % 4) holds tokens g, g + 8 and rows 2u, 2u + 1 of
-// the scores; coordinates within a 16-product are permuted so that its K operand is 16 contiguous
-// codes per shared-memory load, and V's stored token order is that of the P operand.
+// Products are mma.sync with the tokens (scores) or the coordinates (readout) as M and the query rows as
+// N, so 8 rows fill an instruction:
+//   S^T[16 tok x 8 rows] += K[16 x d] Q^T[d x 8],  O^T[16 d x 8 rows] += V^T[16 d x 16 tok] P^T.
+// Both are m16n8k16 on fp16; codes are exact in fp16.  (Scores as m16n8k32 on the stored e4m3 codes, the
+// queries as e4m3 terms, need no conversion of keys but measured slower: 103 us instead of 98 for
+// 8 x 32768 tokens, 138 instead of 116 for 16 rows.)  Thread (g, u) of the warp (g = lane / 4, u = lane % 4)
+// holds tokens g, g + 8 and rows 2u, 2u + 1 of the scores; coordinates within a product are permuted so
+// that its K operand is 16 contiguous codes per shared-memory load, and V's stored token order is that
+// of the P operand.
 #pragma once
 
 #include <atomic>
@@ -33,10 +36,14 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-template <int D, int NR, int TERMS>
+// fp16 terms of the queries and of the probabilities.
+template <typename T>
+constexpr int kTermsOf = sizeof(T) == 4 ? 2 : 1;
+
+template <int D, int NR, typename T>
 struct QFrag {
-  uint32_t v[TERMS][NR][D / 16][2];  // B operand of k-step s: coordinates 4 s' .. of the thread's chunks
-  float f[NR][2];                    // rows 2u, 2u + 1: log2(e) * scale * the row's power-of-two scale
+  uint32_t v[kTermsOf<T>][NR][D / 16][2];  // B operand of k-step s: coordinates 4 s' .. of the thread's chunks
+  float f[NR][2];                          // rows 2u, 2u + 1: log2(e) * scale * the row's power-of-two scale
 };
 
 template <int D, int NR>
@@ -131,8 +138,8 @@ __device__ __forceinline__ void request_q(QRaw<D, NR, T>& q, const Rows& X, int 
 // into [1, 2): bf16 and fp16 values are then exact in fp16 down to 2^-14 of that (below, off by at most
 // 2^-25 of it); fp32 rows take a second fp16 term of what the first leaves (together off by at most
 // 2^-23 or so of a value).
-template <int D, int NR, int TERMS, typename T>
-__device__ __forceinline__ void convert_q(QFrag<D, NR, TERMS>& q, const QRaw<D, NR, T>& raw, float score_scale, int lane) {
+template <int D, int NR, typename T>
+__device__ __forceinline__ void convert_q(QFrag<D, NR, T>& q, const QRaw<D, NR, T>& raw, float score_scale, int lane) {
   const int u = lane & 3;
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
@@ -161,7 +168,7 @@ __device__ __forceinline__ void convert_q(QFrag<D, NR, TERMS>& q, const QRaw<D, 
           const float a = x[4 * k + 2 * w] * inv, bb = x[4 * k + 2 * w + 1] * inv;
           const uint32_t hi = tqd::pack_half2(a, bb);
           q.v[0][r][4 * c + k][w] = hi;
-          if constexpr (TERMS == 2) {
+          if constexpr (kTermsOf<T> == 2) {
             const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi));
             q.v[1][r][4 * c + k][w] = tqd::pack_half2(a - back.x, bb - back.y);
           }
@@ -176,9 +183,10 @@ __device__ __forceinline__ void convert_q(QFrag<D, NR, TERMS>& q, const QRaw<D, 
 // One tile: `blk` is the block in shared memory, tok0 its first token, lim[r][k] the tokens that row
 // 2u + k of group r attends to, edge: some row of the warp does not attend to all 16 tokens, len:
 // the sequence's length (codes of tokens behind it may be anything).
-template <int D, int NR, int TERMS>
-__device__ __forceinline__ void tile_step(const unsigned char* blk, const QFrag<D, NR, TERMS>& q, State<D, NR>& st,
-                                          int tok0, const int (&lim)[NR][2], bool edge, int len, int lane) {
+template <int D, int NR, bool EDGE, typename T>
+__device__ __forceinline__ void tile_step_edge(const unsigned char* blk, const QFrag<D, NR, T>& q, State<D, NR>& st, int tok0,
+                                               const int (&lim)[NR][2], int len, int lane) {
+  constexpr int TERMS = kTermsOf<T>;
   const int g = lane >> 2, u = lane & 3;
   float s[NR][4];
 #pragma unroll
@@ -199,7 +207,8 @@ __device__ __forceinline__ void tile_step(const unsigned char* blk, const QFrag<
 #pragma unroll
       for (int r = 0; r < NR; ++r)
 #pragma unroll
-        for (int t = 0; t < TERMS; ++t) tqd::mma16816(s[r], a0, a1, a2, a3, q.v[t][r][4 * c + k][0], q.v[t][r][4 * c + k][1]);
+        for (int t = 0; t < TERMS; ++t)
+          tqd::mma16816(s[r], a0, a1, a2, a3, q.v[t][r][4 * c + k][0], q.v[t][r][4 * c + k][1]);
     }
   }
   const float2 scales = *reinterpret_cast<const float2*>(blk + 32 * D);
@@ -213,7 +222,7 @@ __device__ __forceinline__ void tile_step(const unsigned char* blk, const QFrag<
     fk[r][1] = q.f[r][1] * scales.x;
 #pragma unroll
     for (int k = 0; k < 4; ++k) s[r][k] *= fk[r][k & 1];
-    if (edge) {
+    if (EDGE) {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (tok0 + g + 8 * (k >> 1) >= lim[r][k & 1]) s[r][k] = -INFINITY;
@@ -263,7 +272,7 @@ __device__ __forceinline__ void tile_step(const unsigned char* blk, const QFrag<
   }
   // codes behind the sequence's end may be NaN: zero them (their probabilities are zero already)
   uint32_t keep = 0xffffffffu;
-  if (edge && tok0 + 16 > len) {
+  if (EDGE && tok0 + 16 > len) {
     const int t = len - tok0;
     keep = (2 * u < t ? 0xffu : 0u) | (2 * u + 1 < t ? 0xff00u : 0u) | (2 * u + 8 < t ? 0xff0000u : 0u) |
            (2 * u + 9 < t ? 0xff000000u : 0u);
@@ -271,8 +280,11 @@ __device__ __forceinline__ void tile_step(const unsigned char* blk, const QFrag<
   const unsigned char* vb = blk + 16 * D + 16 * g + 4 * u;
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) {
-    const uint32_t w0 = *reinterpret_cast<const uint32_t*>(vb + 256 * i) & keep;
-    const uint32_t w1 = *reinterpret_cast<const uint32_t*>(vb + 256 * i + 128) & keep;
+    uint32_t w0 = *reinterpret_cast<const uint32_t*>(vb + 256 * i), w1 = *reinterpret_cast<const uint32_t*>(vb + 256 * i + 128);
+    if (EDGE) {
+      w0 &= keep;
+      w1 &= keep;
+    }
     uint32_t a0, a1, a2, a3;
     codes_half4(w0, a0, a2);
     codes_half4(w1, a1, a3);
@@ -281,6 +293,13 @@ __device__ __forceinline__ void tile_step(const unsigned char* blk, const QFrag<
 #pragma unroll
       for (int t = 0; t < TERMS; ++t) tqd::mma16816(st.o[r][i], a0, a1, a2, a3, p[t][r][0], p[t][r][1]);
   }
+}
+
+template <int D, int NR, typename T>
+__device__ __forceinline__ void tile_step(const unsigned char* blk, const QFrag<D, NR, T>& q, State<D, NR>& st, int tok0,
+                                          const int (&lim)[NR][2], bool edge, int len, int lane) {
+  if (edge) tile_step_edge<D, NR, true, T>(blk, q, st, tok0, lim, len, lane);
+  else tile_step_edge<D, NR, false, T>(blk, q, st, tok0, lim, len, lane);
 }
 
 template <typename T>
