@@ -502,7 +502,7 @@ void rows_split(int d, int tokens, int heads, int* per, int* split) {
   const int rpp = kThreads / (d / 16);
   *split = heads;
   *per = (6 * rpp + heads - 1) / heads;
-  const int fill = tokens / 608;  // four blocks on each of 152 SMs
+  const int fill = (tokens + 455) / 456;  // three blocks on each of 152 SMs
   if (*per > fill) *per = fill;
   if (*per > kMaxTokens) *per = kMaxTokens;
   if (*per < 1) *per = 1;
