@@ -433,7 +433,7 @@ size_t tq_byte_pool_bytes(const tq_byte_config* cfg, int32_t num_pages);
  * (none when negative); NULL: all n.  q (NULL: none): n tokens of queries per entry, normed
  * (q_weight) and rotated with the same positions in the same launch into q_out, contiguous
  * [batch][n][num_q_heads][head_dim] of dtype; all n rows of q are written whatever dev_count says.
- * A block's held tokens are those before dev_start[b]; bytes of positions behind the appended
+ * q_out may be q's buffer when q is contiguous.  A block's held tokens are those before dev_start[b]; bytes of positions behind the appended
  * tokens stay as they are.  A page that receives tokens must belong to one sequence.  Bad pages
  * and positions: see tq_page_table.  dev_error: device int32 or NULL; receives a TQ_DEVERR_* code
  * (the caller zeroes it beforehand).  n = 0 is a no-op. */
@@ -451,10 +451,14 @@ tq_status tq_byte_append_paged(const tq_byte_config* cfg, void* dev_pool, const 
  * or NULL (nq): entry b has c = min(dev_count[b], nq) queries, its last c positions.  Query i < c
  * attends to the first dev_seq_len[b] - c + 1 + i tokens (none when that is <= 0: output zeros);
  * rows i >= c are written as zeros.  scale multiplies the scores (1 / sqrt(head_dim) in most
- * models).  What the pool holds behind a sequence's last token is never used.  Scores, softmax
- * statistics and accumulators are fp32; queries and probabilities enter the matrix products as
- * fp16 (bf16 and fp16 queries exactly, under a power-of-two scale per row; fp32 queries and their
- * probabilities as fp16 hi + lo terms).  ws: device workspace of at least
+ * models).  What the pool holds behind a sequence's last token is never used; out must not overlap q.
+ * Scores, softmax statistics and accumulators are fp32.  fp32 queries and their probabilities enter the
+ * matrix products as fp16 hi + lo terms.  bf16 and fp16 queries enter as fp16 under a power-of-two scale
+ * per row, or, in chunks of more than 64 rows (queries times heads per KV head) at head_dim 128, as two or
+ * three e4m3 terms: exact but for what lies below 2^-18 of the row's largest value (2^-25 as fp16).  Their
+ * probabilities are rounded to fp16.  A query with an infinity or a NaN gives NaN in its own row only.
+ * A bad page reads the redirect page; the outputs of that entry then mean nothing, those of other
+ * entries are unaffected, and TQ_DEVERR_BAD_PAGE is recorded.  ws: device workspace of at least
  * tq_byte_attention_workspace_bytes, 256-byte aligned, uninitialized, owned by the call until it
  * completes on stream.  dev_error as for the append.  Results do not depend on the other entries
  * of the batch beyond the order of the sums over a sequence's parts, which the lengths decide;

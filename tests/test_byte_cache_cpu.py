@@ -94,7 +94,7 @@ def _append(cfg=None, pool=DEV, pt=None, batch=2, n=3, dt=b.TQ_BF16, k=None, v=N
                                   wk, eps, rot, pos, q, wq, qo, err, None)
 
 
-def _attend(cfg=None, pool=DEV, pt=None, batch=2, nq=1, dt=b.TQ_BF16, q=None, seq=DEV, count=None, scale=0.1, out=DEV,
+def _attend(cfg=None, pool=DEV, pt=None, batch=2, nq=1, dt=b.TQ_BF16, q=None, seq=DEV, count=None, scale=0.1, out=2 * DEV,
             ws=DEV, bytes_=1 << 40, err=None):
     return b.tq_byte_attention_paged(cfg or _cfg(), pool, pt or _pt(), batch, nq, dt, q or _h(8, n=nq), seq, count, scale,
                                      out, ws, bytes_, err, None)
@@ -126,7 +126,8 @@ def test_append_refusals(kw):
 
 @pytest.mark.parametrize("kw", BAD_POOL + [
     dict(nq=0), dict(nq=1 << 30), dict(q=_h(4)), dict(q=_h(8, data=DEV + 4)), dict(seq=None), dict(seq=DEV + 2),
-    dict(count=DEV + 2), dict(out=None), dict(out=DEV + 8), dict(ws=None), dict(ws=DEV + 128), dict(scale=math.inf),
+    dict(count=DEV + 2), dict(out=None), dict(out=DEV + 8), dict(out=DEV), dict(ws=None), dict(ws=DEV + 128),
+    dict(scale=math.inf),
     dict(scale=math.nan),
 ])
 def test_attention_refusals(kw):
@@ -187,6 +188,8 @@ def test_python_refusals():
     assert Rotary(64, sections=[16, 8, 8], device="cpu").num_axes == 3
     with pytest.raises(ValueError):
         norm_rotate()
+    with pytest.raises(ValueError):
+        norm_rotate(out_dtype=torch.float16)
     with pytest.raises(ValueError):
         norm_rotate(torch.zeros(1, 1, 2, 64))
     with pytest.raises(TQError):

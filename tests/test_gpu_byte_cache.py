@@ -252,7 +252,8 @@ def _filled(d, hq, hkv, lens, dtype, seed, spread=1.0, extra=2):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("d", [64, 128, 256])
-@pytest.mark.parametrize("hq,hkv,nq", [(4, 4, 1), (8, 1, 1), (7, 1, 1), (8, 2, 3), (32, 2, 1), (6, 2, 11), (4, 1, 40)])
+@pytest.mark.parametrize("hq,hkv,nq", [(4, 4, 1), (8, 1, 1), (7, 1, 1), (8, 2, 3), (32, 2, 1), (6, 2, 11), (4, 1, 40), (71, 1, 1),
+                                       (130, 1, 1)])
 def test_attention(dtype, d, hq, hkv, nq):
     lens = [0, 1, 15, 16, 17, 300, nq, 95]
     c, table, pool = _filled(d, hq, hkv, lens, DT[dtype], seed=d + nq)

@@ -92,9 +92,9 @@ class Rotary:
                                  self.num_axes, host.ctypes.data))
         self.rotary_dim, self.interleaved = int(rotary_dim), bool(interleaved)
         self.host_table = host
-        self.table = torch.from_numpy(host.view(np.int64)).to(_device(device))
-        self._args = (self.table.data_ptr(), self.rotary_dim, int(self.interleaved), self.num_axes,
-                      self.table.get_device())
+        self._table = torch.from_numpy(host.view(np.int64)).to(_device(device))
+        self._args = (self._table.data_ptr(), self.rotary_dim, int(self.interleaved), self.num_axes,
+                      self._table.get_device())
 
 
 def norm_rotate(q=None, k=None, rotary=None, positions=None, start=None, q_weight=None, k_weight=None, eps=1e-6,
@@ -107,6 +107,8 @@ def norm_rotate(q=None, k=None, rotary=None, positions=None, start=None, q_weigh
     is at ``start[b] + j`` (``start``: int32 CUDA [batch]; None: 0).  ``out_dtype``: q's dtype (default) or float32, which the packed caches'
     queries need.  Returns (q_out, k_out), contiguous in the shapes of q and k.
     """
+    if q is None and k is None:
+        raise ValueError("neither q nor k given")
     if out_dtype is not None and out_dtype is not torch.float32 and out_dtype != (k if q is None else q).dtype:
         raise ValueError("out_dtype must be the inputs' dtype or float32")
     args = (q, k, None if rotary is None else rotary._args, positions, start, q_weight, k_weight, eps,
@@ -138,10 +140,19 @@ class PagedByteCache:
             raise ValueError("max_blocks_per_seq must be >= 1")
         self.block_bytes = 32 * self.head_dim + 32
         self.device = _device(device)
-        self.pool = torch.zeros(need, dtype=torch.uint8, device=self.device)
-        self.error = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._pool = torch.zeros(need, dtype=torch.uint8, device=self.device)
+        self._error = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._args = (self.head_dim, self.num_q_heads, self.num_kv_heads, self.num_pages, self.max_blocks_per_seq,
-                      self.pool.data_ptr(), self.error.data_ptr(), self.pool.get_device())
+                      self._pool.data_ptr(), self._error.data_ptr(), self._pool.get_device())
+
+    # (read-only: the calls hold their addresses)
+    @property
+    def pool(self):
+        return self._pool
+
+    @property
+    def error(self):
+        return self._error
 
     def device_error(self):
         """The recorded TQ_DEVERR_* code (0: none), cleared by the call.  Waits for the device."""

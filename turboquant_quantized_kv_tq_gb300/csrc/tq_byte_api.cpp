@@ -236,6 +236,7 @@ tq_status tq_byte_attention_paged(const tq_byte_config* cfg, const void* dev_poo
   if ((s = check_rows(q, "q", cfg->num_q_heads, batch, nq, dtype_bytes(dtype), &a.q)) != TQ_OK) return s;
   if (!aligned(out, 16) || !aligned(ws, 256) || !aligned(dev_seq_len, 4) || !aligned(dev_count, 4))
     return fail(TQ_ERR_INVALID_ARG, "misaligned pointer (ws 256 B, out 16 B, lengths 4 B)");
+  if (out == q->data) return fail(TQ_ERR_INVALID_ARG, "out must not be q's buffer");
   if (!std::isfinite(scale)) return fail(TQ_ERR_INVALID_ARG, "scale must be finite");
   if (ws_bytes < byte_attention_workspace(cfg->head_dim, batch, nq, cfg->num_q_heads, cfg->num_kv_heads, dtype))
     return fail(TQ_ERR_WORKSPACE, "workspace too small");

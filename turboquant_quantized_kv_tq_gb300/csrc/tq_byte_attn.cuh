@@ -342,8 +342,8 @@ struct JoinHead {
   int b, h, group;
 };
 constexpr int kJoinRows = 8;
-constexpr int kMaxRanges = 1024;
-constexpr size_t kJoinHeadBytes = 32768;  // heads of the ranges, at the workspace's start
+constexpr int kMaxRanges = 512;
+constexpr size_t kJoinHeadBytes = 16384;  // heads of the ranges, at the workspace's start
 static_assert(kJoinHeadBytes >= kMaxRanges * sizeof(JoinHead), "heads");
 
 struct JoinParams {

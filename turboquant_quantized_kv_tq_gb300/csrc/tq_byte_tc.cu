@@ -371,7 +371,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
   uint32_t* slot = reinterpret_cast<uint32_t*>(sm + L::BARS + 8 * BAR_COUNT);
   int* pre = reinterpret_cast<int*>(sm + L::PRE);
   if (sb & 1023u) {  // the swizzled operands need it (the plan gives it)
-    if (threadIdx.x == 0 && A.pool.err) atomicExch(A.pool.err, TQ_DEVERR_SMEM_PLAN);
+    if (threadIdx.x == 0) {
+      p.heads[blockIdx.x].last = -1;
+      if (A.pool.err) atomicExch(A.pool.err, TQ_DEVERR_SMEM_PLAN);
+    }
     return;
   }
   if (warp == 13) tqd::tc_alloc((uint32_t)__cvta_generic_to_shared(slot), 512);
