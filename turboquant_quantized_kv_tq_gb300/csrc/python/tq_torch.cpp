@@ -2,7 +2,7 @@
 //
 // A decode step makes these calls once per layer on tensors of a few hundred kilobytes, where the call
 // costs more than the kernel: checked and marshalled in Python through ctypes a call took the host 18-20 us
-// (Grace), here 5-7.  This file only checks tensors, allocates outputs and workspaces through torch (on
+// (Grace), here 5-9.  This file only checks tensors, allocates outputs and workspaces through torch (on
 // the current stream, so their memory belongs to it) and fills the ABI's structs; what the library refuses
 // becomes its TQError.  Arguments come by position from byte_cache.py, which documents them.
 #define PY_SSIZE_T_CLEAN

@@ -3,12 +3,17 @@
 //
 // norm_rotate reads every row once and writes it once: bound by HBM for chunks, by the launch and
 // the chain position -> angle -> row for single tokens.  A block of 256 threads takes a few tokens
-// and all their heads, so a token's sines are computed once for its 2 * heads rows.
+// and all their heads, so a token's sines are computed once for its 2 * heads rows; three blocks an SM
+// with three rows in flight per thread carry the latency.  Measured: 4096 tokens of 64 + 8 heads, d = 128,
+// bf16, 31 us, 4.9 TB/s of the 6.8 of a copy (a copy of this size: 24 us); 56 % of issue slots, so the
+// arithmetic (packed fp32) is the next bound; one token of 8 sequences 2.6 us.
 //
 // byte_append gives each warp one side of one 16-token block of one KV head: it reads the block's
 // new rows, rotates keys, finds the block's scale with a warp maximum, and writes the codes; held
 // codes are rounded to a raised scale by the same warp, so a block has one writer.  The queries of
-// the step ride along as further blocks of the grid.
+// the step ride along as further blocks of the grid.  Measured: 4096 tokens of 64 + 8 heads 35 us (15 us
+// without the queries: a chain of dependent loads in 514 blocks; a copy of all bytes takes 25 us); one
+// token of 8 sequences 5.8 us.
 #include <string>
 
 #include "tq_byte_attn.cuh"

@@ -9,8 +9,8 @@
 // The angle of a pair is position * frequency in turns modulo 1, in 64-bit fixed point: the product
 // of the 64-bit fraction with the position wraps exactly, its top 32 bits are the signed fraction
 // of a turn to 2^-32 (an angle error of 2^-33 turns for any position, plus the frequency's own
-// rounding of 2^-63 turns per position), and sincospi of that fp32 fraction needs no range
-// reduction.  A table of cosines by position would be 64 MB at 131072 positions and d = 128; the
+// rounding of 2^-63 turns per position), and sincospi of the fp32 rest to a quarter turn needs no
+// range reduction.  A table of cosines by position would be 64 MB at 131072 positions and d = 128; the
 // cosines of a token are instead computed once per block and shared by all its heads.
 #pragma once
 
@@ -117,11 +117,15 @@ template <typename F>
 __device__ __forceinline__ float2 pair_angle(uint64_t entry, F pos) {
   const long long at = pos((int)(entry & 3u));
   const uint64_t turns = (entry & ~3ull) * (uint64_t)at;              // modulo one turn
-  // signed fraction of a turn in [-1/2, 1/2), as half-turns for sincospi
-  const float x = (float)(int32_t)(uint32_t)((turns + 0x80000000ull) >> 32) * 4.656612873077393e-10f;  // 2^-31
-  float2 cs;
-  sincospif(x, &cs.y, &cs.x);
-  return cs;
+  // nearest quarter turn and the signed rest in [-1/8, 1/8] turns, in half-turns for sincospi: as fp32 the
+  // rest is off by 2^-27 half-turns at most, a quarter of what the whole fraction would be
+  const uint32_t frac = (uint32_t)((turns + 0x80000000ull) >> 32);
+  const uint32_t quarter = (frac + 0x20000000u) >> 30;
+  const float x = (float)(int32_t)(frac - (quarter << 30)) * 4.656612873077393e-10f;  // 2^-31
+  float s, c;
+  sincospif(x, &s, &c);
+  const float cc = quarter & 1 ? s : c, ss = quarter & 1 ? c : s;
+  return make_float2((quarter + 1) & 2 ? -cc : cc, quarter & 2 ? -ss : ss);
 }
 
 // Pairs of fp32 values in one instruction.
@@ -164,7 +168,9 @@ __device__ __forceinline__ void norm_rotate_row(float (&a)[8], float (&b)[8], in
     ss += s1;
 #pragma unroll
     for (int m = 1; m < TPR; m <<= 1) ss += __shfl_xor_sync(kFull, ss, m);
-    const float rs = rsqrtf(ss / (float)D + eps);
+    // (one Newton step: rsqrtf's last bit would cost codes at rounding borders)
+    const float ms = ss / (float)D + eps, r0 = rsqrtf(ms);
+    const float rs = isfinite(r0) && ms > 1e-30f ? fmaf(0.5f * r0, fmaf(-ms * r0, r0, 1.f), r0) : r0;
     const uint64_t rs2 = pair(rs, rs);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
