@@ -318,6 +318,20 @@ def test_attention_split_over_long_sequences(dtype, nq):
     _check_attention(out, want, spread, reach, max(lens), 128, DT[dtype])
 
 
+@pytest.mark.parametrize("dtype,d,limit", [("f32", 64, 8e-6), ("f32", 128, 8e-6), ("f16", 64, 3e-4)])
+def test_attention_long_chunks_keep_their_sums(dtype, d, limit):
+    """One warp walks 100000 tokens: its sums may not drift.  Bound in the 2-norm, relative to the result:
+    fp32 6250 additions of random rounding (2^-24 sqrt(6250) / 2 = 2.4e-6), probabilities and scores 2^-21 at
+    most; fp16 half a step of the output and of the probabilities, 2^-11 / sqrt(3) each at the worst mantissa,
+    2^-11.5 / sqrt(3) on average: sqrt(2) 2^-11.5 / sqrt(3) = 2.8e-4."""
+    lens, nq = [100000], 70
+    c, table, pool = _filled(d, 2, 1, lens, DT[dtype], seed=7)
+    q = torch.randn(1, nq, 2, d, device="cuda").to(DT[dtype])
+    out = _np(c.attention(q, _i32(lens), _i32(table)))
+    want, _, _ = ref.attention(_np(q), pool, lens, [nq], table, d ** -0.5)
+    assert np.linalg.norm(out - want) <= limit * np.linalg.norm(want)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("nq", [1, 3, 140])
 def test_attention_unlike_scales(dtype, nq):

@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TERMS>::NW * 32, (Cfg<D, NR, TERMS>
         if (A.pool.err) atomicExch(A.pool.err, TQ_DEVERR_WAIT_TIMEOUT);
       }
       if (alive)
-        tile_step<D, NR, T>(ring + slot * C::BLK, q, st, 16 * t, lim, 16 * t + 16 > least, len, lane);
+        tile_step<D, NR, TERMS == 2, T>(ring + slot * C::BLK, q, st, 16 * t, lim, 16 * t + 16 > least, len, lane);
       __syncwarp();
       ++used;
       if (alive) {
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) rows_kernel(const AttnPa
       }
       if (!alive) break;
       if (t < mine)
-        tile_step<D, NR, T>(sm + slot * C::BLK, q, st, 16 * t, lim, 16 * t + 16 > least, len, lane);
+        tile_step<D, NR, true, T>(sm + slot * C::BLK, q, st, 16 * t, lim, 16 * t + 16 > least, len, lane);
       __syncwarp();
       if (lane == 0) asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n" ::"r"(empty + 8 * slot) : "memory");
     }
