@@ -389,7 +389,8 @@ tq_status tq_rotary_table(int32_t rotary_dim, const double* freqs, const int32_t
  * be NULL); q_weight, k_weight: device [head_dim] of dtype, or NULL (no norm).  q_out is
  * contiguous [batch][n][q heads][head_dim] (as the attention calls read queries), k_out
  * contiguous [batch][k heads][n][head_dim] (as the appends read keys), both of out_dtype: dtype
- * or TQ_F32.  An output may be its own input's buffer when the layouts and types are the same.
+ * or TQ_F32.  An output may be its own input's buffer when the layouts and types are the same; any
+ * other overlap with an input is refused.
  * dev_positions: device int32 [num_axes][batch][n]; NULL: token j of entry b is at dev_start[b] + j
  * on every axis (device int32 [batch]; NULL: 0).  head_dim 64, 128, 256 or 512. */
 tq_status tq_norm_rotate(int32_t head_dim, tq_dtype dtype, tq_dtype out_dtype, int32_t batch, int32_t n,

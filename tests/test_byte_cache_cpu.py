@@ -100,7 +100,7 @@ def _attend(cfg=None, pool=DEV, pt=None, batch=2, nq=1, dt=b.TQ_BF16, q=None, se
                                      out, ws, bytes_, err, None)
 
 
-def _rotate(d=128, dt=b.TQ_BF16, odt=b.TQ_BF16, batch=2, n=3, q=True, wq=None, qo=DEV, k=None, wk=None, ko=None,
+def _rotate(d=128, dt=b.TQ_BF16, odt=b.TQ_BF16, batch=2, n=3, q=True, wq=None, qo=2 * DEV, k=None, wk=None, ko=None,
             eps=1e-6, rot=None, pos=None, start=None):
     return b.tq_norm_rotate(d, dt, odt, batch, n, _h(8) if q is True else q, wq, qo, k, wk, ko, eps, rot, pos, start,
                             None)
@@ -118,6 +118,7 @@ BAD_POOL = [dict(pool=None), dict(pool=DEV + 16), dict(pt=_pt(table=None)), dict
     dict(q=_h(8)), dict(q=_h(4), qo=DEV), dict(q=_h(8), qo=DEV + 8), dict(q=_h(8), qo=DEV, wq=DEV + 4),
     dict(rot=_rot(dim=8)), dict(rot=_rot(dim=24)), dict(rot=_rot(dim=256)), dict(rot=_rot(inter=2)),
     dict(rot=_rot(axes=0)), dict(rot=_rot(axes=5)), dict(rot=_rot(table=DEV + 4)),
+    dict(q=_h(8, data=2 * DEV), qo=2 * DEV + 256), dict(q=_h(8, data=2 * DEV), qo=DEV),
 ])
 def test_append_refusals(kw):
     assert _append(**kw) == b.TQ_ERR_INVALID_ARG
@@ -139,6 +140,9 @@ def test_attention_refusals(kw):
     dict(dt=3), dict(odt=b.TQ_F16), dict(q=None), dict(qo=None), dict(k=_h(2)), dict(batch=0), dict(batch=513),
     dict(n=-1), dict(n=1 << 30), dict(q=_h(0)), dict(q=_h(8, s=(1025, 1024, 128))), dict(qo=DEV + 4),
     dict(wq=DEV + 4), dict(pos=DEV + 1), dict(start=DEV + 1), dict(eps=-1.0), dict(rot=_rot(dim=144)),
+    # outputs over inputs: shifted, in another type, in another layout, over the other tensor
+    dict(qo=DEV + 1024), dict(qo=DEV, dt=b.TQ_BF16, odt=b.TQ_F32), dict(qo=DEV, q=_h(8, s=(6144, 2048, 128))),
+    dict(k=_h(2, data=2 * DEV), ko=3 * DEV),
 ])
 def test_norm_rotate_refusals(kw):
     assert _rotate(**kw) == b.TQ_ERR_INVALID_ARG

@@ -41,6 +41,27 @@ tq_status check_rows(const tq_heads* x, const char* what, int heads, int batch, 
   return TQ_OK;
 }
 
+// Bytes [lo, hi) that rows cover.
+struct Span {
+  uintptr_t lo, hi;
+};
+Span span_of(const Rows& x, int batch, int n, int d, int bytes) {
+  if (!x.heads || batch < 1 || n < 1) return {0, 0};
+  const long long last = (batch - 1) * x.sb + (n - 1) * x.st + (x.heads - 1) * x.sh + d;
+  return {(uintptr_t)x.p, (uintptr_t)x.p + (uintptr_t)last * bytes};
+}
+bool overlap(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
+
+// Whether an output of `heads` heads ([batch][n][heads][d], or [batch][heads][n][d] of keys) may be written
+// while x is read: apart, or (same) exactly x's own rows, each of which is read before it is written.
+bool may_write(const void* out, int heads, bool keys, const Rows& x, bool same, int batch, int n, int d, int bytes, int out_bytes) {
+  const Span o = {(uintptr_t)out, (uintptr_t)out + (uintptr_t)batch * n * heads * d * out_bytes};
+  if (!overlap(o, span_of(x, batch, n, d, bytes))) return true;
+  const long long st = keys ? d : (long long)heads * d, sh = keys ? (long long)n * d : d, sb = (long long)n * heads * d;
+  return same && out == x.p && out_bytes == bytes && (batch == 1 || x.sb == sb) && (n == 1 || x.st == st) &&
+         (heads == 1 || x.sh == sh);
+}
+
 tq_status check_rotary(const tq_rotary* r, int head_dim, Rotary* out) {
   *out = Rotary{nullptr, 0, 0, 1};
   if (!r || !r->table) return TQ_OK;
@@ -145,6 +166,12 @@ tq_status tq_norm_rotate(int32_t head_dim, tq_dtype dtype, tq_dtype out_dtype, i
   if (!aligned(dev_positions, 4) || !aligned(dev_start, 4)) return fail(TQ_ERR_INVALID_ARG, "misaligned pointer");
   if ((s = check_eps(eps)) != TQ_OK) return s;
   if ((s = check_rotary(rotary, head_dim, &a.rot)) != TQ_OK) return s;
+  const int in = dtype_bytes(dtype), ob = dtype_bytes(out_dtype);
+  if ((q && (!may_write(q_out, a.q.heads, false, a.q, true, batch, n, head_dim, in, ob) ||
+             !may_write(q_out, a.q.heads, false, a.k, false, batch, n, head_dim, in, ob))) ||
+      (k && (!may_write(k_out, a.k.heads, true, a.k, true, batch, n, head_dim, in, ob) ||
+             !may_write(k_out, a.k.heads, true, a.q, false, batch, n, head_dim, in, ob))))
+    return fail(TQ_ERR_INVALID_ARG, "an output overlaps an input and is not its own buffer in the same layout");
   if (n == 0) return TQ_OK;
   a.d = head_dim;
   a.B = batch;
@@ -191,6 +218,10 @@ tq_status tq_byte_append_paged(const tq_byte_config* cfg, void* dev_pool, const 
     return fail(TQ_ERR_INVALID_ARG, "misaligned pointer");
   if ((s = check_eps(eps)) != TQ_OK) return s;
   if ((s = check_rotary(rotary, cfg->head_dim, &a.rot)) != TQ_OK) return s;
+  if (q && (!may_write(q_out, cfg->num_q_heads, false, a.q, true, batch, n, cfg->head_dim, bytes, bytes) ||
+            !may_write(q_out, cfg->num_q_heads, false, a.k, false, batch, n, cfg->head_dim, bytes, bytes) ||
+            !may_write(q_out, cfg->num_q_heads, false, a.v, false, batch, n, cfg->head_dim, bytes, bytes)))
+    return fail(TQ_ERR_INVALID_ARG, "q_out overlaps an input and is not q's own buffer in the same layout");
   if (n == 0) return TQ_OK;
   a.d = cfg->head_dim;
   a.B = batch;
@@ -236,7 +267,9 @@ tq_status tq_byte_attention_paged(const tq_byte_config* cfg, const void* dev_poo
   if ((s = check_rows(q, "q", cfg->num_q_heads, batch, nq, dtype_bytes(dtype), &a.q)) != TQ_OK) return s;
   if (!aligned(out, 16) || !aligned(ws, 256) || !aligned(dev_seq_len, 4) || !aligned(dev_count, 4))
     return fail(TQ_ERR_INVALID_ARG, "misaligned pointer (ws 256 B, out 16 B, lengths 4 B)");
-  if (out == q->data) return fail(TQ_ERR_INVALID_ARG, "out must not be q's buffer");
+  const int bytes = dtype_bytes(dtype);
+  if (!may_write(out, cfg->num_q_heads, false, a.q, false, batch, nq, cfg->head_dim, bytes, bytes))
+    return fail(TQ_ERR_INVALID_ARG, "out must not overlap q");
   if (!std::isfinite(scale)) return fail(TQ_ERR_INVALID_ARG, "scale must be finite");
   if (ws_bytes < byte_attention_workspace(cfg->head_dim, batch, nq, cfg->num_q_heads, cfg->num_kv_heads, dtype))
     return fail(TQ_ERR_WORKSPACE, "workspace too small");
