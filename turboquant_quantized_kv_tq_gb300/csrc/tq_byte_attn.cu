@@ -10,12 +10,12 @@
 // a slab's range.  Ranges that cover part of a slab leave (M, l, O) in the workspace for join_kernel,
 // which is launched early and waits for this grid.
 // Measured: 8 x 32768 tokens, 32 / 8 heads, bf16, 97 us, 5.55 TB/s (0.82 of the measured copy rate); fp32
-// queries 95 us; 131072 tokens of 64 / 8 heads 56 us; 16 x 16384 tokens with 16 rows 110 us; 1024 tokens
+// queries 97 us; 131072 tokens of 64 / 8 heads 56 us; 16 x 16384 tokens with 16 rows 110 us; 1024 tokens
 // 10 us.  Of the first's 18 us above its floor some 5 pass before the tiles flow (lengths, plan, page
 // table, first copies), 3 in the join, and the rest at the end: SMs differ by up to a fifth in what they
 // stream (groups of 10 to 20 neighbours), and the fast ones idle.
 // rows_kernel: 8 warps of 8 NR rows share one ring; each tile is read once per 64 NR rows.  Bound by the
-// mma.sync rate and the conversions, which every warp repeats: 112 TFLOP/s (fp32, d = 64).
+// mma.sync rate and the conversions, which every warp repeats: 110 TFLOP/s (fp32, d = 64).
 #include <atomic>
 #include <string>
 
@@ -119,7 +119,7 @@ __device__ __forceinline__ int find_entry(const long long* pre, int B, long long
 template <int D, int NR, int TERMS>
 struct Cfg {
   static constexpr int BLK = 32 * D + 32;
-  // warps: fp32 at d = 128 12 of 168 registers (8 x 32768 tokens: 100 us, 8 warps 109 us)
+  // warps: fp32 at d = 128 12 of 168 registers (8 x 32768 tokens: 97 us, 8 warps 109 us)
   static constexpr int NW = NR == 1 && D == 128 && TERMS == 2 ? 12 : 8;
   static constexpr bool TWO = NR == 1 && D <= 128 && TERMS * D <= 128;      // two blocks per SM
   static constexpr int ROOM = (TWO ? 115200 : 231424) - 4160 - 512;         // less the plan and barriers
