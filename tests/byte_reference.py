@@ -133,3 +133,29 @@ def attention(q, pool, seq, cnt, table, scale):
                 spread[b, i, h * G:(h + 1) * G] = p @ np.abs(V[:m])
                 reach[b, i, h * G:(h + 1) * G] = abs(scale) * (np.abs(x) @ np.abs(K[:m]).T).max(-1)
     return out, spread, reach
+
+
+def attention_least(q, pool, seq, cnt, table, scale, step):
+    """[B][nq][Hq][d]: what attention may lose where its weights are stored with a smallest step.
+
+    A token of a value block with scale 2^e enters as w = p 2^e times its code.  Stored to half a step of
+    step * (the row's largest w), a w is off by at most that, and by no more than w itself where it becomes
+    zero: sum over the tokens of min(step / 2 * max w, w) |code|."""
+    B, nq, Hq, d = q.shape
+    G = Hq // pool.heads
+    least = np.zeros(q.shape)
+    for b in range(B):
+        pages = table[b][:(seq[b] + TILE - 1) // TILE]
+        for h in range(pool.heads):
+            K, V = pool.read(0, h, pages, seq[b]), pool.read(1, h, pages, seq[b])
+            size = np.repeat([float(pool.scale(p, h, 1)) for p in pages], TILE)[:seq[b]]
+            for i in range(min(nq, max(0, cnt[b]))):
+                m = seq[b] - cnt[b] + 1 + i
+                if m <= 0:
+                    continue
+                s = scale * (q[b, i, h * G:(h + 1) * G] @ K[:m].T)
+                p = np.exp(s - s.max(-1, keepdims=True))
+                w = p / p.sum(-1, keepdims=True) * size[:m]
+                off = np.minimum(step / 2 * w.max(-1, keepdims=True), w)
+                least[b, i, h * G:(h + 1) * G] = off @ (np.abs(V[:m]) / size[:m, None])
+    return least

@@ -52,10 +52,13 @@ def _cache(d, hq, hkv, pages, blocks, seed=0, garbage=True):
     return c
 
 
-def _check_attention(out, want, spread, reach, T, d, dtype):
+def _check_attention(out, want, spread, reach, T, d, dtype, least=0.0):
     two = 2.0 ** -22 if dtype == torch.float32 else 2.0 ** -11
     score = (d + T / 16 + 64) * 2.0 ** -22 * (1 + reach[..., None])
     tol = spread * (two + 2 * score + (T / 16 + 64) * 2.0 ** -23) + np.abs(want) * _half_step(dtype) + 1e-30
+    # the output's own type: below its smallest normal value it has equal steps, eps * smallest_normal (fp16:
+    # 2^-24), so that rounding is off by up to half of one (2^-25) and not by half an eps of the value
+    tol = tol + torch.finfo(dtype).smallest_normal * _half_step(dtype) + least
     got = _np(out)
     assert np.all(np.isfinite(got))
     worst = np.max(np.abs(got - want) / tol)
@@ -337,12 +340,7 @@ def test_attention_long_chunks_keep_their_sums(dtype, d):
         assert np.linalg.norm(out - want) <= 4.7e-6 * np.linalg.norm(want)
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("nq", [1, 3, 140])
-def test_attention_unlike_scales(dtype, nq):
-    """Value blocks whose scales lie 2^24 apart, keys that make the softmax sharp, large and small queries."""
-    lens = [400, 163]
-    d, hq, hkv = 128, 4, 1
+def _unlike_scales(d, hq, hkv, lens):
     B, blocks, pages = 2, 27, 60
     c = _cache(d, hq, hkv, pages, blocks)
     table = _table(B, blocks, pages)
@@ -352,11 +350,44 @@ def test_attention_unlike_scales(dtype, nq):
     k = rs.randn(B, 1, 400, d) * np.repeat(2.0 ** rs.uniform(-4, 1, (B, 1, 25, 1)), 16, axis=2)
     # (fp32 input of both whatever the queries' type is: the pool does not remember)
     c.append(torch.from_numpy(k).float().cuda(), torch.from_numpy(v).float().cuda(), _i32([0, 0]), _i32(table), count=_i32(lens))
-    pool = ref.Pool(c.pool.cpu().numpy(), hkv, d)
+    return c, table, ref.Pool(c.pool.cpu().numpy(), hkv, d)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("nq", [1, 3, 140])
+def test_attention_unlike_scales(dtype, nq):
+    """Value blocks whose scales lie 2^24 apart, keys that make the softmax sharp, large and small queries."""
+    lens = [400, 163]
+    d, hq, hkv = 128, 4, 1
+    B = 2
+    c, table, pool = _unlike_scales(d, hq, hkv, lens)
     q = (torch.randn(B, nq, hq, d, device="cuda") * torch.tensor([1e-3, 1.0, 3.0, 6.0], device="cuda")[:, None]).to(DT[dtype])
+    _check_unlike_scales(c, pool, table, lens, q)
+
+
+def _check_unlike_scales(c, pool, table, lens, q):
+    # Weights are stored as fp16, whose smallest step is 2^-24, relative to 2^M.  M lies at least 7 below the
+    # row's largest exponent (bf16 and fp16 chunks; 14 elsewhere), so the largest weight is stored as 2^7 (2^14)
+    # or more and the step is at most 2^-31 (2^-38 for fp32, whose second term has the same step) of it.  Where
+    # scales differ by 2^24, weights of the small blocks get there, and a coordinate that the large blocks hold
+    # zeros for shows it.
+    B, nq, d = q.shape[0], q.shape[1], q.shape[3]
     out = c.attention(q, _i32(lens), _i32(table))
-    want, spread, reach = ref.attention(_np(q), pool, lens, [nq] * B, table, d ** -0.5)
-    _check_attention(out, want, spread, reach, max(lens), d, DT[dtype])
+    args = (_np(q), pool, lens, [nq] * B, table, d ** -0.5)
+    want, spread, reach = ref.attention(*args)
+    least = ref.attention_least(*args, 2.0 ** (-38 if q.dtype == torch.float32 else -31))
+    _check_attention(out, want, spread, reach, max(lens), d, q.dtype, least)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_attention_least_weights(dtype):
+    """Queries for which some outputs rest on the smallest weights, or are subnormal fp16 values."""
+    lens, d, hq, hkv, nq = [400, 163], 128, 4, 1, 140
+    c, table, pool = _unlike_scales(d, hq, hkv, lens)
+    for seed in (40, 51, 186, 445, 693, 1130, 1195, 2807):
+        torch.manual_seed(seed)
+        size = torch.tensor([1e-3, 1.0, 3.0, 6.0], device="cuda")[:, None]
+        _check_unlike_scales(c, pool, table, lens, (torch.randn(2, nq, hq, d, device="cuda") * size).to(DT[dtype]))
 
 
 def test_attention_nonfinite_queries_stay_in_their_rows():
