@@ -14,8 +14,9 @@
 // S_0, S_1, O_0, O_1 fill the tensor memory; P_i (fp16) takes the first half of S_i's columns.  While
 // warps 0-3 work on S_0 the tensor cores work on tile 1, and the other way round.  A thread of
 // warps 0-7 owns one row.  Softmax as in tq_byte_attn.cuh: block scales are exponents, so the value
-// scale costs nothing and P keeps fp16's precision whatever the scales are.  The reference M is
-// raised only when a row's maximum passes it by 15 (P <= 2^15), so O is rescaled rarely.
+// scale costs nothing and P keeps fp16's precision whatever the scales are, down to 2^-21 of the row's
+// largest; below that it is off by up to 2^-32 of the largest.  The reference M is raised only when a
+// row's maximum passes it by 15 (P <= 2^15), so O is rescaled rarely.
 //
 // The (row group, token tile) pairs of all slabs form one sequence cut into equal ranges, one per
 // SM; ranges that share a row group leave partials that join_kernel joins.
@@ -24,9 +25,9 @@
 // gives registers to the rows: 192 a thread there, so that a row's 128 scores stay in registers from
 // the maximum to the probabilities, and 64 in the other warps).
 //
-// Measured: 512 queries of 32 heads over 4 x 32768 tokens (8 KV heads, bf16) 855 us, 1275 TFLOP/s, 0.66 of
-// the measured bf16 burst rate (0.74 of the sustained one: the run is at the power cap); fp16 (three
-// query terms) 915 us; the last 64 positions 131 us.  A tile takes about 3100 cycles, 2048 of them MMA.
+// Measured: 512 queries of 32 heads over 4 x 32768 tokens (8 KV heads, bf16) 788 us, 1384 TFLOP/s, 0.72 of
+// the measured bf16 burst rate (0.81 of the sustained one: the run is at the power cap); fp16 (three
+// query terms) 841 us; the last 64 positions 121 us.  A tile takes about 2850 cycles, 2048 of them MMA.
 // What bounds it is the chain of a row tile -- 128 scores to P, P V, the next scores -- beside the other
 // tile's, and shared memory: an fp8 product of N = 128 reads 8 KB in its 64 cycles, all that it delivers.
 // Tiles of 80 tokens, whose P has columns of its own so that scores run ahead, were slower (1480 us): at
@@ -47,7 +48,8 @@ constexpr int kTok = 128;          // tokens per tile
 constexpr int kD = 128;
 constexpr int kThreads = 512;
 constexpr int kRowRegs = 192, kOtherRegs = 64;  // 256 * 192 + 256 * 64 = 512 * 128, the launch's registers
-constexpr int kGroupCost = 4;      // virtual tiles of a row group: what a range costs beside its tiles
+constexpr int kGroupCost = 8;      // virtual tiles of a row group: what a range costs beside its tiles (4: 125 us for
+                                   // the last 64 positions, 8: 122, 14: 124)
 constexpr float kTop = 7.f;        // M lies this far below the maximum it was set from
 constexpr float kSlack = 15.f;     // M is raised when the maximum passes it by this: P <= 2^15
 constexpr int kBlk = 32 * kD + 32;
@@ -63,6 +65,10 @@ struct TcParams {
 template <int NT, int NQ>
 struct Plan {
   static constexpr int ROWS = 128 * NQ;
+  // blocks of a tile in the first of the two parts in which P is handed over: with two query terms the
+  // products keep up and one late hand-over costs least (4 / 6 / 7 blocks: 815 / 805 / 788 us for 512 queries
+  // x 4 x 32768 tokens), with three they start early (4 / 6 / 7: 841 / 866 / 958 us)
+  static constexpr int FIRST = NT == 2 ? 7 : 4;
   static constexpr int SC = 4;                                    // scale stages of 8 x 16 bytes
   static constexpr int Q = 0, KR = Q + NQ * NT * 16384, VR = KR + 2 * 16384, V16 = VR + 2 * 16384;
   // [stage][block]: as copied (K scale, V scale, -, -), then in place (K scale, e, 2^-e, -)
@@ -111,15 +117,18 @@ __device__ __forceinline__ void issue_scores(uint32_t sb, int i) {
   }
   __syncwarp();
 }
-// Half h of O_i += P_i V of the tile in V buffer ST (accumulate: not the range's first tile).
+// Part h (blocks [0, FIRST), [FIRST, 8)) of O_i += P_i V of the tile in V buffer ST (accumulate: not the
+// range's first tile).
 template <int NT, int NQ, int ST>
 __device__ __forceinline__ void issue_readout(uint32_t sb, int i, int h, bool accumulate) {
   using L = Plan<NT, NQ>;
-  const uint64_t v = sdesc128(sb + L::V16 + ST * 32768 + h * 16384);
+  const uint64_t v = sdesc128(sb + L::V16 + ST * 32768);
   if (elected()) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      tqd::tc_mma_f16_ta(256 + 128 * i, 128 * i + 32 * h + 8 * k, v + 2 * k, kIdesc, accumulate || h + k > 0);
+    for (int k = 0; k < 8; ++k)
+      if ((k >= L::FIRST) == (h == 1))
+        tqd::tc_mma_f16_ta(256 + 128 * i, 128 * i + 8 * k, v + (uint64_t)((k >> 2) * (16384 >> 4) + 2 * (k & 3)), kIdesc,
+                           accumulate || k > 0);
     if (h == 1) {
       tqd::tc_commit(sb + L::BARS + 8 * (O_DONE + i));
       if (i == NQ - 1) tqd::tc_commit(sb + L::BARS + 8 * (V_EMPTY + ST));
@@ -517,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
           const float sum = block_p<EDGE>(v + 16 * g, left - 16 * g, a[g], e[g] - mr, w);
           l = fmaf(sum, sc[g].z, l);
           st8_async(t_s + 8 * g, w);
-          if (g == 3 || g == 7) {
+          if (g == L::FIRST - 1 || g == 7) {
             asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
             tqd::tc_fence_before();
             tqd::tc_mbar_arrive(bar(P_FULL, 2 * i + (g == 7)));
