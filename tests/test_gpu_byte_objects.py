@@ -1,0 +1,60 @@
+"""The byte cache's and the rotation's objects beside the calls: what they own on other streams, the error word, errors."""
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def _api():
+    import turboquant_quantized_kv_tq_gb300 as tq
+    return tq
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _busy(s):
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)  # some 50 ms: the call below waits behind it
+
+
+def test_dropped_rotary_lives_until_its_call_ran():
+    tq = _api()
+    q = torch.randn(2, 5, 4, 128, device="cuda")
+    start = _i32([7, 100000])
+    want = tq.norm_rotate(q, rotary=tq.Rotary(128), start=start)[0]
+    s = torch.cuda.Stream()
+    _busy(s)
+    got = tq.norm_rotate(q, rotary=tq.Rotary(128), start=start, stream=s)[0]
+    other = [torch.full((64,), 3, dtype=torch.int64, device="cuda") for _ in range(2000)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    del other
+
+
+def test_dropped_cache_lives_until_its_call_ran():
+    tq = _api()
+    x = torch.randn(2, 1, 2, 40, 128, device="cuda")
+    q, seq, start, table = torch.randn(1, 1, 4, 128, device="cuda"), _i32([40]), _i32([0]), _i32([[2, 0, 1]])
+
+    def filled():
+        c = tq.PagedByteCache(128, 4, 2, 3, 3)
+        c.append(x[0], x[1], start, table)
+        return c
+
+    want = filled().attention(q, seq, table)
+    s = torch.cuda.Stream()
+    c = filled()
+    size = c.pool.numel()
+    _busy(s)
+    got = c.attention(q, seq, table, stream=s)
+    del c
+    other = [torch.full((size,), 126, dtype=torch.uint8, device="cuda") for _ in range(200)]
+    words = [torch.full((1,), 77, dtype=torch.int32, device="cuda") for _ in range(2000)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert all(int(w) == 77 for w in words[:50])
+    del other

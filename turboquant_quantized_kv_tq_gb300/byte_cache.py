@@ -6,6 +6,11 @@ keys, and ``PagedByteCache`` owns a pool of e4m3 codes with a scale for each 16-
 and side.  Tensors may be strided views (a fused projection's slices): only the head dimension has to
 be contiguous, with rows on 16-byte boundaries.  Nothing is copied or converted here; a layout that
 the kernels do not take is refused.
+
+Calls launch on the current stream of the tensors' device, or on ``stream``.  A call given ``stream``
+does not wait for other streams, but holds the memory that it uses, the objects' own included, until
+that stream is done with it.  Under ``torch.cuda.stream`` torch's rule for tensors made on another
+stream applies to the objects too: keep them until the stream is done, or call with ``stream``.
 """
 
 import importlib.machinery
@@ -37,15 +42,16 @@ def _load_ext():
 _c = _load_ext()
 
 
-def _on_stream(stream, inputs, call, *args):
-    """The call with ``stream`` as the current one, so that what it allocates belongs to that stream;
-    the inputs' memory is not handed out again before the stream is done with it."""
-    for t in inputs:
+def _on_stream(stream, held, call, *args):
+    """The call with ``stream`` as the current one, so that what it allocates belongs to that stream.
+    ``held``: every tensor that its kernels reach, the inputs and what the call's objects own; their memory
+    is not handed out again before the stream is done with it."""
+    for t in held:
         if t is not None and t.get_device() != stream.device_index:
             raise ValueError("the tensors must be on the stream's device")
     with torch.cuda.stream(stream):
         out = call(*args)
-    for t in inputs:
+    for t in held:
         if t is not None:
             t.record_stream(stream)
     return out
@@ -97,6 +103,10 @@ class Rotary:
                       self._table.get_device())
 
 
+def _table(rotary):
+    return None if rotary is None else rotary._table
+
+
 def norm_rotate(q=None, k=None, rotary=None, positions=None, start=None, q_weight=None, k_weight=None, eps=1e-6,
                 out_dtype=None, q_out=None, k_out=None, stream=None):
     """RMS norm of every head (where a weight is given) and position rotation (where ``rotary`` is), in
@@ -115,7 +125,8 @@ def norm_rotate(q=None, k=None, rotary=None, positions=None, start=None, q_weigh
             out_dtype is torch.float32, q_out, k_out)
     if stream is None:
         return _c.norm_rotate(*args)
-    return _on_stream(stream, (q, k, positions, start, q_weight, k_weight, q_out, k_out), _c.norm_rotate, *args)
+    return _on_stream(stream, (q, k, positions, start, q_weight, k_weight, q_out, k_out, _table(rotary)), _c.norm_rotate,
+                      *args)
 
 
 class PagedByteCache:
@@ -173,8 +184,8 @@ class PagedByteCache:
                 k_weight, q, q_weight, eps, q_out)
         if stream is None:
             return _c.append(*args)
-        return _on_stream(stream, (k, v, start, block_table, count, positions, k_weight, q, q_weight, q_out), _c.append,
-                          *args)
+        return _on_stream(stream, (k, v, start, block_table, count, positions, k_weight, q, q_weight, q_out, _table(rotary),
+                                   self._pool, self._error), _c.append, *args)
 
     def attention(self, q, seq_len, block_table, count=None, scale=None, out=None, stream=None):
         """q: CUDA tensor [batch][nq][num_q_heads][d] (or [batch][num_q_heads][d] for one query), any
@@ -185,7 +196,7 @@ class PagedByteCache:
         args = (self._args, q, seq_len, block_table, count, self.head_dim ** -0.5 if scale is None else scale, out)
         if stream is None:
             return _c.attention(*args)
-        return _on_stream(stream, (q, seq_len, block_table, count, out), _c.attention, *args)
+        return _on_stream(stream, (q, seq_len, block_table, count, out, self._pool, self._error), _c.attention, *args)
 
     def dequantize(self, b, kvh, t0, t1, block_table):
         """Tokens [t0, t1) of KV head kvh of entry b as fp32 (k, v) [t1 - t0][d]."""
