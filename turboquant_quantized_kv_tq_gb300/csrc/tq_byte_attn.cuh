@@ -174,7 +174,9 @@ __device__ __forceinline__ void convert_q(QFrag<D, NR, T>& q, const QRaw<D, NR, 
           }
         }
     }
-    const float f = exp2i(e) * score_scale * kLog2e;  // (of row g: the threads that hold rows 2u, 2u + 1 need it)
+    // (an infinity makes the row NaN: scores of -inf alone would look like a row that attends to nothing)
+    const float f = amax <= 3.402823466e38f ? exp2i(e) * score_scale * kLog2e : __uint_as_float(0x7fc00000u);
+    // (of row g: the threads that hold rows 2u, 2u + 1 need it)
     q.f[r][0] = __shfl_sync(kFull, f, 8 * u);
     q.f[r][1] = __shfl_sync(kFull, f, 8 * u + 4);
   }
