@@ -456,7 +456,7 @@ tq_status tq_byte_append_paged(const tq_byte_config* cfg, void* dev_pool, const 
  * Scores, softmax statistics and accumulators are fp32.  fp32 queries and their probabilities enter the
  * matrix products as fp16 hi + lo terms.  bf16 and fp16 queries enter as fp16 under a power-of-two scale
  * per row, or, in chunks of more than 64 rows (queries times heads per KV head) at head_dim 128, as two or
- * three e4m3 terms: exact but for what lies below 2^-18 of the row's largest value (2^-25 as fp16).  Their
+ * three e4m3 terms: exact but for what lies below 2^-18 of the row's largest value (2^-39 as fp16).  Their
  * probabilities are rounded to fp16.  A query with an infinity or a NaN gives NaN in its own row only.
  * A bad page reads the redirect page; the outputs of that entry then mean nothing, those of other
  * entries are unaffected, and TQ_DEVERR_BAD_PAGE is recorded.  ws: device workspace of at least

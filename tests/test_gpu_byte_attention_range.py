@@ -52,3 +52,34 @@ def test_infinite_query_is_nan_in_its_row(dtype, d, hq, nq, sign):
     out = c.attention(q, _i32(lens), _i32(table))
     assert torch.isnan(out[hit]).all()
     assert torch.equal(out[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("hq,hkv,nq", [(4, 4, 1), (8, 2, 3), (8, 1, 6), (2, 1, 40)])
+@pytest.mark.parametrize("outlier", [0, 12, 14])
+def test_fp32_keeps_its_bits(d, hq, hkv, nq, outlier):
+    """The 2-norm of an fp32 result's error, with ordinary queries and with one channel 2^outlier above the others
+    that the keys hold zeros for (so that the others decide).
+
+    A score is the sum of d / 8 products (two terms of 16 coordinates each) in the tensor cores' truncating
+    accumulator, at most 2^-23 of the running sum each, and a handful of fp32 roundings; with S the scores' rms it is
+    off by less than (d / 8 + 8) 2^-23 S.  Weights are off by that and by 2^-21 (ex2, the second fp16 term, sums), and
+    both enter the result at most twice (numerator and denominator).  One fp16 term alone for the queries or the weights
+    would be off by 2^-12 / sqrt 3 = 1.4e-4, ten times that and more."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(d + nq)
+    lens = [301, 95]
+    k, v = (torch.randn(2, hkv, 301, d, generator=g, device="cuda") for _ in range(2))
+    q = torch.randn(2, nq, hq, d, generator=g, device="cuda")
+    if outlier:
+        k[..., 3] = 0.0
+        q[..., 3] = 2.0 ** outlier * (1 + q[..., 3].abs())
+    c, table, pool = _filled(d, hq, hkv, lens, k, v)
+    out = _np(c.attention(q, _i32(lens), _i32(table)))
+    want, _, _ = ref.attention(_np(q), pool, lens, [nq] * 2, table, d ** -0.5)
+    keys = np.concatenate([pool.read(0, h, table[0], 301) for h in range(hkv)])
+    S = np.sqrt(np.mean((_np(q[0]).reshape(-1, d) @ keys.T) ** 2) / d)
+    tol = 2 * ((d / 8 + 8) * 2.0 ** -23 * S + 2.0 ** -21)
+    assert tol <= 1.5e-5
+    err = np.linalg.norm(out - want) / np.linalg.norm(want)
+    assert err <= tol, (err, tol)

@@ -28,6 +28,7 @@ namespace tqb {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kShift = 14.f;            // M is this far below the largest s + e
+constexpr int kQueryTop = 14;             // exponent of a query row's largest magnitude as an fp16 operand
 constexpr uint32_t kWaitLimit = 1u << 20; // polls of an mbarrier before giving up
 
 __device__ __forceinline__ float ex2(float x) {
@@ -135,9 +136,11 @@ __device__ __forceinline__ void request_q(QRaw<D, NR, T>& q, const Rows& X, int 
 }
 
 // Query rows as fp16 operands.  Each row is scaled by the power of two that brings its largest magnitude
-// into [1, 2): bf16 and fp16 values are then exact in fp16 down to 2^-14 of that (below, off by at most
-// 2^-25 of it); fp32 rows take a second fp16 term of what the first leaves (together off by at most
-// 2^-23 or so of a value).
+// into [2^14, 2^15), the top of fp16's range: what its smallest step, 2^-24, rounds away is then 2^-39 of the
+// row's largest value at most (at [1, 2) it was 2^-25, so that beside a channel 2^12 times the others fp32 results
+// were off by 1e-4).  bf16 and fp16 values are exact above that; fp32 rows take a second fp16 term of what the first
+// leaves, together off by at most 2^-23 of a value or by 2^-39 of the largest.  Scores stay below
+// 2^15 * 2 * 448 * 256 times the scales, far inside fp32.
 template <int D, int NR, typename T>
 __device__ __forceinline__ void convert_q(QFrag<D, NR, T>& q, const QRaw<D, NR, T>& raw, float score_scale, int lane) {
   const int u = lane & 3;
@@ -153,9 +156,8 @@ __device__ __forceinline__ void convert_q(QFrag<D, NR, T>& q, const QRaw<D, NR, 
     }
     amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
-    // exponent of amax, held where 2^-e is a normal number; 0 for rows of zeros or with infinities
-    int e = log2i(amax);
-    if (e < -120 || e > 120) e = amax > 1.f && e < 128 ? 120 : amax > 0.f && e < 0 ? -120 : 0;
+    // exponent of amax less 14, held where 2^-e is a normal number (rows below 2^-112 keep fewer bits)
+    const int e = max(log2i(amax), -112) - kQueryTop;
     const float inv = exp2i(-e);
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
