@@ -295,25 +295,29 @@ __device__ __forceinline__ bool append_keys(const AppendArgs& A, B block, const 
     float a[8], c[8];
     unpack8(ra[p], a);
     unpack8(rc[p], c);
-    // (rows without a new token are zeros; their cosines are those of an existing slot)
-    norm_rotate_row<TPR>(a, c, l, A.wk != nullptr, wa, wb, D, A.eps, cs + (s >= lo && s < hi ? s : lo) * (A.rot.r / 4),
-                         A.rot.r, A.rot.interleaved);
+    // (slots without a new token go along as zeros, with the cosines of an existing slot, and count for nothing: with
+    // eps = 0 their norm is NaN)
+    const bool live = s >= lo && s < hi;
+    norm_rotate_row<TPR>(a, c, l, A.wk != nullptr, wa, wb, D, A.eps, cs + (live ? s : lo) * (A.rot.r / 4), A.rot.r,
+                         A.rot.interleaved);
+    if (live) {
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      mag.add(a[i], a[i + 1]);
-      mag.add(c[i], c[i + 1]);
+      for (int i = 0; i < 8; i += 2) {
+        mag.add(a[i], a[i + 1]);
+        mag.add(c[i], c[i + 1]);
+      }
+      rot[(4 * p + 0) * 32] = make_float4(a[0], a[1], a[2], a[3]);
+      rot[(4 * p + 1) * 32] = make_float4(a[4], a[5], a[6], a[7]);
+      rot[(4 * p + 2) * 32] = make_float4(c[0], c[1], c[2], c[3]);
+      rot[(4 * p + 3) * 32] = make_float4(c[4], c[5], c[6], c[7]);
     }
-    rot[(4 * p + 0) * 32] = make_float4(a[0], a[1], a[2], a[3]);
-    rot[(4 * p + 1) * 32] = make_float4(a[4], a[5], a[6], a[7]);
-    rot[(4 * p + 2) * 32] = make_float4(c[0], c[1], c[2], c[3]);
-    rot[(4 * p + 3) * 32] = make_float4(c[4], c[5], c[6], c[7]);
   }
   const bool odd = __any_sync(kFull, mag.odd());
   if (odd) {  // infinities and NaN do not count for the scale
     mag.top = 0.f;
     for (int i = 0; i < 4 * NP; ++i) {
-      const int p = i >> 2;
-      if (p * RPW + RPW <= lo || p * RPW >= hi) continue;
+      const int s = (i >> 2) * RPW + r0;
+      if (s < lo || s >= hi) continue;
       const float4 v = rot[i * 32];
       mag.top = fmaxf(mag.top, fmaxf(fmaxf(finite_abs(v.x), finite_abs(v.y)), fmaxf(finite_abs(v.z), finite_abs(v.w))));
     }
