@@ -360,7 +360,9 @@ tq_status tq_decode_attention_paged(const tq_context* ctx, const void* dev_pool,
  * Coordinates from rotary_dim on are not turned.  Each pair follows the position on one of
  * num_axes axes (one axis for text; time, height and width for images and video).  An angle is
  * held as a 64-bit fraction of a turn and multiplied by the position modulo one turn, so it is
- * as exact at position 2^31 as at 1.  Arithmetic is fp32, rounded once to the output's type. */
+ * as exact at position 2^31 as at 1.  Arithmetic is fp32, rounded once to the output's type.  The norm
+ * holds for rows of any finite magnitude, also where their squares leave fp32's range; a row of zeros
+ * with eps = 0 is 0 / 0, NaN. */
 typedef struct {
   const uint64_t* table;  /* device [rotary_dim / 2], from tq_rotary_table; NULL: no rotation  */
   int32_t rotary_dim;     /* a multiple of 16, at most head_dim                                */

@@ -106,6 +106,7 @@ __device__ __forceinline__ void rows_pass(const Rows& X, const TokenAt* tok, con
       __syncthreads();
       filled = true;
     }
+    uint32_t again = 0;  // rows whose squares leave fp32's range
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       if (base + u * RPP >= total) break;  // (uniform over the block)
@@ -113,11 +114,37 @@ __device__ __forceinline__ void rows_pass(const Rows& X, const TokenAt* tok, con
       unpack8(ra[u], a);
       unpack8(rb[u], b);
       const bool live = tks[u] < nt;
-      norm_rotate_row<TPR>(a, b, l, w != nullptr, wa, wb, D, eps, cs + (live ? tks[u] : 0) * (R.r / 4), R.r, R.interleaved);
-      if (live) {
+      const bool far = norm_rotate_row<TPR, kNear>(a, b, l, w != nullptr, wa, wb, D, eps, cs + (live ? tks[u] : 0) * (R.r / 4), R.r,
+                                                   R.interleaved);
+      if (live && !far) {
         O* dst = out + tok[tks[u]].dst + hs[u] * out_head;
         store8(dst + 8 * ca, a);
         store8(dst + 8 * cb, b);
+      }
+      if (live && far) again |= 1u << u;
+    }
+    if (__any_sync(kFull, again)) {  // (indexes and weights once more: nothing of this is held through the loop)
+      float va[8], vb[8];
+      load_weight<T>(w, ca, cb, va, vb);
+#pragma unroll 1
+      for (int u = 0; u < kU; ++u) {
+        const bool mine = again >> u & 1;
+        const int row = base + u * RPP + row0, tk1 = mine ? row / nh : 0, h1 = h0 + row - row / nh * nh;
+        Raw8<T> xa = {}, xb = {};
+        if (mine) {  // (not stored yet, also where the output is the input's buffer)
+          const T* src = reinterpret_cast<const T*>(X.p) + tok[tk1].src + h1 * X.sh;
+          xa = load8_rw(src + 8 * ca);
+          xb = load8_rw(src + 8 * cb);
+        }
+        float a[8], b[8];
+        unpack8(xa, a);
+        unpack8(xb, b);
+        norm_rotate_row<TPR, kFar>(a, b, l, true, va, vb, D, eps, cs + tk1 * (R.r / 4), R.r, R.interleaved);
+        if (mine) {
+          O* dst = out + tok[tk1].dst + h1 * out_head;
+          store8(dst + 8 * ca, a);
+          store8(dst + 8 * cb, b);
+        }
       }
     }
   }
@@ -295,10 +322,9 @@ __device__ __forceinline__ bool append_keys(const AppendArgs& A, B block, const 
     float a[8], c[8];
     unpack8(ra[p], a);
     unpack8(rc[p], c);
-    // (slots without a new token go along as zeros, with the cosines of an existing slot, and count for nothing: with
-    // eps = 0 their norm is NaN)
+    // (slots without a new token go along as zeros, with the cosines of an existing slot, and count for nothing)
     const bool live = s >= lo && s < hi;
-    norm_rotate_row<TPR>(a, c, l, A.wk != nullptr, wa, wb, D, A.eps, cs + (live ? s : lo) * (A.rot.r / 4), A.rot.r,
+    norm_rotate_row<TPR, kAll>(a, c, l, A.wk != nullptr, wa, wb, D, A.eps, cs + (live ? s : lo) * (A.rot.r / 4), A.rot.r,
                          A.rot.interleaved);
     if (live) {
 #pragma unroll

@@ -146,31 +146,86 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// Norm (norm: with wa, wb the row's weights) and rotation of one row's values.
+// 1 / sqrt(ms) for 2^-128 < ms < infinity (one Newton step: rsqrtf's last bit would cost codes at rounding borders);
+// not positive elsewhere: NaN, or -infinity where r * r overflows.  Squares that fell below 2^-126 are off by 2^-150
+// each, so the mean of a row of them by 2^-22 at most.
+__device__ __forceinline__ float norm_factor(float ms) {
+  const float r = rsqrtf(ms);
+  return fmaf(0.5f * r, fmaf(-ms, r * r, 1.f), r);
+}
+
+// The factor of rows whose mean square is out of that range (far; the warp's other rows come along unchanged).  With c
+// the power of two that brings the larger of max |x| and sqrt(eps) to [1, 2), the values become c x and their factor is
+// 1 / sqrt(mean((c x)^2) + c^2 eps).  A row with an infinity gets 0 (finite coordinates become 0, the infinite ones
+// NaN), a row of zeros without eps infinity (NaN, as 0 / 0 is).
 template <int TPR>
-__device__ __forceinline__ void norm_rotate_row(float (&a)[8], float (&b)[8], int l, bool norm, const float (&wa)[8],
+__device__ __forceinline__ float far_norm_factor(uint64_t (&a2)[4], uint64_t (&b2)[4], int D, float eps, bool far) {
+  float top = sqrtf(eps), x, y;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    unpair(a2[i], x, y);
+    top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
+    unpair(b2[i], x, y);
+    top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
+  }
+#pragma unroll
+  for (int m = 1; m < TPR; m <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, m));
+  const int e = min(126, max(-126, (int)(__float_as_uint(top) >> 23) - 127));
+  const float c = far ? __uint_as_float((unsigned)(127 - e) << 23) : 1.f;
+  uint64_t s2 = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a2[i] = mul2(a2[i], pair(c, c));
+    b2[i] = mul2(b2[i], pair(c, c));
+    s2 = fma2(b2[i], b2[i], fma2(a2[i], a2[i], s2));
+  }
+  unpair(s2, x, y);
+  float ss = x + y;
+#pragma unroll
+  for (int m = 1; m < TPR; m <<= 1) ss += __shfl_xor_sync(kFull, ss, m);
+  const float ms = ss / (float)D + eps * c * c;
+  return ms == INFINITY ? 0.f : ms == 0.f ? INFINITY : norm_factor(ms);
+}
+
+// Norm (norm: with wa, wb the row's weights) and rotation of one row's values.  Rows whose squares leave fp32's range
+// are seen to at once (kAll), or only reported (kNear: true, the row's values mean nothing) and taken again from their
+// input by kFar.  Measured: seen to at once in every row of a pass of queries, the append of 4096 tokens takes 38.8 us,
+// with the second pass behind the rows in flight 37.9 (36.8 without either).
+enum RowRange { kAll, kNear, kFar };
+template <int TPR, RowRange RANGE>
+__device__ __forceinline__ bool norm_rotate_row(float (&a)[8], float (&b)[8], int l, bool norm, const float (&wa)[8],
                                                 const float (&wb)[8], int D, float eps, const float4* cs, int r,
                                                 int interleaved) {
   uint64_t a2[4], b2[4];
+  bool far = false;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     a2[i] = pair(a[2 * i], a[2 * i + 1]);
     b2[i] = pair(b[2 * i], b[2 * i + 1]);
   }
   if (norm) {
-    uint64_t s2 = mul2(a2[0], a2[0]);
+    float rs;
+    if constexpr (RANGE == kFar) {
+      rs = far_norm_factor<TPR>(a2, b2, D, eps, true);
+    } else {
+      uint64_t s2 = mul2(a2[0], a2[0]);
 #pragma unroll
-    for (int i = 1; i < 4; ++i) s2 = fma2(a2[i], a2[i], s2);
+      for (int i = 1; i < 4; ++i) s2 = fma2(a2[i], a2[i], s2);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s2 = fma2(b2[i], b2[i], s2);
-    float ss, s1;
-    unpair(s2, ss, s1);
-    ss += s1;
+      for (int i = 0; i < 4; ++i) s2 = fma2(b2[i], b2[i], s2);
+      float ss, s1;
+      unpair(s2, ss, s1);
+      ss += s1;
 #pragma unroll
-    for (int m = 1; m < TPR; m <<= 1) ss += __shfl_xor_sync(kFull, ss, m);
-    // (one Newton step: rsqrtf's last bit would cost codes at rounding borders)
-    const float ms = ss / (float)D + eps, r0 = rsqrtf(ms);
-    const float rs = isfinite(r0) && ms > 1e-30f ? fmaf(0.5f * r0, fmaf(-ms * r0, r0, 1.f), r0) : r0;
+      for (int m = 1; m < TPR; m <<= 1) ss += __shfl_xor_sync(kFull, ss, m);
+      const float ms = ss / (float)D + eps;
+      rs = norm_factor(ms);
+      far = !(rs > 0.f);
+      if (RANGE == kAll && __any_sync(kFull, far)) {
+        const float other = far_norm_factor<TPR>(a2, b2, D, eps, far);
+        if (far) rs = other;
+      }
+    }
     const uint64_t rs2 = pair(rs, rs);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -204,6 +259,7 @@ __device__ __forceinline__ void norm_rotate_row(float (&a)[8], float (&b)[8], in
       m[3] = z * v.w + w * v.y;
     }
   }
+  return far;
 }
 
 // Position of token j of batch entry b on axis a.
