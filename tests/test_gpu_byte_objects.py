@@ -58,3 +58,20 @@ def test_dropped_cache_lives_until_its_call_ran():
     assert torch.equal(got, want)
     assert all(int(w) == 77 for w in words[:50])
     del other
+
+
+def test_device_error_waits_for_every_stream():
+    tq = _api()
+    c = tq.PagedByteCache(64, 2, 2, 4, 2)
+    x, start, bad = torch.randn(1, 2, 3, 64, device="cuda"), _i32([0]), _i32([[9, 9]])
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(50_000_000)  # some 25 ms
+    c.append(x, x, start, bad, stream=s)
+    assert c.device_error() == tq.binding.TQ_DEVERR_BAD_PAGE
+    # cleared before the call returned: a later call's code, on any stream, is not lost
+    c.append(x, x, start, bad, stream=s)
+    s.synchronize()
+    assert c.device_error() == tq.binding.TQ_DEVERR_BAD_PAGE
+    assert c.device_error() == 0

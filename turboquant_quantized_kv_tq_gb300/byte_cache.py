@@ -166,10 +166,13 @@ class PagedByteCache:
         return self._error
 
     def device_error(self):
-        """The recorded TQ_DEVERR_* code (0: none), cleared by the call.  Waits for the device."""
-        code = int(self.error.item())
+        """The recorded TQ_DEVERR_* code (0: none), cleared by the call.  Waits for the device: calls may have
+        run on any of its streams, and the next may, so the word is read behind all and cleared before the return."""
+        torch.cuda.synchronize(self.device)
+        code = int(self._error.item())
         if code:
-            self.error.zero_()
+            self._error.zero_()
+            torch.cuda.synchronize(self.device)
         return code
 
     def append(self, k, v, start, block_table, count=None, rotary=None, positions=None, k_weight=None, q=None,
