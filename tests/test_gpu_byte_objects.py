@@ -75,3 +75,19 @@ def test_device_error_waits_for_every_stream():
     s.synchronize()
     assert c.device_error() == tq.binding.TQ_DEVERR_BAD_PAGE
     assert c.device_error() == 0
+
+
+def test_out_of_memory_is_torchs():
+    """An output or a workspace that torch cannot allocate is its OutOfMemoryError, as from any torch call."""
+    tq = _api()
+    q = torch.zeros(1, 1 << 18, 8, 128, device="cuda", dtype=torch.bfloat16)  # 512 MB
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (64 << 20)) / total)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            tq.norm_rotate(q)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    tq.norm_rotate(q)
