@@ -3,7 +3,8 @@
 Each translation unit is compiled in parallel with nvcc (CUDA sources) or g++ (host sources),
 then linked into ``turboquant_quantized_kv_tq_gb300/_lib/libtq.so`` with the CUDA runtime linked
 statically.  Beside it goes ``_lib/_tq_torch.so``, the Python extension of ``byte_cache`` (torch
-tensors to the C ABI).  Objects go to ``_build/`` at the repository root.
+tensors to the C ABI), where a torch with CUDA is installed; the library itself does not need torch.
+Objects go to ``_build/`` at the repository root.
 """
 
 import os
@@ -54,11 +55,21 @@ def _compile(src, extra_nvcc=()):
     return src, res.returncode, res.stdout + res.stderr, out
 
 
-def _compile_ext():
+def _torch_dir():
+    """The folder of an installed torch with CUDA, or None."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    path = os.path.dirname(torch.__file__)
+    return path if os.path.exists(os.path.join(path, "lib", "libc10_cuda.so")) else None
+
+
+def _compile_ext(torch_dir):
     import sysconfig
 
     import torch
-    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    inc = os.path.join(torch_dir, "include")
     out = os.path.join(OBJ_DIR, "tq_torch.cpp.o")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            "-I", INCLUDE, "-isystem", inc, "-isystem", os.path.join(_cuda_home(), "include"),
@@ -67,9 +78,8 @@ def _compile_ext():
     return EXT_SRC, res.returncode, res.stdout + res.stderr, out
 
 
-def _link_ext(obj):
-    import torch
-    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+def _link_ext(obj, torch_dir):
+    lib = os.path.join(torch_dir, "lib")
     tmp = EXT_PATH + ".tmp"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", LIB_DIR, "-l:libtq.so", "-Wl,-rpath,$ORIGIN", "-L", lib,
            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
@@ -79,23 +89,25 @@ def _link_ext(obj):
     os.replace(tmp, EXT_PATH)
 
 
+def _checked(result, verbose):
+    src, rc, log, out = result
+    if verbose and log.strip():
+        print(f"[{src}]\n{log}", file=sys.stderr)
+    if rc != 0:
+        raise RuntimeError(f"compiling {src} failed:\n{log}")
+    return out
+
+
 def build(verbose=False, extra_nvcc=()):
-    """Compile every source and link libtq.so; raise RuntimeError on the first failure."""
+    """Compile every source and link libtq.so, then the torch extension; raise RuntimeError on the first failure."""
     os.makedirs(OBJ_DIR, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
     srcs = sources()
+    torch_dir = _torch_dir()
     with ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        ext = ex.submit(_compile_ext)
+        ext = ex.submit(_compile_ext, torch_dir) if torch_dir else None
         results = list(ex.map(lambda s: _compile(s, extra_nvcc), srcs))
-        ext = ext.result()
-    objs = []
-    for src, rc, log, out in results + [ext]:
-        if verbose and log.strip():
-            print(f"[{src}]\n{log}", file=sys.stderr)
-        if rc != 0:
-            raise RuntimeError(f"compiling {src} failed:\n{log}")
-        if out != ext[3]:
-            objs.append(out)
+    objs = [_checked(r, verbose) for r in results]
     cuda = _cuda_home()
     tmp = LIB_PATH + ".tmp"
     cmd = [os.path.join(cuda, "bin", "nvcc"), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
@@ -103,7 +115,13 @@ def build(verbose=False, extra_nvcc=()):
     if res.returncode != 0:
         raise RuntimeError("linking libtq.so failed:\n" + res.stdout + res.stderr)
     os.replace(tmp, LIB_PATH)
-    _link_ext(ext[3])
+    if ext is not None:
+        _link_ext(_checked(ext.result(), verbose), torch_dir)
+    else:
+        if os.path.exists(EXT_PATH):  # (of an earlier build, for another library)
+            os.remove(EXT_PATH)
+        if verbose:
+            print("no torch with CUDA: _tq_torch.so (byte_cache) is not built", file=sys.stderr)
     return LIB_PATH
 
 

@@ -28,7 +28,7 @@ from .binding import check
 def _load_ext():
     path = _build.EXT_PATH
     if not os.path.exists(path):
-        raise ImportError(f"{path} is missing: build the library first "
+        raise ImportError(f"{path} is missing: build the library first, where torch with CUDA is installed "
                           "(python -c 'import __graft_entry__ as g; g.build()')")
     loader = importlib.machinery.ExtensionFileLoader("_tq_torch", path)
     mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_tq_torch", loader))
