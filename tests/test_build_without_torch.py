@@ -37,3 +37,34 @@ assert not os.path.exists(m.EXT_PATH), "an extension that this build did not mak
 def test_library_builds_without_torch(tmp_path, torch):
     res = subprocess.run([sys.executable, "-c", BUILD, torch, str(tmp_path)], cwd=ROOT, capture_output=True, text=True)
     assert res.returncode == 0, res.stderr
+
+
+UNBUILT = """
+import importlib.util, sys
+spec = importlib.util.spec_from_file_location("turboquant_quantized_kv_tq_gb300._build", "turboquant_quantized_kv_tq_gb300/_build.py")
+m = importlib.util.module_from_spec(spec)
+spec.loader.exec_module(m)
+m.EXT_PATH = "not/built"
+sys.modules[spec.name] = m
+"""
+
+
+@pytest.mark.parametrize("first,names", [("import sys; sys.modules['torch'] = None\n", False), (UNBUILT, False), ("", True)],
+                         ids=["no torch", "not built", "all"])
+def test_star_import(first, names):
+    """`import *` takes what is there: everything where the torch extension is built, the rest as ever without it."""
+    if names:
+        pytest.importorskip("torch")
+    code = first + ("from turboquant_quantized_kv_tq_gb300 import *\n"
+                    "assert QuantizedKVCache and PagedKVCache and TQError and binding\n"
+                    f"assert all((n in globals()) == {names} for n in ('PagedByteCache', 'Rotary', 'norm_rotate'))\n")
+    res = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr
+
+
+def test_names_are_there_by_name():
+    pytest.importorskip("torch")
+    import turboquant_quantized_kv_tq_gb300 as tq
+    assert {"PagedByteCache", "Rotary", "norm_rotate"} <= set(tq.__all__) and tq.PagedByteCache and tq.Rotary and tq.norm_rotate
+    with pytest.raises(AttributeError):
+        tq.no_such_name

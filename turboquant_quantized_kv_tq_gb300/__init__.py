@@ -7,12 +7,20 @@ tensors to those entry points.  There is no CPU fallback: without the built libr
 fails.
 """
 
+import importlib.util
+import os
+
 import numpy as np
 
+from . import _build
 from . import binding as _b
 from .binding import TQError, check  # noqa: F401
 
-__all__ = ["QuantizedKVCache", "PagedKVCache", "PagedByteCache", "Rotary", "norm_rotate", "TQError", "binding"]
+_TORCH_NAMES = ["PagedByteCache", "Rotary", "norm_rotate"]  # of byte_cache, which needs torch and its extension
+
+__all__ = ["QuantizedKVCache", "PagedKVCache", "TQError", "binding"]
+if os.path.exists(_build.EXT_PATH) and importlib.util.find_spec("torch") is not None:
+    __all__ += _TORCH_NAMES
 
 _DTYPES = None
 
@@ -274,7 +282,7 @@ def _torch():
 
 def __getattr__(name):
     # (torch is imported with the first use, as for the classes above)
-    if name in ("PagedByteCache", "Rotary", "norm_rotate"):
+    if name in _TORCH_NAMES:
         from . import byte_cache
         globals()[name] = value = getattr(byte_cache, name)
         return value
