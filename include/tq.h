@@ -392,7 +392,7 @@ tq_status tq_rotary_table(int32_t rotary_dim, const double* freqs, const int32_t
  * contiguous [batch][n][q heads][head_dim] (as the attention calls read queries), k_out
  * contiguous [batch][k heads][n][head_dim] (as the appends read keys), both of out_dtype: dtype
  * or TQ_F32.  An output may be its own input's buffer when the layouts and types are the same; any
- * other overlap with an input is refused.
+ * other overlap with an input, or of the outputs, is refused.
  * dev_positions: device int32 [num_axes][batch][n]; NULL: token j of entry b is at dev_start[b] + j
  * on every axis (device int32 [batch]; NULL: 0).  head_dim 64, 128, 256 or 512. */
 tq_status tq_norm_rotate(int32_t head_dim, tq_dtype dtype, tq_dtype out_dtype, int32_t batch, int32_t n,
@@ -436,7 +436,8 @@ size_t tq_byte_pool_bytes(const tq_byte_config* cfg, int32_t num_pages);
  * (none when negative); NULL: all n.  q (NULL: none): n tokens of queries per entry, normed
  * (q_weight) and rotated with the same positions in the same launch into q_out, contiguous
  * [batch][n][num_q_heads][head_dim] of dtype; all n rows of q are written whatever dev_count says.
- * q_out may be q's buffer when q is contiguous.  A block's held tokens are those before dev_start[b]; bytes of positions behind the appended
+ * q_out may be q's buffer when q is contiguous; k, v, q and q_out lie outside the pool.  A block's
+ * held tokens are those before dev_start[b]; bytes of positions behind the appended
  * tokens stay as they are.  A page that receives tokens must belong to one sequence.  Bad pages
  * and positions: see tq_page_table.  dev_error: device int32 or NULL; receives a TQ_DEVERR_* code
  * (the caller zeroes it beforehand).  n = 0 is a no-op. */
@@ -454,7 +455,8 @@ tq_status tq_byte_append_paged(const tq_byte_config* cfg, void* dev_pool, const 
  * or NULL (nq): entry b has c = min(dev_count[b], nq) queries, its last c positions.  Query i < c
  * attends to the first dev_seq_len[b] - c + 1 + i tokens (none when that is <= 0: output zeros);
  * rows i >= c are written as zeros.  scale multiplies the scores (1 / sqrt(head_dim) in most
- * models).  What the pool holds behind a sequence's last token is never used; out must not overlap q.
+ * models).  What the pool holds behind a sequence's last token is never used; q, out, ws and the
+ * pool must not overlap.
  * Scores, softmax statistics and accumulators are fp32.  fp32 queries and their probabilities enter the
  * matrix products as fp16 hi + lo terms.  bf16 and fp16 queries enter as fp16 under a power-of-two scale
  * per row, or, in chunks of more than 64 rows (queries times heads per KV head) at head_dim 128, as two or

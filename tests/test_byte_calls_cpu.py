@@ -63,3 +63,47 @@ def test_a_call_on_a_stream_of_another_device_is_refused(monkeypatch):
     with pytest.raises(ValueError):
         m.norm_rotate(x, rotary=rot, stream=_Stream())
     assert not x.streams and not rot._table.streams and not m._c.seen
+
+
+# ---- buffers over buffers (made-up addresses: a refused call touches none of them)
+
+P = 1 << 24           # the pool: 9 x 2 blocks of 4128 bytes
+A, B, C, OUT, WS = (P + (i << 20) for i in range(1, 6))
+POOL_END = P + 9 * 2 * 4128
+
+
+def _bind():
+    return pytest.importorskip("turboquant_quantized_kv_tq_gb300.binding")
+
+
+def _rows(b, heads, data, n=3, d=128):
+    return b.tq_heads(data, n * heads * d, heads * d, d, heads)
+
+
+@pytest.mark.parametrize("kw", [dict(k=P), dict(v=POOL_END - 16), dict(q=P + 4096), dict(qo=P), dict(qo=POOL_END - 256),
+                                dict(qo=P - 6144 + 16)])
+def test_append_refuses_buffers_in_the_pool(kw):
+    b = _bind()
+    at = dict(dict(k=A, v=B, q=C, qo=OUT), **kw)
+    st = b.tq_byte_append_paged(b.tq_byte_config(128, 8, 2), P, b.tq_page_table(WS, 4, 8), 1, 3, b.TQ_BF16, _rows(b, 2, at["k"]),
+                                _rows(b, 2, at["v"]), WS, None, None, 1e-6, None, None, _rows(b, 8, at["q"]), None, at["qo"], None, None)
+    assert st == b.TQ_ERR_INVALID_ARG and b"pool" in b.tq_last_error()
+
+
+@pytest.mark.parametrize("kw,word", [(dict(out=P), b"pool"), (dict(out=POOL_END - 32), b"pool"), (dict(ws=P), b"pool"),
+                                     (dict(ws=P - 256), b"pool"), (dict(out=WS + 1024), b"ws"), (dict(ws=A), b"ws"),
+                                     (dict(ws=A - 256), b"ws"), (dict(q=P), b"pool")])
+def test_attention_refuses_buffers_over_each_other(kw, word):
+    b = _bind()
+    at = dict(dict(q=A, out=OUT, ws=WS), **kw)
+    cfg, pt = b.tq_byte_config(128, 8, 2), b.tq_page_table(C, 4, 8)
+    need = b.tq_byte_attention_workspace_bytes(cfg, pt, 1, 3, b.TQ_BF16)
+    st = b.tq_byte_attention_paged(cfg, P, pt, 1, 3, b.TQ_BF16, _rows(b, 8, at["q"]), C, None, 0.1, at["out"], at["ws"], need, None, None)
+    assert st == b.TQ_ERR_INVALID_ARG and word in b.tq_last_error()
+
+
+@pytest.mark.parametrize("ko", [OUT, OUT + 6144 - 16, OUT - 1536 + 16])
+def test_norm_rotate_refuses_outputs_over_each_other(ko):
+    b = _bind()
+    st = b.tq_norm_rotate(128, b.TQ_BF16, b.TQ_BF16, 1, 3, _rows(b, 8, A), None, OUT, _rows(b, 2, B), None, ko, 1e-6, None, None, None, None)
+    assert st == b.TQ_ERR_INVALID_ARG and b"outputs" in b.tq_last_error()

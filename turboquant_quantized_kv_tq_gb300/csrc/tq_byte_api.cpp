@@ -51,12 +51,16 @@ Span span_of(const Rows& x, int batch, int n, int d, int bytes) {
   return {(uintptr_t)x.p, (uintptr_t)x.p + (uintptr_t)last * bytes};
 }
 bool overlap(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
+Span span_of(const void* p, size_t bytes) { return {(uintptr_t)p, (uintptr_t)p + bytes}; }
+// Contiguous output rows.
+Span span_of(const void* out, int batch, int n, int heads, int d, int bytes) {
+  return span_of(out, (size_t)batch * n * heads * d * bytes);
+}
 
 // Whether an output of `heads` heads ([batch][n][heads][d], or [batch][heads][n][d] of keys) may be written
 // while x is read: apart, or (same) exactly x's own rows, each of which is read before it is written.
 bool may_write(const void* out, int heads, bool keys, const Rows& x, bool same, int batch, int n, int d, int bytes, int out_bytes) {
-  const Span o = {(uintptr_t)out, (uintptr_t)out + (uintptr_t)batch * n * heads * d * out_bytes};
-  if (!overlap(o, span_of(x, batch, n, d, bytes))) return true;
+  if (!overlap(span_of(out, batch, n, heads, d, out_bytes), span_of(x, batch, n, d, bytes))) return true;
   const long long st = keys ? d : (long long)heads * d, sh = keys ? (long long)n * d : d, sb = (long long)n * heads * d;
   return same && out == x.p && out_bytes == bytes && (batch == 1 || x.sb == sb) && (n == 1 || x.st == st) &&
          (heads == 1 || x.sh == sh);
@@ -173,6 +177,8 @@ tq_status tq_norm_rotate(int32_t head_dim, tq_dtype dtype, tq_dtype out_dtype, i
              !may_write(k_out, a.k.heads, true, a.q, false, batch, n, head_dim, in, ob))))
     return fail(TQ_ERR_INVALID_ARG, "an output overlaps an input and is not its own buffer in the same layout");
   if (n == 0) return TQ_OK;
+  if (q && k && overlap(span_of(q_out, batch, n, a.q.heads, head_dim, ob), span_of(k_out, batch, n, a.k.heads, head_dim, ob)))
+    return fail(TQ_ERR_INVALID_ARG, "the outputs overlap");
   a.d = head_dim;
   a.B = batch;
   a.n = n;
@@ -223,6 +229,11 @@ tq_status tq_byte_append_paged(const tq_byte_config* cfg, void* dev_pool, const 
             !may_write(q_out, cfg->num_q_heads, false, a.v, false, batch, n, cfg->head_dim, bytes, bytes)))
     return fail(TQ_ERR_INVALID_ARG, "q_out overlaps an input and is not q's own buffer in the same layout");
   if (n == 0) return TQ_OK;
+  const Span pool = span_of(dev_pool, tq_byte_pool_bytes(cfg, pages->num_pages));
+  const int d = cfg->head_dim;
+  if (overlap(pool, span_of(a.k, batch, n, d, bytes)) || overlap(pool, span_of(a.v, batch, n, d, bytes)) ||
+      (q && (overlap(pool, span_of(a.q, batch, n, d, bytes)) || overlap(pool, span_of(q_out, batch, n, cfg->num_q_heads, d, bytes)))))
+    return fail(TQ_ERR_INVALID_ARG, "k, v, q and q_out must not overlap the pool");
   a.d = cfg->head_dim;
   a.B = batch;
   a.n = n;
@@ -271,8 +282,12 @@ tq_status tq_byte_attention_paged(const tq_byte_config* cfg, const void* dev_poo
   if (!may_write(out, cfg->num_q_heads, false, a.q, false, batch, nq, cfg->head_dim, bytes, bytes))
     return fail(TQ_ERR_INVALID_ARG, "out must not overlap q");
   if (!std::isfinite(scale)) return fail(TQ_ERR_INVALID_ARG, "scale must be finite");
-  if (ws_bytes < byte_attention_workspace(cfg->head_dim, batch, nq, cfg->num_q_heads, cfg->num_kv_heads, dtype))
-    return fail(TQ_ERR_WORKSPACE, "workspace too small");
+  const size_t need = byte_attention_workspace(cfg->head_dim, batch, nq, cfg->num_q_heads, cfg->num_kv_heads, dtype);
+  if (ws_bytes < need) return fail(TQ_ERR_WORKSPACE, "workspace too small");
+  const Span pool = span_of(dev_pool, tq_byte_pool_bytes(cfg, pages->num_pages)), w = span_of(ws, need);
+  const Span o = span_of(out, batch, nq, cfg->num_q_heads, cfg->head_dim, bytes), x = span_of(a.q, batch, nq, cfg->head_dim, bytes);
+  if (overlap(pool, o) || overlap(pool, w) || overlap(pool, x)) return fail(TQ_ERR_INVALID_ARG, "q, out and ws must not overlap the pool");
+  if (overlap(w, o) || overlap(w, x)) return fail(TQ_ERR_INVALID_ARG, "ws must not overlap q or out");
   a.d = cfg->head_dim;
   a.B = batch;
   a.nq = nq;
