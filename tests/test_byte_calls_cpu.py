@@ -107,3 +107,26 @@ def test_norm_rotate_refuses_outputs_over_each_other(ko):
     b = _bind()
     st = b.tq_norm_rotate(128, b.TQ_BF16, b.TQ_BF16, 1, 3, _rows(b, 8, A), None, OUT, _rows(b, 2, B), None, ko, 1e-6, None, None, None, None)
     assert st == b.TQ_ERR_INVALID_ARG and b"outputs" in b.tq_last_error()
+
+
+# ---- inputs
+
+def test_inputs_that_require_a_gradient_are_refused():
+    """The calls compute no gradients: they say so instead of returning tensors without a graph."""
+    from turboquant_quantized_kv_tq_gb300 import PagedByteCache
+    c = PagedByteCache(64, 2, 2, 4, 2, device="cpu")
+    x, start, table = torch.zeros(1, 2, 3, 64), torch.zeros(1, dtype=torch.int32), torch.zeros(1, 2, dtype=torch.int32)
+    q, w = torch.zeros(1, 3, 2, 64), torch.ones(64)
+
+    def grad(t):
+        return t.clone().requires_grad_()
+
+    calls = [lambda: c.append(grad(x), x, start, table), lambda: c.append(x, grad(x), start, table),
+             lambda: c.append(x, x, start, table, k_weight=grad(w)), lambda: c.append(x, x, start, table, q=grad(q)),
+             lambda: c.append(x, x, start, table, q=q, q_weight=grad(w)),
+             lambda: c.attention(grad(q), start, table), lambda: c.attention(grad(q[:, 0]), start, table)]
+    for call in calls:
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA device"):  # (what stops it here)
+            call()

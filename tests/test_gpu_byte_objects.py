@@ -91,3 +91,20 @@ def test_out_of_memory_is_torchs():
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
     tq.norm_rotate(q)
+
+
+def test_norm_rotate_refuses_inputs_that_require_a_gradient():
+    tq = _api()
+    x, w = torch.randn(1, 3, 2, 64, device="cuda"), torch.ones(64, device="cuda")
+    want = tq.norm_rotate(x, q_weight=w)[0]
+    x.requires_grad_()
+    with pytest.raises(ValueError, match="gradient"):
+        tq.norm_rotate(x, q_weight=w)
+    with pytest.raises(ValueError, match="gradient"):
+        tq.norm_rotate(None, x.transpose(1, 2))
+    with pytest.raises(ValueError, match="gradient"):
+        tq.norm_rotate(x.detach(), q_weight=w.requires_grad_())
+    with torch.no_grad():
+        assert torch.equal(tq.norm_rotate(x, q_weight=w)[0], want)
+    with torch.inference_mode():
+        assert torch.equal(tq.norm_rotate(x, q_weight=w)[0], want)

@@ -7,6 +7,8 @@ and side.  Tensors may be strided views (a fused projection's slices): only the 
 be contiguous, with rows on 16-byte boundaries.  Nothing is copied or converted here; a layout that
 the kernels do not take is refused.
 
+The calls compute no gradients: while grad mode is on, inputs that require one are refused.
+
 Calls launch on the current stream of the tensors' device, or on ``stream``.  A call given ``stream``
 does not wait for other streams, but holds the memory that it uses, the objects' own included, until
 that stream is done with it.  Under ``torch.cuda.stream`` torch's rule for tensors made on another

@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -60,6 +61,12 @@ void same_kind(const at::Tensor& t, const char* name, at::ScalarType dt, int dev
                   c10::toString(t.scalar_type()) + " on " + t.device().str());
 }
 
+// An input or output of numbers: no gradient passes through the calls.
+void plain(const at::Tensor& t, const char* name) {
+  if (t.requires_grad() && at::GradMode::is_enabled())
+    throw Refused(std::string(name) + " requires a gradient, which is not computed here: call under torch.no_grad(), or detach it");
+}
+
 void has_shape(const at::Tensor& t, const char* name, at::IntArrayRef shape) {
   if (t.sizes() != shape) {
     std::string want = "[";
@@ -71,6 +78,7 @@ void has_shape(const at::Tensor& t, const char* name, at::IntArrayRef shape) {
 // Rows of a 4-d view whose dims b, n, h are batch, token and head.
 tq_heads heads(const at::Tensor& t, const char* name, at::IntArrayRef shape, at::ScalarType dt, int device, int b, int n, int h) {
   same_kind(t, name, dt, device);
+  plain(t, name);
   has_shape(t, name, shape);
   if (t.stride(3) != 1 && t.size(3) > 1) throw Refused(std::string(name) + ": the head dimension must be contiguous");
   return tq_heads{t.const_data_ptr(), t.stride(b), t.stride(n), t.stride(h), (int32_t)t.size(h)};
@@ -89,6 +97,7 @@ const void* weight(PyObject* o, const char* name, int64_t d, at::ScalarType dt, 
   if (!given(o)) return nullptr;
   const at::Tensor& t = tensor(o, name);
   same_kind(t, name, dt, device);
+  plain(t, name);
   has_shape(t, name, {d});
   if (!t.is_contiguous()) throw Refused(std::string(name) + " must be contiguous");
   return t.const_data_ptr();
@@ -99,6 +108,7 @@ at::Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, at::Scal
   if (!given(o)) return at::empty(shape, at::TensorOptions().dtype(dt).device(c10::Device(c10::kCUDA, (c10::DeviceIndex)device)));
   const at::Tensor& t = tensor(o, name);
   same_kind(t, name, dt, device);
+  plain(t, name);
   has_shape(t, name, shape);
   if (!t.is_contiguous()) throw Refused(std::string(name) + " must be contiguous");
   return t;
@@ -288,6 +298,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     tq_heads qh;
     if (q.dim() == 3) {  // one query per entry
       same_kind(q, "q", dt, c.device);
+      plain(q, "q");
       has_shape(q, "q", {B, c.cfg.num_q_heads, d});
       if (q.stride(2) != 1) throw Refused("q: the head dimension must be contiguous");
       qh = tq_heads{q.const_data_ptr(), q.stride(0), 0, q.stride(1), c.cfg.num_q_heads};
