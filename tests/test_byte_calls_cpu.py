@@ -130,3 +130,12 @@ def test_inputs_that_require_a_gradient_are_refused():
             call()
         with torch.no_grad(), pytest.raises(ValueError, match="CUDA device"):  # (what stops it here)
             call()
+
+
+def test_negated_views_are_refused():
+    """A view whose negation is pending (torch.imag of a conjugate) holds other numbers in memory than it stands for."""
+    from turboquant_quantized_kv_tq_gb300 import PagedByteCache
+    c = PagedByteCache(64, 2, 2, 4, 2, device="cpu")
+    q = torch._neg_view(torch.ones(1, 2, 64))
+    with pytest.raises(ValueError, match="negat"):
+        c.attention(q, torch.zeros(1, dtype=torch.int32), torch.zeros(1, 2, dtype=torch.int32))

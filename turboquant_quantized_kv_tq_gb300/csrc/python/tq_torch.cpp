@@ -61,10 +61,11 @@ void same_kind(const at::Tensor& t, const char* name, at::ScalarType dt, int dev
                   c10::toString(t.scalar_type()) + " on " + t.device().str());
 }
 
-// An input or output of numbers: no gradient passes through the calls.
+// An input or output of numbers: no gradient passes through the calls, and memory is read as it is.
 void plain(const at::Tensor& t, const char* name) {
   if (t.requires_grad() && at::GradMode::is_enabled())
     throw Refused(std::string(name) + " requires a gradient, which is not computed here: call under torch.no_grad(), or detach it");
+  if (t.is_neg()) throw Refused(std::string(name) + " is a view with a pending negation: resolve_neg() it");
 }
 
 void has_shape(const at::Tensor& t, const char* name, at::IntArrayRef shape) {
