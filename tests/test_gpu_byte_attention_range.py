@@ -83,3 +83,34 @@ def test_fp32_keeps_its_bits(d, hq, hkv, nq, outlier):
     assert tol <= 1.5e-5
     err = np.linalg.norm(out - want) / np.linalg.norm(want)
     assert err <= tol, (err, tol)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_whole_prompts(dtype):
+    """Prompts of thousands of queries in one call (64 row groups), of unlike lengths."""
+    lens, count, nq, d = [4096, 5000, 130], [4096, 3333, 130], 4096, 128
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    k, v = (torch.randn(3, 1, 5000, d, generator=g, device="cuda").to(DT[dtype]) for _ in range(2))
+    c, table, pool = _filled(d, 4, 1, lens, k, v)
+    q = torch.randn(3, nq, 4, d, generator=g, device="cuda").to(DT[dtype])
+    out = c.attention(q, _i32(lens), _i32(table), count=_i32(count))
+    assert torch.equal(out, c.attention(q, _i32(lens), _i32(table), count=_i32(count)))
+    assert c.device_error() == 0
+    half = torch.finfo(DT[dtype]).eps / 2
+    for b in range(3):
+        assert not out[b, count[b]:].any()
+        K, V = (torch.from_numpy(pool.read(s, 0, table[b][:(lens[b] + 15) // 16], lens[b])).cuda() for s in (0, 1))
+        for i0 in range(0, count[b], 512):
+            m = min(512, count[b] - i0)
+            x = q[b, i0:i0 + m].double().transpose(0, 1)                                  # [4][m][d]
+            limit = lens[b] - count[b] + 1 + i0 + torch.arange(m, device="cuda")
+            s = (x @ K.T * d ** -0.5).masked_fill_(torch.arange(lens[b], device="cuda") >= limit[:, None], -np.inf)
+            p = torch.softmax(s, -1)
+            want, spread = p @ V, p @ V.abs()
+            reach = (x.abs() @ K.abs().T).amax(-1, keepdim=True) * d ** -0.5
+            # as for the smaller chunks: weights rounded to fp16, twice the scores' error, sums; the output's own step
+            score = (d + lens[b] / 16 + 64) * 2.0 ** -22 * (1 + reach)
+            tol = spread * (2.0 ** -11 + 2 * score + (lens[b] / 16 + 64) * 2.0 ** -23) + want.abs() * half + 2.0 ** -24
+            got = out[b, i0:i0 + m].double().transpose(0, 1)
+            assert bool(((got - want).abs() <= tol).all()), (b, i0)

@@ -108,3 +108,33 @@ def test_norm_rotate_refuses_inputs_that_require_a_gradient():
         assert torch.equal(tq.norm_rotate(x, q_weight=w)[0], want)
     with torch.inference_mode():
         assert torch.equal(tq.norm_rotate(x, q_weight=w)[0], want)
+
+
+def test_captured_calls_with_a_stream():
+    """Calls given the capturing stream, in two graphs of the same objects, which go once the graphs are done."""
+    tq = _api()
+    rot, c = tq.Rotary(128), tq.PagedByteCache(128, 4, 2, 3, 3)
+    x = torch.randn(1, 1, 8, 128, device="cuda")
+    start, seq, table = _i32([0]), _i32([1]), _i32([[2, 0, 1]])
+
+    def step(stream=None):
+        q = c.append(x[:, :, 4:6].transpose(1, 2), x[:, :, 6:].transpose(1, 2), start, table, rotary=rot, q=x[:, :, :4], stream=stream)
+        return c.attention(q, seq, table, stream=stream)
+
+    want = step()
+    c.pool.zero_()
+    graphs = []
+    torch.cuda.synchronize()
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = step(torch.cuda.current_stream())
+        graphs.append((g, out))
+    for g, out in graphs:
+        g.replay()
+        assert torch.equal(out, want)
+    assert c.device_error() == 0
+    graphs[0][0].replay()
+    torch.cuda.synchronize()
+    del c, rot, graphs
+    assert torch.ones(8, device="cuda").sum() == 8
