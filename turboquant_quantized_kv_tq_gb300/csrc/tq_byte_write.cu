@@ -121,15 +121,16 @@ __device__ __forceinline__ void rows_pass(const Rows& X, const TokenAt* tok, con
         store8(dst + 8 * ca, a);
         store8(dst + 8 * cb, b);
       }
-      if (live && far) again |= 1u << u;
+      if (far) again |= 1u << u;
     }
     if (__any_sync(kFull, again)) {  // (indexes and weights once more: nothing of this is held through the loop)
       float va[8], vb[8];
       load_weight<T>(w, ca, cb, va, vb);
 #pragma unroll 1
       for (int u = 0; u < kU; ++u) {
-        const bool mine = again >> u & 1;
-        const int row = base + u * RPP + row0, tk1 = mine ? row / nh : 0, h1 = h0 + row - row / nh * nh;
+        const int row = base + u * RPP + row0;
+        const bool mine = (again >> u & 1) && row < total;
+        const int tk1 = mine ? row / nh : 0, h1 = h0 + row - row / nh * nh;
         Raw8<T> xa = {}, xb = {};
         if (mine) {  // (not stored yet, also where the output is the input's buffer)
           const T* src = reinterpret_cast<const T*>(X.p) + tok[tk1].src + h1 * X.sh;

@@ -146,11 +146,11 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// 1 / sqrt(ms) for 2^-128 < ms < infinity (one Newton step: rsqrtf's last bit would cost codes at rounding borders);
-// not positive elsewhere: NaN, or -infinity where r * r overflows.  Squares that fell below 2^-126 are off by 2^-150
-// each, so the mean of a row of them by 2^-22 at most.
+// 1 / sqrt(ms) for 2^-126 <= ms < infinity (one Newton step: the approximation's last bit would cost codes at rounding
+// borders); NaN elsewhere (below 2^-126 the approximation flushes to 1 / 0).
 __device__ __forceinline__ float norm_factor(float ms) {
-  const float r = rsqrtf(ms);
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(ms));
   return fmaf(0.5f * r, fmaf(-ms, r * r, 1.f), r);
 }
 
@@ -189,8 +189,9 @@ __device__ __forceinline__ float far_norm_factor(uint64_t (&a2)[4], uint64_t (&b
 
 // Norm (norm: with wa, wb the row's weights) and rotation of one row's values.  Rows whose squares leave fp32's range
 // are seen to at once (kAll), or only reported (kNear: true, the row's values mean nothing) and taken again from their
-// input by kFar.  Measured: seen to at once in every row of a pass of queries, the append of 4096 tokens takes 38.8 us,
-// with the second pass behind the rows in flight 37.9 (36.8 without either).
+// input by kFar.  Measured: seen to at once in every row of a pass of queries, the append of 4096 tokens takes 38.5 us,
+// with the second pass behind the rows in flight 37.4 (36.8 without either; the code of two kinds of block is more than
+// the instruction cache holds).
 enum RowRange { kAll, kNear, kFar };
 template <int TPR, RowRange RANGE>
 __device__ __forceinline__ bool norm_rotate_row(float (&a)[8], float (&b)[8], int l, bool norm, const float (&wa)[8],
