@@ -9,13 +9,14 @@
 // copies: a block of the pool is contiguous, codes and scales in one copy.  Warps meet only at the end of
 // a slab's range.  Ranges that cover part of a slab leave (M, l, O) in the workspace for join_kernel,
 // which is launched early and waits for this grid.
-// Measured: 8 x 32768 tokens, 32 / 8 heads, bf16, 97 us, 5.55 TB/s (0.82 of the measured copy rate); fp32
+// Measured: 8 x 32768 tokens, 32 / 8 heads, bf16, 98 us, 5.51 TB/s (0.81 of the measured copy rate); fp32
 // queries 97 us; 131072 tokens of 64 / 8 heads 56 us; 16 x 16384 tokens with 16 rows 110 us; 1024 tokens
 // 10 us.  Of the first's 18 us above its floor some 5 pass before the tiles flow (lengths, plan, page
 // table, first copies), 3 in the join, and the rest at the end: SMs differ by up to a fifth in what they
 // stream (groups of 10 to 20 neighbours), and the fast ones idle.
 // rows_kernel: 8 warps of 8 NR rows share one ring; each tile is read once per 64 NR rows.  Bound by the
-// mma.sync rate and the conversions, which every warp repeats: 110 TFLOP/s (fp32, d = 64).
+// mma.sync rate and the conversions, which every warp repeats: 107 TFLOP/s (fp32, d = 64), 148 (16 bits, d = 64),
+// 193 (d = 256).  It does not split the tokens: with few slabs it leaves SMs idle (see use_rows).
 #include <atomic>
 #include <string>
 
@@ -493,7 +494,10 @@ cudaError_t rows_go(AttnParams p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// More row groups than this read the pool too often: the rows kernel takes them.
+// From five row groups on the rows kernel takes a call, because the split reads the pool once per group.  That is
+// right for grids that fill the GPU and many rows (32 / 8 heads, fp32, d = 128, 8 x 16384 tokens: 256 rows, split 1238 us,
+// rows kernel 1120), and wrong below: 80 rows of the same 399 and 1119 us; one sequence of 131072 tokens 380 and 8821 us;
+// at d = 256 40 rows of one such sequence 404 and 5701 us.  The rule does not look at the grid.
 bool use_rows(int groups) { return groups > 4; }
 
 template <int D, int TERMS, typename T>

@@ -329,6 +329,10 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(f
 int sm_count(int* device);
 cudaError_t allow_smem(const void* kernel, int bytes, int device, std::atomic<uint64_t>& done);
 // The tensor-memory kernel (tq_byte_tc.cu): whether it takes a call, its workspace, its launch.
+// It takes more than kTcMinRows rows: one pass over the pool, where the split makes one per 16 rows.  Both sides (us, 32 / 8
+// heads, bf16, split / tensor memory), 16 x 16384 tokens: 16 rows 110 / 175, 32 rows 204 / 176, 64 rows 388 / 177, 80 rows
+// 484 / 179; one sequence of 131072: 65 / 95, 107 / 95, 192 / 95, 235 / 96.  So above 16 rows it is the faster one already;
+// the split, which it would replace there, keeps more bits of the queries (2^-39 instead of 2^-18 of a row's largest).
 constexpr int kMaxSms = 160;
 constexpr int kTcMinRows = 64;
 bool tc_takes(const AttnArgs& a);

@@ -25,9 +25,10 @@
 // gives registers to the rows: 192 a thread there, so that a row's 128 scores stay in registers from
 // the maximum to the probabilities, and 64 in the other warps).
 //
-// Measured: 512 queries of 32 heads over 4 x 32768 tokens (8 KV heads, bf16) 788 us, 1384 TFLOP/s, 0.72 of
+// Measured: 512 queries of 32 heads over 4 x 32768 tokens (8 KV heads, bf16) 787 us, 1386 TFLOP/s, 0.72 of
 // the measured bf16 burst rate (0.81 of the sustained one: the run is at the power cap); fp16 (three
-// query terms) 841 us; the last 64 positions 121 us.  A tile takes about 2850 cycles, 2048 of them MMA.
+// query terms) 841 us; the last 64 positions 120 us; a prompt of
+// 4096 tokens (one sequence) 203 us, of 32768 6.9 ms, 1270 TFLOP/s.  A tile takes about 2850 cycles, 2048 of them MMA.
 // What bounds it is the chain of a row tile -- 128 scores to P, P V, the next scores -- beside the other
 // tile's, and shared memory: an fp8 product of N = 128 reads 8 KB in its 64 cycles, all that it delivers.
 // Tiles of 80 tokens, whose P has columns of its own so that scores run ahead, were slower (1480 us): at

@@ -5,15 +5,15 @@
 // the chain position -> angle -> row for single tokens.  A block of 256 threads takes a few tokens
 // and all their heads, so a token's sines are computed once for its 2 * heads rows; three blocks an SM
 // with three rows in flight per thread carry the latency.  Measured: 4096 tokens of 64 + 8 heads, d = 128,
-// bf16, 31 us, 4.9 TB/s of the 6.8 of a copy (a copy of this size: 24 us); 56 % of issue slots, so the
+// bf16, 31 us, 4.9 TB/s of the 6.8 of a copy (a copy of this size: 24 us); 57 % of issue slots, so the
 // arithmetic (packed fp32) is the next bound; one token of 8 sequences 2.6 us.
 //
 // byte_append gives each warp one side of one 16-token block of one KV head: it reads the block's
 // new rows, rotates keys, finds the block's scale with a warp maximum, and writes the codes; held
 // codes are rounded to a raised scale by the same warp, so a block has one writer.  The queries of
-// the step ride along as further blocks of the grid.  Measured: 4096 tokens of 64 + 8 heads 35 us (15 us
-// without the queries: a chain of dependent loads in 514 blocks; a copy of all bytes takes 25 us); one
-// token of 8 sequences 5.8 us.
+// the step ride along as further blocks of the grid.  Measured: 4096 tokens of 64 + 8 heads 37 us (17 us
+// without the queries: a chain of dependent loads in 514 blocks; a copy of all bytes takes 25 us; warps also
+// wait for instructions, the code of both kinds of block being live at once); one token of 8 sequences 5.8 us.
 #include <string>
 
 #include "tq_byte_attn.cuh"
@@ -194,8 +194,8 @@ struct AppendParams {
   int groups;      // head groups of 4
   int kv_blocks;   // B * blocks * groups; the other grid blocks take queries
   int every;       // grid block i * every is kv block i: the append's blocks wait on memory in long
-                   // chains, so they are spread among the queries' (4096 tokens of 64 + 8 heads: 15 us
-                   // and 25 us each kind alone, 35 us so, 43 us one kind after the other)
+                   // chains, so they are spread among the queries' (4096 tokens of 64 + 8 heads: 17 us
+                   // and 26 us each kind alone, 37 us so)
   int per, tokens, q_split, q_groups;
 };
 
