@@ -139,3 +139,42 @@ def test_negated_views_are_refused():
     q = torch._neg_view(torch.ones(1, 2, 64))
     with pytest.raises(ValueError, match="negat"):
         c.attention(q, torch.zeros(1, dtype=torch.int32), torch.zeros(1, 2, dtype=torch.int32))
+
+
+# ---- copies of the objects
+
+@pytest.mark.parametrize("how", ["copy", "deepcopy", "pickle"])
+def test_copies_use_their_own_memory(monkeypatch, how):
+    """A copied (or saved and loaded) object's calls reach the copy's tensors, not those it was copied from: a model
+    that holds a Rotary is copied as a whole, and the first may be gone."""
+    import copy
+    import pickle
+    m = _calls(monkeypatch)
+    make = {"copy": copy.copy, "deepcopy": copy.deepcopy, "pickle": lambda x: pickle.loads(pickle.dumps(x))}[how]
+
+    def address(x):
+        return x.data_ptr() if isinstance(x, torch.Tensor) else x
+
+    rot, cache = m.Rotary(64, device="cpu"), m.PagedByteCache(64, 2, 2, 4, 2, device="cpu")
+    cache.pool.fill_(7)
+    r, c = make(rot), make(cache)
+    assert (r._table.data_ptr() == rot._table.data_ptr()) == (how == "copy")
+    assert torch.equal(c.pool, cache.pool) and torch.equal(r._table, rot._table)
+    m._c.seen.clear()
+    c.append(None, None, None, None, rotary=r)
+    c.attention(None, None, None)
+    m.norm_rotate(torch.zeros(1), rotary=r)
+    (_, app), (_, att), (_, nr) = m._c.seen
+    for args in (app[0], att[0]):
+        assert {c.pool.data_ptr(), c.error.data_ptr()} <= {address(x) for x in args}
+    for args in (app[6], nr[2]):
+        assert address(args[0]) == r._table.data_ptr()
+
+
+def test_resized_pools_are_refused():
+    from turboquant_quantized_kv_tq_gb300 import PagedByteCache
+    c = PagedByteCache(64, 2, 2, 4, 2, device="cpu")
+    q, seq, table = torch.zeros(1, 2, 64), torch.zeros(1, dtype=torch.int32), torch.zeros(1, 2, dtype=torch.int32)
+    c.pool.resize_(c.pool.numel() - 1)
+    with pytest.raises(ValueError, match="pool"):
+        c.attention(q, seq, table)

@@ -138,3 +138,25 @@ def test_captured_calls_with_a_stream():
     torch.cuda.synchronize()
     del c, rot, graphs
     assert torch.ones(8, device="cuda").sum() == 8
+
+
+def test_copied_objects_stand_alone():
+    import copy
+    tq = _api()
+    rot, c = tq.Rotary(128), tq.PagedByteCache(128, 4, 2, 3, 3)
+    x = torch.randn(2, 1, 2, 20, 128, device="cuda")
+    q, table = torch.randn(1, 1, 4, 128, device="cuda"), _i32([[2, 0, 1]])
+    c.append(x[0], x[1], _i32([0]), table, rotary=rot)
+    want = c.attention(q, _i32([20]), table)
+    r2, c2 = copy.deepcopy(rot), copy.deepcopy(c)
+    before = c.pool.clone()
+    c2.append(x[1, :, :, :5], x[0, :, :, :5], _i32([20]), table, rotary=r2)
+    assert torch.equal(c.pool, before)
+    c.append(x[1, :, :, :5], x[0, :, :, :5], _i32([20]), table, rotary=rot)
+    assert torch.equal(c.pool, c2.pool)
+    del c, rot
+    junk = torch.full((1 << 20,), 3, dtype=torch.uint8, device="cuda")
+    assert torch.equal(c2.attention(q, _i32([20]), table), want)
+    c2.append(x[0], x[1], _i32([0]), _i32([[99, 99, 99]]), rotary=r2)
+    assert c2.device_error() == tq.binding.TQ_DEVERR_BAD_PAGE
+    del junk

@@ -101,8 +101,7 @@ class Rotary:
         self.rotary_dim, self.interleaved = int(rotary_dim), bool(interleaved)
         self.host_table = host
         self._table = torch.from_numpy(host.view(np.int64)).to(_device(device))
-        self._args = (self._table.data_ptr(), self.rotary_dim, int(self.interleaved), self.num_axes,
-                      self._table.get_device())
+        self._args = (self._table, self.rotary_dim, int(self.interleaved), self.num_axes)
 
 
 def _table(rotary):
@@ -155,10 +154,11 @@ class PagedByteCache:
         self.device = _device(device)
         self._pool = torch.zeros(need, dtype=torch.uint8, device=self.device)
         self._error = torch.zeros(1, dtype=torch.int32, device=self.device)
+        # (of tensors, not of their addresses: copies of the object have their own)
         self._args = (self.head_dim, self.num_q_heads, self.num_kv_heads, self.num_pages, self.max_blocks_per_seq,
-                      self._pool.data_ptr(), self._error.data_ptr(), self._pool.get_device())
+                      self._pool, self._error)
 
-    # (read-only: the calls hold their addresses)
+    # (read-only: the calls hold the tensors)
     @property
     def pool(self):
         return self._pool

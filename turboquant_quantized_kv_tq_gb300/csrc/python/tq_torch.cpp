@@ -117,15 +117,17 @@ at::Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, at::Scal
 
 long long item(PyObject* tuple, int i) { return PyLong_AsLongLong(PyTuple_GET_ITEM(tuple, i)); }
 
-// Rotary._args: (table address, rotary_dim, interleaved, num_axes, device)
+// Rotary._args: (table, rotary_dim, interleaved, num_axes)
 std::optional<tq_rotary> rotary(PyObject* o, int device) {
   if (!given(o)) return std::nullopt;
-  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 5) throw Refused("bad rotary");
-  if (item(o, 4) != device) throw Refused("the rotary table must be on cuda:" + std::to_string(device));
-  return tq_rotary{(const uint64_t*)item(o, 0), (int32_t)item(o, 1), (int32_t)item(o, 2), (int32_t)item(o, 3)};
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 4) throw Refused("bad rotary");
+  const at::Tensor& t = tensor(PyTuple_GET_ITEM(o, 0), "the rotary table");
+  if (t.get_device() != device) throw Refused("the rotary table must be on cuda:" + std::to_string(device));
+  if (t.numel() != item(o, 1) / 2 || !t.is_contiguous()) throw Refused("the rotary table was resized");
+  return tq_rotary{(const uint64_t*)t.const_data_ptr(), (int32_t)item(o, 1), (int32_t)item(o, 2), (int32_t)item(o, 3)};
 }
 
-// PagedByteCache._args: (head_dim, q heads, kv heads, num_pages, max_blocks, pool address, error address, device)
+// PagedByteCache._args: (head_dim, q heads, kv heads, num_pages, max_blocks, pool, error)
 struct Cache {
   tq_byte_config cfg;
   int32_t pages, blocks;
@@ -134,9 +136,14 @@ struct Cache {
   int device;
 };
 Cache cache(PyObject* o) {
-  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 8) throw Refused("bad cache");
-  return Cache{{(int32_t)item(o, 0), (int32_t)item(o, 1), (int32_t)item(o, 2)}, (int32_t)item(o, 3), (int32_t)item(o, 4),
-               (void*)item(o, 5), (int32_t*)item(o, 6), (int)item(o, 7)};
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 7) throw Refused("bad cache");
+  const at::Tensor &pool = tensor(PyTuple_GET_ITEM(o, 5), "pool"), &error = tensor(PyTuple_GET_ITEM(o, 6), "error");
+  const tq_byte_config cfg = {(int32_t)item(o, 0), (int32_t)item(o, 1), (int32_t)item(o, 2)};
+  const int32_t pages = (int32_t)item(o, 3);
+  if (pool.numel() != (int64_t)tq_byte_pool_bytes(&cfg, pages) || !pool.is_contiguous() || error.numel() != 1 ||
+      error.get_device() != pool.get_device())
+    throw Refused("the pool or its error word was resized or moved");
+  return Cache{cfg, pages, (int32_t)item(o, 4), pool.data_ptr(), (int32_t*)error.data_ptr(), pool.get_device()};
 }
 tq_page_table page_table(PyObject* o, const Cache& c, int64_t* batch) {
   const at::Tensor& t = tensor(o, "block_table");
