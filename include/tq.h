@@ -403,7 +403,8 @@ tq_status tq_norm_rotate(int32_t head_dim, tq_dtype dtype, tq_dtype out_dtype, i
 /* ---- Byte cache: a paged pool of one e4m3 code per coordinate -------------------------------
  * The 8-bit format beside the packed schemes: no rotation of coordinates, no norm split; each
  * block of 16 tokens of one KV head has one power-of-two scale per side.  scale = 2^e with e the
- * smallest integer in [-30, 30] such that the block's largest magnitude is at most 448 * 2^e, and
+ * smallest integer in [-30, 30] such that the block's largest magnitude is at most 448 * 2^e (30 where
+ * none is: finite values beyond 448 * 2^30 saturate, which is not recorded), and
  * a code is e4m3(x / scale), rounded to nearest even.  Powers of two change only a code's
  * exponent, so an append that raises the scale of a block (its new tokens are larger than those
  * it holds) leaves the held codes' significands alone, except where they become subnormal.
