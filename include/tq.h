@@ -329,6 +329,7 @@ typedef struct {
 #define TQ_DEVERR_BAD_PAGE 3      /* a block-table entry or position outside the pool/table    */
 #define TQ_DEVERR_BAD_LENGTH 4    /* a device sequence length outside [0, 16 * max_blocks]     */
 #define TQ_DEVERR_NONFINITE 5     /* a byte-cache append met an infinity or a NaN              */
+#define TQ_DEVERR_BAD_PATH 6      /* a path of kept drafts that does not rise from 0 or more  */
 
 /* Layout of a pool of num_pages pages (plus the one redirect page): total_bytes and the block
  * offsets/sizes of the K and V arrays, each [(num_pages + 1) * H_kv] blocks. */
@@ -475,6 +476,62 @@ tq_status tq_byte_attention_paged(const tq_byte_config* cfg, const void* dev_poo
                                   int32_t batch, int32_t nq, tq_dtype dtype, const tq_heads* q,
                                   const int32_t* dev_seq_len, const int32_t* dev_count, float scale, void* out,
                                   void* ws, size_t ws_bytes, int32_t* dev_error, tq_stream stream);
+
+/* ---- Trees of drafted tokens -----------------------------------------------------------------
+ * A step that verifies a tree of c drafts appends them in one row (tq_byte_append_paged, at the
+ * positions of tq_draft_tree), lets each attend to the sequence before the drafts and to its own
+ * ancestors (tq_byte_tree_attention_paged), and moves the accepted path's tokens together
+ * (tq_byte_keep_paged).  Drafts are numbered so that a parent comes before its children.  All
+ * device integers may change between replays of a captured graph. */
+#define TQ_MAX_DRAFTS 1024
+
+/* Masks and positions of trees.  dev_parents: device int32 [batch][n], the parent of each draft,
+ * -1 for the sequence before the drafts (several drafts may have it).  dev_count: device int32
+ * [batch] or NULL (n): entry b has min(dev_count[b], n) drafts (none when negative).
+ * dev_masks [batch][n][(n + 31) / 32]: bit j % 32 of word j / 32 of draft i is set where j is i or
+ * one of its ancestors.  dev_positions [batch][n], as tq_norm_rotate and tq_byte_append_paged take
+ * them with one axis: dev_start[b] (NULL: 0) plus the number of i's ancestors.  A draft past the count, or
+ * with a parent outside [-1, i) or such an ancestor, has no bits and the position dev_start[b].
+ * n = 0 is a no-op. */
+tq_status tq_draft_tree(int32_t batch, int32_t n, const int32_t* dev_parents, const int32_t* dev_start,
+                        const int32_t* dev_count, int32_t* dev_masks, int32_t* dev_positions, tq_stream stream);
+
+/* tq_byte_attention_paged for a tree: entry b's c = min(dev_count[b], nq) drafts are the last c of its
+ * dev_seq_len[b] tokens.  Draft i < c attends to the first dev_seq_len[b] - c tokens, and to draft j < c
+ * where bit j of its mask is set (dev_masks [batch][nq][(nq + 31) / 32], any bits: they need not come
+ * from a tree; bits from c on count for nothing).  Where c > dev_seq_len[b] the drafts before the first token
+ * do not exist.  Rows that attend to nothing, and rows i >= c, are zeros.  nq: at most TQ_MAX_DRAFTS.
+ * The rest as for tq_byte_attention_paged; e4m3 terms of 16-bit queries are taken at head_dim 64 and
+ * 128 for more than 16 rows (queries times heads per KV head). */
+size_t tq_byte_tree_attention_workspace_bytes(const tq_byte_config* cfg, int32_t batch, int32_t nq, tq_dtype dtype);
+tq_status tq_byte_tree_attention_paged(const tq_byte_config* cfg, const void* dev_pool, const tq_page_table* pages,
+                                       int32_t batch, int32_t nq, tq_dtype dtype, const tq_heads* q,
+                                       const int32_t* dev_seq_len, const int32_t* dev_count, const int32_t* dev_masks,
+                                       float scale, void* out, void* ws, size_t ws_bytes, int32_t* dev_error,
+                                       tq_stream stream);
+
+/* Keep a path of drafts: for j < min(dev_count[b], n) (dev_count NULL: n) the token at position
+ * dev_start[b] + dev_path[b][j] of entry b moves to dev_start[b] + j.  dev_path: device int32 [batch][n],
+ * rising (path[j] > path[j - 1] >= 0) over the count; where it does not, or dev_start[b] < 0 with a count, the entry
+ * is left as it is and TQ_DEVERR_BAD_PATH is recorded.  A block that receives a token gets the largest
+ * scale of the blocks that its 16 tokens come from, on each side, and every code of it is rounded to that
+ * scale (exact but for codes that become subnormal); other blocks stay.  Positions behind the kept
+ * tokens hold what they held, at their block's scale.  Pages of an entry's drafts must be its own, each at
+ * one place of its table.  dev_seq_len: device int32 [batch] or NULL, receives dev_start[b] plus the number
+ * of kept tokens (dev_start[b] for a bad path).  It overlaps no other argument.  Bad pages: see tq_page_table.
+ * n = 0 keeps nothing; at most TQ_MAX_DRAFTS. */
+tq_status tq_byte_keep_paged(const tq_byte_config* cfg, void* dev_pool, const tq_page_table* pages, int32_t batch,
+                             int32_t n, const int32_t* dev_path, const int32_t* dev_start, const int32_t* dev_count,
+                             int32_t* dev_seq_len, int32_t* dev_error, tq_stream stream);
+
+/* Values of a batch: row j of entry b is its token at dev_start[b] + j, for j < min(dev_count[b], n)
+ * (dev_count NULL: n); the other rows are zeros.  k_out, v_out: contiguous [batch][num_kv_heads][n][head_dim] of dtype,
+ * the layout that the appends take.  A value is code * scale rounded once to dtype (fp16: infinite where it
+ * leaves the range).  Tokens before position 0 and bad pages read the redirect page and record
+ * TQ_DEVERR_BAD_PAGE.  n = 0 is a no-op. */
+tq_status tq_byte_read_paged(const tq_byte_config* cfg, const void* dev_pool, const tq_page_table* pages, int32_t batch,
+                             int32_t n, tq_dtype dtype, const int32_t* dev_start, const int32_t* dev_count, void* k_out,
+                             void* v_out, int32_t* dev_error, tq_stream stream);
 
 /* Reconstruct tokens [t0, t1) of KV head kvh of batch entry b as fp32 [t1 - t0][head_dim] (device):
  * code * scale, exact.  For tests and debugging. */

@@ -16,7 +16,7 @@ from . import _build
 from . import binding as _b
 from .binding import TQError, check  # noqa: F401
 
-_TORCH_NAMES = ["PagedByteCache", "Rotary", "norm_rotate"]  # of byte_cache, which needs torch and its extension
+_TORCH_NAMES = ["PagedByteCache", "Rotary", "draft_tree", "norm_rotate"]  # of byte_cache, which needs torch and its extension
 
 __all__ = ["QuantizedKVCache", "PagedKVCache", "TQError", "binding"]
 if os.path.exists(_build.EXT_PATH) and importlib.util.find_spec("torch") is not None:

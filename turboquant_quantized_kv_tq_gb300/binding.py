@@ -66,6 +66,7 @@ TQ_DEVERR_SMEM_PLAN = 2
 TQ_DEVERR_BAD_PAGE = 3
 TQ_DEVERR_BAD_LENGTH = 4
 TQ_DEVERR_NONFINITE = 5
+TQ_DEVERR_BAD_PATH = 6
 
 
 class tq_rotary(ctypes.Structure):
@@ -148,6 +149,16 @@ DECLARATIONS = [
     ("tq_byte_attention_paged", c_int32, [ctypes.POINTER(tq_byte_config), c_void_p, ctypes.POINTER(tq_page_table),
                                           c_int32, c_int32, c_int32, ctypes.POINTER(tq_heads), c_void_p, c_void_p,
                                           ctypes.c_float, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
+    ("tq_draft_tree", c_int32, [c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    ("tq_byte_tree_attention_workspace_bytes", c_size_t, [ctypes.POINTER(tq_byte_config), c_int32, c_int32, c_int32]),
+    ("tq_byte_tree_attention_paged", c_int32, [ctypes.POINTER(tq_byte_config), c_void_p, ctypes.POINTER(tq_page_table),
+                                               c_int32, c_int32, c_int32, ctypes.POINTER(tq_heads), c_void_p, c_void_p,
+                                               c_void_p, ctypes.c_float, c_void_p, c_void_p, c_size_t, c_void_p,
+                                               c_void_p]),
+    ("tq_byte_keep_paged", c_int32, [ctypes.POINTER(tq_byte_config), c_void_p, ctypes.POINTER(tq_page_table), c_int32,
+                                     c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    ("tq_byte_read_paged", c_int32, [ctypes.POINTER(tq_byte_config), c_void_p, ctypes.POINTER(tq_page_table), c_int32,
+                                     c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
     ("tq_byte_dequantize", c_int32, [ctypes.POINTER(tq_byte_config), c_void_p, ctypes.POINTER(tq_page_table),
                                      c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p, c_void_p, c_void_p]),
     ("tq_get_device_error", c_int32, [c_void_p, ctypes.POINTER(c_int32), c_void_p]),

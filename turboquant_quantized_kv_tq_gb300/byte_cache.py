@@ -2,7 +2,7 @@
 ``tq_byte_*`` entry points of ``include/tq.h``).
 
 ``Rotary`` holds a rotation's device table, ``norm_rotate`` applies it (and the norms) to queries and
-keys, and ``PagedByteCache`` owns a pool of e4m3 codes with a scale for each 16-token block, KV head
+keys, ``draft_tree`` makes the masks and positions of trees of drafted tokens, and ``PagedByteCache`` owns a pool of e4m3 codes with a scale for each 16-token block, KV head
 and side.  Tensors may be strided views (a fused projection's slices): only the head dimension has to
 be contiguous, with rows on 16-byte boundaries.  Nothing is copied or converted here; a layout that
 the kernels do not take is refused.
@@ -130,6 +130,22 @@ def norm_rotate(q=None, k=None, rotary=None, positions=None, start=None, q_weigh
                       *args)
 
 
+def draft_tree(parents, start=None, count=None, masks=None, positions=None, stream=None):
+    """Masks and positions of trees of drafted tokens.
+
+    parents: int32 CUDA [batch][n], the parent of each draft, which comes before it; -1: the sequence before the
+    drafts.  ``count[b]``: entry b has only its first count[b] drafts.  Returns masks ([batch][n][(n + 31) // 32]
+    int32: bit j % 32 of word j // 32 of draft i is set where j is i or one of its ancestors), which
+    ``PagedByteCache.attention`` takes as ``tree``, and positions ([1][batch][n] int32: ``start[b]``, default 0, plus
+    the number of ancestors), which ``PagedByteCache.append`` and ``norm_rotate`` take.  A draft past the count, with a
+    parent outside [-1, i), or below such a one has no bits and the position ``start[b]``.  n: at most 1024.
+    """
+    args = (parents, start, count, masks, positions)
+    if stream is None:
+        return _c.draft_tree(*args)
+    return _on_stream(stream, args, _c.draft_tree, *args)
+
+
 class PagedByteCache:
     """A pool of ``num_pages`` pages on a CUDA device, each holding one 16-token block per KV head: e4m3
     codes of keys and values with a power-of-two scale per side (``tq_byte_config``).  ``block_table``
@@ -192,16 +208,39 @@ class PagedByteCache:
         return _on_stream(stream, (k, v, start, block_table, count, positions, k_weight, q, q_weight, q_out, _table(rotary),
                                    self._pool, self._error), _c.append, *args)
 
-    def attention(self, q, seq_len, block_table, count=None, scale=None, out=None, stream=None):
+    def attention(self, q, seq_len, block_table, count=None, scale=None, out=None, stream=None, tree=None):
         """q: CUDA tensor [batch][nq][num_q_heads][d] (or [batch][num_q_heads][d] for one query), any
         strides along the first dims.  The last ``count[b]`` (default nq) positions of sequence b are its
         queries: query i attends to the first ``seq_len[b] - count[b] + 1 + i`` tokens, and rows
         i >= count[b] come out as zeros.  ``scale`` multiplies the scores (default 1 / sqrt(d)).  Returns
-        out, contiguous in q's shape and dtype."""
-        args = (self._args, q, seq_len, block_table, count, self.head_dim ** -0.5 if scale is None else scale, out)
+        out, contiguous in q's shape and dtype.
+
+        ``tree`` (``draft_tree``'s masks, int32 [batch][nq][(nq + 31) // 32]): query i attends to the first
+        ``seq_len[b] - count[b]`` tokens and, of the count[b] after them, to those whose bit is set in its mask."""
+        args = (self._args, q, seq_len, block_table, count, self.head_dim ** -0.5 if scale is None else scale, out, tree)
         if stream is None:
             return _c.attention(*args)
-        return _on_stream(stream, (q, seq_len, block_table, count, out, self._pool, self._error), _c.attention, *args)
+        return _on_stream(stream, (q, seq_len, block_table, count, out, tree, self._pool, self._error), _c.attention, *args)
+
+    def keep(self, path, start, block_table, count=None, seq_len=None, stream=None):
+        """Keep a path of drafts: the token at ``start[b] + path[b][j]`` moves to ``start[b] + j``, for j < count[b]
+        (default all).  path: int32 CUDA [batch][n], rising from 0 or more over the count; an entry whose path does
+        not rise is left as it is (TQ_DEVERR_BAD_PATH).  Blocks that receive tokens take the largest scale of the blocks
+        that these and their other tokens come from.  Returns seq_len, int32 [batch]: ``start[b]`` plus the number of kept
+        tokens.  n: at most 1024."""
+        args = (self._args, path, start, block_table, count, seq_len)
+        if stream is None:
+            return _c.keep(*args)
+        return _on_stream(stream, (path, start, block_table, count, seq_len, self._pool, self._error), _c.keep, *args)
+
+    def read(self, start, block_table, n, count=None, dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
+        """Values of n tokens of every entry from ``start[b]`` on: (k, v), contiguous [batch][num_kv_heads][n][d] of
+        dtype (float32, bfloat16 or float16), the layout that the appends take.  ``count[b]``: rows from count[b] on are
+        zeros.  A value is its code times its block's scale, rounded once."""
+        args = (self._args, start, block_table, n, count, dtype, k_out, v_out)
+        if stream is None:
+            return _c.read(*args)
+        return _on_stream(stream, (start, block_table, count, k_out, v_out, self._pool, self._error), _c.read, *args)
 
     def dequantize(self, b, kvh, t0, t1, block_table):
         """Tokens [t0, t1) of KV head kvh of entry b as fp32 (k, v) [t1 - t0][d]."""

@@ -46,14 +46,15 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
   return THPVariable_Unpack(o);
 }
 
-tq_dtype dtype_of(const at::Tensor& t) {
-  switch (t.scalar_type()) {
+tq_dtype dtype_code(at::ScalarType t) {
+  switch (t) {
     case at::kFloat: return TQ_F32;
     case at::kBFloat16: return TQ_BF16;
     case at::kHalf: return TQ_F16;
-    default: throw Refused(std::string("unsupported dtype ") + c10::toString(t.scalar_type()) + ": float32, bfloat16 or float16");
+    default: throw Refused(std::string("unsupported dtype ") + c10::toString(t) + ": float32, bfloat16 or float16");
   }
 }
+tq_dtype dtype_of(const at::Tensor& t) { return dtype_code(t.scalar_type()); }
 
 void same_kind(const at::Tensor& t, const char* name, at::ScalarType dt, int device) {
   if (t.scalar_type() != dt || t.get_device() != device)
@@ -292,9 +293,9 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   });
 }
 
-// attention(cache, q, seq_len, block_table, count, scale, out) -> out
+// attention(cache, q, seq_len, block_table, count, scale, out, tree) -> out
 PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
-  if (!count_args(n_args, 7)) return nullptr;
+  if (!count_args(n_args, 8)) return nullptr;
   return guarded([&]() -> PyObject* {
     const Cache c = cache(a[0]);
     int64_t B;
@@ -317,16 +318,100 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const int32_t* seq = ints(a[2], "seq_len", {B}, c.device);
     const int32_t* count = ints(a[4], "count", {B}, c.device);
     const float scale = number(a[5]);
+    const int32_t* tree = ints(a[7], "tree", {B, nq, (nq + 31) / 32}, c.device);
     const On on(c.device);
     at::Tensor out = output(a[6], "out", q.sizes(), dt, c.device);
     if (B > 0 && nq > 0) {
-      const size_t need = tq_byte_attention_workspace_bytes(&c.cfg, &pt, narrow(B, "batch"), narrow(nq, "nq"), code);
+      const size_t need = tree ? tq_byte_tree_attention_workspace_bytes(&c.cfg, narrow(B, "batch"), narrow(nq, "nq"), code)
+                               : tq_byte_attention_workspace_bytes(&c.cfg, &pt, narrow(B, "batch"), narrow(nq, "nq"), code);
       at::Tensor ws;
       if (need) ws = at::empty({(int64_t)need}, at::TensorOptions().dtype(at::kByte).device(out.device()));
-      check(tq_byte_attention_paged(&c.cfg, c.pool, &pt, (int32_t)B, (int32_t)nq, code, &qh, seq, count, scale, out.data_ptr(),
-                                    need ? ws.data_ptr() : nullptr, need, c.error, on.stream));
+      void* w = need ? ws.data_ptr() : nullptr;
+      check(tree ? tq_byte_tree_attention_paged(&c.cfg, c.pool, &pt, (int32_t)B, (int32_t)nq, code, &qh, seq, count, tree, scale,
+                                                out.data_ptr(), w, need, c.error, on.stream)
+                 : tq_byte_attention_paged(&c.cfg, c.pool, &pt, (int32_t)B, (int32_t)nq, code, &qh, seq, count, scale,
+                                           out.data_ptr(), w, need, c.error, on.stream));
     }
     return THPVariable_Wrap(out);
+  });
+}
+
+// draft_tree(parents, start, count, masks, positions) -> (masks, positions)
+PyObject* draft_tree(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  if (!count_args(n_args, 5)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor& p = tensor(a[0], "parents");
+    if (p.dim() != 2 || !p.is_cuda()) throw Refused("parents must be a CUDA tensor [batch][n], not " + shape_text(p));
+    const int device = p.get_device();
+    const int64_t B = p.size(0), n = p.size(1);
+    const int32_t* parents = ints(a[0], "parents", {B, n}, device);
+    const int32_t* start = ints(a[1], "start", {B}, device);
+    const int32_t* count = ints(a[2], "count", {B}, device);
+    const On on(device);
+    at::Tensor masks = output(a[3], "masks", {B, n, (n + 31) / 32}, at::kInt, device);
+    at::Tensor positions = output(a[4], "positions", {1, B, n}, at::kInt, device);
+    if (B > 0 && n > 0)
+      check(tq_draft_tree(narrow(B, "batch"), narrow(n, "n"), parents, start, count, (int32_t*)masks.data_ptr(),
+                          (int32_t*)positions.data_ptr(), on.stream));
+    PyObject* out = PyTuple_New(2);
+    if (!out) throw Failed();
+    PyTuple_SET_ITEM(out, 0, THPVariable_Wrap(masks));
+    PyTuple_SET_ITEM(out, 1, THPVariable_Wrap(positions));
+    return out;
+  });
+}
+
+// keep(cache, path, start, block_table, count, seq_len) -> seq_len
+PyObject* keep(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  if (!count_args(n_args, 6)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Cache c = cache(a[0]);
+    int64_t B;
+    const tq_page_table pt = page_table(a[3], c, &B);
+    const at::Tensor& p = tensor(a[1], "path");
+    if (p.dim() != 2) throw Refused("path must be a tensor [batch][n], not " + shape_text(p));
+    const int64_t n = p.size(1);
+    const int32_t* path = ints(a[1], "path", {B, n}, c.device);
+    if (!given(a[2])) throw Refused("start must be given");
+    const int32_t* start = ints(a[2], "start", {B}, c.device);
+    const int32_t* count = ints(a[4], "count", {B}, c.device);
+    const On on(c.device);
+    at::Tensor len = output(a[5], "seq_len", {B}, at::kInt, c.device);
+    if (B > 0)
+      check(tq_byte_keep_paged(&c.cfg, c.pool, &pt, narrow(B, "batch"), narrow(n, "n"), path, start, count,
+                               (int32_t*)len.data_ptr(), c.error, on.stream));
+    return THPVariable_Wrap(len);
+  });
+}
+
+// read(cache, start, block_table, n, count, dtype, k_out, v_out) -> (k, v)
+PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  if (!count_args(n_args, 8)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Cache c = cache(a[0]);
+    int64_t B;
+    const tq_page_table pt = page_table(a[2], c, &B);
+    if (!given(a[1])) throw Refused("start must be given");
+    const int32_t* start = ints(a[1], "start", {B}, c.device);
+    const long long n = PyLong_AsLongLong(a[3]);
+    if (n == -1 && PyErr_Occurred()) throw Failed();
+    const int32_t* count = ints(a[4], "count", {B}, c.device);
+    if (!THPDtype_Check(a[5])) throw Refused("dtype must be a torch.dtype");
+    const at::ScalarType dt = reinterpret_cast<THPDtype*>(a[5])->scalar_type;
+    const tq_dtype code = dtype_code(dt);
+    if (n < 0) throw Refused("n must be >= 0");
+    narrow(n, "n");
+    const On on(c.device);
+    const int64_t shape[4] = {B, c.cfg.num_kv_heads, n, c.cfg.head_dim};
+    at::Tensor k = output(a[6], "k_out", shape, dt, c.device), v = output(a[7], "v_out", shape, dt, c.device);
+    if (B > 0 && n > 0)
+      check(tq_byte_read_paged(&c.cfg, c.pool, &pt, narrow(B, "batch"), (int32_t)n, code, start, count, k.data_ptr(), v.data_ptr(),
+                               c.error, on.stream));
+    PyObject* out = PyTuple_New(2);
+    if (!out) throw Failed();
+    PyTuple_SET_ITEM(out, 0, THPVariable_Wrap(k));
+    PyTuple_SET_ITEM(out, 1, THPVariable_Wrap(v));
+    return out;
   });
 }
 
@@ -340,6 +425,9 @@ PyMethodDef kMethods[] = {
     {"norm_rotate", (PyCFunction)(void (*)(void))norm_rotate, METH_FASTCALL, nullptr},
     {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, nullptr},
     {"attention", (PyCFunction)(void (*)(void))attention, METH_FASTCALL, nullptr},
+    {"draft_tree", (PyCFunction)(void (*)(void))draft_tree, METH_FASTCALL, nullptr},
+    {"keep", (PyCFunction)(void (*)(void))keep, METH_FASTCALL, nullptr},
+    {"read", (PyCFunction)(void (*)(void))read, METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_tq_torch", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

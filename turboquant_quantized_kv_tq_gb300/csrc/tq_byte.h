@@ -70,6 +70,13 @@ struct AppendArgs {
   Positions pos;
 };
 
+// Ancestor bits of drafts: [B][n][words], bit j of word w of row (b, i): draft 32 w + j.
+struct TreeMasks {
+  const uint32_t* bits;  // nullptr: causal
+  int n, words;
+  TQB_HD const uint32_t* row(int b, int i) const { return bits + ((long long)b * n + i) * words; }
+};
+
 struct AttnArgs {
   int d, B, nq, Hq, Hkv;
   tq_dtype dtype;
@@ -79,6 +86,28 @@ struct AttnArgs {
   float scale;
   void* out;
   void* ws;
+  TreeMasks tree;
+};
+
+struct TreeArgs {
+  int B, n;
+  const int32_t *parents, *start, *count;
+  int32_t *masks, *positions;
+};
+
+struct KeepArgs {
+  int d, B, n;
+  Pool pool;
+  const int32_t *path, *start, *count;
+  int32_t* seq_len;
+};
+
+struct ReadArgs {
+  int d, B, n;
+  tq_dtype dtype;
+  Pool pool;
+  const int32_t *start, *count;
+  void *k, *v;
 };
 
 tq_status cuda_error(const char* what, int e);
@@ -88,5 +117,11 @@ tq_status launch_byte_attention(const AttnArgs& a, Stream s);
 tq_status launch_byte_dequantize(const Pool& pool, int d, int b, int h, int t0, int t1, float* k, float* v, Stream s);
 // Bytes of attention workspace of a call (0 is never returned).
 size_t byte_attention_workspace(int d, int B, int nq, int Hq, int Hkv, tq_dtype dtype);
+// The same with a tree's masks (a.tree).
+tq_status launch_tree_attention(const AttnArgs& a, Stream s);
+size_t tree_attention_workspace(int d, int B, int nq, int Hq, int Hkv, tq_dtype dtype);
+tq_status launch_draft_tree(const TreeArgs& a, Stream s);
+tq_status launch_byte_keep(const KeepArgs& a, Stream s);
+tq_status launch_byte_read(const ReadArgs& a, Stream s);
 
 }  // namespace tqb

@@ -266,13 +266,13 @@ size_t tq_byte_attention_workspace_bytes(const tq_byte_config* cfg, const tq_pag
   return byte_attention_workspace(cfg->head_dim, batch, nq, cfg->num_q_heads, cfg->num_kv_heads, dtype);
 }
 
-tq_status tq_byte_attention_paged(const tq_byte_config* cfg, const void* dev_pool, const tq_page_table* pages,
-                                  int32_t batch, int32_t nq, tq_dtype dtype, const tq_heads* q,
-                                  const int32_t* dev_seq_len, const int32_t* dev_count, float scale, void* out,
-                                  void* ws, size_t ws_bytes, int32_t* dev_error, tq_stream stream) {
-  tq_status s = check_attention(cfg, batch, nq, dtype);
-  if (s != TQ_OK) return s;
-  AttnArgs a = {};
+// The checks and arguments of both attention calls; `need`: bytes of workspace.
+static tq_status attention_args(const tq_byte_config* cfg, const void* dev_pool, const tq_page_table* pages, int32_t batch,
+                                int32_t nq, tq_dtype dtype, const tq_heads* q, const int32_t* dev_seq_len,
+                                const int32_t* dev_count, float scale, void* out, void* ws, size_t ws_bytes, size_t need,
+                                int32_t* dev_error, AttnArgs* args) {
+  tq_status s;
+  AttnArgs& a = *args;
   if ((s = check_pool(cfg, dev_pool, pages, dev_error, &a.pool)) != TQ_OK) return s;
   if (!q || !dev_seq_len || !out || !ws) return fail(TQ_ERR_INVALID_ARG, "null argument");
   if ((s = check_rows(q, "q", cfg->num_q_heads, batch, nq, dtype_bytes(dtype), &a.q)) != TQ_OK) return s;
@@ -282,7 +282,6 @@ tq_status tq_byte_attention_paged(const tq_byte_config* cfg, const void* dev_poo
   if (!may_write(out, cfg->num_q_heads, false, a.q, false, batch, nq, cfg->head_dim, bytes, bytes))
     return fail(TQ_ERR_INVALID_ARG, "out must not overlap q");
   if (!std::isfinite(scale)) return fail(TQ_ERR_INVALID_ARG, "scale must be finite");
-  const size_t need = byte_attention_workspace(cfg->head_dim, batch, nq, cfg->num_q_heads, cfg->num_kv_heads, dtype);
   if (ws_bytes < need) return fail(TQ_ERR_WORKSPACE, "workspace too small");
   const Span pool = span_of(dev_pool, tq_byte_pool_bytes(cfg, pages->num_pages)), w = span_of(ws, need);
   const Span o = span_of(out, batch, nq, cfg->num_q_heads, cfg->head_dim, bytes), x = span_of(a.q, batch, nq, cfg->head_dim, bytes);
@@ -299,7 +298,130 @@ tq_status tq_byte_attention_paged(const tq_byte_config* cfg, const void* dev_poo
   a.scale = scale;
   a.out = out;
   a.ws = ws;
-  return launch_byte_attention(a, stream);
+  return TQ_OK;
+}
+
+tq_status tq_byte_attention_paged(const tq_byte_config* cfg, const void* dev_pool, const tq_page_table* pages,
+                                  int32_t batch, int32_t nq, tq_dtype dtype, const tq_heads* q,
+                                  const int32_t* dev_seq_len, const int32_t* dev_count, float scale, void* out,
+                                  void* ws, size_t ws_bytes, int32_t* dev_error, tq_stream stream) {
+  tq_status s = check_attention(cfg, batch, nq, dtype);
+  if (s != TQ_OK) return s;
+  const size_t need = byte_attention_workspace(cfg->head_dim, batch, nq, cfg->num_q_heads, cfg->num_kv_heads, dtype);
+  AttnArgs a = {};
+  s = attention_args(cfg, dev_pool, pages, batch, nq, dtype, q, dev_seq_len, dev_count, scale, out, ws, ws_bytes, need, dev_error, &a);
+  return s != TQ_OK ? s : launch_byte_attention(a, stream);
+}
+
+size_t tq_byte_tree_attention_workspace_bytes(const tq_byte_config* cfg, int32_t batch, int32_t nq, tq_dtype dtype) {
+  if (check_attention(cfg, batch, nq, dtype) != TQ_OK || nq > TQ_MAX_DRAFTS) return 0;
+  return tree_attention_workspace(cfg->head_dim, batch, nq, cfg->num_q_heads, cfg->num_kv_heads, dtype);
+}
+
+tq_status tq_byte_tree_attention_paged(const tq_byte_config* cfg, const void* dev_pool, const tq_page_table* pages,
+                                       int32_t batch, int32_t nq, tq_dtype dtype, const tq_heads* q,
+                                       const int32_t* dev_seq_len, const int32_t* dev_count, const int32_t* dev_masks,
+                                       float scale, void* out, void* ws, size_t ws_bytes, int32_t* dev_error,
+                                       tq_stream stream) {
+  tq_status s = check_attention(cfg, batch, nq, dtype);
+  if (s != TQ_OK) return s;
+  if (nq > TQ_MAX_DRAFTS) return fail(TQ_ERR_UNSUPPORTED, "nq: at most TQ_MAX_DRAFTS drafts");
+  if (!dev_masks) return fail(TQ_ERR_INVALID_ARG, "null masks");
+  if (!aligned(dev_masks, 4)) return fail(TQ_ERR_INVALID_ARG, "masks must be 4-byte aligned");
+  const size_t need = tree_attention_workspace(cfg->head_dim, batch, nq, cfg->num_q_heads, cfg->num_kv_heads, dtype);
+  AttnArgs a = {};
+  s = attention_args(cfg, dev_pool, pages, batch, nq, dtype, q, dev_seq_len, dev_count, scale, out, ws, ws_bytes, need, dev_error, &a);
+  if (s != TQ_OK) return s;
+  a.tree = TreeMasks{(const uint32_t*)dev_masks, nq, (nq + 31) / 32};
+  const Span m = span_of(dev_masks, (size_t)batch * nq * a.tree.words * 4);
+  if (overlap(m, span_of(ws, need)) || overlap(m, span_of(out, batch, nq, cfg->num_q_heads, cfg->head_dim, dtype_bytes(dtype))))
+    return fail(TQ_ERR_INVALID_ARG, "ws and out must not overlap the masks");
+  return launch_tree_attention(a, stream);
+}
+
+tq_status tq_draft_tree(int32_t batch, int32_t n, const int32_t* dev_parents, const int32_t* dev_start,
+                        const int32_t* dev_count, int32_t* dev_masks, int32_t* dev_positions, tq_stream stream) {
+  if (batch < 1 || batch > TQ_MAX_BATCH) return fail(TQ_ERR_INVALID_ARG, "batch must be in [1, TQ_MAX_BATCH]");
+  if (n < 0) return fail(TQ_ERR_INVALID_ARG, "n must be >= 0");
+  if (n > TQ_MAX_DRAFTS) return fail(TQ_ERR_UNSUPPORTED, "n: at most TQ_MAX_DRAFTS drafts");
+  if (!dev_parents || !dev_masks || !dev_positions) return fail(TQ_ERR_INVALID_ARG, "null argument");
+  if (!aligned(dev_parents, 4) || !aligned(dev_start, 4) || !aligned(dev_count, 4) || !aligned(dev_masks, 4) ||
+      !aligned(dev_positions, 4))
+    return fail(TQ_ERR_INVALID_ARG, "misaligned pointer");
+  if (n == 0) return TQ_OK;
+  const size_t rows = (size_t)batch * n * 4, list = (size_t)batch * 4;
+  const Span m = span_of(dev_masks, rows * ((n + 31) / 32)), x = span_of(dev_positions, rows);
+  const Span in[3] = {span_of(dev_parents, rows), span_of(dev_start, dev_start ? list : 0), span_of(dev_count, dev_count ? list : 0)};
+  for (const Span& i : in)
+    if (overlap(m, i) || overlap(x, i)) return fail(TQ_ERR_INVALID_ARG, "an output overlaps an input");
+  if (overlap(m, x)) return fail(TQ_ERR_INVALID_ARG, "the outputs overlap");
+  return launch_draft_tree(TreeArgs{batch, n, dev_parents, dev_start, dev_count, dev_masks, dev_positions}, stream);
+}
+
+tq_status tq_byte_keep_paged(const tq_byte_config* cfg, void* dev_pool, const tq_page_table* pages, int32_t batch,
+                             int32_t n, const int32_t* dev_path, const int32_t* dev_start, const int32_t* dev_count,
+                             int32_t* dev_seq_len, int32_t* dev_error, tq_stream stream) {
+  tq_status s = check_config(cfg);
+  if (s != TQ_OK) return s;
+  KeepArgs a = {};
+  if ((s = check_pool(cfg, dev_pool, pages, dev_error, &a.pool)) != TQ_OK) return s;
+  if ((s = check_batch(batch, n, 1, "n")) != TQ_OK) return s;
+  if (n > TQ_MAX_DRAFTS) return fail(TQ_ERR_UNSUPPORTED, "n: at most TQ_MAX_DRAFTS drafts");
+  if ((!dev_path && n > 0) || !dev_start) return fail(TQ_ERR_INVALID_ARG, "null argument");
+  if (!aligned(dev_path, 4) || !aligned(dev_start, 4) || !aligned(dev_count, 4) || !aligned(dev_seq_len, 4))
+    return fail(TQ_ERR_INVALID_ARG, "misaligned pointer");
+  const size_t list = (size_t)batch * 4;
+  const Span path = span_of(dev_path, (size_t)n * list), start = span_of(dev_start, list);
+  const Span count = span_of(dev_count, dev_count ? list : 0), len = span_of(dev_seq_len, dev_seq_len ? list : 0);
+  const Span pool = span_of(dev_pool, tq_byte_pool_bytes(cfg, pages->num_pages));
+  const Span table = span_of(pages->block_table, list * pages->max_blocks_per_seq);
+  // (other entries' starts and counts are read while an entry's length is written)
+  if (overlap(len, path) || overlap(len, start) || overlap(len, count) || overlap(len, table))
+    return fail(TQ_ERR_INVALID_ARG, "seq_len must not overlap an input");
+  if (overlap(pool, path) || overlap(pool, start) || overlap(pool, count) || overlap(pool, len))
+    return fail(TQ_ERR_INVALID_ARG, "path, start, count and seq_len must not overlap the pool");
+  a.d = cfg->head_dim;
+  a.B = batch;
+  a.n = n;
+  a.path = dev_path;
+  a.start = dev_start;
+  a.count = dev_count;
+  a.seq_len = dev_seq_len;
+  return launch_byte_keep(a, stream);
+}
+
+tq_status tq_byte_read_paged(const tq_byte_config* cfg, const void* dev_pool, const tq_page_table* pages, int32_t batch,
+                             int32_t n, tq_dtype dtype, const int32_t* dev_start, const int32_t* dev_count, void* k_out,
+                             void* v_out, int32_t* dev_error, tq_stream stream) {
+  tq_status s = check_config(cfg);
+  if (s != TQ_OK) return s;
+  ReadArgs a = {};
+  if ((s = check_pool(cfg, dev_pool, pages, dev_error, &a.pool)) != TQ_OK) return s;
+  if ((s = check_dtype(dtype, "dtype")) != TQ_OK) return s;
+  if ((s = check_batch(batch, n, cfg->num_kv_heads, "n")) != TQ_OK) return s;
+  if (!dev_start) return fail(TQ_ERR_INVALID_ARG, "null argument");
+  if (!aligned(dev_start, 4) || !aligned(dev_count, 4)) return fail(TQ_ERR_INVALID_ARG, "misaligned pointer");
+  if (n == 0) return TQ_OK;
+  if (!k_out || !v_out) return fail(TQ_ERR_INVALID_ARG, "null output");
+  if (!aligned(k_out, 16) || !aligned(v_out, 16)) return fail(TQ_ERR_INVALID_ARG, "outputs must be 16-byte aligned");
+  const int bytes = dtype_bytes(dtype);
+  const Span pool = span_of(dev_pool, tq_byte_pool_bytes(cfg, pages->num_pages));
+  const Span k = span_of(k_out, batch, n, cfg->num_kv_heads, cfg->head_dim, bytes), v = span_of(v_out, batch, n, cfg->num_kv_heads, cfg->head_dim, bytes);
+  if (overlap(k, v)) return fail(TQ_ERR_INVALID_ARG, "the outputs overlap");
+  const size_t list = (size_t)batch * 4;
+  const Span in[4] = {pool, span_of(dev_start, list), span_of(dev_count, dev_count ? list : 0),
+                      span_of(pages->block_table, list * pages->max_blocks_per_seq)};
+  for (const Span& i : in)
+    if (overlap(k, i) || overlap(v, i)) return fail(TQ_ERR_INVALID_ARG, "the outputs must not overlap the pool or an input");
+  a.d = cfg->head_dim;
+  a.B = batch;
+  a.n = n;
+  a.dtype = dtype;
+  a.start = dev_start;
+  a.count = dev_count;
+  a.k = k_out;
+  a.v = v_out;
+  return launch_byte_read(a, stream);
 }
 
 tq_status tq_byte_dequantize(const tq_byte_config* cfg, const void* dev_pool, const tq_page_table* pages,

@@ -135,7 +135,7 @@ struct Cfg {
   static constexpr int PART = 8 * NR * (D + 2);                             // floats of a partial
 };
 
-template <int D, int NR, int TERMS, typename T>
+template <int D, int NR, int TERMS, bool TREE, typename T>
 __global__ void __launch_bounds__(Cfg<D, NR, TERMS>::NW * 32, (Cfg<D, NR, TERMS>::TWO ? 2 : 1)) split_kernel(const AttnParams p) {
   using C = Cfg<D, NR, TERMS>;
   extern __shared__ __align__(128) unsigned char sm[];
@@ -178,7 +178,10 @@ __global__ void __launch_bounds__(Cfg<D, NR, TERMS>::NW * 32, (Cfg<D, NR, TERMS>
   };
   c_page = pages(c_base);
   QRaw<D, NR, T> raw;  // of the next stretch
-  request_q<D, NR, T>(raw, A.q, c.b, c.h, p.G, c.rg * 8 * NR, p.rows, lane);
+  // Rows of entry b that ask.  (A tree's rows past the count are zero queries whose sums are dropped, so that they
+  // hide nothing; without a tree their limit of 0 does it.)
+  auto asking = [&](int b) { return TREE ? min(p.rows, clamped_count(A.count, b, A.nq) * p.G) : p.rows; };
+  request_q<D, NR, T>(raw, A.q, c.b, c.h, p.G, c.rg * 8 * NR, asking(c.b), lane);
   int raw_b = c.b, raw_h = c.h, raw_rg = c.rg;
   uint32_t issued = 0;
   auto issue = [&]() {  // the warp's next tile into the next stage, if there is one
@@ -220,9 +223,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, TERMS>::NW * 32, (Cfg<D, NR, TERMS>
     at = s.next;
     if (s.t0 == s.t1) continue;
     const int len = min(max(__ldg(A.seq_len + s.b), 0), most), cnt = clamped_count(A.count, s.b, A.nq);
-    const int row0 = s.rg * 8 * NR;
+    const int row0 = s.rg * 8 * NR, asks = asking(s.b), drafts = len - cnt;  // drafts: the first one's position (TREE)
     QFrag<D, NR, T> q;
-    if (raw_b != s.b || raw_h != s.h || raw_rg != s.rg) request_q<D, NR, T>(raw, A.q, s.b, s.h, p.G, row0, p.rows, lane);
+    if (raw_b != s.b || raw_h != s.h || raw_rg != s.rg) request_q<D, NR, T>(raw, A.q, s.b, s.h, p.G, row0, asks, lane);
     convert_q<D, NR, T>(q, raw, A.scale, lane);
     int lim[NR][2], least = 0x7fffffff;
 #pragma unroll
@@ -230,11 +233,15 @@ __global__ void __launch_bounds__(Cfg<D, NR, TERMS>::NW * 32, (Cfg<D, NR, TERMS>
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int row = row0 + 8 * r + 2 * u + k;
-        lim[r][k] = row < p.rows ? row_limit(row / p.G, len, cnt) : 0;
-        least = min(least, row < p.rows ? lim[r][k] : 0x7fffffff);
+        lim[r][k] = row >= asks ? 0 : TREE ? max(0, drafts) : row_limit(row / p.G, len, cnt);
+        least = min(least, row < asks ? lim[r][k] : 0x7fffffff);
       }
     least = __reduce_min_sync(kFull, least);
     least = min(least, len);
+    auto hide = [&] {
+      if constexpr (TREE) return TreeLimits{A.tree, s.b, row0 + 2 * u, p.G, drafts, cnt};
+      else return Limits<NR>{lim};
+    }();
     State<D, NR> st;
     st.clear();
 #pragma unroll 1
@@ -245,7 +252,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TERMS>::NW * 32, (Cfg<D, NR, TERMS>
         if (A.pool.err) atomicExch(A.pool.err, TQ_DEVERR_WAIT_TIMEOUT);
       }
       if (alive)
-        tile_step<D, NR, TERMS == 2, T>(ring + slot * C::BLK, q, st, 16 * t, lim, 16 * t + 16 > least, len, lane);
+        tile_step<D, NR, TERMS == 2>(ring + slot * C::BLK, q, st, 16 * t, hide, 16 * t + 16 > least, len, lane);
       __syncwarp();
       ++used;
       if (alive) {
@@ -255,7 +262,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TERMS>::NW * 32, (Cfg<D, NR, TERMS>
     }
     if (at < end) {  // the next stretch's queries, while the warps meet
       const Seg nx = seg_at(p, pre, at, end, b_from);
-      request_q<D, NR, T>(raw, A.q, nx.b, nx.h, p.G, nx.rg * 8 * NR, p.rows, lane);
+      request_q<D, NR, T>(raw, A.q, nx.b, nx.h, p.G, nx.rg * 8 * NR, asking(nx.b), lane);
       raw_b = nx.b, raw_h = nx.h, raw_rg = nx.rg;
     }
     // the warps' states of this stretch into one
@@ -267,6 +274,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TERMS>::NW * 32, (Cfg<D, NR, TERMS>
       for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int m = 4; m <= 16; m <<= 1) st.l[r][k] += __shfl_xor_sync(kFull, st.l[r][k], m);
+        if (TREE && row0 + 8 * r + 2 * u + k >= asks) st.l[r][k] = 0.f;
         if (g == 0) {
           ml[2 * (warp * 8 * NR + 8 * r + 2 * u + k)] = st.m[r][k];
           ml[2 * (warp * 8 * NR + 8 * r + 2 * u + k) + 1] = st.l[r][k];
@@ -419,7 +427,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) rows_kernel(const AttnPa
       }
       if (!alive) break;
       if (t < mine)
-        tile_step<D, NR, true, T>(sm + slot * C::BLK, q, st, 16 * t, lim, 16 * t + 16 > least, len, lane);
+        tile_step<D, NR, true>(sm + slot * C::BLK, q, st, 16 * t, Limits<NR>{lim}, 16 * t + 16 > least, len, lane);
       __syncwarp();
       if (lane == 0) asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n" ::"r"(empty + 8 * slot) : "memory");
     }
@@ -449,7 +457,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) rows_kernel(const AttnPa
 // Rows per warp: 16 where the registers hold them and there are more than 8.
 int row_groups_of(int d, int terms, int rows) { return rows > 8 && d <= 128 ? 2 : 1; }
 
-template <int D, int NR, int TERMS, typename T>
+template <int D, int NR, int TERMS, bool TREE, typename T>
 cudaError_t split_go(AttnParams p, cudaStream_t s) {
   using C = Cfg<D, NR, TERMS>;
   static_assert(C::STAGES >= 2, "ring");
@@ -463,9 +471,9 @@ cudaError_t split_go(AttnParams p, cudaStream_t s) {
   if (grid > need) grid = need;
   p.grid = (int)grid;
   const int smem = C::smem(p.a.B);
-  cudaError_t e = allow_smem((const void*)split_kernel<D, NR, TERMS, T>, C::smem(TQ_MAX_BATCH), dev, done);
+  cudaError_t e = allow_smem((const void*)split_kernel<D, NR, TERMS, TREE, T>, C::smem(TQ_MAX_BATCH), dev, done);
   if (e != cudaSuccess) return e;
-  split_kernel<D, NR, TERMS, T><<<p.grid, C::NW * 32, smem, s>>>(p);
+  split_kernel<D, NR, TERMS, TREE, T><<<p.grid, C::NW * 32, smem, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (p.grid == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
@@ -506,16 +514,45 @@ cudaError_t attention_d(const AttnParams& p, cudaStream_t s) {
   const int nr = row_groups_of(D, TERMS, p.rows);
   const bool rows = use_rows((p.rows + 8 * nr - 1) / (8 * nr));
   if constexpr (wide) {
-    if (nr == 2) return rows ? rows_go<D, 2, TERMS, T>(p, s) : split_go<D, 2, TERMS, T>(p, s);
+    if (nr == 2) return rows ? rows_go<D, 2, TERMS, T>(p, s) : split_go<D, 2, TERMS, false, T>(p, s);
   }
-  return rows ? rows_go<D, 1, TERMS, T>(p, s) : split_go<D, 1, TERMS, T>(p, s);
+  return rows ? rows_go<D, 1, TERMS, T>(p, s) : split_go<D, 1, TERMS, false, T>(p, s);
+}
+
+template <int D, int TERMS, typename T>
+cudaError_t tree_d(const AttnParams& p, cudaStream_t s) {
+  if constexpr (D <= 128) {
+    if (row_groups_of(D, TERMS, p.rows) == 2) return split_go<D, 2, TERMS, true, T>(p, s);
+  }
+  return split_go<D, 1, TERMS, true, T>(p, s);
 }
 
 template <int D>
 cudaError_t attention_type(const AttnParams& p, cudaStream_t s) {
+  if (p.a.tree.bits) {
+    if (p.a.dtype == TQ_F32) return tree_d<D, 2, float>(p, s);
+    return p.a.dtype == TQ_BF16 ? tree_d<D, 1, __nv_bfloat16>(p, s) : tree_d<D, 1, __half>(p, s);
+  }
   if (p.a.dtype == TQ_F32) return attention_d<D, 2, float>(p, s);
   if (p.a.dtype == TQ_BF16) return attention_d<D, 1, __nv_bfloat16>(p, s);
   return attention_d<D, 1, __half>(p, s);
+}
+
+cudaError_t by_head_dim(const AttnArgs& a, cudaStream_t s) {
+  AttnParams p;
+  p.a = a;
+  p.G = a.Hq / a.Hkv;
+  p.rows = p.G * a.nq;
+  p.groups = 0;
+  p.grid = 0;
+  p.heads = (JoinHead*)a.ws;
+  p.part = (float*)((unsigned char*)a.ws + kJoinHeadBytes);
+  switch (a.d) {
+    case 64: return attention_type<64>(p, s);
+    case 128: return attention_type<128>(p, s);
+    case 256: return attention_type<256>(p, s);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -550,23 +587,20 @@ size_t byte_attention_workspace(int d, int B, int nq, int Hq, int Hkv, tq_dtype 
   return need;
 }
 
+size_t tree_attention_workspace(int d, int B, int nq, int Hq, int Hkv, tq_dtype dtype) {
+  (void)B;
+  const int rows = Hq / Hkv * nq, nr = row_groups_of(d, dtype == TQ_F32 ? 2 : 1, rows);
+  const size_t split = kJoinHeadBytes + (size_t)2 * kMaxGrid * 8 * nr * (d + 2) * sizeof(float);
+  const size_t tc = tree_tc_workspace(d, rows, dtype);
+  return tc > split ? tc : split;
+}
+
 tq_status launch_byte_attention(const AttnArgs& a, Stream s) {
-  if (tc_takes(a)) return cuda_error("byte attention", launch_tc(a, (cudaStream_t)s));
-  AttnParams p;
-  p.a = a;
-  p.G = a.Hq / a.Hkv;
-  p.rows = p.G * a.nq;
-  p.groups = 0;
-  p.grid = 0;
-  p.heads = (JoinHead*)a.ws;
-  p.part = (float*)((unsigned char*)a.ws + kJoinHeadBytes);
-  cudaError_t e = cudaErrorInvalidValue;
-  switch (a.d) {
-    case 64: e = attention_type<64>(p, (cudaStream_t)s); break;
-    case 128: e = attention_type<128>(p, (cudaStream_t)s); break;
-    case 256: e = attention_type<256>(p, (cudaStream_t)s); break;
-  }
-  return cuda_error("byte attention", e);
+  return cuda_error("byte attention", tc_takes(a) ? launch_tc(a, (cudaStream_t)s) : by_head_dim(a, (cudaStream_t)s));
+}
+
+tq_status launch_tree_attention(const AttnArgs& a, Stream s) {
+  return cuda_error("tree attention", tree_tc_takes(a) ? launch_tree_tc(a, (cudaStream_t)s) : by_head_dim(a, (cudaStream_t)s));
 }
 
 }  // namespace tqb

@@ -184,12 +184,39 @@ __device__ __forceinline__ void convert_q(QFrag<D, NR, T>& q, const QRaw<D, NR, 
   }
 }
 
-// One tile: `blk` is the block in shared memory, tok0 its first token, lim[r][k] the tokens that row
-// 2u + k of group r attends to, edge: some row of the warp does not attend to all 16 tokens, len:
+// Bits j .. j + 31 of a draft's mask m, j counted from the entry's first draft: tokens before it are seen, those
+// past the count are not.
+__device__ __forceinline__ uint32_t tree_word(const uint32_t* m, int words, int cnt, int j) {
+  if (j <= -32) return 0xffffffffu;
+  if (j >= cnt) return 0u;
+  const int w = j >> 5;  // (floor: -1 for the word that reaches back over the first draft)
+  const uint32_t lo = w < 0 ? 0xffffffffu : __ldg(m + w), hi = w + 1 < words ? __ldg(m + w + 1) : 0u;
+  const uint32_t v = __funnelshift_r(lo, hi, j & 31);
+  return cnt - j >= 32 ? v : v & ((1u << (cnt - j)) - 1u);
+}
+
+// Which tokens rows 2u + k of group r do not attend to: those from the row's limit on.
+template <int NR>
+struct Limits {
+  const int (&lim)[NR][2];
+  __device__ __forceinline__ bool operator()(int r, int k, int tok) const { return tok >= lim[r][k]; }
+};
+// The same of a tree: drafts whose bit is clear, and every draft for rows past the count.
+struct TreeLimits {
+  const TreeMasks& M;
+  int b, row0, G, drafts, cnt;  // row0: of the thread's row (0, 0); drafts: the first draft's position
+  __device__ __forceinline__ bool operator()(int r, int k, int tok) const {
+    const int i = (row0 + 8 * r + k) / G, j = tok - drafts;
+    return j >= 0 && (i >= cnt || j >= cnt || !(__ldg(M.row(b, i) + (j >> 5)) >> (j & 31) & 1u));
+  }
+};
+
+// One tile: `blk` is the block in shared memory, tok0 its first token, hide(r, k, tok) the tokens that row
+// 2u + k of group r does not attend to, edge: some row of the warp does not attend to all 16 tokens, len:
 // the sequence's length (codes of tokens behind it may be anything).
-template <int D, int NR, bool EDGE, bool ADD, typename T>
+template <int D, int NR, bool EDGE, bool ADD, typename H, typename T>
 __device__ __forceinline__ void tile_step_edge(const unsigned char* blk, const QFrag<D, NR, T>& q, State<D, NR>& st, int tok0,
-                                               const int (&lim)[NR][2], int len, int lane) {
+                                               H hide, int len, int lane) {
   constexpr int TERMS = kTermsOf<T>;
   const int g = lane >> 2, u = lane & 3;
   float s[NR][4];
@@ -229,7 +256,7 @@ __device__ __forceinline__ void tile_step_edge(const unsigned char* blk, const Q
     if (EDGE) {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (tok0 + g + 8 * (k >> 1) >= lim[r][k & 1]) s[r][k] = -INFINITY;
+        if (hide(r, k & 1, tok0 + g + 8 * (k >> 1))) s[r][k] = -INFINITY;
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) up |= fmaxf(s[r][k], s[r][k + 2]) + (e - kShift) > st.m[r][k];
@@ -311,11 +338,11 @@ __device__ __forceinline__ void tile_step_edge(const unsigned char* blk, const Q
 // ADD: the tile's readout is a product from zero that is then added in fp32.  The tensor cores' own
 // accumulation truncates: chained over the 7600 tiles of a long sequence it was off by 2.8e-4 of the result.
 // fp32 takes it always, 16-bit types where one warp walks a whole sequence.
-template <int D, int NR, bool ADD, typename T>
+template <int D, int NR, bool ADD, typename H, typename T>
 __device__ __forceinline__ void tile_step(const unsigned char* blk, const QFrag<D, NR, T>& q, State<D, NR>& st, int tok0,
-                                          const int (&lim)[NR][2], bool edge, int len, int lane) {
-  if (edge) tile_step_edge<D, NR, true, ADD, T>(blk, q, st, tok0, lim, len, lane);
-  else tile_step_edge<D, NR, false, ADD, T>(blk, q, st, tok0, lim, len, lane);
+                                          H hide, bool edge, int len, int lane) {
+  if (edge) tile_step_edge<D, NR, true, ADD>(blk, q, st, tok0, hide, len, lane);
+  else tile_step_edge<D, NR, false, ADD>(blk, q, st, tok0, hide, len, lane);
 }
 
 template <typename T>
@@ -338,6 +365,12 @@ constexpr int kTcMinRows = 64;
 bool tc_takes(const AttnArgs& a);
 size_t tc_workspace(int rows);
 cudaError_t launch_tc(const AttnArgs& a, cudaStream_t s);
+// A tree's calls on the tensor memory (tq_byte_tree.cu): whether it takes a call, its workspace (0: it never takes
+// such calls), its launch; and its kernel for more than 128 rows (tq_byte_tc.cu).
+bool tree_tc_takes(const AttnArgs& a);
+size_t tree_tc_workspace(int d, int rows, tq_dtype dtype);
+cudaError_t launch_tree_tc(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_tc_tree(const AttnArgs& a, cudaStream_t s);
 
 // Length and count of sequence b as the kernels use them.
 __device__ __forceinline__ int clamped_len(const int32_t* seq_len, int b, int most, int32_t* err) {

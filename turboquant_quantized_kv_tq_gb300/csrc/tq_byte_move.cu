@@ -1,0 +1,305 @@
+// What a step of drafted trees does beside its attention, and reading a cache back:
+//
+// draft_tree: a thread walks from its draft to the root (parents in shared memory) and writes its mask's words from
+// the last to the first as it passes them.  Bound by the launch; a tree's depth is its chain.
+//
+// byte_keep: the accepted path's tokens to where a plain decode would have put them.  A warp per (entry, KV head,
+// side) takes the blocks that receive tokens in order: every token comes from its own place or a later one, so what
+// a block takes is still there when its turn comes, and nobody else writes these blocks.  Bound by the launch and
+// the chain path -> table -> scales -> codes -> store, once per 16 kept tokens.
+//
+// byte_read: values of a batch, both sides, code * 2^e.  A warp per (entry, KV head, block).  Bound by HBM: a byte
+// read and an element written per value.
+#include <algorithm>
+#include <string>
+
+#include "tq_byte.cuh"
+
+namespace tqb {
+namespace {
+
+__device__ __forceinline__ int clamped(const int32_t* count, int b, int n) { return count ? min(max(__ldg(count + b), 0), n) : n; }
+
+__global__ void __launch_bounds__(256) draft_tree_kernel(const TreeArgs a) {
+  constexpr int kDead = -2;
+  __shared__ int up[TQ_MAX_DRAFTS];
+  const int b = blockIdx.x, cnt = clamped(a.count, b, a.n), words = (a.n + 31) / 32;
+  const int start = a.start ? __ldg(a.start + b) : 0;
+  for (int i = threadIdx.x; i < a.n; i += blockDim.x) {
+    const int p = __ldg(a.parents + (long long)b * a.n + i);
+    up[i] = i < cnt && p >= -1 && p < i ? p : kDead;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.n; i += blockDim.x) {
+    int32_t* row = a.masks + ((long long)b * a.n + i) * words;
+    uint32_t bits = 0;
+    int word = words - 1, above = -1, j = i;
+    for (; j >= 0; j = up[j], ++above) {
+      for (; word > j >> 5; --word, bits = 0) row[word] = (int32_t)bits;
+      bits |= 1u << (j & 31);
+    }
+    const bool dead = j == kDead;
+    if (dead) bits = 0, word = words - 1;
+    for (; word >= 0; --word, bits = 0) row[word] = (int32_t)bits;
+    a.positions[(long long)b * a.n + i] = (int32_t)((uint32_t)start + (uint32_t)(dead ? 0 : above));
+  }
+}
+
+// One code at a scale 2^-f times its own.
+__device__ __forceinline__ unsigned char rescaled(unsigned char c, float f) { return (unsigned char)encode2(decode1(c) * f, 0.f); }
+__device__ __forceinline__ uint32_t rescaled4(uint32_t w, float f) {
+  float x[4];
+#pragma unroll
+  for (int m = 0; m < 4; ++m) x[m] = decode1((unsigned char)(w >> (8 * m))) * f;
+  return encode4(x);
+}
+
+constexpr int kKeepWarps = 4;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kKeepWarps) byte_keep_kernel(const KeepArgs a) {
+  const int lane = threadIdx.x & 31, slot = lane & 15;
+  const int unit = blockIdx.x * kKeepWarps + (threadIdx.x >> 5);
+  const int side = unit & 1, h = (unit >> 1) % a.pool.heads, b = (unit >> 1) / a.pool.heads;
+  if (b >= a.B) return;
+  const int start = __ldg(a.start + b), cnt = clamped(a.count, b, a.n);
+  const int32_t* path = a.path + (long long)b * a.n;
+  bool bad = cnt > 0 && start < 0;
+  for (int j = lane; j < cnt; j += 32) bad |= __ldg(path + j) <= (j ? __ldg(path + j - 1) : -1);
+  bad = __any_sync(kFull, bad);
+  if (lane == 0 && h == 0 && side == 0) {
+    if (a.seq_len) a.seq_len[b] = bad ? start : start + cnt;
+    if (bad && a.pool.err) atomicExch(a.pool.err, TQ_DEVERR_BAD_PATH);
+  }
+  if (bad || cnt == 0) return;
+  for (long long tile = start >> 4; tile <= ((long long)start + cnt - 1) >> 4; ++tile) {
+    // lane: where slot `lane % 16` of the block takes its token from
+    const long long pos = tile * 16 + slot, j = pos - start;
+    const long long src = j >= 0 && j < cnt ? (long long)start + __ldg(path + j) : pos;
+    const uint32_t moved = __ballot_sync(kFull, src != pos) & 0xffffu;
+    if (moved == 0) continue;
+    unsigned char* dst = a.pool.base + pool_block(a.pool, page_of(a.pool, b, tile), h) * block_bytes(D);
+    const unsigned char* from = src >> 4 == tile ? dst : a.pool.base + pool_block(a.pool, page_of(a.pool, b, src >> 4), h) * block_bytes(D);
+    const int own = min(kEMax, max(kEMin, log2i(*reinterpret_cast<const float*>(dst + 32 * D + 4 * side))));
+    const int e = min(kEMax, max(kEMin, log2i(*reinterpret_cast<const float*>(from + 32 * D + 4 * side))));
+    const int top = __reduce_max_sync(kFull, e);
+    const float f = exp2i(e - top);
+    const bool round = __any_sync(kFull, e != top);
+    if (side == 0) {
+      constexpr int C = D / 16, PER = D / 32;  // chunks of a row, of a lane
+      uint4 v[PER];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int at = lane + 32 * i, s = at / C, c = at % C;
+        const unsigned char* blk = reinterpret_cast<const unsigned char*>(__shfl_sync(kFull, (unsigned long long)from, s));
+        v[i] = *reinterpret_cast<const uint4*>(blk + k_chunk<D>((int)(__shfl_sync(kFull, src, s) & 15), c));
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int at = lane + 32 * i, s = at / C, c = at % C;
+        const float fs = __shfl_sync(kFull, f, s);
+        if (round && fs != 1.f) {
+          v[i].x = rescaled4(v[i].x, fs);
+          v[i].y = rescaled4(v[i].y, fs);
+          v[i].z = rescaled4(v[i].z, fs);
+          v[i].w = rescaled4(v[i].w, fs);
+        }
+        if (fs != 1.f || (moved >> s & 1)) *reinterpret_cast<uint4*>(dst + k_chunk<D>(s, c)) = v[i];
+      }
+    } else {
+#pragma unroll 1
+      for (int x0 = lane; x0 < D; x0 += 128) {
+        constexpr int E = D < 128 ? D / 32 : 4;  // coordinates at a time: x0, x0 + 32, ...
+        uint4 v[E];
+        unsigned char take[16][E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = *reinterpret_cast<const uint4*>(dst + 16 * D + 16 * (x0 + 32 * i));
+#pragma unroll
+        for (int s = 0; s < 16; ++s) {
+          const unsigned char* blk = reinterpret_cast<const unsigned char*>(__shfl_sync(kFull, (unsigned long long)from, s));
+          const int at = v_slot((int)(__shfl_sync(kFull, src, s) & 15));
+#pragma unroll
+          for (int i = 0; i < E; ++i) {
+            take[s][i] = 0;
+            if (moved >> s & 1) take[s][i] = blk[16 * D + 16 * (x0 + 32 * i) + at];
+          }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+          for (int s = 0; s < 16; ++s) {
+            const int k = v_slot(s) >> 2, sh = 8 * (v_slot(s) & 3);
+            if (moved >> s & 1) w[k] = (w[k] & ~(0xffu << sh)) | ((uint32_t)take[s][i] << sh);
+          }
+          if (round) {
+#pragma unroll
+            for (int s = 0; s < 16; ++s) {
+              const float fs = __shfl_sync(kFull, f, s);
+              const int k = v_slot(s) >> 2, sh = 8 * (v_slot(s) & 3);
+              if (fs != 1.f) w[k] = (w[k] & ~(0xffu << sh)) | ((uint32_t)rescaled((unsigned char)(w[k] >> sh), fs) << sh);
+            }
+          }
+          *reinterpret_cast<uint4*>(dst + 16 * D + 16 * (x0 + 32 * i)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0 && top != own) *reinterpret_cast<float*>(dst + 32 * D + 4 * side) = exp2i(top);
+  }
+}
+
+// N codes (2 or 4 to a 32-bit word's low end) times a power of two, as T.
+template <int N>
+__device__ __forceinline__ void decode_some(const uint32_t* w, float scale, float (&x)[N]) {
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const uint32_t h = codes_half2(w[i >> 1] >> (16 * (i & 1)));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    x[2 * i] = f.x * scale;
+    x[2 * i + 1] = f.y * scale;
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_some(float* p, const float (&x)[N]) {
+  if constexpr (N == 2) {
+    *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      reinterpret_cast<float4*>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+  }
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, const __half*) { return tqd::pack_half2(a, b); }
+__device__ __forceinline__ uint32_t pack2(float a, float b, const __nv_bfloat16*) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <int N, typename T>
+__device__ __forceinline__ void store_some(T* p, const float (&x)[N]) {
+  uint32_t w[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) w[i] = pack2(x[2 * i], x[2 * i + 1], p);
+  if constexpr (N == 2) *reinterpret_cast<uint32_t*>(p) = w[0];
+  else if constexpr (N == 4) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  else *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+constexpr int kReadWarps = 8;
+
+template <int D, typename T>
+__global__ void __launch_bounds__(32 * kReadWarps) byte_read_kernel(const ReadArgs a) {
+  const int lane = threadIdx.x & 31, h = blockIdx.y, b = blockIdx.z;
+  const int start = __ldg(a.start + b), cnt = clamped(a.count, b, a.n);
+  const long long tile = (long long)(start >> 4) + blockIdx.x * kReadWarps + (threadIdx.x >> 5);
+  const long long j0 = tile * 16 - start;  // the token at the block's slot 0
+  if (j0 >= a.n) return;
+  const long long row0 = ((long long)b * a.pool.heads + h) * a.n + j0;
+  T* k = reinterpret_cast<T*>(a.k) + row0 * D;
+  T* v = reinterpret_cast<T*>(a.v) + row0 * D;
+  const int lo = (int)max(0ll, -j0), hi = (int)min(16ll, a.n - j0);   // slots written,
+  const int live = (int)min((long long)hi, max(0ll, cnt - j0));       // and those of them below that are read
+  constexpr int E = D / 32;                                           // V: coordinates E lane ..
+  constexpr int KE = sizeof(T) == 4 ? 4 : 8, LPR = D / KE;           // K: codes of a lane, lanes of a row
+  constexpr int KI = 16 * LPR / 32;                                   // K: pieces of a lane
+  uint32_t kw[KI][KE / 4];
+  uint4 vw[E];
+  float2 scale = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < KI; ++i)
+#pragma unroll
+    for (int m = 0; m < KE / 4; ++m) kw[i][m] = 0;
+#pragma unroll
+  for (int i = 0; i < E; ++i) vw[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (live > lo) {
+    const unsigned char* blk = a.pool.base + pool_block(a.pool, page_of(a.pool, b, tile), h) * block_bytes(D);
+    scale = __ldg(reinterpret_cast<const float2*>(blk + 32 * D));
+#pragma unroll
+    for (int i = 0; i < KI; ++i) {
+      const int at = lane + 32 * i, t = at / LPR, x = at % LPR * KE;
+      const unsigned char* p = blk + k_chunk<D>(t, x >> 4) + (x & 15);
+      if constexpr (KE == 8) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+        kw[i][0] = w.x, kw[i][1] = w.y;
+      } else {
+        kw[i][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) vw[i] = __ldg(reinterpret_cast<const uint4*>(blk + 16 * D + 16 * (E * lane + i)));
+  }
+#pragma unroll
+  for (int i = 0; i < KI; ++i) {
+    const int at = lane + 32 * i, t = at / LPR, x = at % LPR * KE;
+    float y[KE];
+    decode_some<KE>(kw[i], scale.x, y);
+    if (t >= live)
+#pragma unroll
+      for (int m = 0; m < KE; ++m) y[m] = 0.f;
+    if (t >= lo && t < hi) store_some<KE>(k + (long long)t * D + x, y);
+  }
+#pragma unroll
+  for (int t = 0; t < 16; ++t) {
+    // byte v_slot(t) of each of the lane's coordinates
+    uint32_t w[(E + 3) / 4] = {};
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const uint32_t q[4] = {vw[i].x, vw[i].y, vw[i].z, vw[i].w};
+      w[i >> 2] |= (q[v_slot(t) >> 2] >> (8 * (v_slot(t) & 3)) & 0xffu) << (8 * (i & 3));
+    }
+    float y[E];
+    decode_some<E>(w, scale.y, y);
+    if (t >= live)
+#pragma unroll
+      for (int m = 0; m < E; ++m) y[m] = 0.f;
+    if (t >= lo && t < hi) store_some<E>(v + (long long)t * D + E * lane, y);
+  }
+}
+
+template <int D>
+cudaError_t keep_go(const KeepArgs& a, cudaStream_t s) {
+  const long long units = 2ll * a.B * a.pool.heads;
+  byte_keep_kernel<D><<<(unsigned)((units + kKeepWarps - 1) / kKeepWarps), 32 * kKeepWarps, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t read_go(const ReadArgs& a, cudaStream_t s) {
+  const int blocks = (int)(((long long)a.n + 15 + 15) / 16);  // that the tokens touch, at most
+  const dim3 grid((blocks + kReadWarps - 1) / kReadWarps, a.pool.heads, a.B);
+  if (a.dtype == TQ_F32) byte_read_kernel<D, float><<<grid, 32 * kReadWarps, 0, s>>>(a);
+  else if (a.dtype == TQ_BF16) byte_read_kernel<D, __nv_bfloat16><<<grid, 32 * kReadWarps, 0, s>>>(a);
+  else byte_read_kernel<D, __half><<<grid, 32 * kReadWarps, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+tq_status launch_draft_tree(const TreeArgs& a, Stream s) {
+  draft_tree_kernel<<<a.B, std::min(256, (a.n + 31) / 32 * 32), 0, (cudaStream_t)s>>>(a);
+  return cuda_error("draft tree", cudaGetLastError());
+}
+
+tq_status launch_byte_keep(const KeepArgs& a, Stream s) {
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (a.d) {
+    case 64: e = keep_go<64>(a, (cudaStream_t)s); break;
+    case 128: e = keep_go<128>(a, (cudaStream_t)s); break;
+    case 256: e = keep_go<256>(a, (cudaStream_t)s); break;
+  }
+  return cuda_error("byte keep", e);
+}
+
+tq_status launch_byte_read(const ReadArgs& a, Stream s) {
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (a.d) {
+    case 64: e = read_go<64>(a, (cudaStream_t)s); break;
+    case 128: e = read_go<128>(a, (cudaStream_t)s); break;
+    case 256: e = read_go<256>(a, (cudaStream_t)s); break;
+  }
+  return cuda_error("byte read", e);
+}
+
+}  // namespace tqb

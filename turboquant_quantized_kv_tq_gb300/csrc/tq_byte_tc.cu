@@ -37,31 +37,15 @@
 #include <string>
 #include <type_traits>
 
-#include "tq_byte_attn.cuh"
-#include "tq_tc05.cuh"
+#include "tq_byte_tc.cuh"
 
 namespace tqb {
 namespace {
 
 using tqd::mbar_wait;
 
-constexpr int kTok = 128;          // tokens per tile
 constexpr int kD = 128;
-constexpr int kThreads = 512;
-constexpr int kRowRegs = 192, kOtherRegs = 64;  // 256 * 192 + 256 * 64 = 512 * 128, the launch's registers
-constexpr int kGroupCost = 8;      // virtual tiles of a row group: what a range costs beside its tiles (4: 125 us for
-                                   // the last 64 positions, 8: 122, 14: 124)
-constexpr float kTop = 7.f;        // M lies this far below the maximum it was set from
-constexpr float kSlack = 15.f;     // M is raised when the maximum passes it by this: P <= 2^15
 constexpr int kBlk = 32 * kD + 32;
-
-struct TcParams {
-  AttnArgs a;
-  int G, rows, groups;  // groups: row groups of a slab
-  JoinHead* heads;  // [grid]
-  float* part;      // [grid][first stretch, last](M[ROWS], l[ROWS], O[ROWS][128])
-  int grid;
-};
 
 template <int NT, int NQ>
 struct Plan {
@@ -82,22 +66,6 @@ struct Plan {
 enum Bar { K_FULL = 0, K_EMPTY = 2, VR_FULL = 4, VR_EMPTY = 6, V_FULL = 8, V_EMPTY = 10, S_FULL = 12, O_DONE = 14,
            Q_FULL = 16, P_FULL = 18, SC_FULL = 22, SC_EMPTY = 26, SC_READY = 30, BAR_COUNT = 34 };
 static_assert(8 * BAR_COUNT + 4 <= 320, "barriers and the tensor-memory slot");
-
-// 128-byte-swizzled K-major operand: rows of 128 bytes in groups of 8 (1024 bytes).
-__device__ __forceinline__ uint64_t sdesc128(uint32_t addr) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
-__device__ __forceinline__ bool elected() {
-  uint32_t r;
-  asm volatile("{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\nselp.u32 %0, 1, 0, e;\n}\n" : "=r"(r));
-  return r != 0;
-}
-__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
-      :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
-}
 
 // Products of one elected lane of a converged warp, from constant operands.
 constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);  // M = N = 128, fp32 D
@@ -138,245 +106,7 @@ __device__ __forceinline__ void issue_readout(uint32_t sb, int i, int h, bool ac
   __syncwarp();
 }
 
-// Tokens that the rows of group rg of an entry attend to at most, and tiles.
-__device__ __forceinline__ int group_limit(const TcParams& p, int rows_per, int rg, int len, int cnt) {
-  const int last = min((rg + 1) * rows_per, p.rows) - 1;
-  const int i = min(cnt - 1, last / p.G);
-  return i * p.G + p.G - 1 < rg * rows_per ? 0 : row_limit(i, len, cnt);
-}
-__device__ __forceinline__ int tiles_of(int limit) { return (limit + kTok - 1) / kTok; }
-__device__ __forceinline__ int cost_of(int tiles) { return tiles > 0 ? tiles + kGroupCost : 0; }
-
-// Costs before each entry (order: entry, row group, head); written by warp 0.
-__device__ __forceinline__ void fill_plan(const TcParams& p, int rows_per, int* pre, int32_t* err) {
-  const int lane = threadIdx.x & 31, most = p.a.pool.max_blocks * 16;
-  if (threadIdx.x < 32) {
-    int run = 0;
-    for (int b0 = 0; b0 < p.a.B; b0 += 32) {
-      const int b = b0 + lane;
-      int t = 0;
-      if (b < p.a.B) {
-        const int len = clamped_len(p.a.seq_len, b, most, err), cnt = clamped_count(p.a.count, b, p.a.nq);
-        for (int rg = 0; rg < p.groups; ++rg) t += cost_of(tiles_of(group_limit(p, rows_per, rg, len, cnt)));
-        t *= p.a.Hkv;
-      }
-#pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const int o = __shfl_up_sync(kFull, t, m);
-        if (lane >= m) t += o;
-      }
-      if (b < p.a.B) pre[b + 1] = run + t;
-      run += __shfl_sync(kFull, t, 31);
-    }
-    if (lane == 0) pre[0] = 0;
-  }
-}
-
-struct Seg {
-  int b, h, rg, len, cnt, limit;
-  int t0, t1, tiles;
-  int start, next;  // of the slab's group, of the stretch after this one
-};
-__device__ __forceinline__ Seg seg_at(const TcParams& p, int rows_per, const int* pre, int at, int end) {
-  Seg s;
-  int lo = 0, hi = p.a.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid + 1] <= at) lo = mid + 1;
-    else hi = mid;
-  }
-  s.b = lo;
-  const int most = p.a.pool.max_blocks * 16;
-  s.len = clamped_len(p.a.seq_len, s.b, most, nullptr);
-  s.cnt = clamped_count(p.a.count, s.b, p.a.nq);
-  int x = at - pre[s.b], span = 1;
-  s.rg = 0;
-  for (;; ++s.rg) {
-    s.limit = group_limit(p, rows_per, s.rg, s.len, s.cnt);
-    s.tiles = tiles_of(s.limit);
-    span = cost_of(s.tiles);
-    if (x < span * p.a.Hkv || s.rg + 1 >= p.groups) break;
-    x -= span * p.a.Hkv;
-  }
-  span = max(span, 1);
-  s.h = x / span;
-  x -= s.h * span;
-  s.start = at - x;
-  s.t0 = min(x, s.tiles);
-  s.t1 = min(s.tiles, x + (end - at));
-  s.next = min(end, at + span - x);
-  return s;
-}
-
-__device__ __forceinline__ int range_of(int total, int grid) { return (total + grid - 1) / grid; }
-
-template <typename T>
-__device__ __forceinline__ T* out_row(const TcParams& p, int b, int h, int row) {
-  const int i = row / p.G, hd = h * p.G + row - i * p.G;
-  return reinterpret_cast<T*>(p.a.out) + (((long long)b * p.a.nq + i) * p.a.Hq + hd) * kD;
-}
-
-__device__ __forceinline__ void store16(__nv_bfloat16* dst, const float* x) {
-  uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-}
-__device__ __forceinline__ void store16(__half* dst, const float* x) {
-  uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = tqd::pack_half2(x[2 * i], x[2 * i + 1]);
-  reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-}
-
-// One query row as NT e4m3 terms in the swizzled operand tiles at q (term t at q + 16384 t); returns
-// the factor of its scores, log2(e) |scale| 2^e (the sign of `scale` goes into the terms).
-template <typename T, int NT>
-__device__ __forceinline__ float query_row(const T* src, bool live, float scale, unsigned char* q, int r) {
-  uint4 raw[16];
-#pragma unroll
-  for (int c = 0; c < 16; ++c) raw[c] = live ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0u, 0u, 0u, 0u);
-  float amax = 0.f;
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    float x[16];
-    unpack16(Raw16<T>{{raw[2 * c], raw[2 * c + 1]}}, x, src);
-#pragma unroll
-    for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(x[k]));
-  }
-  const bool odd = !(amax <= 3.402823466e38f);  // an infinity: the row's result is NaN, as the formula's is
-  const unsigned u = __float_as_uint(amax);
-  int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);  // amax <= 448 2^e
-  e = min(120, max(-120, e));
-  if (amax == 0.f || odd) e = 0;
-  const float inv = scale < 0.f ? -exp2i(-e) : exp2i(-e);
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    float x[16];
-    unpack16(Raw16<T>{{raw[2 * c], raw[2 * c + 1]}}, x, src);
-    const int at = r * 128 + ((c ^ (r & 7)) << 4);
-#pragma unroll
-    for (int k = 0; k < 16; ++k) x[k] *= inv;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      uint32_t w[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t two[2];
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          float &a = x[4 * k + 2 * m], &b = x[4 * k + 2 * m + 1];
-          two[m] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-          const uint32_t back = codes_half2(two[m]);
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
-          a -= f.x;
-          b -= f.y;
-        }
-        w[k] = two[0] | (two[1] << 16);
-      }
-      *reinterpret_cast<uint4*>(q + 16384 * t + at) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  }
-  return odd ? __uint_as_float(0x7fc00000u) : fabsf(scale) * kLog2e * exp2i(e);
-}
-
-// Pairs of fp32 values in one instruction.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
-// 32 columns of this thread's lane, without the wait for the load.
-__device__ __forceinline__ void ld32_async(uint32_t taddr, float* v) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
-        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
-        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-      : "r"(taddr));
-}
-// The wait for the loads before it, tied to the N values it makes valid.
-template <int N>
-__device__ __forceinline__ void ld_wait(float* v) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
-}
-// 8 columns stored, without the wait.
-__device__ __forceinline__ void st8_async(uint32_t taddr, const uint32_t* v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n"
-               :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
-// The largest s + e of one block's 16 scores (left: those the row attends to, when EDGE).
-template <bool EDGE>
-__device__ __forceinline__ float block_top(float* v, int left, float a, float e) {
-  if (EDGE) {
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-      if (k >= left) v[k] = -INFINITY;
-  }
-  float m = v[0];
-#pragma unroll
-  for (int k = 1; k < 15; k += 2) m = fmaxf(m, fmaxf(v[k], v[k + 1]));
-  m = fmaxf(m, v[15]);
-  const float top = fmaf(m, a, e);
-  // (a block without a token of the row stays out: its scale may be anything)
-  return EDGE && m == -INFINITY ? -INFINITY : top;
-}
-// P of one block as fp16 pairs in V's stored token order; the sum of its 16 values is returned.
-template <bool EDGE>
-__device__ __forceinline__ float block_p(const float* v, int left, float a, float b, uint32_t* w) {
-  const uint64_t a2 = pair(a, a), b2 = pair(b, b);
-  float x[16];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    unpair(fma2(pair(v[2 * k], v[2 * k + 1]), a2, b2), x[2 * k], x[2 * k + 1]);
-    x[2 * k] = ex2(x[2 * k]);
-    x[2 * k + 1] = ex2(x[2 * k + 1]);
-  }
-  if (EDGE) {
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-      if (k >= left) x[k] = 0.f;
-  }
-  uint64_t s0 = pair(x[0], x[1]), s1 = pair(x[2], x[3]);
-#pragma unroll
-  for (int k = 2; k < 8; k += 2) {
-    s0 = add2(s0, pair(x[2 * k], x[2 * k + 1]));
-    s1 = add2(s1, pair(x[2 * k + 2], x[2 * k + 3]));
-  }
-  float t0, t1;
-  unpair(add2(s0, s1), t0, t1);
-#pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    w[2 * m] = tqd::pack_half2(x[2 * m], x[2 * m + 1]);
-    w[2 * m + 1] = tqd::pack_half2(x[2 * m + 8], x[2 * m + 9]);
-  }
-  return t0 + t1;
-}
-
-template <typename T, int NT, int NQ>
+template <typename T, int NT, int NQ, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
   using L = Plan<NT, NQ>;
   extern __shared__ __align__(1024) unsigned char sm[];
@@ -417,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
     }
     tqd::fence_mbar_init();
   }
-  fill_plan(p, L::ROWS, pre, blockIdx.x == 0 ? A.pool.err : nullptr);
+  fill_plan<TREE>(p, L::ROWS, pre, blockIdx.x == 0 ? A.pool.err : nullptr);
   tqd::tc_fence_before();
   __syncthreads();
   tqd::tc_fence_after();
@@ -447,10 +177,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
       for (int s = blockIdx.x; s < slabs; s += gridDim.x) {
         const int h = s % A.Hkv, rg = s / A.Hkv % p.groups, b = s / A.Hkv / p.groups;
         const int len = clamped_len(A.seq_len, b, most, nullptr), cnt = clamped_count(A.count, b, A.nq);
-        if (group_limit(p, L::ROWS, rg, len, cnt) > 0) continue;
+        if (group_limit<TREE>(p, L::ROWS, rg, len, cnt) > 0) continue;
         const int row = rg * L::ROWS + i * 128 + r;
         if (row < p.rows) {
-          T* o = out_row<T>(p, b, h, row);
+          T* o = out_row<kD, T>(p, b, h, row);
           for (int c = 0; c < 16; ++c) reinterpret_cast<uint4*>(o)[c] = make_uint4(0u, 0u, 0u, 0u);
         }
       }
@@ -458,17 +188,20 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
     int at = begin;
     bool headed = false;
     while (at < end && ok) {
-      const Seg s = seg_at(p, L::ROWS, pre, at, end);
+      const Seg s = seg_at<TREE>(p, L::ROWS, pre, at, end);
       const bool first = at == begin;
       at = s.next;
       if (s.t0 == s.t1) continue;
       const int row = s.rg * L::ROWS + i * 128 + r;
       const bool live = row < p.rows;
       const int qi = live ? row / p.G : 0, hd = s.h * p.G + (live ? row - qi * p.G : 0);
-      const int lim = live ? row_limit(qi, s.len, s.cnt) : 0;
-      const int least = __reduce_min_sync(kFull, live ? lim : 0x7fffffff);
-      const float f = query_row<T, NT>(reinterpret_cast<const T*>(A.q.p) + s.b * A.q.sb + qi * A.q.st + hd * A.q.sh, live,
-                                       A.scale, sm + L::Q + i * NT * 16384, r);
+      // (a tree's rows past the count are zero queries whose sums are dropped, so that they hide nothing)
+      const bool asks = live && (!TREE || qi < s.cnt);
+      const int drafts = s.len - s.cnt;  // the first draft's position (TREE)
+      const int lim = !live ? 0 : TREE ? max(0, drafts) : row_limit(qi, s.len, s.cnt);
+      const int least = __reduce_min_sync(kFull, asks ? lim : 0x7fffffff);
+      const float f = query_row<kD, NT, T>(reinterpret_cast<const T*>(A.q.p) + s.b * A.q.sb + qi * A.q.st + hd * A.q.sh, asks,
+                                           A.scale, sm + L::Q + i * NT * 16384, r);
       tqd::tc_fence_smem();
       tqd::tc_mbar_arrive(bar(Q_FULL, i));
       float M = -INFINITY, l = 0.f;
@@ -481,6 +214,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
         tqd::tc_fence_after();
         const float4* sc = reinterpret_cast<const float4*>(sm + L::SCALES + 128 * ss);
         const int left = lim - kTok * t;  // tokens of this tile that the row attends to
+        uint32_t window[4];               // (of a tree: those whose bit is set)
+        if constexpr (TREE && EDGE) tree_window(A.tree, s.b, qi, asks, s.cnt, kTok * t - drafts, window);
+        auto hide = [&](int g) {
+          if constexpr (TREE && EDGE) return HideClear{window[g >> 1] >> (16 * (g & 1))};
+          else return HideFrom{left - 16 * g};
+        };
         float v[128];
         ld32_async(t_s, v);
         ld32_async(t_s + 32, v + 32);
@@ -494,12 +233,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
         ld_wait<64>(v);
         ld32_async(t_s + 64, v + 64);
         ld32_async(t_s + 96, v + 96);
-        float top = block_top<EDGE>(v, left, a[0], e[0]);
+        float top = block_top<EDGE>(v, hide(0), a[0], e[0]);
 #pragma unroll
-        for (int g = 1; g < 4; ++g) top = fmaxf(top, block_top<EDGE>(v + 16 * g, left - 16 * g, a[g], e[g]));
+        for (int g = 1; g < 4; ++g) top = fmaxf(top, block_top<EDGE>(v + 16 * g, hide(g), a[g], e[g]));
         ld_wait<64>(v + 64);
 #pragma unroll
-        for (int g = 4; g < 8; ++g) top = fmaxf(top, block_top<EDGE>(v + 16 * g, left - 16 * g, a[g], e[g]));
+        for (int g = 4; g < 8; ++g) top = fmaxf(top, block_top<EDGE>(v + 16 * g, hide(g), a[g], e[g]));
         const bool raise = top > M + kSlack;
         if (__any_sync(kFull, raise)) {
           const float m_new = raise ? top - kTop : M;
@@ -524,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
           uint32_t w[8];
-          const float sum = block_p<EDGE>(v + 16 * g, left - 16 * g, a[g], e[g] - mr, w);
+          const float sum = block_p<EDGE>(v + 16 * g, hide(g), a[g], e[g] - mr, w);
           l = fmaf(sum, sc[g].z, l);
           st8_async(t_s + 8 * g, w);
           if (g == L::FIRST - 1 || g == 7) {
@@ -543,17 +282,18 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
       }
       if (!ok || !wait(bar(O_DONE, i), (n - 1) & 1)) break;
       tqd::tc_fence_after();
+      if (TREE && !asks) l = 0.f;
       const bool whole = s.t0 == 0 && s.t1 == s.tiles;
       if (whole) {
         const float il = l > 0.f || l != l ? 1.f / l : 0.f;
-        T* o = out_row<T>(p, s.b, s.h, live ? row : 0);
+        T* o = out_row<kD, T>(p, s.b, s.h, live ? row : 0);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float v[32];
           tqd::tc_ld32(t_o + 32 * c, v);
           if (live) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] *= il;
+            for (int k = 0; k < 32; ++k) v[k] = !TREE || asks ? v[k] * il : 0.f;
             store16(o + 32 * c, v);
             store16(o + 32 * c + 16, v + 16);
           }
@@ -568,6 +308,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
         for (int c = 0; c < 4; ++c) {
           float v[32];
           tqd::tc_ld32(t_o + 32 * c, v);
+          if (TREE && !asks) {  // (they may hold NaN: what lies behind the tokens is hidden from the others only)
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = 0.f;
+          }
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             reinterpret_cast<float4*>(o + 32 * c)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
@@ -585,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
     uint32_t n = 0;
     int at = begin;
     while (at < end && ok) {
-      const Seg s = seg_at(p, L::ROWS, pre, at, end);
+      const Seg s = seg_at<TREE>(p, L::ROWS, pre, at, end);
       at = s.next;
       for (int t = s.t0; t < s.t1; ++t, ++n) {
         const int st = n & 1, ss = n % L::SC;
@@ -641,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
     uint32_t n = 0;
     int at = begin;
     while (at < end && ok) {
-      const Seg s = seg_at(p, L::ROWS, pre, at, end);
+      const Seg s = seg_at<TREE>(p, L::ROWS, pre, at, end);
       at = s.next;
       const int blocks = (s.limit + 15) >> 4;
       int page = 0;
@@ -684,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
     uint32_t n = 0, segs = 0;
     int at = begin;
     while (at < end && ok) {
-      const Seg s = seg_at(p, L::ROWS, pre, at, end);
+      const Seg s = seg_at<TREE>(p, L::ROWS, pre, at, end);
       at = s.next;
       if (s.t0 == s.t1) continue;
       if (!wait(bar(K_FULL, n & 1), (n >> 1) & 1)) break;
@@ -727,15 +471,15 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
   }
 }
 
-template <typename T, int NT, int NQ>
+template <typename T, int NT, int NQ, bool TREE>
 cudaError_t tc_go(TcParams p, int sms, int device, cudaStream_t s) {
   using L = Plan<NT, NQ>;
   static std::atomic<uint64_t> done{0};
   p.groups = (p.rows + L::ROWS - 1) / L::ROWS;
   p.grid = sms;
-  cudaError_t e = allow_smem((const void*)tc_kernel<T, NT, NQ>, L::SMEM, device, done);
+  cudaError_t e = allow_smem((const void*)tc_kernel<T, NT, NQ, TREE>, L::SMEM, device, done);
   if (e != cudaSuccess) return e;
-  tc_kernel<T, NT, NQ><<<p.grid, kThreads, L::SMEM, s>>>(p);
+  tc_kernel<T, NT, NQ, TREE><<<p.grid, kThreads, L::SMEM, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (p.grid == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
@@ -767,17 +511,29 @@ size_t tc_workspace(int rows) {
 
 cudaError_t launch_tc(const AttnArgs& a, cudaStream_t s) {
   TcParams p;
-  p.a = a;
-  p.G = a.Hq / a.Hkv;
-  p.rows = p.G * a.nq;
-  p.groups = p.grid = 0;
-  p.heads = (JoinHead*)a.ws;
-  p.part = (float*)((unsigned char*)a.ws + kJoinHeadBytes);
-  int dev, sms = sm_count(&dev);
-  if (sms > kMaxSms) sms = kMaxSms;
+  int dev;
+  const int sms = tc_params(a, &p, &dev);
   if (a.dtype == TQ_BF16)
-    return p.rows > 128 ? tc_go<__nv_bfloat16, 2, 2>(p, sms, dev, s) : tc_go<__nv_bfloat16, 2, 1>(p, sms, dev, s);
-  return p.rows > 128 ? tc_go<__half, 3, 2>(p, sms, dev, s) : tc_go<__half, 3, 1>(p, sms, dev, s);
+    return p.rows > 128 ? tc_go<__nv_bfloat16, 2, 2, false>(p, sms, dev, s) : tc_go<__nv_bfloat16, 2, 1, false>(p, sms, dev, s);
+  return p.rows > 128 ? tc_go<__half, 3, 2, false>(p, sms, dev, s) : tc_go<__half, 3, 1, false>(p, sms, dev, s);
+}
+
+int tc_params(const AttnArgs& a, TcParams* p, int* dev) {
+  p->a = a;
+  p->G = a.Hq / a.Hkv;
+  p->rows = p->G * a.nq;
+  p->groups = p->grid = 0;
+  p->heads = (JoinHead*)a.ws;
+  p->part = (float*)((unsigned char*)a.ws + kJoinHeadBytes);
+  const int sms = sm_count(dev);
+  return sms > kMaxSms ? kMaxSms : sms;
+}
+
+cudaError_t launch_tc_tree(const AttnArgs& a, cudaStream_t s) {
+  TcParams p;
+  int dev;
+  const int sms = tc_params(a, &p, &dev);
+  return a.dtype == TQ_BF16 ? tc_go<__nv_bfloat16, 2, 2, true>(p, sms, dev, s) : tc_go<__half, 3, 2, true>(p, sms, dev, s);
 }
 
 }  // namespace tqb

@@ -1,0 +1,529 @@
+// Attention of a tree's drafts over the byte cache on the 5th-generation tensor cores: up to 128 (query, head) rows
+// of a slab (batch entry, KV head) at a time, head dims 64 and 128, bf16 and fp16 queries.
+//
+// The mathematics, the operands and the softmax are those of tq_byte_tc.cu, where two tiles of 128 rows take turns
+// on one token tile, so that one's softmax runs beside the other's products.  A tree has rarely more than 128 rows
+// (16 drafts of 4 heads per KV head: 64), and a lone row tile would leave the tensor cores idle through its softmax.
+// Here the two groups of row warps hold the same rows and take turns on the token tiles: group i takes tiles
+// n = i (mod 2), with scores S_i, sums O_i, reference M_i and l_i of its own,
+//   o = (2^(M_0 - M) O_0 + 2^(M_1 - M) O_1) / (2^(M_0 - M) l_0 + 2^(M_1 - M) l_1),  M = max(M_0, M_1),
+// joined from tensor memory at the end of a stretch (both groups' warps reach the same lanes).  More than 128 rows
+// go to tc_kernel with two row tiles (head dim 128), which reads the pool half as often, or take turns here (64).
+//
+// Which drafts a row sees matters only in the last tiles: rows read their masks there, a window of 128 bits a tile,
+// and tiles before the first draft are the same as without a tree.
+//
+// Warps: as in tq_byte_tc.cu.
+#include <atomic>
+#include <string>
+#include <type_traits>
+
+#include "tq_byte_tc.cuh"
+
+namespace tqb {
+namespace {
+
+using tqd::mbar_wait;
+
+template <int D, int NT>
+struct Plan {
+  static constexpr int BLK = 32 * D + 32;
+  static constexpr int TILE = 128 * D;                            // bytes of a term of Q, of a tile's codes
+  static constexpr int FIRST = 4;                                 // blocks of a tile in the first part of P
+  static constexpr int KS = 4;                                    // K stages: scores run two tiles ahead
+  static constexpr int SC = 4;                                    // scale stages of 8 x 16 bytes
+  static constexpr int Q = 0, KR = Q + NT * TILE, VR = KR + KS * TILE, V16 = VR + 2 * TILE;
+  // [stage][block]: as copied (K scale, V scale, -, -), then in place (K scale, e, 2^-e, -)
+  static constexpr int SCALES = V16 + 4 * TILE, ML = SCALES + SC * 128, BARS = ML + 2 * 128 * 8, PRE = BARS + 320;
+  static constexpr int SMEM = PRE + (TQ_MAX_BATCH + 1) * 4;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static constexpr int PART = 128 * (D + 2);                      // floats of a partial
+};
+// (P_FULL: half h of group i at 2 i + h)
+enum Bar { K_FULL = 0, K_EMPTY = 4, VR_FULL = 8, VR_EMPTY = 10, V_FULL = 12, V_EMPTY = 14, S_FULL = 16, O_DONE = 18,
+           P_FULL = 20, SC_FULL = 24, SC_EMPTY = 28, SC_READY = 32, Q_FULL = 36, ML_FULL = 37, OUT_READ = 38, BAR_COUNT = 39 };
+static_assert(8 * BAR_COUNT + 4 <= 320, "barriers and the tensor-memory slot");
+
+// Swizzled K-major operand of rows of D codes: 128-byte swizzle in groups of 1024 bytes, 64-byte in 512.
+template <int D>
+__device__ __forceinline__ uint64_t sdesc_codes(uint32_t addr) {
+  if constexpr (D == 128) return sdesc128(addr);
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (1ull << 16) | ((uint64_t)(512 >> 4) << 32) | (1ull << 46) | (4ull << 61);
+}
+__host__ __device__ constexpr uint32_t idesc(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24); }  // M = 128
+
+// S of the tile in K buffer ST, for group ST % 2.
+template <int D, int NT, int ST>
+__device__ __forceinline__ void issue_scores(uint32_t sb) {
+  using L = Plan<D, NT>;
+  constexpr int i = ST & 1;
+  const uint64_t q = sdesc_codes<D>(sb + L::Q), k = sdesc_codes<D>(sb + L::KR + ST * L::TILE);
+  if (elected()) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j)
+        mma_f8(128 * i, q + (uint64_t)(t * (L::TILE >> 4) + 2 * j), k + 2 * j, idesc(kTok), t + j > 0);
+    tqd::tc_commit(sb + L::BARS + 8 * (S_FULL + i));
+    tqd::tc_commit(sb + L::BARS + 8 * (K_EMPTY + ST));
+  }
+  __syncwarp();
+}
+template <int D, int NT>
+__device__ __forceinline__ void issue_scores(uint32_t sb, uint32_t n) {
+  switch (n & 3) {
+    case 0: return issue_scores<D, NT, 0>(sb);
+    case 1: return issue_scores<D, NT, 1>(sb);
+    case 2: return issue_scores<D, NT, 2>(sb);
+    default: return issue_scores<D, NT, 3>(sb);
+  }
+}
+// Part h (blocks [0, FIRST), [FIRST, 8)) of O_i += P_i V of the tile in V buffer i (accumulate: not the group's
+// first tile of a stretch).
+template <int D, int NT, int i>
+__device__ __forceinline__ void issue_readout(uint32_t sb, int h, bool accumulate) {
+  using L = Plan<D, NT>;
+  const uint64_t v = sdesc128(sb + L::V16 + i * 2 * L::TILE);
+  if (elected()) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if ((k >= L::FIRST) == (h == 1))
+        tqd::tc_mma_f16_ta(256 + D * i, 128 * i + 8 * k, v + (uint64_t)((k >> 2) * (L::TILE >> 4) + 2 * (k & 3)), idesc(D),
+                           accumulate || k > 0);
+    if (h == 1) {
+      tqd::tc_commit(sb + L::BARS + 8 * (O_DONE + i));
+      tqd::tc_commit(sb + L::BARS + 8 * (V_EMPTY + i));
+    }
+  }
+  __syncwarp();
+}
+
+template <int D, int NT, typename T>
+__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
+  using L = Plan<D, NT>;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  const AttnArgs& A = p.a;
+  const int warp = __shfl_sync(kFull, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const uint32_t sb = (uint32_t)__cvta_generic_to_shared(sm);
+  const uint32_t bars = sb + L::BARS;
+  auto bar = [&](int kind, int i) { return bars + 8 * (kind + i); };
+  uint32_t* slot = reinterpret_cast<uint32_t*>(sm + L::BARS + 8 * BAR_COUNT);
+  int* pre = reinterpret_cast<int*>(sm + L::PRE);
+  if (sb & 1023u) {  // the swizzled operands need it (the plan gives it)
+    if (threadIdx.x == 0) {
+      p.heads[blockIdx.x].last = -1;
+      if (A.pool.err) atomicExch(A.pool.err, TQ_DEVERR_SMEM_PLAN);
+    }
+    return;
+  }
+  if (warp == 13) tqd::tc_alloc((uint32_t)__cvta_generic_to_shared(slot), 512);
+  if (threadIdx.x == 32) {
+    for (int i = 0; i < 2; ++i) {
+      tqd::mbar_init(bar(VR_FULL, i), 1);
+      tqd::mbar_init(bar(VR_EMPTY, i), 4);
+      tqd::mbar_init(bar(V_FULL, i), 4);
+      tqd::mbar_init(bar(V_EMPTY, i), 1);
+      tqd::mbar_init(bar(S_FULL, i), 1);
+      tqd::mbar_init(bar(P_FULL, 2 * i), 128);
+      tqd::mbar_init(bar(P_FULL, 2 * i + 1), 128);
+      tqd::mbar_init(bar(O_DONE, i), 1);
+    }
+    for (int i = 0; i < L::KS; ++i) {
+      tqd::mbar_init(bar(K_FULL, i), 1);
+      tqd::mbar_init(bar(K_EMPTY, i), 1);
+    }
+    for (int i = 0; i < L::SC; ++i) {
+      tqd::mbar_init(bar(SC_FULL, i), 1);
+      tqd::mbar_init(bar(SC_EMPTY, i), 4);
+      tqd::mbar_init(bar(SC_READY, i), 1);
+    }
+    tqd::mbar_init(bar(Q_FULL, 0), 256);
+    tqd::mbar_init(bar(ML_FULL, 0), 256);
+    tqd::mbar_init(bar(OUT_READ, 0), 256);
+    tqd::fence_mbar_init();
+  }
+  fill_plan<true>(p, 128, pre, blockIdx.x == 0 ? A.pool.err : nullptr);
+  tqd::tc_fence_before();
+  __syncthreads();
+  tqd::tc_fence_after();
+  // all 512 columns are this block's: they begin at column 0, lane 0 (S_i at 128 i, O_i at 256 + D i)
+  const bool whole_tmem = *slot == 0;
+  const int total = pre[A.B], per = range_of(total, p.grid);
+  const int begin = min(total, (int)blockIdx.x * per), end = min(total, begin + per);
+
+  bool ok = whole_tmem;  // cleared by a wait that gave up: the role stops working and ends
+  auto wait = [&](uint32_t b, uint32_t parity) {
+    if (ok && !mbar_wait(b, parity, kWaitLimit)) ok = false;
+    return ok;
+  };
+
+  if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRowRegs));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+  if (warp < 8) {
+    // ---- rows: group i takes the tiles n = i (mod 2) of the block's sequence
+    const int i = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_s = lanes + 128 * i, t_o = lanes + 256 + D * i;
+    float2* ml = reinterpret_cast<float2*>(sm + L::ML);  // [group][row]
+    // groups without a live row: zeros, spread over the grid
+    {
+      const int slabs = A.B * p.groups * A.Hkv, most = A.pool.max_blocks * 16;
+      for (int s = blockIdx.x; s < slabs; s += gridDim.x) {
+        const int h = s % A.Hkv, rg = s / A.Hkv % p.groups, b = s / A.Hkv / p.groups;
+        const int len = clamped_len(A.seq_len, b, most, nullptr), cnt = clamped_count(A.count, b, A.nq);
+        if (group_limit<true>(p, 128, rg, len, cnt) > 0) continue;
+        const int row = rg * 128 + r;
+        if (row < p.rows) {
+          uint4* o = reinterpret_cast<uint4*>(out_row<D, T>(p, b, h, row)) + i * (D / 16);
+          for (int c = 0; c < D / 16; ++c) o[c] = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+    }
+    uint32_t n = 0, segs = 0;  // tiles and stretches so far
+    int at = begin;
+    bool headed = false;
+    while (at < end && ok) {
+      const Seg s = seg_at<true>(p, 128, pre, at, end);
+      const bool first = at == begin;
+      at = s.next;
+      if (s.t0 == s.t1) continue;
+      const int row = s.rg * 128 + r;
+      const bool live = row < p.rows;
+      const int qi = live ? row / p.G : 0, hd = s.h * p.G + (live ? row - qi * p.G : 0);
+      // (rows past the count are zero queries whose sums are dropped, so that they hide nothing)
+      const bool asks = live && qi < s.cnt;
+      const int drafts = s.len - s.cnt;  // the first one's position
+      // (both groups write the same terms)
+      const float f = query_row<D, NT, T>(reinterpret_cast<const T*>(A.q.p) + s.b * A.q.sb + qi * A.q.st + hd * A.q.sh, asks,
+                                          A.scale, sm + L::Q, r);
+      tqd::tc_fence_smem();
+      tqd::tc_mbar_arrive(bar(Q_FULL, 0));
+      float M = -INFINITY, l = 0.f;
+      const int t_first = s.t0 + (int)((n ^ (uint32_t)i) & 1u);
+      // one tile; false: a wait gave up
+      auto tile = [&](auto edge_tag, int t) {
+        constexpr bool EDGE = decltype(edge_tag)::value;
+        const uint32_t g_tile = n + (uint32_t)(t - s.t0), turn = g_tile >> 1;
+        if (!wait(bar(S_FULL, i), turn & 1)) return false;
+        const int ss = g_tile % L::SC;
+        if (!wait(bar(SC_READY, ss), (g_tile / L::SC) & 1)) return false;
+        tqd::tc_fence_after();
+        const float4* sc = reinterpret_cast<const float4*>(sm + L::SCALES + 128 * ss);
+        uint32_t window[4];
+        if constexpr (EDGE) tree_window(A.tree, s.b, qi, asks, s.cnt, kTok * t - drafts, window);
+        auto hide = [&](int g) { return HideClear{EDGE ? window[g >> 1] >> (16 * (g & 1)) : 0u}; };
+        float v[128];
+        ld32_async(t_s, v);
+        ld32_async(t_s + 32, v + 32);
+        float a[8], e[8];
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          const float4 x = sc[g];
+          a[g] = f * x.x;
+          e[g] = x.y;
+        }
+        ld_wait<64>(v);
+        ld32_async(t_s + 64, v + 64);
+        ld32_async(t_s + 96, v + 96);
+        float top = block_top<EDGE>(v, hide(0), a[0], e[0]);
+#pragma unroll
+        for (int g = 1; g < 4; ++g) top = fmaxf(top, block_top<EDGE>(v + 16 * g, hide(g), a[g], e[g]));
+        ld_wait<64>(v + 64);
+#pragma unroll
+        for (int g = 4; g < 8; ++g) top = fmaxf(top, block_top<EDGE>(v + 16 * g, hide(g), a[g], e[g]));
+        const bool raise = top > M + kSlack;
+        if (__any_sync(kFull, raise)) {
+          const float m_new = raise ? top - kTop : M;
+          const float cor = raise ? ex2(M - m_new) : 1.f;
+          M = m_new;
+          if (t > t_first) {
+            l *= cor;
+            if (!wait(bar(O_DONE, i), (turn - 1) & 1)) return false;
+            tqd::tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              float o[16];
+              uint32_t w[16];
+              tqd::tc_ld16(t_o + 16 * c, o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(o[k] * cor);
+              tqd::tc_st16(t_o + 16 * c, w);
+            }
+          }
+        }
+        const float mr = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          uint32_t w[8];
+          const float sum = block_p<EDGE>(v + 16 * g, hide(g), a[g], e[g] - mr, w);
+          l = fmaf(sum, sc[g].z, l);
+          st8_async(t_s + 8 * g, w);
+          if (g == L::FIRST - 1 || g == 7) {
+            asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+            tqd::tc_fence_before();
+            tqd::tc_mbar_arrive(bar(P_FULL, 2 * i + (g == 7)));
+          }
+        }
+        __syncwarp();
+        if (lane == 0) tqd::tc_mbar_arrive(bar(SC_EMPTY, ss));
+        return true;
+      };
+      for (int t = t_first; t < s.t1; t += 2) {
+        if (kTok * (t + 1) > drafts ? !tile(std::true_type{}, t) : !tile(std::false_type{}, t)) break;
+      }
+      // every product of the stretch: its last tile's and the one before, of the other group
+      const int tiles = s.t1 - s.t0;
+      const uint32_t last = n + (uint32_t)tiles - 1;
+      n += (uint32_t)tiles;
+      if (!wait(bar(O_DONE, last & 1), (last >> 1) & 1)) break;
+      if (tiles > 1 && !wait(bar(O_DONE, (last - 1) & 1), ((last - 1) >> 1) & 1)) break;
+      tqd::tc_fence_after();
+      ml[128 * i + r] = make_float2(M, asks ? l : 0.f);
+      tqd::tc_mbar_arrive(bar(ML_FULL, 0));
+      if (!wait(bar(ML_FULL, 0), segs & 1)) break;
+      ++segs;
+      // the two groups' sums into one: each group takes half of the coordinates
+      const float2 x0 = ml[r], x1 = ml[128 + r];
+      const float top = fmaxf(x0.x, x1.x), ref = top == -INFINITY ? 0.f : top;
+      const float w0 = ex2(x0.x - ref), w1 = ex2(x1.x - ref), sum = fmaf(x0.y, w0, x1.y * w1);
+      const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+      const float scale = !whole ? 1.f : sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+      // (a group without a tile has whatever the columns held)
+      const bool has0 = tiles > 1 || !(last & 1), has1 = tiles > 1 || (last & 1);
+      float* part = p.part + (2ll * blockIdx.x + (first ? 0 : 1)) * L::PART;
+      T* o = out_row<D, T>(p, s.b, s.h, live ? row : 0);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        const int col = i * (D / 2) + 32 * c;
+        float u[32], v[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = 0.f;
+        if (has0) {
+          tqd::tc_ld32(lanes + 256 + col, u);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = u[k] * w0;
+        }
+        if (has1) {
+          tqd::tc_ld32(lanes + 256 + D + col, u);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = fmaf(u[k], w1, v[k]);
+        }
+        // (rows that do not ask may hold NaN: what lies behind the tokens is hidden from the others only)
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = asks ? v[k] * scale : 0.f;
+        if (whole) {
+          if (live) {
+            store16(o + col, v);
+            store16(o + col + 16, v + 16);
+          }
+        } else {
+          float4* to = reinterpret_cast<float4*>(part + 256 + (long long)r * D + col);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) to[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        }
+      }
+      if (!whole && i == 0) {
+        part[r] = top;
+        part[128 + r] = sum;
+      }
+      tqd::tc_fence_before();
+      tqd::tc_mbar_arrive(bar(OUT_READ, 0));  // (the next stretch's first products overwrite the sums)
+      if (threadIdx.x == 0 && s.t0 == 0 && s.t1 < s.tiles) {  // this range's last stretch begins a group that goes on
+        p.heads[blockIdx.x] = JoinHead{(s.start + s.tiles - 1) / per, first ? 0 : 1, s.b, s.h, s.rg};
+        headed = true;
+      }
+    }
+    if (threadIdx.x == 0 && !headed) p.heads[blockIdx.x].last = -1;
+  } else if (warp < 12) {
+    // ---- V codes to fp16, K-major [coordinate][token], 64 tokens per 128-byte row
+    uint32_t n = 0;
+    int at = begin;
+    while (at < end && ok) {
+      const Seg s = seg_at<true>(p, 128, pre, at, end);
+      at = s.next;
+      for (int t = s.t0; t < s.t1; ++t, ++n) {
+        const int st = n & 1, ss = n % L::SC;
+        if (warp == 8) {
+          if (!wait(bar(SC_FULL, ss), (n / L::SC) & 1)) break;
+          if (lane < 8) {
+            float4* x = reinterpret_cast<float4*>(sm + L::SCALES + 128 * ss + 16 * lane);
+            const int e = log2i(x->y);  // (of a block behind the tokens: any exponent; 2^-e stays finite)
+            x->y = (float)e;
+            x->z = exp2i(max(-126, min(126, -e)));
+          }
+          __syncwarp();
+          if (lane == 0) tqd::tc_mbar_arrive(bar(SC_READY, ss));
+        }
+        if (!wait(bar(VR_FULL, st), (n >> 1) & 1)) break;
+        if (n >= 2 && !wait(bar(V_EMPTY, st), ((n >> 1) - 1) & 1)) break;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int j = (warp - 8) + 4 * k;
+          const int have = s.limit - kTok * t - 16 * j;  // tokens of the block in use; the rest become zeros
+          uint32_t keep[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            keep[u] = have >= 16 ? 0xffffffffu
+                                 : (2 * u < have ? 0xffu : 0u) | (2 * u + 1 < have ? 0xff00u : 0u) |
+                                       (2 * u + 8 < have ? 0xff0000u : 0u) | (2 * u + 9 < have ? 0xff000000u : 0u);
+          const unsigned char* src = sm + L::VR + st * L::TILE + j * 16 * D;
+          unsigned char* dst = sm + L::V16 + st * 2 * L::TILE + (j >> 2) * L::TILE;
+#pragma unroll
+          for (int m = 0; m < D / 32; ++m) {
+            const int d = lane + 32 * m;
+            const uint4 v = *reinterpret_cast<const uint4*>(src + 16 * d);
+            uint32_t w[8];
+            codes_half4(v.x & keep[0], w[0], w[1]);
+            codes_half4(v.y & keep[1], w[2], w[3]);
+            codes_half4(v.z & keep[2], w[4], w[5]);
+            codes_half4(v.w & keep[3], w[6], w[7]);
+            const int c = 2 * (j & 3);
+            *reinterpret_cast<uint4*>(dst + d * 128 + ((c ^ (d & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(dst + d * 128 + (((c + 1) ^ (d & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+        }
+        tqd::tc_fence_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tqd::tc_mbar_arrive(bar(VR_EMPTY, st));
+          tqd::tc_mbar_arrive(bar(V_FULL, st));
+        }
+      }
+    }
+  } else if (warp == 12) {
+    // ---- copies: lanes 0-7 the K codes of a block each, 8-15 the V codes, 16-23 the scales
+    uint32_t n = 0;
+    int at = begin;
+    while (at < end && ok) {
+      const Seg s = seg_at<true>(p, 128, pre, at, end);
+      at = s.next;
+      const int blocks = (s.limit + 15) >> 4;
+      int page = 0;
+      for (int t = s.t0; t < s.t1; ++t, ++n) {
+        const int u = (t - s.t0) & 3;
+        if (u == 0) page = 8 * t + lane < blocks ? page_of(A.pool, s.b, 8 * t + lane) : 0;
+        const int pg = __shfl_sync(kFull, page, 8 * u + (lane & 7));
+        const int nb = min(8, blocks - 8 * t), ks = n % L::KS, st = n & 1, ss = n % L::SC;
+        if (n >= L::KS && !wait(bar(K_EMPTY, ks), (n / L::KS - 1) & 1)) break;
+        if (n >= 2 && !wait(bar(VR_EMPTY, st), ((n >> 1) - 1) & 1)) break;
+        if (n >= L::SC && !wait(bar(SC_EMPTY, ss), (n / L::SC - 1) & 1)) break;
+        if (lane == 0) {
+          tqd::mbar_arrive_expect_tx(bar(K_FULL, ks), nb * 16 * D);
+          tqd::mbar_arrive_expect_tx(bar(VR_FULL, st), nb * 16 * D);
+          tqd::mbar_arrive_expect_tx(bar(SC_FULL, ss), nb * 16);
+        }
+        __syncwarp();
+        const int j = lane & 7;
+        if (j < nb && lane < 24) {
+          const unsigned char* blk = A.pool.base + pool_block(A.pool, pg, s.h) * L::BLK;
+          if (lane < 8) tqd::bulk_g2s(sb + L::KR + ks * L::TILE + j * 16 * D, blk, 16 * D, bar(K_FULL, ks));
+          else if (lane < 16) tqd::bulk_g2s(sb + L::VR + st * L::TILE + j * 16 * D, blk + 16 * D, 16 * D, bar(VR_FULL, st));
+          else tqd::bulk_g2s(sb + L::SCALES + ss * 128 + j * 16, blk + 32 * D, 16, bar(SC_FULL, ss));
+        }
+        __syncwarp();
+      }
+    }
+    // every copy has landed before the block gives up its shared memory
+    for (uint32_t k = n > L::KS ? n - L::KS : 0; k < n; ++k) {
+      mbar_wait(bar(K_FULL, k % L::KS), (k / L::KS) & 1, kWaitLimit);
+      mbar_wait(bar(SC_FULL, k % L::SC), (k / L::SC) & 1, kWaitLimit);
+    }
+    for (uint32_t k = n > 2 ? n - 2 : 0; k < n; ++k) mbar_wait(bar(VR_FULL, k & 1), (k >> 1) & 1, kWaitLimit);
+  } else if (warp == 13) {
+    // ---- MMA issue, from operands that are constants of the stage
+    uint32_t n = 0, segs = 0;
+    int at = begin;
+    while (at < end && ok) {
+      const Seg s = seg_at<true>(p, 128, pre, at, end);
+      at = s.next;
+      if (s.t0 == s.t1) continue;
+      const uint32_t tiles = (uint32_t)(s.t1 - s.t0);
+      if (!wait(bar(Q_FULL, 0), segs & 1)) break;
+      for (uint32_t k = 0; k < min(2u, tiles); ++k) {
+        if (!wait(bar(K_FULL, (n + k) % L::KS), ((n + k) / L::KS) & 1)) break;
+        tqd::tc_fence_after();
+        issue_scores<D, NT>(sb, n + k);
+      }
+      if (segs && !wait(bar(OUT_READ, 0), (segs - 1) & 1)) break;
+      ++segs;
+      for (uint32_t k = 0; k < tiles && ok; ++k) {
+        const uint32_t g = n + k;
+        if (!wait(bar(V_FULL, g & 1), (g >> 1) & 1)) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!wait(bar(P_FULL, 2 * (g & 1) + h), (g >> 1) & 1)) break;
+          tqd::tc_fence_after();
+          if (g & 1) issue_readout<D, NT, 1>(sb, h, k >= 2);
+          else issue_readout<D, NT, 0>(sb, h, k >= 2);
+        }
+        if (!ok) break;
+        if (k + 2 < tiles) {
+          if (!wait(bar(K_FULL, (g + 2) % L::KS), ((g + 2) / L::KS) & 1)) break;
+          issue_scores<D, NT>(sb, g + 2);
+        }
+      }
+      n += tiles;
+    }
+  }
+  if (!ok && lane == 0 && A.pool.err) atomicExch(A.pool.err, TQ_DEVERR_WAIT_TIMEOUT);
+  tqd::tc_fence_before();
+  __syncthreads();  // (the rows waited for every readout, so every MMA has completed)
+  if (warp == 13) {
+    tqd::tc_fence_after();
+    tqd::tc_dealloc(*slot, 512);
+  }
+}
+
+template <int D, int NT, typename T>
+cudaError_t tree_go(TcParams p, int sms, int device, cudaStream_t s) {
+  using L = Plan<D, NT>;
+  static std::atomic<uint64_t> done{0};
+  p.groups = (p.rows + 127) / 128;
+  p.grid = sms;
+  cudaError_t e = allow_smem((const void*)tree_kernel<D, NT, T>, L::SMEM, device, done);
+  if (e != cudaSuccess) return e;
+  tree_kernel<D, NT, T><<<p.grid, kThreads, L::SMEM, s>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (p.grid == 1) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  const int rows = p.rows < 128 ? p.rows : 128;
+  cfg.gridDim = dim3(p.grid - 1, (rows + kJoinRows - 1) / kJoinRows);
+  cfg.blockDim = dim3(32 * kJoinRows);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, 128, 1, T>, JoinParams{p.heads, p.part, p.a.out, p.a.nq, p.a.Hq, p.G, p.rows});
+}
+
+constexpr int kTreeMinRows = 16;
+
+}  // namespace
+
+bool tree_tc_takes(const AttnArgs& a) {
+  const int rows = a.Hq / a.Hkv * a.nq;
+  if ((a.d != 64 && a.d != 128) || a.dtype == TQ_F32 || rows <= kTreeMinRows) return false;
+  // the plan counts tiles in 32 bits
+  const long long groups = (rows + 127) / 128, tiles = (a.pool.max_blocks + 7) / 8 + kGroupCost;
+  return (long long)a.B * a.Hkv * groups * tiles < (1ll << 31) - (1ll << 20);
+}
+
+size_t tree_tc_workspace(int d, int rows, tq_dtype dtype) {
+  if ((d != 64 && d != 128) || dtype == TQ_F32 || rows <= kTreeMinRows) return 0;
+  if (d == 128 && rows > 128) return tc_workspace(rows);
+  return kJoinHeadBytes + (size_t)2 * kMaxSms * 128 * (d + 2) * sizeof(float);
+}
+
+cudaError_t launch_tree_tc(const AttnArgs& a, cudaStream_t s) {
+  TcParams p;
+  int dev;
+  const int sms = tc_params(a, &p, &dev);
+  if (a.d == 64) return a.dtype == TQ_BF16 ? tree_go<64, 2, __nv_bfloat16>(p, sms, dev, s) : tree_go<64, 3, __half>(p, sms, dev, s);
+  if (p.rows > 128) return launch_tc_tree(a, s);
+  return a.dtype == TQ_BF16 ? tree_go<128, 2, __nv_bfloat16>(p, sms, dev, s) : tree_go<128, 3, __half>(p, sms, dev, s);
+}
+
+}  // namespace tqb
