@@ -28,16 +28,18 @@ __device__ __forceinline__ long long pool_block(const Pool& P, int page, int h) 
 }
 
 // Page of block `tile` of sequence b; anything outside the table or the pool goes to the redirect
-// page and is recorded.
-__device__ __forceinline__ int page_of(const Pool& P, int b, long long tile) {
-  int page = -1;
-  if (tile >= 0 && tile < P.max_blocks) page = __ldg(P.table + (long long)b * P.max_blocks + tile);
-  if ((unsigned)page >= (unsigned)P.num_pages) {
-    if (P.err) atomicExch(P.err, TQ_DEVERR_BAD_PAGE);
-    page = P.num_pages;
-  }
-  return page;
+// page and is recorded.  (In two steps for callers that request an entry ahead of its use.)
+__device__ __forceinline__ int page_entry(const Pool& P, int b, long long tile) {
+  return tile >= 0 && tile < P.max_blocks ? __ldg(P.table + (long long)b * P.max_blocks + tile) : -1;
 }
+__device__ __forceinline__ int checked_page(const Pool& P, int entry) {
+  if ((unsigned)entry >= (unsigned)P.num_pages) {
+    if (P.err) atomicExch(P.err, TQ_DEVERR_BAD_PAGE);
+    return P.num_pages;
+  }
+  return entry;
+}
+__device__ __forceinline__ int page_of(const Pool& P, int b, long long tile) { return checked_page(P, page_entry(P, b, tile)); }
 
 // 2^e as fp32, |e| <= 126
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((unsigned)(e + 127) << 23); }

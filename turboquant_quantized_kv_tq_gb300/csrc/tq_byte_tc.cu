@@ -198,10 +198,17 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
       // (a tree's rows past the count are zero queries whose sums are dropped, so that they hide nothing)
       const bool asks = live && (!TREE || qi < s.cnt);
       const int drafts = s.len - s.cnt;  // the first draft's position (TREE)
-      const int lim = !live ? 0 : TREE ? max(0, drafts) : row_limit(qi, s.len, s.cnt);
-      const int least = __reduce_min_sync(kFull, asks ? lim : 0x7fffffff);
-      const float f = query_row<kD, NT, T>(reinterpret_cast<const T*>(A.q.p) + s.b * A.q.sb + qi * A.q.st + hd * A.q.sh, asks,
-                                           A.scale, sm + L::Q + i * NT * 16384, r);
+      const int lim = live && !TREE ? row_limit(qi, s.len, s.cnt) : 0;
+      const int least = TREE ? 0 : __reduce_min_sync(kFull, live ? lim : 0x7fffffff);
+      const T* q_row = reinterpret_cast<const T*>(A.q.p) + s.b * A.q.sb + qi * A.q.st + hd * A.q.sh;
+      unsigned char* q_tile = sm + L::Q + i * NT * 16384;
+      float f;
+      if constexpr (TREE)
+        f = query_terms<kD, NT>(q_row, asks, A.scale, [&](int t, int c, const uint32_t* w) {
+          *reinterpret_cast<uint4*>(q_tile + 16384 * t + k_chunk<kD>(r, c)) = make_uint4(w[0], w[1], w[2], w[3]);
+        });
+      else
+        f = query_row<kD, NT, T>(q_row, live, A.scale, q_tile, r);
       tqd::tc_fence_smem();
       tqd::tc_mbar_arrive(bar(Q_FULL, i));
       float M = -INFINITY, l = 0.f;
@@ -214,12 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
         tqd::tc_fence_after();
         const float4* sc = reinterpret_cast<const float4*>(sm + L::SCALES + 128 * ss);
         const int left = lim - kTok * t;  // tokens of this tile that the row attends to
-        uint32_t window[4];               // (of a tree: those whose bit is set)
-        if constexpr (TREE && EDGE) tree_window(A.tree, s.b, qi, asks, s.cnt, kTok * t - drafts, window);
-        auto hide = [&](int g) {
-          if constexpr (TREE && EDGE) return HideClear{window[g >> 1] >> (16 * (g & 1))};
-          else return HideFrom{left - 16 * g};
-        };
+        if (TREE && kTok * (t + 1) > drafts) hide_scores(t_s, A.tree, s.b, qi, asks, s.cnt, drafts, t);
         float v[128];
         ld32_async(t_s, v);
         ld32_async(t_s + 32, v + 32);
@@ -233,12 +235,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
         ld_wait<64>(v);
         ld32_async(t_s + 64, v + 64);
         ld32_async(t_s + 96, v + 96);
-        float top = block_top<EDGE>(v, hide(0), a[0], e[0]);
+        float top = block_top<EDGE>(v, left, a[0], e[0]);
 #pragma unroll
-        for (int g = 1; g < 4; ++g) top = fmaxf(top, block_top<EDGE>(v + 16 * g, hide(g), a[g], e[g]));
+        for (int g = 1; g < 4; ++g) top = fmaxf(top, block_top<EDGE>(v + 16 * g, left - 16 * g, a[g], e[g]));
         ld_wait<64>(v + 64);
 #pragma unroll
-        for (int g = 4; g < 8; ++g) top = fmaxf(top, block_top<EDGE>(v + 16 * g, hide(g), a[g], e[g]));
+        for (int g = 4; g < 8; ++g) top = fmaxf(top, block_top<EDGE>(v + 16 * g, left - 16 * g, a[g], e[g]));
         const bool raise = top > M + kSlack;
         if (__any_sync(kFull, raise)) {
           const float m_new = raise ? top - kTop : M;
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
           uint32_t w[8];
-          const float sum = block_p<EDGE>(v + 16 * g, hide(g), a[g], e[g] - mr, w);
+          const float sum = block_p<EDGE>(v + 16 * g, left - 16 * g, a[g], e[g] - mr, w);
           l = fmaf(sum, sc[g].z, l);
           st8_async(t_s + 8 * g, w);
           if (g == L::FIRST - 1 || g == 7) {
@@ -278,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
         return true;
       };
       for (int t = s.t0; t < s.t1; ++t) {
-        if (kTok * (t + 1) > least ? !tile(std::true_type{}, t) : !tile(std::false_type{}, t)) break;
+        if (!TREE && kTok * (t + 1) > least ? !tile(std::bool_constant<!TREE>{}, t) : !tile(std::false_type{}, t)) break;
       }
       if (!ok || !wait(bar(O_DONE, i), (n - 1) & 1)) break;
       tqd::tc_fence_after();
@@ -337,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
           if (!wait(bar(SC_FULL, ss), (n / L::SC) & 1)) break;
           if (lane < 8) {
             float4* x = reinterpret_cast<float4*>(sm + L::SCALES + 128 * ss + 16 * lane);
+            if (TREE && kTok * t + 16 * lane >= s.limit) *x = make_float4(1.f, 1.f, 0.f, 0.f);  // (hidden scores stay -infinity)
             const int e = log2i(x->y);  // (of a block behind the tokens: any exponent; 2^-e stays finite)
             x->y = (float)e;
             x->z = exp2i(max(-126, min(126, -e)));

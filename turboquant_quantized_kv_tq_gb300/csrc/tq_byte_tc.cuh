@@ -235,31 +235,82 @@ __device__ __forceinline__ void st8_async(uint32_t taddr, const uint32_t* v) {
                : "memory");
 }
 
-// Bits j .. j + 127 of draft i's mask in entry b (in order from the low end), j counted from the entry's first
-// draft: tokens before it are seen, those past the count are not.
-__device__ __forceinline__ void tree_window(const TreeMasks& M, int b, int i, bool live, int cnt, int j, uint32_t (&w)[4]) {
-  const uint32_t* m = M.row(b, i);
+// The same for a tree's kernels, which keep their code small: what a block runs once a stretch waits for its
+// instructions (unrolled, the terms of a row and a second copy of the tile for hidden tokens took 17 us a stretch).
+// put(t, c, w) takes codes 16 c .. of term t.  The factor is never so small that a scaled one of -infinity is not.
+template <int D, int NT, typename T, typename F>
+__device__ __forceinline__ float query_terms(const T* src, bool live, float scale, F put) {
+  float amax = 0.f;
+#pragma unroll 4
+  for (int c = 0; c < D / 16; ++c) {
+    float x[16];
+    Raw16<T> raw = {};
+    if (live) raw = Raw16<T>{{__ldg(reinterpret_cast<const uint4*>(src) + 2 * c), __ldg(reinterpret_cast<const uint4*>(src) + 2 * c + 1)}};
+    unpack16(raw, x, src);
 #pragma unroll
-  for (int x = 0; x < 4; ++x) w[x] = live ? tree_word(m, M.words, cnt, j + 32 * x) : 0u;
+    for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(x[k]));
+  }
+  const bool odd = !(amax <= 3.402823466e38f);  // an infinity: the row's result is NaN, as the formula's is
+  const unsigned u = __float_as_uint(amax);
+  int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);  // amax <= 448 2^e
+  e = min(120, max(-120, e));
+  if (amax == 0.f || odd) e = 0;
+  const float inv = scale < 0.f ? -exp2i(-e) : exp2i(-e);
+#pragma unroll 1
+  for (int c = 0; c < D / 16; ++c) {
+    float x[16];
+    Raw16<T> raw = {};
+    if (live) raw = Raw16<T>{{__ldg(reinterpret_cast<const uint4*>(src) + 2 * c), __ldg(reinterpret_cast<const uint4*>(src) + 2 * c + 1)}};
+    unpack16(raw, x, src);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] *= inv;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float &a = x[2 * k], &b = x[2 * k + 1];
+        const uint32_t two = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t back = codes_half2(two);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
+        a -= f.x;
+        b -= f.y;
+        w[k >> 1] = k & 1 ? w[k >> 1] | (two << 16) : two;
+      }
+      put(t, c, w);
+    }
+  }
+  const float f = fabsf(scale) * kLog2e * exp2i(e);
+  return odd ? __uint_as_float(0x7fc00000u) : fmaxf(f, 8.07793567e-28f);  // 2^-90
 }
 
-// Tokens of a block that a row does not attend to: those from `left` on, or those whose bit is clear.
-struct HideFrom {
-  int left;
-  __device__ __forceinline__ bool operator()(int k) const { return k >= left; }
-};
-struct HideClear {
-  uint32_t bits;
-  __device__ __forceinline__ bool operator()(int k) const { return !(bits >> k & 1u); }
-};
+// Scores of tile t, 128 columns from t_s of this thread's lane, to -infinity where the row (draft i, first draft at
+// position `drafts`) does not attend to the token.  Their factors are positive, so it hides them.
+__device__ __forceinline__ void hide_scores(uint32_t t_s, const TreeMasks& M, int b, int i, bool asks, int cnt, int drafts, int t) {
+  const uint32_t* m = M.row(b, i);
+  uint32_t w[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) w[x] = asks ? tree_word(m, M.words, cnt, kTok * t - drafts + 32 * x) : 0u;
+#pragma unroll 1
+  for (int g = 0; g < 4; ++g, t_s += 32) {
+    const uint32_t bits = w[0];
+    w[0] = w[1], w[1] = w[2], w[2] = w[3];
+    if (!__any_sync(kFull, bits != 0xffffffffu)) continue;
+    float v[32];
+    tqd::tc_ld32(t_s, v);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = bits >> k & 1u ? v[k] : -INFINITY;
+    tqd::tc_st32(t_s, v);
+  }
+}
 
-// The largest s + e of one block's 16 scores (hide: those the row does not attend to, when EDGE).
-template <bool EDGE, typename H>
-__device__ __forceinline__ float block_top(float* v, H hide, float a, float e) {
+// The largest s + e of one block's 16 scores (left: those the row attends to, when EDGE).
+template <bool EDGE>
+__device__ __forceinline__ float block_top(float* v, int left, float a, float e) {
   if (EDGE) {
 #pragma unroll
     for (int k = 0; k < 16; ++k)
-      if (hide(k)) v[k] = -INFINITY;
+      if (k >= left) v[k] = -INFINITY;
   }
   float m = v[0];
 #pragma unroll
@@ -270,8 +321,8 @@ __device__ __forceinline__ float block_top(float* v, H hide, float a, float e) {
   return EDGE && m == -INFINITY ? -INFINITY : top;
 }
 // P of one block as fp16 pairs in V's stored token order; the sum of its 16 values is returned.
-template <bool EDGE, typename H>
-__device__ __forceinline__ float block_p(const float* v, H hide, float a, float b, uint32_t* w) {
+template <bool EDGE>
+__device__ __forceinline__ float block_p(const float* v, int left, float a, float b, uint32_t* w) {
   const uint64_t a2 = pair(a, a), b2 = pair(b, b);
   float x[16];
 #pragma unroll
@@ -283,7 +334,7 @@ __device__ __forceinline__ float block_p(const float* v, H hide, float a, float 
   if (EDGE) {
 #pragma unroll
     for (int k = 0; k < 16; ++k)
-      if (hide(k)) x[k] = 0.f;
+      if (k >= left) x[k] = 0.f;
   }
   uint64_t s0 = pair(x[0], x[1]), s1 = pair(x[2], x[3]);
 #pragma unroll

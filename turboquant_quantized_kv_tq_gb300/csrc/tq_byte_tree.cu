@@ -1,22 +1,24 @@
 // Attention of a tree's drafts over the byte cache on the 5th-generation tensor cores: up to 128 (query, head) rows
 // of a slab (batch entry, KV head) at a time, head dims 64 and 128, bf16 and fp16 queries.
 //
-// The mathematics, the operands and the softmax are those of tq_byte_tc.cu, where two tiles of 128 rows take turns
+// The mathematics, the products and the softmax are those of tq_byte_tc.cu, where two tiles of 128 rows take turns
 // on one token tile, so that one's softmax runs beside the other's products.  A tree has rarely more than 128 rows
 // (16 drafts of 4 heads per KV head: 64), and a lone row tile would leave the tensor cores idle through its softmax.
 // Here the two groups of row warps hold the same rows and take turns on the token tiles: group i takes tiles
-// n = i (mod 2), with scores S_i, sums O_i, reference M_i and l_i of its own,
-//   o = (2^(M_0 - M) O_0 + 2^(M_1 - M) O_1) / (2^(M_0 - M) l_0 + 2^(M_1 - M) l_1),  M = max(M_0, M_1),
-// joined from tensor memory at the end of a stretch (both groups' warps reach the same lanes).  More than 128 rows
-// go to tc_kernel with two row tiles (head dim 128), which reads the pool half as often, or take turns here (64).
+// n = i (mod 2) with scores S_i, and both add to one O.  So a row has one reference M, which goes from tile to tile
+// (through shared memory, posted as soon as a tile's maximum is known); the group that raises it rescales O between
+// the products of the tile before and its own.  Each group sums its own l.
+// The queries' terms lie in tensor memory, which a second O would fill: a score product reads only its keys from
+// shared memory, and the room that they took there holds tiles in flight.  Rows that do not exist cost nothing:
+// their warps only pass the barriers.  More than 128 rows go to tc_kernel with two row tiles (head dim 128), which
+// reads the pool half as often, or in groups of 128 here (64).
 //
 // Which drafts a row sees matters only in the last tiles: rows read their masks there, a window of 128 bits a tile,
 // and tiles before the first draft are the same as without a tree.
 //
-// Warps: as in tq_byte_tc.cu.
+// Warps: 0-7 rows, 8-11 V to fp16, 12 K copies, 13 MMA issue, 14 V copies (15 only completes the warpgroup).
 #include <atomic>
 #include <string>
-#include <type_traits>
 
 #include "tq_byte_tc.cuh"
 
@@ -25,24 +27,27 @@ namespace {
 
 using tqd::mbar_wait;
 
-template <int D, int NT>
+template <int D>
 struct Plan {
   static constexpr int BLK = 32 * D + 32;
-  static constexpr int TILE = 128 * D;                            // bytes of a term of Q, of a tile's codes
+  static constexpr int TILE = 128 * D;                            // bytes of a tile's codes
   static constexpr int FIRST = 4;                                 // blocks of a tile in the first part of P
   static constexpr int KS = 4;                                    // K stages: scores run two tiles ahead
-  static constexpr int SC = 4;                                    // scale stages of 8 x 16 bytes
-  static constexpr int Q = 0, KR = Q + NT * TILE, VR = KR + KS * TILE, V16 = VR + 2 * TILE;
-  // [stage][block]: as copied (K scale, V scale, -, -), then in place (K scale, e, 2^-e, -)
-  static constexpr int SCALES = V16 + 4 * TILE, ML = SCALES + SC * 128, BARS = ML + 2 * 128 * 8, PRE = BARS + 320;
+  static constexpr int VS = 5;                                    // stages of V's codes: copies take 2 us under load
+  static constexpr int VB = 16 * D + 16;                          // V's codes of a block and the scales behind them: one copy
+  static constexpr int SC = 4;                                    // stages of scales, [block] (K scale, e, 2^-e, -)
+  static constexpr int KR = 0, V16 = KR + KS * TILE, VR = V16 + 4 * TILE;
+  static constexpr int SCALES = VR + VS * 8 * VB, REF = SCALES + SC * 128, SUM = REF + 2 * 128 * 4, BARS = SUM + 2 * 128 * 4;
+  static constexpr int PRE = BARS + 384;
+  static constexpr int T_O = 256, T_Q = 384;                      // columns of O and of the queries' terms (S_i at 128 i)
   static constexpr int SMEM = PRE + (TQ_MAX_BATCH + 1) * 4;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static constexpr int PART = 128 * (D + 2);                      // floats of a partial
 };
 // (P_FULL: half h of group i at 2 i + h)
-enum Bar { K_FULL = 0, K_EMPTY = 4, VR_FULL = 8, VR_EMPTY = 10, V_FULL = 12, V_EMPTY = 14, S_FULL = 16, O_DONE = 18,
-           P_FULL = 20, SC_FULL = 24, SC_EMPTY = 28, SC_READY = 32, Q_FULL = 36, ML_FULL = 37, OUT_READ = 38, BAR_COUNT = 39 };
-static_assert(8 * BAR_COUNT + 4 <= 320, "barriers and the tensor-memory slot");
+enum Bar { K_FULL = 0, K_EMPTY = 4, VR_FULL = 8, VR_EMPTY = 13, V_FULL = 18, V_EMPTY = 20, S_FULL = 22, O_DONE = 24, REF_SET = 26,
+           P_FULL = 28, SC_EMPTY = 32, SC_READY = 36, Q_FULL = 40, SUM_SET = 41, OUT_READ = 42, BAR_COUNT = 43 };
+static_assert(8 * BAR_COUNT + 4 <= 384, "barriers and the tensor-memory slot");
 
 // Swizzled K-major operand of rows of D codes: 128-byte swizzle in groups of 1024 bytes, 64-byte in 512.
 template <int D>
@@ -52,18 +57,29 @@ __device__ __forceinline__ uint64_t sdesc_codes(uint32_t addr) {
 }
 __host__ __device__ constexpr uint32_t idesc(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24); }  // M = 128
 
+// D = A B (+ D) on 8-bit floats with A in tensor memory (row i in lane i, four values to a column).
+__device__ __forceinline__ void mma_f8_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n"
+      :: "r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void st4_async(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};\n" :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+
 // S of the tile in K buffer ST, for group ST % 2.
 template <int D, int NT, int ST>
 __device__ __forceinline__ void issue_scores(uint32_t sb) {
-  using L = Plan<D, NT>;
+  using L = Plan<D>;
   constexpr int i = ST & 1;
-  const uint64_t q = sdesc_codes<D>(sb + L::Q), k = sdesc_codes<D>(sb + L::KR + ST * L::TILE);
+  const uint64_t k = sdesc_codes<D>(sb + L::KR + ST * L::TILE);
   if (elected()) {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j)
-        mma_f8(128 * i, q + (uint64_t)(t * (L::TILE >> 4) + 2 * j), k + 2 * j, idesc(kTok), t + j > 0);
+      for (int j = 0; j < D / 32; ++j) mma_f8_ta(128 * i, L::T_Q + t * (D / 4) + 8 * j, k + 2 * j, idesc(kTok), t + j > 0);
     tqd::tc_commit(sb + L::BARS + 8 * (S_FULL + i));
     tqd::tc_commit(sb + L::BARS + 8 * (K_EMPTY + ST));
   }
@@ -78,17 +94,17 @@ __device__ __forceinline__ void issue_scores(uint32_t sb, uint32_t n) {
     default: return issue_scores<D, NT, 3>(sb);
   }
 }
-// Part h (blocks [0, FIRST), [FIRST, 8)) of O_i += P_i V of the tile in V buffer i (accumulate: not the group's
-// first tile of a stretch).
-template <int D, int NT, int i>
+// Part h (blocks [0, FIRST), [FIRST, 8)) of O += P_i V of the tile in V buffer i (accumulate: not the first tile of
+// a stretch).
+template <int D, int i>
 __device__ __forceinline__ void issue_readout(uint32_t sb, int h, bool accumulate) {
-  using L = Plan<D, NT>;
+  using L = Plan<D>;
   const uint64_t v = sdesc128(sb + L::V16 + i * 2 * L::TILE);
   if (elected()) {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       if ((k >= L::FIRST) == (h == 1))
-        tqd::tc_mma_f16_ta(256 + D * i, 128 * i + 8 * k, v + (uint64_t)((k >> 2) * (L::TILE >> 4) + 2 * (k & 3)), idesc(D),
+        tqd::tc_mma_f16_ta(L::T_O, 128 * i + 8 * k, v + (uint64_t)((k >> 2) * (L::TILE >> 4) + 2 * (k & 3)), idesc(D),
                            accumulate || k > 0);
     if (h == 1) {
       tqd::tc_commit(sb + L::BARS + 8 * (O_DONE + i));
@@ -100,7 +116,7 @@ __device__ __forceinline__ void issue_readout(uint32_t sb, int h, bool accumulat
 
 template <int D, int NT, typename T>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
-  using L = Plan<D, NT>;
+  using L = Plan<D>;
   extern __shared__ __align__(1024) unsigned char sm[];
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const AttnArgs& A = p.a;
@@ -120,26 +136,28 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
   if (warp == 13) tqd::tc_alloc((uint32_t)__cvta_generic_to_shared(slot), 512);
   if (threadIdx.x == 32) {
     for (int i = 0; i < 2; ++i) {
-      tqd::mbar_init(bar(VR_FULL, i), 1);
-      tqd::mbar_init(bar(VR_EMPTY, i), 4);
       tqd::mbar_init(bar(V_FULL, i), 4);
       tqd::mbar_init(bar(V_EMPTY, i), 1);
       tqd::mbar_init(bar(S_FULL, i), 1);
       tqd::mbar_init(bar(P_FULL, 2 * i), 128);
       tqd::mbar_init(bar(P_FULL, 2 * i + 1), 128);
       tqd::mbar_init(bar(O_DONE, i), 1);
+      tqd::mbar_init(bar(REF_SET, i), 128);
     }
     for (int i = 0; i < L::KS; ++i) {
       tqd::mbar_init(bar(K_FULL, i), 1);
       tqd::mbar_init(bar(K_EMPTY, i), 1);
     }
+    for (int i = 0; i < L::VS; ++i) {
+      tqd::mbar_init(bar(VR_FULL, i), 1);
+      tqd::mbar_init(bar(VR_EMPTY, i), 4);
+    }
     for (int i = 0; i < L::SC; ++i) {
-      tqd::mbar_init(bar(SC_FULL, i), 1);
       tqd::mbar_init(bar(SC_EMPTY, i), 4);
       tqd::mbar_init(bar(SC_READY, i), 1);
     }
     tqd::mbar_init(bar(Q_FULL, 0), 256);
-    tqd::mbar_init(bar(ML_FULL, 0), 256);
+    tqd::mbar_init(bar(SUM_SET, 0), 256);
     tqd::mbar_init(bar(OUT_READ, 0), 256);
     tqd::fence_mbar_init();
   }
@@ -147,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
   tqd::tc_fence_before();
   __syncthreads();
   tqd::tc_fence_after();
-  // all 512 columns are this block's: they begin at column 0, lane 0 (S_i at 128 i, O_i at 256 + D i)
+  // all 512 columns are this block's: they begin at column 0, lane 0
   const bool whole_tmem = *slot == 0;
   const int total = pre[A.B], per = range_of(total, p.grid);
   const int begin = min(total, (int)blockIdx.x * per), end = min(total, begin + per);
@@ -164,8 +182,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
     // ---- rows: group i takes the tiles n = i (mod 2) of the block's sequence
     const int i = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_s = lanes + 128 * i, t_o = lanes + 256 + D * i;
-    float2* ml = reinterpret_cast<float2*>(sm + L::ML);  // [group][row]
+    const uint32_t t_s = lanes + 128 * i, t_o = lanes + L::T_O;
+    float* refs = reinterpret_cast<float*>(sm + L::REF);  // [tile % 2][row]: M from this tile on
+    float* sums = reinterpret_cast<float*>(sm + L::SUM);  // [group][row]
     // groups without a live row: zeros, spread over the grid
     {
       const int slabs = A.B * p.groups * A.Hkv, most = A.pool.max_blocks * 16;
@@ -194,25 +213,33 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
       // (rows past the count are zero queries whose sums are dropped, so that they hide nothing)
       const bool asks = live && qi < s.cnt;
       const int drafts = s.len - s.cnt;  // the first one's position
-      // (both groups write the same terms)
-      const float f = query_row<D, NT, T>(reinterpret_cast<const T*>(A.q.p) + s.b * A.q.sb + qi * A.q.st + hd * A.q.sh, asks,
-                                          A.scale, sm + L::Q, r);
-      tqd::tc_fence_smem();
+      const bool idle = !__any_sync(kFull, asks);  // (uniform over the two groups' warps of the same rows)
+      // group i writes terms i, i + 2
+      const float f = query_terms<D, NT>(reinterpret_cast<const T*>(A.q.p) + s.b * A.q.sb + qi * A.q.st + hd * A.q.sh, asks,
+                                         A.scale, [&](int t, int c, const uint32_t* w) {
+                                           if ((t & 1) == i) st4_async(lanes + L::T_Q + t * (D / 4) + 4 * c, w);
+                                         });
+      asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+      tqd::tc_fence_before();
       tqd::tc_mbar_arrive(bar(Q_FULL, 0));
-      float M = -INFINITY, l = 0.f;
+      float M = -INFINITY, l = 0.f;  // l under the reference M
       const int t_first = s.t0 + (int)((n ^ (uint32_t)i) & 1u);
       // one tile; false: a wait gave up
-      auto tile = [&](auto edge_tag, int t) {
-        constexpr bool EDGE = decltype(edge_tag)::value;
+      auto tile = [&](int t) {
         const uint32_t g_tile = n + (uint32_t)(t - s.t0), turn = g_tile >> 1;
         if (!wait(bar(S_FULL, i), turn & 1)) return false;
         const int ss = g_tile % L::SC;
         if (!wait(bar(SC_READY, ss), (g_tile / L::SC) & 1)) return false;
+        if (idle) {
+          tqd::tc_mbar_arrive(bar(REF_SET, i));
+          tqd::tc_mbar_arrive(bar(P_FULL, 2 * i));
+          tqd::tc_mbar_arrive(bar(P_FULL, 2 * i + 1));
+          if (lane == 0) tqd::tc_mbar_arrive(bar(SC_EMPTY, ss));
+          return true;
+        }
         tqd::tc_fence_after();
         const float4* sc = reinterpret_cast<const float4*>(sm + L::SCALES + 128 * ss);
-        uint32_t window[4];
-        if constexpr (EDGE) tree_window(A.tree, s.b, qi, asks, s.cnt, kTok * t - drafts, window);
-        auto hide = [&](int g) { return HideClear{EDGE ? window[g >> 1] >> (16 * (g & 1)) : 0u}; };
+        if (kTok * (t + 1) > drafts) hide_scores(t_s, A.tree, s.b, qi, asks, s.cnt, drafts, t);
         float v[128];
         ld32_async(t_s, v);
         ld32_async(t_s + 32, v + 32);
@@ -226,37 +253,44 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
         ld_wait<64>(v);
         ld32_async(t_s + 64, v + 64);
         ld32_async(t_s + 96, v + 96);
-        float top = block_top<EDGE>(v, hide(0), a[0], e[0]);
+        float top = block_top<false>(v, 0, a[0], e[0]);
 #pragma unroll
-        for (int g = 1; g < 4; ++g) top = fmaxf(top, block_top<EDGE>(v + 16 * g, hide(g), a[g], e[g]));
+        for (int g = 1; g < 4; ++g) top = fmaxf(top, block_top<false>(v + 16 * g, 0, a[g], e[g]));
         ld_wait<64>(v + 64);
 #pragma unroll
-        for (int g = 4; g < 8; ++g) top = fmaxf(top, block_top<EDGE>(v + 16 * g, hide(g), a[g], e[g]));
-        const bool raise = top > M + kSlack;
-        if (__any_sync(kFull, raise)) {
-          const float m_new = raise ? top - kTop : M;
-          const float cor = raise ? ex2(M - m_new) : 1.f;
+        for (int g = 4; g < 8; ++g) top = fmaxf(top, block_top<false>(v + 16 * g, 0, a[g], e[g]));
+        float m_old = -INFINITY;
+        if (t > s.t0) {
+          if (!wait(bar(REF_SET, i ^ 1), ((g_tile - 1) >> 1) & 1)) return false;
+          m_old = refs[128 * (i ^ 1) + r];
+        }
+        const bool raise = top > m_old + kSlack;
+        const float m_new = raise ? top - kTop : m_old;
+        refs[128 * i + r] = m_new;
+        tqd::tc_mbar_arrive(bar(REF_SET, i));
+        if (M != m_new) {
+          l *= ex2(M - m_new);
           M = m_new;
-          if (t > t_first) {
-            l *= cor;
-            if (!wait(bar(O_DONE, i), (turn - 1) & 1)) return false;
-            tqd::tc_fence_after();
+        }
+        if (t > s.t0 && __any_sync(kFull, raise)) {
+          const float cor = raise ? ex2(m_old - m_new) : 1.f;
+          if (!wait(bar(O_DONE, i ^ 1), ((g_tile - 1) >> 1) & 1)) return false;
+          tqd::tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              float o[16];
-              uint32_t w[16];
-              tqd::tc_ld16(t_o + 16 * c, o);
+          for (int c = 0; c < D / 16; ++c) {
+            float o[16];
+            uint32_t w[16];
+            tqd::tc_ld16(t_o + 16 * c, o);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(o[k] * cor);
-              tqd::tc_st16(t_o + 16 * c, w);
-            }
+            for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(o[k] * cor);
+            tqd::tc_st16(t_o + 16 * c, w);
           }
         }
         const float mr = M == -INFINITY ? 0.f : M;
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
           uint32_t w[8];
-          const float sum = block_p<EDGE>(v + 16 * g, hide(g), a[g], e[g] - mr, w);
+          const float sum = block_p<false>(v + 16 * g, 0, a[g], e[g] - mr, w);
           l = fmaf(sum, sc[g].z, l);
           st8_async(t_s + 8 * g, w);
           if (g == L::FIRST - 1 || g == 7) {
@@ -270,45 +304,33 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
         return true;
       };
       for (int t = t_first; t < s.t1; t += 2) {
-        if (kTok * (t + 1) > drafts ? !tile(std::true_type{}, t) : !tile(std::false_type{}, t)) break;
+        if (!tile(t)) break;
       }
-      // every product of the stretch: its last tile's and the one before, of the other group
-      const int tiles = s.t1 - s.t0;
-      const uint32_t last = n + (uint32_t)tiles - 1;
-      n += (uint32_t)tiles;
+      if (!ok) break;
+      // Every product of the stretch is done with its last tile's.  (The tile before it is waited for first: a wait for a
+      // phase tells nothing while the barrier is two phases behind.)
+      const uint32_t last = n + (uint32_t)(s.t1 - s.t0) - 1;
+      if (last > n && !wait(bar(O_DONE, (last - 1) & 1), ((last - 1) >> 1) & 1)) break;
       if (!wait(bar(O_DONE, last & 1), (last >> 1) & 1)) break;
-      if (tiles > 1 && !wait(bar(O_DONE, (last - 1) & 1), ((last - 1) >> 1) & 1)) break;
+      n = last + 1;
       tqd::tc_fence_after();
-      ml[128 * i + r] = make_float2(M, asks ? l : 0.f);
-      tqd::tc_mbar_arrive(bar(ML_FULL, 0));
-      if (!wait(bar(ML_FULL, 0), segs & 1)) break;
+      const float top = idle ? -INFINITY : refs[128 * (last & 1) + r];
+      if (M != top) l *= ex2(M - top);  // (the other group raised it last; a group without a tile has l = 0)
+      sums[128 * i + r] = asks ? l : 0.f;
+      tqd::tc_mbar_arrive(bar(SUM_SET, 0));
+      if (!wait(bar(SUM_SET, 0), segs & 1)) break;
       ++segs;
-      // the two groups' sums into one: each group takes half of the coordinates
-      const float2 x0 = ml[r], x1 = ml[128 + r];
-      const float top = fmaxf(x0.x, x1.x), ref = top == -INFINITY ? 0.f : top;
-      const float w0 = ex2(x0.x - ref), w1 = ex2(x1.x - ref), sum = fmaf(x0.y, w0, x1.y * w1);
+      // each group takes half of the coordinates
+      const float sum = sums[r] + sums[128 + r];
       const bool whole = s.t0 == 0 && s.t1 == s.tiles;
       const float scale = !whole ? 1.f : sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-      // (a group without a tile has whatever the columns held)
-      const bool has0 = tiles > 1 || !(last & 1), has1 = tiles > 1 || (last & 1);
       float* part = p.part + (2ll * blockIdx.x + (first ? 0 : 1)) * L::PART;
       T* o = out_row<D, T>(p, s.b, s.h, live ? row : 0);
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
         const int col = i * (D / 2) + 32 * c;
-        float u[32], v[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = 0.f;
-        if (has0) {
-          tqd::tc_ld32(lanes + 256 + col, u);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = u[k] * w0;
-        }
-        if (has1) {
-          tqd::tc_ld32(lanes + 256 + D + col, u);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = fmaf(u[k], w1, v[k]);
-        }
+        float v[32];
+        tqd::tc_ld32(t_o + col, v);
         // (rows that do not ask may hold NaN: what lies behind the tokens is hidden from the others only)
 #pragma unroll
         for (int k = 0; k < 32; ++k) v[k] = asks ? v[k] * scale : 0.f;
@@ -343,42 +365,56 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
       const Seg s = seg_at<true>(p, 128, pre, at, end);
       at = s.next;
       for (int t = s.t0; t < s.t1; ++t, ++n) {
-        const int st = n & 1, ss = n % L::SC;
+        const int st = n & 1, vs = n % L::VS, ss = n % L::SC;
+        if (!wait(bar(VR_FULL, vs), (n / L::VS) & 1)) break;
         if (warp == 8) {
-          if (!wait(bar(SC_FULL, ss), (n / L::SC) & 1)) break;
+          if (n >= L::SC && !wait(bar(SC_EMPTY, ss), (n / L::SC - 1) & 1)) break;
           if (lane < 8) {
-            float4* x = reinterpret_cast<float4*>(sm + L::SCALES + 128 * ss + 16 * lane);
-            const int e = log2i(x->y);  // (of a block behind the tokens: any exponent; 2^-e stays finite)
-            x->y = (float)e;
-            x->z = exp2i(max(-126, min(126, -e)));
+            float2 x = *reinterpret_cast<const float2*>(sm + L::VR + (vs * 8 + lane) * L::VB + 16 * D);
+            if (kTok * t + 16 * lane >= s.limit) x = make_float2(1.f, 1.f);  // (a block behind the tokens: hidden scores stay -infinity)
+            const int e = log2i(x.y);
+            *reinterpret_cast<float4*>(sm + L::SCALES + 128 * ss + 16 * lane) =
+                make_float4(x.x, (float)e, exp2i(max(-126, min(126, -e))), 0.f);
           }
           __syncwarp();
           if (lane == 0) tqd::tc_mbar_arrive(bar(SC_READY, ss));
         }
-        if (!wait(bar(VR_FULL, st), (n >> 1) & 1)) break;
         if (n >= 2 && !wait(bar(V_EMPTY, st), ((n >> 1) - 1) & 1)) break;
+        uint4 raw[2][D / 32];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int m = 0; m < D / 32; ++m)
+            raw[k][m] = *reinterpret_cast<const uint4*>(sm + L::VR + (vs * 8 + (warp - 8) + 4 * k) * L::VB + 16 * (lane + 32 * m));
+        if (kTok * (t + 1) > s.limit) {  // tokens behind the last become zeros
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int have = s.limit - kTok * t - 16 * ((warp - 8) + 4 * k);
+            uint32_t keep[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              keep[u] = (2 * u < have ? 0xffu : 0u) | (2 * u + 1 < have ? 0xff00u : 0u) | (2 * u + 8 < have ? 0xff0000u : 0u) |
+                        (2 * u + 9 < have ? 0xff000000u : 0u);
+#pragma unroll
+            for (int m = 0; m < D / 32; ++m) {
+              raw[k][m].x &= keep[0];
+              raw[k][m].y &= keep[1];
+              raw[k][m].z &= keep[2];
+              raw[k][m].w &= keep[3];
+            }
+          }
+        }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int j = (warp - 8) + 4 * k;
-          const int have = s.limit - kTok * t - 16 * j;  // tokens of the block in use; the rest become zeros
-          uint32_t keep[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            keep[u] = have >= 16 ? 0xffffffffu
-                                 : (2 * u < have ? 0xffu : 0u) | (2 * u + 1 < have ? 0xff00u : 0u) |
-                                       (2 * u + 8 < have ? 0xff0000u : 0u) | (2 * u + 9 < have ? 0xff000000u : 0u);
-          const unsigned char* src = sm + L::VR + st * L::TILE + j * 16 * D;
-          unsigned char* dst = sm + L::V16 + st * 2 * L::TILE + (j >> 2) * L::TILE;
+          unsigned char* dst = sm + L::V16 + st * 2 * L::TILE + k * L::TILE;
 #pragma unroll
           for (int m = 0; m < D / 32; ++m) {
-            const int d = lane + 32 * m;
-            const uint4 v = *reinterpret_cast<const uint4*>(src + 16 * d);
+            const int d = lane + 32 * m, c = 2 * (warp - 8);
             uint32_t w[8];
-            codes_half4(v.x & keep[0], w[0], w[1]);
-            codes_half4(v.y & keep[1], w[2], w[3]);
-            codes_half4(v.z & keep[2], w[4], w[5]);
-            codes_half4(v.w & keep[3], w[6], w[7]);
-            const int c = 2 * (j & 3);
+            codes_half4(raw[k][m].x, w[0], w[1]);
+            codes_half4(raw[k][m].y, w[2], w[3]);
+            codes_half4(raw[k][m].z, w[4], w[5]);
+            codes_half4(raw[k][m].w, w[6], w[7]);
             *reinterpret_cast<uint4*>(dst + d * 128 + ((c ^ (d & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
             *reinterpret_cast<uint4*>(dst + d * 128 + (((c + 1) ^ (d & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
           }
@@ -386,50 +422,52 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
         tqd::tc_fence_smem();
         __syncwarp();
         if (lane == 0) {
-          tqd::tc_mbar_arrive(bar(VR_EMPTY, st));
+          tqd::tc_mbar_arrive(bar(VR_EMPTY, vs));
           tqd::tc_mbar_arrive(bar(V_FULL, st));
         }
       }
     }
-  } else if (warp == 12) {
-    // ---- copies: lanes 0-7 the K codes of a block each, 8-15 the V codes, 16-23 the scales
+  } else if (warp != 13) {
+    // ---- copies: warp 12 the K codes, 14 the V codes and scales.  (A warp takes some 80 cycles a copy: one for
+    // both, and copies of the scales beside them, took 2000 cycles a tile and bounded the kernel.)
+    const bool keys = warp == 12;
     uint32_t n = 0;
-    int at = begin;
+    int at = warp == 15 ? end : begin;
     while (at < end && ok) {
       const Seg s = seg_at<true>(p, 128, pre, at, end);
       at = s.next;
       const int blocks = (s.limit + 15) >> 4;
-      int page = 0;
+      auto entries = [&](int t) { return 8 * t + lane < blocks ? page_entry(A.pool, s.b, 8 * t + lane) : 0; };
+      int ahead = entries(s.t0), page = 0;  // of four tiles, requested four tiles before their use
       for (int t = s.t0; t < s.t1; ++t, ++n) {
-        const int u = (t - s.t0) & 3;
-        if (u == 0) page = 8 * t + lane < blocks ? page_of(A.pool, s.b, 8 * t + lane) : 0;
-        const int pg = __shfl_sync(kFull, page, 8 * u + (lane & 7));
-        const int nb = min(8, blocks - 8 * t), ks = n % L::KS, st = n & 1, ss = n % L::SC;
-        if (n >= L::KS && !wait(bar(K_EMPTY, ks), (n / L::KS - 1) & 1)) break;
-        if (n >= 2 && !wait(bar(VR_EMPTY, st), ((n >> 1) - 1) & 1)) break;
-        if (n >= L::SC && !wait(bar(SC_EMPTY, ss), (n / L::SC - 1) & 1)) break;
-        if (lane == 0) {
-          tqd::mbar_arrive_expect_tx(bar(K_FULL, ks), nb * 16 * D);
-          tqd::mbar_arrive_expect_tx(bar(VR_FULL, st), nb * 16 * D);
-          tqd::mbar_arrive_expect_tx(bar(SC_FULL, ss), nb * 16);
+        const int u = (t - s.t0) & 3, j = lane & 7, nb = min(8, blocks - 8 * t);
+        if (u == 0) {
+          page = checked_page(A.pool, ahead);
+          ahead = entries(t + 4);
         }
-        __syncwarp();
-        const int j = lane & 7;
-        if (j < nb && lane < 24) {
-          const unsigned char* blk = A.pool.base + pool_block(A.pool, pg, s.h) * L::BLK;
-          if (lane < 8) tqd::bulk_g2s(sb + L::KR + ks * L::TILE + j * 16 * D, blk, 16 * D, bar(K_FULL, ks));
-          else if (lane < 16) tqd::bulk_g2s(sb + L::VR + st * L::TILE + j * 16 * D, blk + 16 * D, 16 * D, bar(VR_FULL, st));
-          else tqd::bulk_g2s(sb + L::SCALES + ss * 128 + j * 16, blk + 32 * D, 16, bar(SC_FULL, ss));
+        const int pg = __shfl_sync(kFull, page, 8 * u + j);
+        const unsigned char* blk = A.pool.base + pool_block(A.pool, pg, s.h) * L::BLK;
+        if (keys) {
+          const int st = n % L::KS;
+          if (n >= L::KS && !wait(bar(K_EMPTY, st), (n / L::KS - 1) & 1)) break;
+          if (lane == 0) tqd::mbar_arrive_expect_tx(bar(K_FULL, st), nb * 16 * D);
+          __syncwarp();
+          if (lane < nb) tqd::bulk_g2s(sb + L::KR + st * L::TILE + j * 16 * D, blk, 16 * D, bar(K_FULL, st));
+        } else {
+          const int st = n % L::VS;
+          if (n >= L::VS && !wait(bar(VR_EMPTY, st), (n / L::VS - 1) & 1)) break;
+          if (lane == 0) tqd::mbar_arrive_expect_tx(bar(VR_FULL, st), nb * L::VB);
+          __syncwarp();
+          if (lane < nb) tqd::bulk_g2s(sb + L::VR + (st * 8 + j) * L::VB, blk + 16 * D, L::VB, bar(VR_FULL, st));
         }
         __syncwarp();
       }
     }
     // every copy has landed before the block gives up its shared memory
-    for (uint32_t k = n > L::KS ? n - L::KS : 0; k < n; ++k) {
-      mbar_wait(bar(K_FULL, k % L::KS), (k / L::KS) & 1, kWaitLimit);
-      mbar_wait(bar(SC_FULL, k % L::SC), (k / L::SC) & 1, kWaitLimit);
-    }
-    for (uint32_t k = n > 2 ? n - 2 : 0; k < n; ++k) mbar_wait(bar(VR_FULL, k & 1), (k >> 1) & 1, kWaitLimit);
+    if (keys)
+      for (uint32_t k = n > L::KS ? n - L::KS : 0; k < n; ++k) mbar_wait(bar(K_FULL, k % L::KS), (k / L::KS) & 1, kWaitLimit);
+    else
+      for (uint32_t k = n > L::VS ? n - L::VS : 0; k < n; ++k) mbar_wait(bar(VR_FULL, k % L::VS), (k / L::VS) & 1, kWaitLimit);
   } else if (warp == 13) {
     // ---- MMA issue, from operands that are constants of the stage
     uint32_t n = 0, segs = 0;
@@ -454,8 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
         for (int h = 0; h < 2; ++h) {
           if (!wait(bar(P_FULL, 2 * (g & 1) + h), (g >> 1) & 1)) break;
           tqd::tc_fence_after();
-          if (g & 1) issue_readout<D, NT, 1>(sb, h, k >= 2);
-          else issue_readout<D, NT, 0>(sb, h, k >= 2);
+          if (g & 1) issue_readout<D, 1>(sb, h, k > 0);
+          else issue_readout<D, 0>(sb, h, k > 0);
         }
         if (!ok) break;
         if (k + 2 < tiles) {
@@ -477,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
 
 template <int D, int NT, typename T>
 cudaError_t tree_go(TcParams p, int sms, int device, cudaStream_t s) {
-  using L = Plan<D, NT>;
+  using L = Plan<D>;
   static std::atomic<uint64_t> done{0};
   p.groups = (p.rows + 127) / 128;
   p.grid = sms;
