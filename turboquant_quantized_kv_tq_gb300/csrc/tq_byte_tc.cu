@@ -203,12 +203,16 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
       const T* q_row = reinterpret_cast<const T*>(A.q.p) + s.b * A.q.sb + qi * A.q.st + hd * A.q.sh;
       unsigned char* q_tile = sm + L::Q + i * NT * 16384;
       float f;
-      if constexpr (TREE)
-        f = query_terms<kD, NT>(q_row, asks, A.scale, [&](int t, int c, const uint32_t* w) {
+      if constexpr (TREE) {
+        QueryRow<kD> q;
+        q.request(q_row, asks);
+        f = query_terms<kD, NT, T>(q, A.scale, t_s, 0, kD / 16, [&](int t, int c, const uint32_t* w) {
           *reinterpret_cast<uint4*>(q_tile + 16384 * t + k_chunk<kD>(r, c)) = make_uint4(w[0], w[1], w[2], w[3]);
         });
-      else
+        tqd::tc_fence_before();
+      } else {
         f = query_row<kD, NT, T>(q_row, live, A.scale, q_tile, r);
+      }
       tqd::tc_fence_smem();
       tqd::tc_mbar_arrive(bar(Q_FULL, i));
       float M = -INFINITY, l = 0.f;
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
         tqd::tc_fence_after();
         const float4* sc = reinterpret_cast<const float4*>(sm + L::SCALES + 128 * ss);
         const int left = lim - kTok * t;  // tokens of this tile that the row attends to
-        if (TREE && kTok * (t + 1) > drafts) hide_scores(t_s, A.tree, s.b, qi, asks, s.cnt, drafts, t);
+        if (TREE && kTok * (t + 1) > drafts) hide_scores<4>(t_s, A.tree, s.b, qi, asks, s.cnt, kTok * t - drafts);
         float v[128];
         ld32_async(t_s, v);
         ld32_async(t_s + 32, v + 32);

@@ -235,20 +235,53 @@ __device__ __forceinline__ void st8_async(uint32_t taddr, const uint32_t* v) {
                : "memory");
 }
 
-// The same for a tree's kernels, which keep their code small: what a block runs once a stretch waits for its
-// instructions (unrolled, the terms of a row and a second copy of the tile for hidden tokens took 17 us a stretch).
-// put(t, c, w) takes codes 16 c .. of term t.  The factor is never so small that a scaled one of -infinity is not.
+// 32 W scores from column t_s of this thread's lane to -infinity where the row (draft i of entry b) does not attend to
+// the token; j0: the draft at the first (negative: a token before the drafts).  Their factors are positive, so it hides them.
+template <int W>
+__device__ __forceinline__ void hide_scores(uint32_t t_s, const TreeMasks& M, int b, int i, bool asks, int cnt, int j0) {
+  const uint32_t* m = M.row(b, i);
+  uint32_t w[W];
+#pragma unroll
+  for (int x = 0; x < W; ++x) w[x] = asks ? tree_word(m, M.words, cnt, j0 + 32 * x) : 0u;
+#pragma unroll 1
+  for (int g = 0; g < W; ++g, t_s += 32) {
+    const uint32_t bits = w[0];
+#pragma unroll
+    for (int x = 1; x < W; ++x) w[x - 1] = w[x];
+    if (!__any_sync(kFull, bits != 0xffffffffu)) continue;
+    float v[32];
+    tqd::tc_ld32(t_s, v);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = bits >> k & 1u ? v[k] : -INFINITY;
+    tqd::tc_st32(t_s, v);
+  }
+}
+
+// query_row for a tree's kernels, which keep their code small: what a block runs once a stretch waits for its
+// instructions.  The row is loaded ahead (request), so that it does not wait behind the next tiles' copies; its
+// words are then put through 64 (D / 2) columns of tensor memory from t_raw on, so that a loop can take them 16 values at a
+// time: put(t, c, w) takes codes 16 c .. of term t, for chunks c in [c0, c1).  The factor is never so small that a scaled
+// one of -infinity is not.
+template <int D>
+struct QueryRow {
+  uint4 raw[D / 8];
+  __device__ __forceinline__ void request(const void* src, bool live) {
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) raw[c] = live ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0u, 0u, 0u, 0u);
+  }
+};
 template <int D, int NT, typename T, typename F>
-__device__ __forceinline__ float query_terms(const T* src, bool live, float scale, F put) {
+__device__ __forceinline__ float query_terms(const QueryRow<D>& q, float scale, uint32_t t_raw, int c0, int c1, F put) {
   float amax = 0.f;
-#pragma unroll 4
+#pragma unroll
   for (int c = 0; c < D / 16; ++c) {
     float x[16];
-    Raw16<T> raw = {};
-    if (live) raw = Raw16<T>{{__ldg(reinterpret_cast<const uint4*>(src) + 2 * c), __ldg(reinterpret_cast<const uint4*>(src) + 2 * c + 1)}};
-    unpack16(raw, x, src);
+    unpack16(Raw16<T>{{q.raw[2 * c], q.raw[2 * c + 1]}}, x, (const T*)nullptr);
 #pragma unroll
     for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(x[k]));
+    const uint32_t w[8] = {q.raw[2 * c].x, q.raw[2 * c].y, q.raw[2 * c].z, q.raw[2 * c].w,
+                           q.raw[2 * c + 1].x, q.raw[2 * c + 1].y, q.raw[2 * c + 1].z, q.raw[2 * c + 1].w};
+    st8_async(t_raw + 8 * c, w);
   }
   const bool odd = !(amax <= 3.402823466e38f);  // an infinity: the row's result is NaN, as the formula's is
   const unsigned u = __float_as_uint(amax);
@@ -256,12 +289,16 @@ __device__ __forceinline__ float query_terms(const T* src, bool live, float scal
   e = min(120, max(-120, e));
   if (amax == 0.f || odd) e = 0;
   const float inv = scale < 0.f ? -exp2i(-e) : exp2i(-e);
+  asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 #pragma unroll 1
-  for (int c = 0; c < D / 16; ++c) {
+  for (int c = c0; c < c1; ++c) {
+    Raw16<T> raw;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\ntcgen05.wait::ld.sync.aligned;\n"
+                 : "=r"(raw.v[0].x), "=r"(raw.v[0].y), "=r"(raw.v[0].z), "=r"(raw.v[0].w), "=r"(raw.v[1].x), "=r"(raw.v[1].y),
+                   "=r"(raw.v[1].z), "=r"(raw.v[1].w)
+                 : "r"(t_raw + 8 * c) : "memory");
     float x[16];
-    Raw16<T> raw = {};
-    if (live) raw = Raw16<T>{{__ldg(reinterpret_cast<const uint4*>(src) + 2 * c), __ldg(reinterpret_cast<const uint4*>(src) + 2 * c + 1)}};
-    unpack16(raw, x, src);
+    unpack16(raw, x, (const T*)nullptr);
 #pragma unroll
     for (int k = 0; k < 16; ++k) x[k] *= inv;
 #pragma unroll
@@ -282,26 +319,6 @@ __device__ __forceinline__ float query_terms(const T* src, bool live, float scal
   }
   const float f = fabsf(scale) * kLog2e * exp2i(e);
   return odd ? __uint_as_float(0x7fc00000u) : fmaxf(f, 8.07793567e-28f);  // 2^-90
-}
-
-// Scores of tile t, 128 columns from t_s of this thread's lane, to -infinity where the row (draft i, first draft at
-// position `drafts`) does not attend to the token.  Their factors are positive, so it hides them.
-__device__ __forceinline__ void hide_scores(uint32_t t_s, const TreeMasks& M, int b, int i, bool asks, int cnt, int drafts, int t) {
-  const uint32_t* m = M.row(b, i);
-  uint32_t w[4];
-#pragma unroll
-  for (int x = 0; x < 4; ++x) w[x] = asks ? tree_word(m, M.words, cnt, kTok * t - drafts + 32 * x) : 0u;
-#pragma unroll 1
-  for (int g = 0; g < 4; ++g, t_s += 32) {
-    const uint32_t bits = w[0];
-    w[0] = w[1], w[1] = w[2], w[2] = w[3];
-    if (!__any_sync(kFull, bits != 0xffffffffu)) continue;
-    float v[32];
-    tqd::tc_ld32(t_s, v);
-#pragma unroll
-    for (int k = 0; k < 32; ++k) v[k] = bits >> k & 1u ? v[k] : -INFINITY;
-    tqd::tc_st32(t_s, v);
-  }
 }
 
 // The largest s + e of one block's 16 scores (left: those the row attends to, when EDGE).

@@ -32,22 +32,31 @@ struct Plan {
   static constexpr int BLK = 32 * D + 32;
   static constexpr int TILE = 128 * D;                            // bytes of a tile's codes
   static constexpr int FIRST = 4;                                 // blocks of a tile in the first part of P
-  static constexpr int KS = 4;                                    // K stages: scores run two tiles ahead
-  static constexpr int VS = 5;                                    // stages of V's codes: copies take 2 us under load
+  static constexpr int KS = D == 128 ? 4 : 8;                     // K stages: scores run two tiles ahead
+  static constexpr int VS = D == 128 ? 5 : 8;                     // stages of V's codes: copies take 2 us under load
   static constexpr int VB = 16 * D + 16;                          // V's codes of a block and the scales behind them: one copy
   static constexpr int SC = 4;                                    // stages of scales, [block] (K scale, e, 2^-e, -)
   static constexpr int KR = 0, V16 = KR + KS * TILE, VR = V16 + 4 * TILE;
-  static constexpr int SCALES = VR + VS * 8 * VB, REF = SCALES + SC * 128, SUM = REF + 2 * 128 * 4, BARS = SUM + 2 * 128 * 4;
-  static constexpr int PRE = BARS + 384;
+  static constexpr int SCALES = VR + VS * 8 * VB, REF = SCALES + SC * 128, SUM = REF + 2 * 128 * 4, STRETCH = SUM + 2 * 128 * 4;
+  static constexpr int TOP = STRETCH + 8 * 2 * 64;                // [row warp][turn]: what Stretch holds
+  static constexpr int SWAP = TOP + 128 * 4, BARS = SWAP + 2 * 8 * 128 * 4;  // halves of rows that two lanes share
+  static constexpr int PRE = BARS + 512;
   static constexpr int T_O = 256, T_Q = 384;                      // columns of O and of the queries' terms (S_i at 128 i)
   static constexpr int SMEM = PRE + (TQ_MAX_BATCH + 1) * 4;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static constexpr int PART = 128 * (D + 2);                      // floats of a partial
 };
 // (P_FULL: half h of group i at 2 i + h)
-enum Bar { K_FULL = 0, K_EMPTY = 4, VR_FULL = 8, VR_EMPTY = 13, V_FULL = 18, V_EMPTY = 20, S_FULL = 22, O_DONE = 24, REF_SET = 26,
-           P_FULL = 28, SC_EMPTY = 32, SC_READY = 36, Q_FULL = 40, SUM_SET = 41, OUT_READ = 42, BAR_COUNT = 43 };
-static_assert(8 * BAR_COUNT + 4 <= 384, "barriers and the tensor-memory slot");
+enum Bar { K_FULL = 0, K_EMPTY = 8, VR_FULL = 16, VR_EMPTY = 24, V_FULL = 32, V_EMPTY = 34, S_FULL = 36, O_DONE = 38, REF_SET = 40,
+           P_FULL = 42, SC_EMPTY = 46, SC_READY = 50, Q_FULL = 54, SUM_SET = 55, OUT_READ = 56, SWAPPED = 57, BAR_COUNT = 59 };
+static_assert(8 * BAR_COUNT + 4 <= 512, "barriers and the tensor-memory slot");
+
+// A stretch of a slab's tiles as the row warps keep it.
+struct Stretch {
+  int b, h, rg, cnt, drafts;  // drafts: the first one's position
+  int t0, t1, tiles, start, place;
+};
+static_assert(sizeof(Stretch) <= 64, "its place in shared memory");
 
 // Swizzled K-major operand of rows of D codes: 128-byte swizzle in groups of 1024 bytes, 64-byte in 512.
 template <int D>
@@ -87,11 +96,15 @@ __device__ __forceinline__ void issue_scores(uint32_t sb) {
 }
 template <int D, int NT>
 __device__ __forceinline__ void issue_scores(uint32_t sb, uint32_t n) {
-  switch (n & 3) {
+  switch (n % Plan<D>::KS) {
     case 0: return issue_scores<D, NT, 0>(sb);
     case 1: return issue_scores<D, NT, 1>(sb);
     case 2: return issue_scores<D, NT, 2>(sb);
-    default: return issue_scores<D, NT, 3>(sb);
+    case 3: return issue_scores<D, NT, 3>(sb);
+    case 4: return issue_scores<D, NT, (Plan<D>::KS > 4 ? 4 : 0)>(sb);
+    case 5: return issue_scores<D, NT, (Plan<D>::KS > 4 ? 5 : 0)>(sb);
+    case 6: return issue_scores<D, NT, (Plan<D>::KS > 4 ? 6 : 0)>(sb);
+    default: return issue_scores<D, NT, (Plan<D>::KS > 4 ? 7 : 0)>(sb);
   }
 }
 // Part h (blocks [0, FIRST), [FIRST, 8)) of O += P_i V of the tile in V buffer i (accumulate: not the first tile of
@@ -114,9 +127,25 @@ __device__ __forceinline__ void issue_readout(uint32_t sb, int h, bool accumulat
   __syncwarp();
 }
 
-template <int D, int NT, typename T>
+__device__ __forceinline__ uint32_t pack2(const __nv_bfloat16*, float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(const __half*, float a, float b) { return tqd::pack_half2(a, b); }
+template <typename T>
+__device__ __forceinline__ void store4(T* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack2(p, v.x, v.y), pack2(p, v.z, v.w));
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float* v) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack2(p, v[0], v[1]), pack2(p, v[2], v[3]), pack2(p, v[4], v[5]), pack2(p, v[6], v[7]));
+}
+
+template <int D, int NT, int F, typename T>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
   using L = Plan<D>;
+  constexpr int ROWS = 128 / F;     // rows of a group: each has F lanes,
+  constexpr int NB = 8 / F;         // each of which takes this many blocks of a tile
   extern __shared__ __align__(1024) unsigned char sm[];
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const AttnArgs& A = p.a;
@@ -143,6 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
       tqd::mbar_init(bar(P_FULL, 2 * i + 1), 128);
       tqd::mbar_init(bar(O_DONE, i), 1);
       tqd::mbar_init(bar(REF_SET, i), 128);
+      tqd::mbar_init(bar(SWAPPED, i), 128);
     }
     for (int i = 0; i < L::KS; ++i) {
       tqd::mbar_init(bar(K_FULL, i), 1);
@@ -161,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
     tqd::mbar_init(bar(OUT_READ, 0), 256);
     tqd::fence_mbar_init();
   }
-  fill_plan<true>(p, 128, pre, blockIdx.x == 0 ? A.pool.err : nullptr);
+  fill_plan<true>(p, ROWS, pre, blockIdx.x == 0 ? A.pool.err : nullptr);
   tqd::tc_fence_before();
   __syncthreads();
   tqd::tc_fence_after();
@@ -180,53 +210,72 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
   if (warp < 8) {
     // ---- rows: group i takes the tiles n = i (mod 2) of the block's sequence
-    const int i = warp >> 2, r = (warp & 3) * 32 + lane;
+    const int i = warp >> 2, r = (warp & 3) * 32 + lane, rr = r % ROWS, part = r / ROWS;  // lane r: part `part` of row rr
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = lanes + 128 * i, t_o = lanes + L::T_O;
-    float* refs = reinterpret_cast<float*>(sm + L::REF);  // [tile % 2][row]: M from this tile on
-    float* sums = reinterpret_cast<float*>(sm + L::SUM);  // [group][row]
+    const uint32_t t_mine = t_s + 16 * NB * part, t_p = t_s + 8 * NB * part;  // the lane's scores and its part of P
+    float* refs = reinterpret_cast<float*>(sm + L::REF);  // [tile % 2][lane]: M from this tile on
+    float* sums = reinterpret_cast<float*>(sm + L::SUM);  // [group][lane]
+    float* tops = reinterpret_cast<float*>(sm + L::TOP);  // [lane]
+    float* swap = reinterpret_cast<float*>(sm + L::SWAP) + i * 8 * 128;
     // groups without a live row: zeros, spread over the grid
     {
       const int slabs = A.B * p.groups * A.Hkv, most = A.pool.max_blocks * 16;
       for (int s = blockIdx.x; s < slabs; s += gridDim.x) {
         const int h = s % A.Hkv, rg = s / A.Hkv % p.groups, b = s / A.Hkv / p.groups;
         const int len = clamped_len(A.seq_len, b, most, nullptr), cnt = clamped_count(A.count, b, A.nq);
-        if (group_limit<true>(p, 128, rg, len, cnt) > 0) continue;
-        const int row = rg * 128 + r;
-        if (row < p.rows) {
+        if (group_limit<true>(p, ROWS, rg, len, cnt) > 0) continue;
+        const int row = rg * ROWS + rr;
+        if (row < p.rows && part == 0) {
           uint4* o = reinterpret_cast<uint4*>(out_row<D, T>(p, b, h, row)) + i * (D / 16);
           for (int c = 0; c < D / 16; ++c) o[c] = make_uint4(0u, 0u, 0u, 0u);
         }
       }
     }
-    uint32_t n = 0, segs = 0;  // tiles and stretches so far
-    int at = begin;
-    bool headed = false;
-    while (at < end && ok) {
-      const Seg s = seg_at<true>(p, 128, pre, at, end);
-      const bool first = at == begin;
-      at = s.next;
-      if (s.t0 == s.t1) continue;
-      const int row = s.rg * 128 + r;
-      const bool live = row < p.rows;
-      const int qi = live ? row / p.G : 0, hd = s.h * p.G + (live ? row - qi * p.G : 0);
+    uint32_t n = 0, segs = 0, swaps = 0;  // tiles, stretches and phases of SWAPPED so far
+    int at = begin, t0, t1, qi;
+    bool headed = false, live, asks;
+    QueryRow<D> q;
+    // The next stretch with a tile, and its queries on their way; false: none is left.  What the tiles do not need of it
+    // waits in shared memory: a row's 128 scores leave few registers.
+    auto stretch = [&](uint32_t k) { return reinterpret_cast<Stretch*>(sm + L::STRETCH + (warp * 2 + (k & 1)) * 64); };
+    auto next = [&](uint32_t k) {
+      Seg s;
+      bool first;
+      do {
+        if (at >= end) return false;
+        s = seg_at<true>(p, ROWS, pre, at, end);
+        first = at == begin;
+        at = s.next;
+      } while (s.t0 == s.t1);
+      t0 = s.t0;
+      t1 = s.t1;
+      const int row = s.rg * ROWS + rr;
+      live = row < p.rows;
+      qi = live ? row / p.G : 0;
       // (rows past the count are zero queries whose sums are dropped, so that they hide nothing)
-      const bool asks = live && qi < s.cnt;
-      const int drafts = s.len - s.cnt;  // the first one's position
+      asks = live && qi < s.cnt;
+      const int hd = s.h * p.G + (live ? row - qi * p.G : 0);
+      q.request(reinterpret_cast<const T*>(A.q.p) + s.b * A.q.sb + qi * A.q.st + hd * A.q.sh, asks);
+      if (lane == 0) *stretch(k) = Stretch{s.b, s.h, s.rg, s.cnt, s.len - s.cnt, s.t0, s.t1, s.tiles, s.start, first ? 0 : 1};
+      __syncwarp();
+      return true;
+    };
+    bool more = next(0);
+    while (more && ok) {
       const bool idle = !__any_sync(kFull, asks);  // (uniform over the two groups' warps of the same rows)
-      // group i writes terms i, i + 2
-      const float f = query_terms<D, NT>(reinterpret_cast<const T*>(A.q.p) + s.b * A.q.sb + qi * A.q.st + hd * A.q.sh, asks,
-                                         A.scale, [&](int t, int c, const uint32_t* w) {
-                                           if ((t & 1) == i) st4_async(lanes + L::T_Q + t * (D / 4) + 4 * c, w);
-                                         });
+      // (each group converts half of the coordinates)
+      const float f = query_terms<D, NT, T>(q, A.scale, t_s, i * (D / 32), (i + 1) * (D / 32), [&](int t, int c, const uint32_t* w) {
+        st4_async(lanes + L::T_Q + t * (D / 4) + 4 * c, w);
+      });
       asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
       tqd::tc_fence_before();
       tqd::tc_mbar_arrive(bar(Q_FULL, 0));
       float M = -INFINITY, l = 0.f;  // l under the reference M
-      const int t_first = s.t0 + (int)((n ^ (uint32_t)i) & 1u);
+      const int t_first = t0 + (int)((n ^ (uint32_t)i) & 1u), drafts = stretch(segs)->drafts;
       // one tile; false: a wait gave up
       auto tile = [&](int t) {
-        const uint32_t g_tile = n + (uint32_t)(t - s.t0), turn = g_tile >> 1;
+        const uint32_t g_tile = n + (uint32_t)(t - t0), turn = g_tile >> 1;
         if (!wait(bar(S_FULL, i), turn & 1)) return false;
         const int ss = g_tile % L::SC;
         if (!wait(bar(SC_READY, ss), (g_tile / L::SC) & 1)) return false;
@@ -238,29 +287,30 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
           return true;
         }
         tqd::tc_fence_after();
-        const float4* sc = reinterpret_cast<const float4*>(sm + L::SCALES + 128 * ss);
-        if (kTok * (t + 1) > drafts) hide_scores(t_s, A.tree, s.b, qi, asks, s.cnt, drafts, t);
-        float v[128];
-        ld32_async(t_s, v);
-        ld32_async(t_s + 32, v + 32);
-        float a[8], e[8];
+        const float4* sc = reinterpret_cast<const float4*>(sm + L::SCALES + 128 * ss) + NB * part;
+        const int j0 = kTok * t + 16 * NB * part - drafts;  // the draft at the lane's first score
+        if (j0 + 16 * NB > 0) hide_scores<NB / 2>(t_mine, A.tree, stretch(segs)->b, qi, asks, stretch(segs)->cnt, j0);
+        // A whole row's scores are read twice, 32 at a time, for the maximum and for P: held from one to the other they
+        // left the warps too few registers (138 us for 8 x 32768 tokens and 64 rows).  P takes the first half of the columns:
+        // block g's lie at 8 g, below the scores of block g that it comes from.
+        float a[NB], e[NB], v[2][32];
+        ld32_async(t_mine, v[0]);
+        if (F == 2) ld32_async(t_mine + 32, v[1]);
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          const float4 x = sc[g];
+        for (int g = 0; g < NB; ++g) {
+          const float2 x = *reinterpret_cast<const float2*>(sc + g);
           a[g] = f * x.x;
           e[g] = x.y;
         }
-        ld_wait<64>(v);
-        ld32_async(t_s + 64, v + 64);
-        ld32_async(t_s + 96, v + 96);
-        float top = block_top<false>(v, 0, a[0], e[0]);
+        float top = -INFINITY;
 #pragma unroll
-        for (int g = 1; g < 4; ++g) top = fmaxf(top, block_top<false>(v + 16 * g, 0, a[g], e[g]));
-        ld_wait<64>(v + 64);
-#pragma unroll
-        for (int g = 4; g < 8; ++g) top = fmaxf(top, block_top<false>(v + 16 * g, 0, a[g], e[g]));
+        for (int c = 0; c < NB / 2; ++c) {
+          ld_wait<32>(v[c & 1]);
+          if (F == 1) ld32_async(t_mine + 32 * ((c + 1) & 3), v[(c + 1) & 1]);
+          top = fmaxf(top, fmaxf(block_top<false>(v[c & 1], 0, a[2 * c], e[2 * c]), block_top<false>(v[c & 1] + 16, 0, a[2 * c + 1], e[2 * c + 1])));
+        }
         float m_old = -INFINITY;
-        if (t > s.t0) {
+        if (t > t0) {
           if (!wait(bar(REF_SET, i ^ 1), ((g_tile - 1) >> 1) & 1)) return false;
           m_old = refs[128 * (i ^ 1) + r];
         }
@@ -272,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
           l *= ex2(M - m_new);
           M = m_new;
         }
-        if (t > s.t0 && __any_sync(kFull, raise)) {
+        if (t > t0 && __any_sync(kFull, raise)) {
           const float cor = raise ? ex2(m_old - m_new) : 1.f;
           if (!wait(bar(O_DONE, i ^ 1), ((g_tile - 1) >> 1) & 1)) return false;
           tqd::tc_fence_after();
@@ -287,72 +337,122 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
           }
         }
         const float mr = M == -INFINITY ? 0.f : M;
+        float z[NB];
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          uint32_t w[8];
-          const float sum = block_p<false>(v + 16 * g, 0, a[g], e[g] - mr, w);
-          l = fmaf(sum, sc[g].z, l);
-          st8_async(t_s + 8 * g, w);
-          if (g == L::FIRST - 1 || g == 7) {
+        for (int g = 0; g < NB; ++g) z[g] = sc[g].z;
+        if (F == 2) {  // the tokens of the row's other lane count for nothing here
+          const uint32_t none[8] = {};
+#pragma unroll
+          for (int g = 0; g < NB; ++g) st8_async(t_s + 8 * (NB * (1 - part) + g), none);
+          asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+          tqd::tc_fence_before();
+          tqd::tc_mbar_arrive(bar(P_FULL, 2 * i + 1 - part));
+        }
+#pragma unroll
+        for (int c = 0; c < NB / 2; ++c) {
+          if (F == 1) {
+            ld_wait<32>(v[c & 1]);
+            if (c < 3) ld32_async(t_mine + 32 * (c + 1), v[(c + 1) & 1]);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int g = 2 * c + h;
+            uint32_t w[8];
+            const float sum = block_p<false>(v[c & 1] + 16 * h, 0, a[g], e[g] - mr, w);
+            l = fmaf(sum, z[g], l);
+            st8_async(t_p + 8 * g, w);
+          }
+          if (2 * c + 2 == L::FIRST || 2 * c + 2 == NB) {
             asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
             tqd::tc_fence_before();
-            tqd::tc_mbar_arrive(bar(P_FULL, 2 * i + (g == 7)));
+            tqd::tc_mbar_arrive(bar(P_FULL, 2 * i + (F == 2 ? part : (int)(c == 3))));
           }
         }
         __syncwarp();
         if (lane == 0) tqd::tc_mbar_arrive(bar(SC_EMPTY, ss));
         return true;
       };
-      for (int t = t_first; t < s.t1; t += 2) {
+      for (int t = t_first; t < t1; t += 2) {
         if (!tile(t)) break;
       }
       if (!ok) break;
+      // the next stretch's queries are requested before this one's last products are waited for
+      const uint32_t tiles = (uint32_t)(t1 - t0);
+      const bool was_live = live, asked = asks;
+      more = next(segs + 1);
       // Every product of the stretch is done with its last tile's.  (The tile before it is waited for first: a wait for a
       // phase tells nothing while the barrier is two phases behind.)
-      const uint32_t last = n + (uint32_t)(s.t1 - s.t0) - 1;
+      const uint32_t last = n + tiles - 1;
       if (last > n && !wait(bar(O_DONE, (last - 1) & 1), ((last - 1) >> 1) & 1)) break;
       if (!wait(bar(O_DONE, last & 1), (last >> 1) & 1)) break;
       n = last + 1;
       tqd::tc_fence_after();
       const float top = idle ? -INFINITY : refs[128 * (last & 1) + r];
       if (M != top) l *= ex2(M - top);  // (the other group raised it last; a group without a tile has l = 0)
-      sums[128 * i + r] = asks ? l : 0.f;
+      sums[128 * i + r] = asked ? l : 0.f;
+      if (i == 0) tops[r] = top;
       tqd::tc_mbar_arrive(bar(SUM_SET, 0));
       if (!wait(bar(SUM_SET, 0), segs & 1)) break;
-      ++segs;
-      // each group takes half of the coordinates
-      const float sum = sums[r] + sums[128 + r];
-      const bool whole = s.t0 == 0 && s.t1 == s.tiles;
-      const float scale = !whole ? 1.f : sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-      float* part = p.part + (2ll * blockIdx.x + (first ? 0 : 1)) * L::PART;
-      T* o = out_row<D, T>(p, s.b, s.h, live ? row : 0);
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        const int col = i * (D / 2) + 32 * c;
-        float v[32];
-        tqd::tc_ld32(t_o + col, v);
-        // (rows that do not ask may hold NaN: what lies behind the tokens is hidden from the others only)
-#pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = asks ? v[k] * scale : 0.f;
-        if (whole) {
-          if (live) {
-            store16(o + col, v);
-            store16(o + col + 16, v + 16);
-          }
-        } else {
-          float4* to = reinterpret_cast<float4*>(part + 256 + (long long)r * D + col);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) to[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-        }
+      const Stretch now = *stretch(segs++);
+      // each group takes half of the coordinates; a row's lanes join
+      float sum = sums[r] + sums[128 + r], most = top, mine = 1.f;  // mine: the weight of this lane's sums
+      if (F == 2) {
+        const int o = r ^ 64;
+        most = fmaxf(top, tops[o]);
+        const float ref = most == -INFINITY ? 0.f : most;
+        mine = ex2(top - ref);
+        sum = fmaf(sum, mine, (sums[o] + sums[128 + o]) * ex2(tops[o] - ref));
       }
-      if (!whole && i == 0) {
-        part[r] = top;
-        part[128 + r] = sum;
+      const bool whole = now.t0 == 0 && now.t1 == now.tiles;
+      if (whole) mine *= sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+      T* out = out_row<D, T>(p, now.b, now.h, was_live ? now.rg * ROWS + rr : 0);
+      float* partial = p.part + (2ll * blockIdx.x + now.place) * L::PART;
+      // [4 coordinates][row]: a warp writes 512 bytes in a row (as rows of their own they took 6000 cycles)
+      float4* to = reinterpret_cast<float4*>(partial + 256) + rr;
+      if (!whole && i == 0 && part == 0) {
+        partial[rr] = most;
+        partial[128 + rr] = sum;
+      }
+      if (F == 2 || whole || !idle) {  // (a partial's rows without a sum are left out by the join)
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          const int col = i * (D / 2) + 16 * c;
+          float v[16];
+          tqd::tc_ld16(t_o + col, v);
+          // (rows that do not ask may hold NaN: what lies behind the tokens is hidden from the others only)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k] = asked ? v[k] * mine : 0.f;
+          if constexpr (F == 1) {
+            if (whole) {
+              if (was_live) store16(out + col, v);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) to[(col / 4 + k) * 128] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            }
+          } else {  // lane 0 of a row finishes the first eight coordinates, lane 1 the others
+            if (c > 0 && !wait(bar(SWAPPED, i), (swaps - 1) & 1)) break;  // (the last values were read)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) swap[128 * k + r] = part ? v[k] : v[8 + k];
+            tqd::tc_mbar_arrive(bar(SWAPPED, i));
+            if (!wait(bar(SWAPPED, i), swaps++ & 1)) break;
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = (part ? v[8 + k] : v[k]) + swap[128 * k + (r ^ 64)];
+            tqd::tc_mbar_arrive(bar(SWAPPED, i));
+            ++swaps;
+            if (whole) {
+              if (was_live) store8(out + col + 8 * part, x);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) to[(col / 4 + 2 * part + k) * 128] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+            }
+          }
+        }
       }
       tqd::tc_fence_before();
       tqd::tc_mbar_arrive(bar(OUT_READ, 0));  // (the next stretch's first products overwrite the sums)
-      if (threadIdx.x == 0 && s.t0 == 0 && s.t1 < s.tiles) {  // this range's last stretch begins a group that goes on
-        p.heads[blockIdx.x] = JoinHead{(s.start + s.tiles - 1) / per, first ? 0 : 1, s.b, s.h, s.rg};
+      if (threadIdx.x == 0 && now.t0 == 0 && now.t1 < now.tiles) {  // this range's last stretch begins a group that goes on
+        p.heads[blockIdx.x] = JoinHead{(now.start + now.tiles - 1) / per, now.place, now.b, now.h, now.rg};
         headed = true;
       }
     }
@@ -362,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
     uint32_t n = 0;
     int at = begin;
     while (at < end && ok) {
-      const Seg s = seg_at<true>(p, 128, pre, at, end);
+      const Seg s = seg_at<true>(p, ROWS, pre, at, end);
       at = s.next;
       for (int t = s.t0; t < s.t1; ++t, ++n) {
         const int st = n & 1, vs = n % L::VS, ss = n % L::SC;
@@ -434,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
     uint32_t n = 0;
     int at = warp == 15 ? end : begin;
     while (at < end && ok) {
-      const Seg s = seg_at<true>(p, 128, pre, at, end);
+      const Seg s = seg_at<true>(p, ROWS, pre, at, end);
       at = s.next;
       const int blocks = (s.limit + 15) >> 4;
       auto entries = [&](int t) { return 8 * t + lane < blocks ? page_entry(A.pool, s.b, 8 * t + lane) : 0; };
@@ -473,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
     uint32_t n = 0, segs = 0;
     int at = begin;
     while (at < end && ok) {
-      const Seg s = seg_at<true>(p, 128, pre, at, end);
+      const Seg s = seg_at<true>(p, ROWS, pre, at, end);
       at = s.next;
       if (s.t0 == s.t1) continue;
       const uint32_t tiles = (uint32_t)(s.t1 - s.t0);
@@ -513,28 +613,69 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
   }
 }
 
-template <int D, int NT, typename T>
+// join_kernel for the partials of tree_kernel: a thread takes four coordinates of a row, rows beside each other in a
+// warp, as the partials hold them.  Rows that did not ask have no sum, and whatever lies in their place is left out.
+constexpr int kJoinThreads = 256;
+template <int D, int F, typename T>
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const JoinParams p) {
+  constexpr int ROWS = kJoinThreads / (D / 4);
+  constexpr long long PART = Plan<D>::PART;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const JoinHead H = p.heads[blockIdx.x];
+  const int rr = blockIdx.y * ROWS + threadIdx.x % ROWS, c = threadIdx.x / ROWS, row = H.group * (128 / F) + rr;
+  if (H.last < 0 || rr >= 128 / F || row >= p.rows) return;
+  const int n = H.last - (int)blockIdx.x + 1;
+  const float* first = p.part + (2ll * blockIdx.x + H.place) * PART;
+  const float* rest = p.part + 2ll * blockIdx.x * PART;  // part i >= 1 at rest + 2 i PART
+  auto at = [&](int i) { return i ? rest + 2ll * i * PART : first; };
+  float top = -INFINITY;
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) top = fmaxf(top, at(i)[rr]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float* x = at(i);
+    const float w = ex2(x[rr] - ref);
+    const float4 v = reinterpret_cast<const float4*>(x + 256)[c * 128 + rr];
+    l = fmaf(x[128 + rr], w, l);
+    o.x = fmaf(v.x, w, o.x);
+    o.y = fmaf(v.y, w, o.y);
+    o.z = fmaf(v.z, w, o.z);
+    o.w = fmaf(v.w, w, o.w);
+  }
+  const bool some = l > 0.f || l != l;
+  const float il = 1.f / l;
+  const int qi = row / p.G, hd = H.h * p.G + row - qi * p.G;
+  T* out = reinterpret_cast<T*>(p.out) + (((long long)H.b * p.nq + qi) * p.Hq + hd) * D + 4 * c;
+  store4(out, some ? make_float4(o.x * il, o.y * il, o.z * il, o.w * il) : make_float4(0.f, 0.f, 0.f, 0.f));
+}
+
+template <int D, int NT, int F, typename T>
 cudaError_t tree_go(TcParams p, int sms, int device, cudaStream_t s) {
   using L = Plan<D>;
+  constexpr int ROWS = 128 / F;
   static std::atomic<uint64_t> done{0};
-  p.groups = (p.rows + 127) / 128;
+  p.groups = (p.rows + ROWS - 1) / ROWS;
   p.grid = sms;
-  cudaError_t e = allow_smem((const void*)tree_kernel<D, NT, T>, L::SMEM, device, done);
+  cudaError_t e = allow_smem((const void*)tree_kernel<D, NT, F, T>, L::SMEM, device, done);
   if (e != cudaSuccess) return e;
-  tree_kernel<D, NT, T><<<p.grid, kThreads, L::SMEM, s>>>(p);
+  tree_kernel<D, NT, F, T><<<p.grid, kThreads, L::SMEM, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (p.grid == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
-  const int rows = p.rows < 128 ? p.rows : 128;
-  cfg.gridDim = dim3(p.grid - 1, (rows + kJoinRows - 1) / kJoinRows);
-  cfg.blockDim = dim3(32 * kJoinRows);
+  const int rows = p.rows < ROWS ? p.rows : ROWS;
+  constexpr int join_rows = kJoinThreads / (D / 4);
+  cfg.gridDim = dim3(p.grid - 1, (rows + join_rows - 1) / join_rows);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, 128, 1, T>, JoinParams{p.heads, p.part, p.a.out, p.a.nq, p.a.Hq, p.G, p.rows});
+  return cudaLaunchKernelEx(&cfg, tree_join_kernel<D, F, T>, JoinParams{p.heads, p.part, p.a.out, p.a.nq, p.a.Hq, p.G, p.rows});
 }
 
 constexpr int kTreeMinRows = 16;
@@ -545,7 +686,7 @@ bool tree_tc_takes(const AttnArgs& a) {
   const int rows = a.Hq / a.Hkv * a.nq;
   if ((a.d != 64 && a.d != 128) || a.dtype == TQ_F32 || rows <= kTreeMinRows) return false;
   // the plan counts tiles in 32 bits
-  const long long groups = (rows + 127) / 128, tiles = (a.pool.max_blocks + 7) / 8 + kGroupCost;
+  const long long groups = (rows + 63) / 64, tiles = (a.pool.max_blocks + 7) / 8 + kGroupCost;
   return (long long)a.B * a.Hkv * groups * tiles < (1ll << 31) - (1ll << 20);
 }
 
@@ -555,13 +696,18 @@ size_t tree_tc_workspace(int d, int rows, tq_dtype dtype) {
   return kJoinHeadBytes + (size_t)2 * kMaxSms * 128 * (d + 2) * sizeof(float);
 }
 
+template <typename T, int NT>
+static cudaError_t tree_type(const TcParams& p, int sms, int dev, cudaStream_t s) {
+  if (p.a.d == 64) return tree_go<64, NT, 2, T>(p, sms, dev, s);
+  return p.rows <= 64 ? tree_go<128, NT, 2, T>(p, sms, dev, s) : tree_go<128, NT, 1, T>(p, sms, dev, s);
+}
+
 cudaError_t launch_tree_tc(const AttnArgs& a, cudaStream_t s) {
+  if (a.d == 128 && a.Hq / a.Hkv * a.nq > 128) return launch_tc_tree(a, s);
   TcParams p;
   int dev;
   const int sms = tc_params(a, &p, &dev);
-  if (a.d == 64) return a.dtype == TQ_BF16 ? tree_go<64, 2, __nv_bfloat16>(p, sms, dev, s) : tree_go<64, 3, __half>(p, sms, dev, s);
-  if (p.rows > 128) return launch_tc_tree(a, s);
-  return a.dtype == TQ_BF16 ? tree_go<128, 2, __nv_bfloat16>(p, sms, dev, s) : tree_go<128, 3, __half>(p, sms, dev, s);
+  return a.dtype == TQ_BF16 ? tree_type<__nv_bfloat16, 2>(p, sms, dev, s) : tree_type<__half, 3>(p, sms, dev, s);
 }
 
 }  // namespace tqb
