@@ -38,9 +38,9 @@ struct Plan {
   static constexpr int SC = 4;                                    // stages of scales, [block] (K scale, e, 2^-e, -)
   static constexpr int KR = 0, V16 = KR + KS * TILE, VR = V16 + 4 * TILE;
   static constexpr int SCALES = VR + VS * 8 * VB, REF = SCALES + SC * 128, SUM = REF + 2 * 128 * 4, STRETCH = SUM + 2 * 128 * 4;
-  static constexpr int TOP = STRETCH + 8 * 2 * 64;                // [row warp][turn]: what Stretch holds
+  static constexpr int TOP = STRETCH + 8 * 2 * 40;                // [row warp][turn]
   static constexpr int SWAP = TOP + 128 * 4, BARS = SWAP + 2 * 8 * 128 * 4;  // halves of rows that two lanes share
-  static constexpr int PRE = BARS + 512;
+  static constexpr int LEN = BARS + 496, PRE = LEN + TQ_MAX_BATCH * 8;
   static constexpr int T_O = 256, T_Q = 384;                      // columns of O and of the queries' terms (S_i at 128 i)
   static constexpr int SMEM = PRE + (TQ_MAX_BATCH + 1) * 4;
   static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -48,15 +48,61 @@ struct Plan {
 };
 // (P_FULL: half h of group i at 2 i + h)
 enum Bar { K_FULL = 0, K_EMPTY = 8, VR_FULL = 16, VR_EMPTY = 24, V_FULL = 32, V_EMPTY = 34, S_FULL = 36, O_DONE = 38, REF_SET = 40,
-           P_FULL = 42, SC_EMPTY = 46, SC_READY = 50, Q_FULL = 54, SUM_SET = 55, OUT_READ = 56, SWAPPED = 57, BAR_COUNT = 59 };
-static_assert(8 * BAR_COUNT + 4 <= 512, "barriers and the tensor-memory slot");
+           P_FULL = 42, SC_EMPTY = 46, SC_READY = 50, Q_FULL = 54, SUM_SET = 55, OUT_READ = 56, SWAPPED = 57, BAR_COUNT = 61 };
+static_assert(8 * BAR_COUNT + 4 <= 496, "barriers and the tensor-memory slot");
 
-// A stretch of a slab's tiles as the row warps keep it.
+// The plan: all live row groups of an entry cover its whole sequence.  len[b]: (tokens, drafts).
+template <int ROWS>
+__device__ __forceinline__ int live_groups(const TcParams& p, int2 len) { return len.x > 0 ? (len.y * p.G + ROWS - 1) / ROWS : 0; }
+
+// Costs before each entry (order: entry, row group, head), and the entries' lengths; written by warp 0.
+template <int ROWS>
+__device__ __forceinline__ void fill_tree_plan(const TcParams& p, int* pre, int2* len, int32_t* err) {
+  const int lane = threadIdx.x & 31, most = p.a.pool.max_blocks * 16;
+  if (threadIdx.x < 32) {
+    int run = 0;
+    for (int b0 = 0; b0 < p.a.B; b0 += 32) {
+      const int b = b0 + lane;
+      int t = 0;
+      if (b < p.a.B) {
+        const int2 x = make_int2(clamped_len(p.a.seq_len, b, most, err), clamped_count(p.a.count, b, p.a.nq));
+        len[b] = x;
+        t = live_groups<ROWS>(p, x) * p.a.Hkv * cost_of(tiles_of(x.x));
+      }
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const int o = __shfl_up_sync(kFull, t, m);
+        if (lane >= m) t += o;
+      }
+      if (b < p.a.B) pre[b + 1] = run + t;
+      run += __shfl_sync(kFull, t, 31);
+    }
+    if (lane == 0) pre[0] = 0;
+  }
+}
+
+// A stretch of a slab's tiles [t0, t1), the first from cost `at` (< end) on that has a tile; t0 = t1: there is none.
 struct Stretch {
-  int b, h, rg, cnt, drafts;  // drafts: the first one's position
-  int t0, t1, tiles, start, place;
+  int b, h, rg, len, cnt;
+  int t0, t1, tiles;
+  int start, next;  // of the slab's group, of the stretch after this one
 };
-static_assert(sizeof(Stretch) <= 64, "its place in shared memory");
+static_assert(sizeof(Stretch) <= 40, "its place in shared memory");
+__device__ __forceinline__ Stretch stretch_from(const TcParams& p, const int* pre, const int2* len, int b, int at, int end) {
+  Stretch s = {};
+  while (at < end) {
+    while (pre[b + 1] <= at) ++b;
+    const int2 n = len[b];
+    const int tiles = tiles_of(n.x), span = cost_of(tiles), x = at - pre[b], k = x / span, y = x - k * span;
+    if (y < tiles) {
+      const int rg = k / p.a.Hkv;
+      return Stretch{b, k - rg * p.a.Hkv, rg, n.x, n.y, y, min(tiles, y + (end - at)), tiles, at - y, min(end, at + span - y)};
+    }
+    at += span - y;
+  }
+  s.next = end;
+  return s;
+}
 
 // Swizzled K-major operand of rows of D codes: 128-byte swizzle in groups of 1024 bytes, 64-byte in 512.
 template <int D>
@@ -155,6 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
   auto bar = [&](int kind, int i) { return bars + 8 * (kind + i); };
   uint32_t* slot = reinterpret_cast<uint32_t*>(sm + L::BARS + 8 * BAR_COUNT);
   int* pre = reinterpret_cast<int*>(sm + L::PRE);
+  int2* lens = reinterpret_cast<int2*>(sm + L::LEN);
   if (sb & 1023u) {  // the swizzled operands need it (the plan gives it)
     if (threadIdx.x == 0) {
       p.heads[blockIdx.x].last = -1;
@@ -172,7 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
       tqd::mbar_init(bar(P_FULL, 2 * i + 1), 128);
       tqd::mbar_init(bar(O_DONE, i), 1);
       tqd::mbar_init(bar(REF_SET, i), 128);
-      tqd::mbar_init(bar(SWAPPED, i), 128);
+      tqd::mbar_init(bar(SWAPPED, 2 * i), 64);
+      tqd::mbar_init(bar(SWAPPED, 2 * i + 1), 64);
     }
     for (int i = 0; i < L::KS; ++i) {
       tqd::mbar_init(bar(K_FULL, i), 1);
@@ -191,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
     tqd::mbar_init(bar(OUT_READ, 0), 256);
     tqd::fence_mbar_init();
   }
-  fill_plan<true>(p, ROWS, pre, blockIdx.x == 0 ? A.pool.err : nullptr);
+  fill_tree_plan<ROWS>(p, pre, lens, blockIdx.x == 0 ? A.pool.err : nullptr);
   tqd::tc_fence_before();
   __syncthreads();
   tqd::tc_fence_after();
@@ -219,35 +267,28 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
     float* tops = reinterpret_cast<float*>(sm + L::TOP);  // [lane]
     float* swap = reinterpret_cast<float*>(sm + L::SWAP) + i * 8 * 128;
     // groups without a live row: zeros, spread over the grid
-    {
-      const int slabs = A.B * p.groups * A.Hkv, most = A.pool.max_blocks * 16;
-      for (int s = blockIdx.x; s < slabs; s += gridDim.x) {
-        const int h = s % A.Hkv, rg = s / A.Hkv % p.groups, b = s / A.Hkv / p.groups;
-        const int len = clamped_len(A.seq_len, b, most, nullptr), cnt = clamped_count(A.count, b, A.nq);
-        if (group_limit<true>(p, ROWS, rg, len, cnt) > 0) continue;
-        const int row = rg * ROWS + rr;
-        if (row < p.rows && part == 0) {
-          uint4* o = reinterpret_cast<uint4*>(out_row<D, T>(p, b, h, row)) + i * (D / 16);
-          for (int c = 0; c < D / 16; ++c) o[c] = make_uint4(0u, 0u, 0u, 0u);
-        }
+    for (int k = blockIdx.x; k < A.B * p.groups; k += gridDim.x) {
+      const int b = k / p.groups, rg = k - b * p.groups, row = rg * ROWS + rr;
+      if (rg < live_groups<ROWS>(p, lens[b]) || row >= p.rows) continue;
+      for (int h = part; h < A.Hkv; h += F) {
+        uint4* o = reinterpret_cast<uint4*>(out_row<D, T>(p, b, h, row)) + i * (D / 16);
+        for (int c = 0; c < D / 16; ++c) o[c] = make_uint4(0u, 0u, 0u, 0u);
       }
     }
     uint32_t n = 0, segs = 0, swaps = 0;  // tiles, stretches and phases of SWAPPED so far
-    int at = begin, t0, t1, qi;
-    bool headed = false, live, asks;
+    int t0 = 0, t1 = 0, qi = 0;
+    bool headed = false, live = false, asks = false;
     QueryRow<D> q;
-    // The next stretch with a tile, and its queries on their way; false: none is left.  What the tiles do not need of it
-    // waits in shared memory: a row's 128 scores leave few registers.
-    auto stretch = [&](uint32_t k) { return reinterpret_cast<Stretch*>(sm + L::STRETCH + (warp * 2 + (k & 1)) * 64); };
-    auto next = [&](uint32_t k) {
-      Seg s;
-      bool first;
-      do {
-        if (at >= end) return false;
-        s = seg_at<true>(p, ROWS, pre, at, end);
-        first = at == begin;
-        at = s.next;
-      } while (s.t0 == s.t1);
+    // The stretches wait in shared memory (a row's scores leave few registers): each is looked for while the one before
+    // it runs, and its queries are requested before that one's sums are written.
+    auto stretch = [&](uint32_t k) { return reinterpret_cast<Stretch*>(sm + L::STRETCH + (warp * 2 + (k & 1)) * 40); };
+    auto look = [&](uint32_t k, int b, int at) {
+      const Stretch s = stretch_from(p, pre, lens, b, at, end);
+      if (lane == 0) *stretch(k) = s;
+      __syncwarp();
+    };
+    auto begin_stretch = [&](uint32_t k) {
+      const Stretch& s = *stretch(k);
       t0 = s.t0;
       t1 = s.t1;
       const int row = s.rg * ROWS + rr;
@@ -257,11 +298,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
       asks = live && qi < s.cnt;
       const int hd = s.h * p.G + (live ? row - qi * p.G : 0);
       q.request(reinterpret_cast<const T*>(A.q.p) + s.b * A.q.sb + qi * A.q.st + hd * A.q.sh, asks);
-      if (lane == 0) *stretch(k) = Stretch{s.b, s.h, s.rg, s.cnt, s.len - s.cnt, s.t0, s.t1, s.tiles, s.start, first ? 0 : 1};
-      __syncwarp();
-      return true;
+      return t0 < t1;
     };
-    bool more = next(0);
+    look(0, 0, begin);
+    bool more = begin_stretch(0);
     while (more && ok) {
       const bool idle = !__any_sync(kFull, asks);  // (uniform over the two groups' warps of the same rows)
       // (each group converts half of the coordinates)
@@ -271,8 +311,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
       asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
       tqd::tc_fence_before();
       tqd::tc_mbar_arrive(bar(Q_FULL, 0));
+      look(segs + 1, stretch(segs)->b, stretch(segs)->next);
       float M = -INFINITY, l = 0.f;  // l under the reference M
-      const int t_first = t0 + (int)((n ^ (uint32_t)i) & 1u), drafts = stretch(segs)->drafts;
+      const int t_first = t0 + (int)((n ^ (uint32_t)i) & 1u), drafts = stretch(segs)->len - stretch(segs)->cnt;  // drafts: the first one's position
       // one tile; false: a wait gave up
       auto tile = [&](int t) {
         const uint32_t g_tile = n + (uint32_t)(t - t0), turn = g_tile >> 1;
@@ -309,6 +350,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
           if (F == 1) ld32_async(t_mine + 32 * ((c + 1) & 3), v[(c + 1) & 1]);
           top = fmaxf(top, fmaxf(block_top<false>(v[c & 1], 0, a[2 * c], e[2 * c]), block_top<false>(v[c & 1] + 16, 0, a[2 * c + 1], e[2 * c + 1])));
         }
+        if (F == 2) {  // the tokens of the row's other lane count for nothing here
+          const uint32_t none[8] = {};
+#pragma unroll
+          for (int g = 0; g < NB; ++g) st8_async(t_s + 8 * (NB * (1 - part) + g), none);
+        }
         float m_old = -INFINITY;
         if (t > t0) {
           if (!wait(bar(REF_SET, i ^ 1), ((g_tile - 1) >> 1) & 1)) return false;
@@ -340,14 +386,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
         float z[NB];
 #pragma unroll
         for (int g = 0; g < NB; ++g) z[g] = sc[g].z;
-        if (F == 2) {  // the tokens of the row's other lane count for nothing here
-          const uint32_t none[8] = {};
-#pragma unroll
-          for (int g = 0; g < NB; ++g) st8_async(t_s + 8 * (NB * (1 - part) + g), none);
-          asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
-          tqd::tc_fence_before();
-          tqd::tc_mbar_arrive(bar(P_FULL, 2 * i + 1 - part));
-        }
 #pragma unroll
         for (int c = 0; c < NB / 2; ++c) {
           if (F == 1) {
@@ -365,7 +403,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
           if (2 * c + 2 == L::FIRST || 2 * c + 2 == NB) {
             asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
             tqd::tc_fence_before();
-            tqd::tc_mbar_arrive(bar(P_FULL, 2 * i + (F == 2 ? part : (int)(c == 3))));
+            tqd::tc_mbar_arrive(bar(P_FULL, 2 * i + (int)(c == 3)));
+            if (F == 2) tqd::tc_mbar_arrive(bar(P_FULL, 2 * i + 1));
           }
         }
         __syncwarp();
@@ -379,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
       // the next stretch's queries are requested before this one's last products are waited for
       const uint32_t tiles = (uint32_t)(t1 - t0);
       const bool was_live = live, asked = asks;
-      more = next(segs + 1);
+      more = begin_stretch(segs + 1);
       // Every product of the stretch is done with its last tile's.  (The tile before it is waited for first: a wait for a
       // phase tells nothing while the barrier is two phases behind.)
       const uint32_t last = n + tiles - 1;
@@ -397,23 +436,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
       // each group takes half of the coordinates; a row's lanes join
       float sum = sums[r] + sums[128 + r], most = top, mine = 1.f;  // mine: the weight of this lane's sums
       if (F == 2) {
-        const int o = r ^ 64;
-        most = fmaxf(top, tops[o]);
+        const float other = tops[r ^ 64];
+        most = fmaxf(top, other);
         const float ref = most == -INFINITY ? 0.f : most;
         mine = ex2(top - ref);
-        sum = fmaf(sum, mine, (sums[o] + sums[128 + o]) * ex2(tops[o] - ref));
+        sum = fmaf(sum, mine, (sums[r ^ 64] + sums[128 + (r ^ 64)]) * ex2(other - ref));
       }
       const bool whole = now.t0 == 0 && now.t1 == now.tiles;
       if (whole) mine *= sum > 0.f || sum != sum ? 1.f / sum : 0.f;
       T* out = out_row<D, T>(p, now.b, now.h, was_live ? now.rg * ROWS + rr : 0);
-      float* partial = p.part + (2ll * blockIdx.x + now.place) * L::PART;
+      float* partial = p.part + (2ll * blockIdx.x + (now.t0 + now.start == begin ? 0 : 1)) * L::PART;
       // [4 coordinates][row]: a warp writes 512 bytes in a row (as rows of their own they took 6000 cycles)
       float4* to = reinterpret_cast<float4*>(partial + 256) + rr;
       if (!whole && i == 0 && part == 0) {
         partial[rr] = most;
         partial[128 + rr] = sum;
       }
-      if (F == 2 || whole || !idle) {  // (a partial's rows without a sum are left out by the join)
+      if (whole || !idle) {  // (a partial's rows without a sum are left out by the join)
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           const int col = i * (D / 2) + 16 * c;
@@ -429,16 +468,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
 #pragma unroll
               for (int k = 0; k < 4; ++k) to[(col / 4 + k) * 128] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
             }
-          } else {  // lane 0 of a row finishes the first eight coordinates, lane 1 the others
-            if (c > 0 && !wait(bar(SWAPPED, i), (swaps - 1) & 1)) break;  // (the last values were read)
+          } else {  // lane 0 of a row finishes the first eight coordinates, lane 1 the others; the two warps meet
+            const uint32_t met = bar(SWAPPED, 2 * i + (warp & 1));
+            if (c > 0 && !wait(met, (swaps - 1) & 1)) break;  // (the last values were read)
 #pragma unroll
             for (int k = 0; k < 8; ++k) swap[128 * k + r] = part ? v[k] : v[8 + k];
-            tqd::tc_mbar_arrive(bar(SWAPPED, i));
-            if (!wait(bar(SWAPPED, i), swaps++ & 1)) break;
+            tqd::tc_mbar_arrive(met);
+            if (!wait(met, swaps++ & 1)) break;
             float x[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) x[k] = (part ? v[8 + k] : v[k]) + swap[128 * k + (r ^ 64)];
-            tqd::tc_mbar_arrive(bar(SWAPPED, i));
+            tqd::tc_mbar_arrive(met);
             ++swaps;
             if (whole) {
               if (was_live) store8(out + col + 8 * part, x);
@@ -452,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
       tqd::tc_fence_before();
       tqd::tc_mbar_arrive(bar(OUT_READ, 0));  // (the next stretch's first products overwrite the sums)
       if (threadIdx.x == 0 && now.t0 == 0 && now.t1 < now.tiles) {  // this range's last stretch begins a group that goes on
-        p.heads[blockIdx.x] = JoinHead{(now.start + now.tiles - 1) / per, now.place, now.b, now.h, now.rg};
+        p.heads[blockIdx.x] = JoinHead{(now.start + now.tiles - 1) / per, now.start == begin ? 0 : 1, now.b, now.h, now.rg};
         headed = true;
       }
     }
@@ -460,10 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
   } else if (warp < 12) {
     // ---- V codes to fp16, K-major [coordinate][token], 64 tokens per 128-byte row
     uint32_t n = 0;
-    int at = begin;
-    while (at < end && ok) {
-      const Seg s = seg_at<true>(p, ROWS, pre, at, end);
-      at = s.next;
+    for (Stretch s = stretch_from(p, pre, lens, 0, begin, end); s.t0 < s.t1 && ok; s = stretch_from(p, pre, lens, s.b, s.next, end)) {
       for (int t = s.t0; t < s.t1; ++t, ++n) {
         const int st = n & 1, vs = n % L::VS, ss = n % L::SC;
         if (!wait(bar(VR_FULL, vs), (n / L::VS) & 1)) break;
@@ -471,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
           if (n >= L::SC && !wait(bar(SC_EMPTY, ss), (n / L::SC - 1) & 1)) break;
           if (lane < 8) {
             float2 x = *reinterpret_cast<const float2*>(sm + L::VR + (vs * 8 + lane) * L::VB + 16 * D);
-            if (kTok * t + 16 * lane >= s.limit) x = make_float2(1.f, 1.f);  // (a block behind the tokens: hidden scores stay -infinity)
+            if (kTok * t + 16 * lane >= s.len) x = make_float2(1.f, 1.f);  // (a block behind the tokens: hidden scores stay -infinity)
             const int e = log2i(x.y);
             *reinterpret_cast<float4*>(sm + L::SCALES + 128 * ss + 16 * lane) =
                 make_float4(x.x, (float)e, exp2i(max(-126, min(126, -e))), 0.f);
@@ -486,10 +523,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
 #pragma unroll
           for (int m = 0; m < D / 32; ++m)
             raw[k][m] = *reinterpret_cast<const uint4*>(sm + L::VR + (vs * 8 + (warp - 8) + 4 * k) * L::VB + 16 * (lane + 32 * m));
-        if (kTok * (t + 1) > s.limit) {  // tokens behind the last become zeros
+        if (kTok * (t + 1) > s.len) {  // tokens behind the last become zeros
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int have = s.limit - kTok * t - 16 * ((warp - 8) + 4 * k);
+            const int have = s.len - kTok * t - 16 * ((warp - 8) + 4 * k);
             uint32_t keep[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u)
@@ -532,11 +569,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
     // both, and copies of the scales beside them, took 2000 cycles a tile and bounded the kernel.)
     const bool keys = warp == 12;
     uint32_t n = 0;
-    int at = warp == 15 ? end : begin;
-    while (at < end && ok) {
-      const Seg s = seg_at<true>(p, ROWS, pre, at, end);
-      at = s.next;
-      const int blocks = (s.limit + 15) >> 4;
+    for (Stretch s = stretch_from(p, pre, lens, 0, warp == 15 ? end : begin, end); s.t0 < s.t1 && ok;
+         s = stretch_from(p, pre, lens, s.b, s.next, end)) {
+      const int blocks = (s.len + 15) >> 4;
       auto entries = [&](int t) { return 8 * t + lane < blocks ? page_entry(A.pool, s.b, 8 * t + lane) : 0; };
       int ahead = entries(s.t0), page = 0;  // of four tiles, requested four tiles before their use
       for (int t = s.t0; t < s.t1; ++t, ++n) {
@@ -571,11 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
   } else if (warp == 13) {
     // ---- MMA issue, from operands that are constants of the stage
     uint32_t n = 0, segs = 0;
-    int at = begin;
-    while (at < end && ok) {
-      const Seg s = seg_at<true>(p, ROWS, pre, at, end);
-      at = s.next;
-      if (s.t0 == s.t1) continue;
+    for (Stretch s = stretch_from(p, pre, lens, 0, begin, end); s.t0 < s.t1 && ok; s = stretch_from(p, pre, lens, s.b, s.next, end)) {
       const uint32_t tiles = (uint32_t)(s.t1 - s.t0);
       if (!wait(bar(Q_FULL, 0), segs & 1)) break;
       for (uint32_t k = 0; k < min(2u, tiles); ++k) {
@@ -678,7 +709,7 @@ cudaError_t tree_go(TcParams p, int sms, int device, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, tree_join_kernel<D, F, T>, JoinParams{p.heads, p.part, p.a.out, p.a.nq, p.a.Hq, p.G, p.rows});
 }
 
-constexpr int kTreeMinRows = 16;
+constexpr int kTreeMinRows = 8;
 
 }  // namespace
 
