@@ -457,6 +457,10 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1) rows_kernel(const AttnPa
 // Rows per warp: 16 where the registers hold them and there are more than 8.
 int row_groups_of(int d, int terms, int rows) { return rows > 8 && d <= 128 ? 2 : 1; }
 
+// A tree's rows per warp: more drafts than 8 rows are the rule, and one pass for 16 is worth the spilled registers of
+// 16 bits at d = 256 (64 rows of 4 x 16384 tokens 197 us, 226 with 8 rows).
+int tree_row_groups(int d, int terms, int rows) { return rows > 8 && d * terms <= 256 ? 2 : 1; }
+
 template <int D, int NR, int TERMS, bool TREE, typename T>
 cudaError_t split_go(AttnParams p, cudaStream_t s) {
   using C = Cfg<D, NR, TERMS>;
@@ -521,8 +525,8 @@ cudaError_t attention_d(const AttnParams& p, cudaStream_t s) {
 
 template <int D, int TERMS, typename T>
 cudaError_t tree_d(const AttnParams& p, cudaStream_t s) {
-  if constexpr (D <= 128) {
-    if (row_groups_of(D, TERMS, p.rows) == 2) return split_go<D, 2, TERMS, true, T>(p, s);
+  if constexpr (D * TERMS <= 256) {
+    if (tree_row_groups(D, TERMS, p.rows) == 2) return split_go<D, 2, TERMS, true, T>(p, s);
   }
   return split_go<D, 1, TERMS, true, T>(p, s);
 }
@@ -589,7 +593,7 @@ size_t byte_attention_workspace(int d, int B, int nq, int Hq, int Hkv, tq_dtype 
 
 size_t tree_attention_workspace(int d, int B, int nq, int Hq, int Hkv, tq_dtype dtype) {
   (void)B;
-  const int rows = Hq / Hkv * nq, nr = row_groups_of(d, dtype == TQ_F32 ? 2 : 1, rows);
+  const int rows = Hq / Hkv * nq, nr = tree_row_groups(d, dtype == TQ_F32 ? 2 : 1, rows);
   const size_t split = kJoinHeadBytes + (size_t)2 * kMaxGrid * 8 * nr * (d + 2) * sizeof(float);
   const size_t tc = tree_tc_workspace(d, rows, dtype);
   return tc > split ? tc : split;

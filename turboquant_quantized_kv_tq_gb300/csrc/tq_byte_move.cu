@@ -1,7 +1,8 @@
 // What a step of drafted trees does beside its attention, and reading a cache back:
 //
-// draft_tree: a thread walks from its draft to the root (parents in shared memory) and writes its mask's words from
-// the last to the first as it passes them.  Bound by the launch; a tree's depth is its chain.
+// draft_tree: a thread per draft, rows of bits in shared memory.  Each round a row takes in the row of the ancestor that
+// it points at and points where that one does, so a tree of depth h takes log2(h) rounds.  (Threads that walked to the
+// root took 140 ns a step: 16 us for 256 trees of 250 drafts and depth 100, 398 us for a chain of 1024; here X and X.)
 //
 // byte_keep: the accepted path's tokens to where a plain decode would have put them.  A warp per (entry, KV head,
 // side) takes the blocks that receive tokens in order: every token comes from its own place or a later one, so what
@@ -10,38 +11,59 @@
 //
 // byte_read: values of a batch, both sides, code * 2^e.  A warp per (entry, KV head, block).  Bound by HBM: a byte
 // read and an element written per value.
-#include <algorithm>
+#include <atomic>
 #include <string>
 
-#include "tq_byte.cuh"
+#include "tq_byte_attn.cuh"
 
 namespace tqb {
 namespace {
 
 __device__ __forceinline__ int clamped(const int32_t* count, int b, int n) { return count ? min(max(__ldg(count + b), 0), n) : n; }
 
-__global__ void __launch_bounds__(256) draft_tree_kernel(const TreeArgs a) {
-  constexpr int kDead = -2;
+__global__ void __launch_bounds__(TQ_MAX_DRAFTS) draft_tree_kernel(const TreeArgs a) {
+  constexpr int kRoot = -1, kDead = -2, kAtOnce = 8;  // words read before any is written
+  extern __shared__ uint32_t bits[];                  // [word][draft], the rows one word apart
   __shared__ int up[TQ_MAX_DRAFTS];
-  const int b = blockIdx.x, cnt = clamped(a.count, b, a.n), words = (a.n + 31) / 32;
+  const int i = threadIdx.x, b = blockIdx.x, cnt = clamped(a.count, b, a.n), words = (a.n + 31) / 32, pitch = a.n | 1;
   const int start = a.start ? __ldg(a.start + b) : 0;
-  for (int i = threadIdx.x; i < a.n; i += blockDim.x) {
-    const int p = __ldg(a.parents + (long long)b * a.n + i);
-    up[i] = i < cnt && p >= -1 && p < i ? p : kDead;
+  int p = kRoot;
+  if (i < a.n) {
+    const int x = __ldg(a.parents + (long long)b * a.n + i);
+    p = i < cnt && x >= kRoot && x < i ? x : kDead;
+    up[i] = p;
+    for (int w = 0; w < words; ++w) bits[w * pitch + i] = w == i >> 5 ? 1u << (i & 31) : 0u;
+  }
+  // a draft's row holds itself and its ancestors before p; p's row and what p points at double the way
+  while (__syncthreads_or(p >= 0)) {
+    const int q = p >= 0 ? up[p] : p;
+    for (int w0 = 0; w0 < words; w0 += kAtOnce) {
+      uint32_t x[kAtOnce];
+#pragma unroll
+      for (int w = 0; w < kAtOnce; ++w) x[w] = p >= 0 && w0 + w < words ? bits[(w0 + w) * pitch + p] : 0u;
+      __syncthreads();
+      if (p >= 0)
+#pragma unroll
+        for (int w = 0; w < kAtOnce; ++w)
+          if (w0 + w < words) bits[(w0 + w) * pitch + i] |= x[w];
+      __syncthreads();
+    }
+    p = q;
+    if (i < a.n) up[i] = p;
+  }
+  if (i < a.n) {
+    int above = -1;
+    for (int w = 0; w < words; ++w) {
+      if (p == kDead) bits[w * pitch + i] = 0;
+      above += __popc(bits[w * pitch + i]);
+    }
+    a.positions[(long long)b * a.n + i] = (int32_t)((uint32_t)start + (uint32_t)max(above, 0));
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < a.n; i += blockDim.x) {
-    int32_t* row = a.masks + ((long long)b * a.n + i) * words;
-    uint32_t bits = 0;
-    int word = words - 1, above = -1, j = i;
-    for (; j >= 0; j = up[j], ++above) {
-      for (; word > j >> 5; --word, bits = 0) row[word] = (int32_t)bits;
-      bits |= 1u << (j & 31);
-    }
-    const bool dead = j == kDead;
-    if (dead) bits = 0, word = words - 1;
-    for (; word >= 0; --word, bits = 0) row[word] = (int32_t)bits;
-    a.positions[(long long)b * a.n + i] = (int32_t)((uint32_t)start + (uint32_t)(dead ? 0 : above));
+  int32_t* out = a.masks + (long long)b * a.n * words;
+  for (int k = i; k < a.n * words; k += blockDim.x) {
+    const int d = k / words;
+    out[k] = (int32_t)bits[(k - d * words) * pitch + d];
   }
 }
 
@@ -57,8 +79,8 @@ __device__ __forceinline__ uint32_t rescaled4(uint32_t w, float f) {
 constexpr int kKeepWarps = 4;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kKeepWarps) byte_keep_kernel(const KeepArgs a) {
-  const int lane = threadIdx.x & 31, slot = lane & 15;
+__global__ void __launch_bounds__(32 * kKeepWarps, D == 256 ? 2 : 4) byte_keep_kernel(const KeepArgs a) {
+  const int lane = threadIdx.x & 31;
   const int unit = blockIdx.x * kKeepWarps + (threadIdx.x >> 5);
   const int side = unit & 1, h = (unit >> 1) % a.pool.heads, b = (unit >> 1) / a.pool.heads;
   if (b >= a.B) return;
@@ -72,32 +94,55 @@ __global__ void __launch_bounds__(32 * kKeepWarps) byte_keep_kernel(const KeepAr
     if (bad && a.pool.err) atomicExch(a.pool.err, TQ_DEVERR_BAD_PATH);
   }
   if (bad || cnt == 0) return;
-  for (long long tile = start >> 4; tile <= ((long long)start + cnt - 1) >> 4; ++tile) {
-    // lane: where slot `lane % 16` of the block takes its token from
-    const long long pos = tile * 16 + slot, j = pos - start;
-    const long long src = j >= 0 && j < cnt ? (long long)start + __ldg(path + j) : pos;
-    const uint32_t moved = __ballot_sync(kFull, src != pos) & 0xffffu;
+  const long long first = start >> 4, last = ((long long)start + cnt - 1) >> 4;
+  // Two blocks at a time: lane l looks up where slot l % 16 of block l / 16 takes its token from.  (One after the
+  // other the lookups were a third of the time.)
+  long long src2 = 0;
+  const unsigned char *dst2 = nullptr, *from2 = nullptr;
+  for (long long tile = first; tile <= last; ++tile) {
+    const int half = (int)(tile - first) & 1;
+    if (half == 0) {
+      const long long t = tile + (lane >> 4), pos = t * 16 + (lane & 15), j = pos - start;
+      src2 = t <= last && j >= 0 && j < cnt ? (long long)start + __ldg(path + j) : pos;
+      if (t <= last) {
+        dst2 = a.pool.base + pool_block(a.pool, page_of(a.pool, b, t), h) * block_bytes(D);
+        from2 = src2 >> 4 == t ? dst2 : a.pool.base + pool_block(a.pool, page_of(a.pool, b, src2 >> 4), h) * block_bytes(D);
+      }
+    }
+    // (of this block, on both halves of the warp)
+    const int at = 16 * half + (lane & 15);
+    const long long src = __shfl_sync(kFull, src2, at);
+    const uint32_t moved = __ballot_sync(kFull, src != tile * 16 + (lane & 15)) & 0xffffu;
     if (moved == 0) continue;
-    unsigned char* dst = a.pool.base + pool_block(a.pool, page_of(a.pool, b, tile), h) * block_bytes(D);
-    const unsigned char* from = src >> 4 == tile ? dst : a.pool.base + pool_block(a.pool, page_of(a.pool, b, src >> 4), h) * block_bytes(D);
-    const int own = min(kEMax, max(kEMin, log2i(*reinterpret_cast<const float*>(dst + 32 * D + 4 * side))));
-    const int e = min(kEMax, max(kEMin, log2i(*reinterpret_cast<const float*>(from + 32 * D + 4 * side))));
-    const int top = __reduce_max_sync(kFull, e);
-    const float f = exp2i(e - top);
-    const bool round = __any_sync(kFull, e != top);
+    unsigned char* dst = reinterpret_cast<unsigned char*>(__shfl_sync(kFull, (unsigned long long)dst2, at));
+    const unsigned char* from = reinterpret_cast<const unsigned char*>(__shfl_sync(kFull, (unsigned long long)from2, at));
+    const float own_scale = *reinterpret_cast<const float*>(dst + 32 * D + 4 * side);
+    const float from_scale = *reinterpret_cast<const float*>(from + 32 * D + 4 * side);
+    // (looked at once the codes are on their way)
+    int own, top;
+    float f;
+    bool round;
+    auto scales = [&] {
+      own = min(kEMax, max(kEMin, log2i(own_scale)));
+      const int e = min(kEMax, max(kEMin, log2i(from_scale)));
+      top = __reduce_max_sync(kFull, e);
+      f = exp2i(e - top);
+      round = __any_sync(kFull, e != top);
+    };
     if (side == 0) {
       constexpr int C = D / 16, PER = D / 32;  // chunks of a row, of a lane
       uint4 v[PER];
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const int at = lane + 32 * i, s = at / C, c = at % C;
+        const int k = lane + 32 * i, s = k / C, c = k % C;
         const unsigned char* blk = reinterpret_cast<const unsigned char*>(__shfl_sync(kFull, (unsigned long long)from, s));
         v[i] = *reinterpret_cast<const uint4*>(blk + k_chunk<D>((int)(__shfl_sync(kFull, src, s) & 15), c));
       }
+      scales();
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const int at = lane + 32 * i, s = at / C, c = at % C;
+        const int k = lane + 32 * i, s = k / C, c = k % C;
         const float fs = __shfl_sync(kFull, f, s);
         if (round && fs != 1.f) {
           v[i].x = rescaled4(v[i].x, fs);
@@ -125,6 +170,7 @@ __global__ void __launch_bounds__(32 * kKeepWarps) byte_keep_kernel(const KeepAr
             if (moved >> s & 1) take[s][i] = blk[16 * D + 16 * (x0 + 32 * i) + at];
           }
         }
+        scales();
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < E; ++i) {
@@ -278,7 +324,14 @@ cudaError_t read_go(const ReadArgs& a, cudaStream_t s) {
 }  // namespace
 
 tq_status launch_draft_tree(const TreeArgs& a, Stream s) {
-  draft_tree_kernel<<<a.B, std::min(256, (a.n + 31) / 32 * 32), 0, (cudaStream_t)s>>>(a);
+  static std::atomic<uint64_t> done{0};
+  int dev;
+  sm_count(&dev);
+  constexpr int most = TQ_MAX_DRAFTS / 32 * (TQ_MAX_DRAFTS + 1) * 4;
+  const cudaError_t e = allow_smem((const void*)draft_tree_kernel, most, dev, done);
+  if (e != cudaSuccess) return cuda_error("draft tree", e);
+  const int words = (a.n + 31) / 32;
+  draft_tree_kernel<<<a.B, 32 * words, words * (a.n | 1) * 4, (cudaStream_t)s>>>(a);
   return cuda_error("draft tree", cudaGetLastError());
 }
 

@@ -31,8 +31,8 @@ template <int D>
 struct Plan {
   static constexpr int BLK = 32 * D + 32;
   static constexpr int TILE = 128 * D;                            // bytes of a tile's codes
-  static constexpr int FIRST = 4;                                 // blocks of a tile in the first part of P
-  static constexpr int KS = D == 128 ? 4 : 8;                     // K stages: scores run two tiles ahead
+  static constexpr int FIRST = 6;                                 // blocks of a tile in the first part of P
+  static constexpr int KS = 4;                                    // K stages: scores run two tiles ahead
   static constexpr int VS = D == 128 ? 5 : 8;                     // stages of V's codes: copies take 2 us under load
   static constexpr int VB = 16 * D + 16;                          // V's codes of a block and the scales behind them: one copy
   static constexpr int SC = 4;                                    // stages of scales, [block] (K scale, e, 2^-e, -)
@@ -51,6 +51,9 @@ enum Bar { K_FULL = 0, K_EMPTY = 8, VR_FULL = 16, VR_EMPTY = 24, V_FULL = 32, V_
            P_FULL = 42, SC_EMPTY = 46, SC_READY = 50, Q_FULL = 54, SUM_SET = 55, OUT_READ = 56, SWAPPED = 57, BAR_COUNT = 61 };
 static_assert(8 * BAR_COUNT + 4 <= 496, "barriers and the tensor-memory slot");
 
+constexpr int kTreeGroupCost = 6;  // virtual tiles of a row group: what a range costs beside its tiles
+__device__ __forceinline__ int tree_cost(int tiles) { return tiles > 0 ? tiles + kTreeGroupCost : 0; }
+
 // The plan: all live row groups of an entry cover its whole sequence.  len[b]: (tokens, drafts).
 template <int ROWS>
 __device__ __forceinline__ int live_groups(const TcParams& p, int2 len) { return len.x > 0 ? (len.y * p.G + ROWS - 1) / ROWS : 0; }
@@ -67,7 +70,7 @@ __device__ __forceinline__ void fill_tree_plan(const TcParams& p, int* pre, int2
       if (b < p.a.B) {
         const int2 x = make_int2(clamped_len(p.a.seq_len, b, most, err), clamped_count(p.a.count, b, p.a.nq));
         len[b] = x;
-        t = live_groups<ROWS>(p, x) * p.a.Hkv * cost_of(tiles_of(x.x));
+        t = live_groups<ROWS>(p, x) * p.a.Hkv * tree_cost(tiles_of(x.x));
       }
 #pragma unroll
       for (int m = 1; m < 32; m <<= 1) {
@@ -93,7 +96,7 @@ __device__ __forceinline__ Stretch stretch_from(const TcParams& p, const int* pr
   while (at < end) {
     while (pre[b + 1] <= at) ++b;
     const int2 n = len[b];
-    const int tiles = tiles_of(n.x), span = cost_of(tiles), x = at - pre[b], k = x / span, y = x - k * span;
+    const int tiles = tiles_of(n.x), span = tree_cost(tiles), x = at - pre[b], k = x / span, y = x - k * span;
     if (y < tiles) {
       const int rg = k / p.a.Hkv;
       return Stretch{b, k - rg * p.a.Hkv, rg, n.x, n.y, y, min(tiles, y + (end - at)), tiles, at - y, min(end, at + span - y)};
@@ -142,15 +145,12 @@ __device__ __forceinline__ void issue_scores(uint32_t sb) {
 }
 template <int D, int NT>
 __device__ __forceinline__ void issue_scores(uint32_t sb, uint32_t n) {
-  switch (n % Plan<D>::KS) {
+  static_assert(Plan<D>::KS == 4, "one case a buffer");
+  switch (n & 3) {
     case 0: return issue_scores<D, NT, 0>(sb);
     case 1: return issue_scores<D, NT, 1>(sb);
     case 2: return issue_scores<D, NT, 2>(sb);
-    case 3: return issue_scores<D, NT, 3>(sb);
-    case 4: return issue_scores<D, NT, (Plan<D>::KS > 4 ? 4 : 0)>(sb);
-    case 5: return issue_scores<D, NT, (Plan<D>::KS > 4 ? 5 : 0)>(sb);
-    case 6: return issue_scores<D, NT, (Plan<D>::KS > 4 ? 6 : 0)>(sb);
-    default: return issue_scores<D, NT, (Plan<D>::KS > 4 ? 7 : 0)>(sb);
+    default: return issue_scores<D, NT, 3>(sb);
   }
 }
 // Part h (blocks [0, FIRST), [FIRST, 8)) of O += P_i V of the tile in V buffer i (accumulate: not the first tile of
@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
     tqd::mbar_init(bar(OUT_READ, 0), 256);
     tqd::fence_mbar_init();
   }
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // (what is above may run beside the kernel before this one)
   fill_tree_plan<ROWS>(p, pre, lens, blockIdx.x == 0 ? A.pool.err : nullptr);
   tqd::tc_fence_before();
   __syncthreads();
@@ -652,6 +653,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const JoinParam
   constexpr int ROWS = kJoinThreads / (D / 4);
   constexpr long long PART = Plan<D>::PART;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const JoinHead H = p.heads[blockIdx.x];
   const int rr = blockIdx.y * ROWS + threadIdx.x % ROWS, c = threadIdx.x / ROWS, row = H.group * (128 / F) + rr;
   if (H.last < 0 || rr >= 128 / F || row >= p.rows) return;
@@ -692,37 +694,40 @@ cudaError_t tree_go(TcParams p, int sms, int device, cudaStream_t s) {
   p.grid = sms;
   cudaError_t e = allow_smem((const void*)tree_kernel<D, NT, F, T>, L::SMEM, device, done);
   if (e != cudaSuccess) return e;
-  tree_kernel<D, NT, F, T><<<p.grid, kThreads, L::SMEM, s>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (p.grid == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
-  const int rows = p.rows < ROWS ? p.rows : ROWS;
-  constexpr int join_rows = kJoinThreads / (D / 4);
-  cfg.gridDim = dim3(p.grid - 1, (rows + join_rows - 1) / join_rows);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  cfg.stream = s;
+  cfg.gridDim = dim3(p.grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = L::SMEM;
+  if ((e = cudaLaunchKernelEx(&cfg, tree_kernel<D, NT, F, T>, p)) != cudaSuccess || p.grid == 1) return e;
+  cfg.dynamicSmemBytes = 0;
+  const int rows = p.rows < ROWS ? p.rows : ROWS;
+  constexpr int join_rows = kJoinThreads / (D / 4);
+  cfg.gridDim = dim3(p.grid - 1, (rows + join_rows - 1) / join_rows);
+  cfg.blockDim = dim3(kJoinThreads);
   return cudaLaunchKernelEx(&cfg, tree_join_kernel<D, F, T>, JoinParams{p.heads, p.part, p.a.out, p.a.nq, p.a.Hq, p.G, p.rows});
 }
 
-constexpr int kTreeMinRows = 8;
+// Rows above which the tensor cores take a call.
+constexpr int tree_min_rows(int d) { return d == 128 ? 8 : 16; }
 
 }  // namespace
 
 bool tree_tc_takes(const AttnArgs& a) {
   const int rows = a.Hq / a.Hkv * a.nq;
-  if ((a.d != 64 && a.d != 128) || a.dtype == TQ_F32 || rows <= kTreeMinRows) return false;
+  if ((a.d != 64 && a.d != 128) || a.dtype == TQ_F32 || rows <= tree_min_rows(a.d)) return false;
   // the plan counts tiles in 32 bits
-  const long long groups = (rows + 63) / 64, tiles = (a.pool.max_blocks + 7) / 8 + kGroupCost;
+  const long long groups = (rows + 63) / 64, tiles = (a.pool.max_blocks + 7) / 8 + kTreeGroupCost;
   return (long long)a.B * a.Hkv * groups * tiles < (1ll << 31) - (1ll << 20);
 }
 
 size_t tree_tc_workspace(int d, int rows, tq_dtype dtype) {
-  if ((d != 64 && d != 128) || dtype == TQ_F32 || rows <= kTreeMinRows) return 0;
+  if ((d != 64 && d != 128) || dtype == TQ_F32 || rows <= tree_min_rows(d)) return 0;
   if (d == 128 && rows > 128) return tc_workspace(rows);
   return kJoinHeadBytes + (size_t)2 * kMaxSms * 128 * (d + 2) * sizeof(float);
 }
