@@ -46,7 +46,7 @@ struct Plan {
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static constexpr int PART = 128 * (D + 2);                      // floats of a partial
 };
-// (P_FULL: half h of group i at 2 i + h)
+// (P_FULL: part h of group i at 2 i + h)
 enum Bar { K_FULL = 0, K_EMPTY = 8, VR_FULL = 16, VR_EMPTY = 24, V_FULL = 32, V_EMPTY = 34, S_FULL = 36, O_DONE = 38, REF_SET = 40,
            P_FULL = 42, SC_EMPTY = 46, SC_READY = 50, Q_FULL = 54, SUM_SET = 55, OUT_READ = 56, SWAPPED = 57, BAR_COUNT = 61 };
 static_assert(8 * BAR_COUNT + 4 <= 496, "barriers and the tensor-memory slot");
@@ -153,19 +153,19 @@ __device__ __forceinline__ void issue_scores(uint32_t sb, uint32_t n) {
     default: return issue_scores<D, NT, 3>(sb);
   }
 }
-// Part h (blocks [0, FIRST), [FIRST, 8)) of O += P_i V of the tile in V buffer i (accumulate: not the first tile of
-// a stretch).
-template <int D, int i>
-__device__ __forceinline__ void issue_readout(uint32_t sb, int h, bool accumulate) {
+// Part h of O += P_i V of the tile in V buffer i (accumulate: not the first tile of a stretch).  F = 1: blocks
+// [0, FIRST), then the others; F = 2: all at once, a row's lanes end together.
+template <int D, int F, int i, int h>
+__device__ __forceinline__ void issue_readout(uint32_t sb, bool accumulate) {
   using L = Plan<D>;
+  constexpr int k0 = h == 0 ? 0 : L::FIRST, k1 = h == 0 && F == 1 ? L::FIRST : 8;
   const uint64_t v = sdesc128(sb + L::V16 + i * 2 * L::TILE);
   if (elected()) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if ((k >= L::FIRST) == (h == 1))
-        tqd::tc_mma_f16_ta(L::T_O, 128 * i + 8 * k, v + (uint64_t)((k >> 2) * (L::TILE >> 4) + 2 * (k & 3)), idesc(D),
-                           accumulate || k > 0);
-    if (h == 1) {
+    for (int k = k0; k < k1; ++k)
+      tqd::tc_mma_f16_ta(L::T_O, 128 * i + 8 * k, v + (uint64_t)((k >> 2) * (L::TILE >> 4) + 2 * (k & 3)), idesc(D),
+                         accumulate || k > 0);
+    if (k1 == 8) {
       tqd::tc_commit(sb + L::BARS + 8 * (O_DONE + i));
       tqd::tc_commit(sb + L::BARS + 8 * (V_EMPTY + i));
     }
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
         if (idle) {
           tqd::tc_mbar_arrive(bar(REF_SET, i));
           tqd::tc_mbar_arrive(bar(P_FULL, 2 * i));
-          tqd::tc_mbar_arrive(bar(P_FULL, 2 * i + 1));
+          if (F == 1) tqd::tc_mbar_arrive(bar(P_FULL, 2 * i + 1));
           if (lane == 0) tqd::tc_mbar_arrive(bar(SC_EMPTY, ss));
           return true;
         }
@@ -401,11 +401,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
             l = fmaf(sum, z[g], l);
             st8_async(t_p + 8 * g, w);
           }
-          if (2 * c + 2 == L::FIRST || 2 * c + 2 == NB) {
+          if ((F == 1 && 2 * c + 2 == L::FIRST) || 2 * c + 2 == NB) {
             asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
             tqd::tc_fence_before();
-            tqd::tc_mbar_arrive(bar(P_FULL, 2 * i + (int)(c == 3)));
-            if (F == 2) tqd::tc_mbar_arrive(bar(P_FULL, 2 * i + 1));
+            tqd::tc_mbar_arrive(bar(P_FULL, 2 * i + (F == 1 && c == 3)));
           }
         }
         __syncwarp();
@@ -620,14 +619,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
       for (uint32_t k = 0; k < tiles && ok; ++k) {
         const uint32_t g = n + k;
         if (!wait(bar(V_FULL, g & 1), (g >> 1) & 1)) break;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!wait(bar(P_FULL, 2 * (g & 1) + h), (g >> 1) & 1)) break;
+        if (!wait(bar(P_FULL, 2 * (g & 1)), (g >> 1) & 1)) break;
+        tqd::tc_fence_after();
+        if (g & 1) issue_readout<D, F, 1, 0>(sb, k > 0);
+        else issue_readout<D, F, 0, 0>(sb, k > 0);
+        if constexpr (F == 1) {
+          if (!wait(bar(P_FULL, 2 * (g & 1) + 1), (g >> 1) & 1)) break;
           tqd::tc_fence_after();
-          if (g & 1) issue_readout<D, 1>(sb, h, k > 0);
-          else issue_readout<D, 0>(sb, h, k > 0);
+          if (g & 1) issue_readout<D, F, 1, 1>(sb, true);
+          else issue_readout<D, F, 0, 1>(sb, true);
         }
-        if (!ok) break;
         if (k + 2 < tiles) {
           if (!wait(bar(K_FULL, (g + 2) % L::KS), ((g + 2) / L::KS) & 1)) break;
           issue_scores<D, NT>(sb, g + 2);
