@@ -1,7 +1,7 @@
 """Trees of drafted tokens over the byte cache, keep and read on the GPU against their plain forms.
 
 Tolerances: attention as in test_gpu_byte_cache.py (the same arithmetic; bits select tokens and add none).  16-bit
-queries of more than 16 rows enter as e4m3 terms, off by 2^-18 of the row's largest value a coordinate: a score is off
+queries of more than 8 rows may enter as e4m3 terms, off by 2^-18 of the row's largest value a coordinate: a score is off
 by at most 2^-18 d max|q| max|k| scale, which is counted on top.  Everything else is equal: masks, positions, bytes and
 values (a value of 4 significant bits times a power of two is rounded by no type but where it leaves the range).
 """
@@ -121,9 +121,12 @@ def _run(d, dtype, Hq, H, seq, cnt, nq, scale=None, seed=0, bits=0.5, from_tree=
     out = c.attention(q, _i32(seq), _i32(table), count=_i32(cnt), scale=scale, tree=_i32(masks))
     pool = ref.Pool(c.pool.cpu().numpy(), H, d)
     s = d ** -0.5 if scale is None else scale
-    want, spread, reach, least = tree.attention(_np(q), pool, seq, cnt, table, s, sees)
-    wide = _terms(_np(q), pool, seq, cnt, table, s, dtype != "f32" and d != 256 and Hq // H * nq > 16)
-    _check(out, want, spread, reach, max(seq), d, DT[dtype], wide)
+    # (least: a weight is an fp16 number below 2^M, M at least 7 under the row's largest, so it has a smallest step of
+    # 2^-31 of the largest and is off by half of one.  It shows where the heaviest token's value is 0: all that is left there
+    # are weights near the step.)
+    want, spread, reach, least = tree.attention(_np(q), pool, seq, cnt, table, s, sees, 2.0 ** -31)
+    wide = _terms(_np(q), pool, seq, cnt, table, s, dtype != "f32" and d != 256 and Hq // H * nq > 8)
+    _check(out, want, spread, reach, max(seq), d, DT[dtype], wide, least)
     assert c.device_error() == 0
     dead = np.ones(want.shape[:2], dtype=bool)
     for b in range(B):
@@ -197,7 +200,7 @@ def test_unlike_scales_and_odd_queries(dtype, d, nq):
     plain = c.attention(q, *args, count=_i32(cnt), tree=_i32(tree.pack(sees)))
     pool = ref.Pool(c.pool.cpu().numpy(), 2, d)
     want, spread, reach, least = tree.attention(_np(q), pool, seq, cnt, table, d ** -0.5, sees, 2.0 ** -31)
-    wide = _terms(_np(q), pool, seq, cnt, table, d ** -0.5, dtype != "f32" and d != 256 and 4 * nq > 16)
+    wide = _terms(_np(q), pool, seq, cnt, table, d ** -0.5, dtype != "f32" and d != 256 and 4 * nq > 8)
     _check(plain, want, spread, reach, 400, d, DT[dtype], wide, least)
     odd = q.clone()
     odd[0, 1, 3, 5] = float("inf")
@@ -208,6 +211,83 @@ def test_unlike_scales_and_odd_queries(dtype, d, nq):
     bad[0, 1, 3] = bad[1, 0, 6] = True
     assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], plain[~bad])
     assert torch.all(got[1, nq - 1] == 0)
+
+
+ROUTES = [("bf16", 128, 8, 2, 2), ("bf16", 128, 8, 2, 12), ("f16", 128, 8, 2, 25), ("bf16", 128, 8, 1, 40), ("bf16", 64, 8, 2, 30),
+          ("f16", 64, 4, 2, 6), ("bf16", 256, 8, 2, 5), ("f32", 128, 8, 2, 3), ("f32", 64, 8, 2, 9)]
+
+
+@pytest.mark.parametrize("dtype,d,Hq,H,nq", ROUTES)
+@pytest.mark.parametrize("rise", [0.13, -0.13, 0.5])
+def test_maxima_that_rise_and_fall(dtype, d, Hq, H, nq, rise):
+    """Scores that grow (fall) by 17 (64) powers of two a tile of 128 tokens: the running reference rises in every tile, and
+    the sums so far are rescaled each time."""
+    seq, cnt = [1500, 700, 200], [nq, nq, max(1, nq - 1)]
+    c, table, g = _filled(d, Hq, H, seq, 94, dtype)
+    n, B = max(seq), len(seq)
+    u = torch.sign(torch.randn(d, generator=g, device="cuda"))
+    level = (torch.arange(n, device="cuda") - n / 2) * rise / 1.4427 / d ** 0.5
+    k = level[None, None, :, None] * u + 0.2 * torch.randn(B, H, n, d, generator=g, device="cuda")
+    v = torch.randn(B, H, n, d, generator=g, device="cuda")
+    c.append(k.to(DT[dtype]), v.to(DT[dtype]), _i32([0] * B), _i32(table), count=_i32(seq))
+    q = (u + 0.05 * torch.randn(B, nq, Hq, d, generator=g, device="cuda")).to(DT[dtype])
+    sees = np.random.RandomState(1).rand(B, nq, nq) < 0.6
+    out = c.attention(q, _i32(seq), _i32(table), count=_i32(cnt), tree=_i32(tree.pack(sees)))
+    pool = ref.Pool(c.pool.cpu().numpy(), H, d)
+    want, spread, reach, least = tree.attention(_np(q), pool, seq, cnt, table, d ** -0.5, sees, 2.0 ** -31)
+    wide = _terms(_np(q), pool, seq, cnt, table, d ** -0.5, dtype != "f32" and d != 256 and Hq // H * nq > 8)
+    _check(out, want, spread, reach, max(seq), d, DT[dtype], wide, least)
+
+
+@pytest.mark.parametrize("dtype,d,Hq,H,nq", ROUTES)
+@pytest.mark.parametrize("scale", [0.0, -0.07, 1e-30, 3.0])
+def test_scales_of_the_scores(dtype, d, Hq, H, nq, scale):
+    """No scale at all leaves the mean of what a row sees, and hides what it does not."""
+    _run(d, dtype, Hq, H, [300, 128, 31], [nq, max(1, nq - 1), min(nq, 31)], nq, scale=scale, seed=2)
+
+
+@pytest.mark.parametrize("dtype,d,Hq,H,nq", ROUTES)
+def test_queries_near_the_ends_of_the_range(dtype, d, Hq, H, nq):
+    """Rows of 1e-30 (fp16: 1e-7, subnormal) and of zeros attend evenly; rows of 1e4 to what they hit hardest."""
+    seq, cnt = [260, 129], [nq, nq]
+    c, table, g = _filled(d, Hq, H, seq, 17, dtype)
+    q = torch.randn(2, nq, Hq, d, generator=g, device="cuda")
+    q[0, 0] *= 1e-7 if dtype == "f16" else 1e-30
+    q[0, 1] = 0
+    q[1, 0] *= 1e4
+    q = q.to(DT[dtype])
+    sees = np.random.RandomState(3).rand(2, nq, nq) < 0.6
+    out = c.attention(q, _i32(seq), _i32(table), count=_i32(cnt), tree=_i32(tree.pack(sees)))
+    pool = ref.Pool(c.pool.cpu().numpy(), H, d)
+    want, spread, reach, least = tree.attention(_np(q), pool, seq, cnt, table, d ** -0.5, sees, 2.0 ** -31)
+    wide = _terms(_np(q), pool, seq, cnt, table, d ** -0.5, dtype != "f32" and d != 256 and Hq // H * nq > 8)
+    _check(out, want, spread, reach, max(seq), d, DT[dtype], wide, least)
+
+
+@pytest.mark.parametrize("dtype,d,nq", [("bf16", 128, 6), ("bf16", 128, 20), ("bf16", 64, 12), ("f32", 128, 3), ("bf16", 128, 3)])
+def test_a_batch_of_512(dtype, d, nq):
+    """The largest batch: most entries short, some empty, some without drafts."""
+    rs = np.random.RandomState(nq)
+    B, Hq, H = 512, 8, 2
+    seq = [int(x) for x in rs.randint(0, 40, B)]
+    seq[300], seq[511] = 700, 260
+    cnt = [int(x) for x in rs.randint(0, nq + 1, B)]
+    c, table, g = _filled(d, Hq, H, seq, 44, dtype)
+    q = torch.randn(B, nq, Hq, d, generator=g, device="cuda").to(DT[dtype])
+    sees = rs.rand(B, nq, nq) < 0.5
+    out = c.attention(q, _i32(seq), _i32(table), count=_i32(cnt), tree=_i32(tree.pack(sees)))
+    some = [0, 1, 2, 100, 299, 300, 301, 400, 510, 511]
+    pool = ref.Pool(c.pool.cpu().numpy(), H, d)
+    pick = lambda x: [x[b] for b in some]  # noqa: E731
+    want, spread, reach, least = tree.attention(_np(q)[some], pool, pick(seq), pick(cnt), table[some], d ** -0.5, sees[some])
+    wide = _terms(_np(q)[some], pool, pick(seq), pick(cnt), table[some], d ** -0.5, dtype != "f32" and Hq // H * nq > 8)
+    _check(out[some], want, spread, reach, 700, d, DT[dtype], wide)
+    dead = torch.arange(nq, device="cuda")[None] >= _i32(cnt)[:, None]
+    assert torch.all(out[dead] == 0)
+    assert torch.all(out[[b for b in range(B) if seq[b] == 0]] == 0) and torch.isfinite(out.float()).all()
+    with pytest.raises(_api().TQError):
+        c.attention(torch.zeros(513, nq, Hq, d, dtype=DT[dtype], device="cuda"), torch.zeros(513, dtype=torch.int32, device="cuda"),
+                    torch.zeros(513, 44, dtype=torch.int32, device="cuda"), tree=torch.zeros(513, nq, 1, dtype=torch.int32, device="cuda"))
 
 
 def test_strided_queries_one_query_outputs_and_refusals():
@@ -258,14 +338,23 @@ def test_captured_steps_follow_their_tensors():
     base, tab = _i32([60, 333, 16]), _i32(table)
     parents, count, seq = _i32(_parents(rs, B, nq, 3)), _i32([nq, 5, 11]), _i32([0] * B)
     path, kept = _i32(np.tile(np.arange(4), (B, 1))), _i32([4, 2, 0])
+    other, mine = torch.cuda.Stream(), torch.zeros(B, nq, 1, dtype=torch.int32, device="cuda")
     k, v = (torch.randn(B, H, nq, d, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
     q = torch.randn(B, nq, Hq, d, generator=g, device="cuda").to(torch.bfloat16)
 
     def step():
         masks, pos = tq.draft_tree(parents, start=base, count=count)
         qr = c.append(k, v, base, tab, count=count, rotary=rot, positions=pos, q=q)
-        torch.add(base, count, out=seq)
-        out = c.attention(qr, seq, tab, count=count, tree=masks)
+        # a copy, and work of another stream, right before the attention
+        ready = torch.cuda.Event()
+        main = torch.cuda.current_stream()
+        ready.record()
+        with torch.cuda.stream(other):
+            other.wait_event(ready)
+            torch.add(base, count, out=seq)
+        main.wait_stream(other)
+        mine.copy_(masks)
+        out = c.attention(qr, seq, tab, count=count, tree=mine)
         length = c.keep(path, base, tab, count=kept)
         return out, length, *c.read(base, tab, 4, count=kept, dtype=torch.float32)
 

@@ -10,11 +10,24 @@
 // the products of the tile before and its own.  Each group sums its own l.
 // The queries' terms lie in tensor memory, which a second O would fill: a score product reads only its keys from
 // shared memory, and the room that they took there holds tiles in flight.  Rows that do not exist cost nothing:
-// their warps only pass the barriers.  More than 128 rows go to tc_kernel with two row tiles (head dim 128), which
-// reads the pool half as often, or in groups of 128 here (64).
+// their warps only pass the barriers.
 //
-// Which drafts a row sees matters only in the last tiles: rows read their masks there, a window of 128 bits a tile,
-// and tiles before the first draft are the same as without a tree.
+// F = 2, up to 64 rows (and head dim 64 always, in groups of 64): a row has two lanes, r and r + 64, one for each half of
+// a tile's tokens.  Each has an M and an O of its own; its P holds zeros for the other half's tokens, and the lanes
+// join as partials of a range do.  So all four warps of a group work on 64 rows, each on half as many scores.
+// More than 128 rows of head dim 128 go to tc_kernel with two row tiles, which reads the pool half as often.
+//
+// Which drafts a row sees matters only in the last tiles: there a pass over the scores puts -infinity where a mask's
+// bit is clear, from a window of 32 bits at a time, before the tile's softmax, which is the same for all tiles.
+//
+// Measured (us, bf16, 32 / 8 heads, 8 x 32768 tokens; the pool partly in L2): 64 rows 99, 16 rows 96, 128 rows 118;
+// fp16 with 64 rows 106; d = 64 81 for 64 rows.  A tile's time is that of a group's chain, two tiles long: scores to
+// registers 350 cycles, maximum to P 900, the readout's issue 430, the next scores' 360 and their 500 in the tensor
+// cores (F = 2, d = 64; 2500 in all).  At d = 128 and 64 rows that meets what HBM gives (5.4 TB/s of 6.8); at d = 64 it is
+// twice that, at 128 rows 1.3 times.  Tried and not kept: an O for each group (a second join, queries in shared
+// memory: 157), P in columns of its own so that scores run ahead of the readout (146 instead of 116 for 128 rows, 121
+// instead of 86 at d = 64, also with the readout issued by another warp), a row's 128 scores held in registers (124
+// instead of 117), copies of keys, values and scales by one warp (172), partials by row (6000 cycles a stretch).
 //
 // Warps: 0-7 rows, 8-11 V to fp16, 12 K copies, 13 MMA issue, 14 V copies (15 only completes the warpgroup).
 #include <atomic>
@@ -51,7 +64,9 @@ enum Bar { K_FULL = 0, K_EMPTY = 8, VR_FULL = 16, VR_EMPTY = 24, V_FULL = 32, V_
            P_FULL = 42, SC_EMPTY = 46, SC_READY = 50, Q_FULL = 54, SUM_SET = 55, OUT_READ = 56, SWAPPED = 57, BAR_COUNT = 61 };
 static_assert(8 * BAR_COUNT + 4 <= 496, "barriers and the tensor-memory slot");
 
-constexpr int kTreeGroupCost = 6;  // virtual tiles of a row group: what a range costs beside its tiles
+// Virtual tiles of a row group: what a range costs beside its tiles (4 / 6 / 8 / 12: a batch of 64 unlike lengths, 91 rows
+// 43 / 45 / 47 / 49 us; of 32, 64 rows 42 / 39 / 39 / 43; 8 x 32768 tokens 100 / 100 / 99 / 99).
+constexpr int kTreeGroupCost = 6;
 __device__ __forceinline__ int tree_cost(int tiles) { return tiles > 0 ? tiles + kTreeGroupCost : 0; }
 
 // The plan: all live row groups of an entry cover its whole sequence.  len[b]: (tokens, drafts).
@@ -91,6 +106,17 @@ struct Stretch {
   int start, next;  // of the slab's group, of the stretch after this one
 };
 static_assert(sizeof(Stretch) <= 40, "its place in shared memory");
+// The entry that holds cost `at` (< the total).
+__device__ __forceinline__ int entry_at(const int* pre, int B, int at) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid + 1] <= at) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+// b: the entry to look from.
 __device__ __forceinline__ Stretch stretch_from(const TcParams& p, const int* pre, const int2* len, int b, int at, int end) {
   Stretch s = {};
   while (at < end) {
@@ -203,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
   int* pre = reinterpret_cast<int*>(sm + L::PRE);
   int2* lens = reinterpret_cast<int2*>(sm + L::LEN);
   if (sb & 1023u) {  // the swizzled operands need it (the plan gives it)
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
     if (threadIdx.x == 0) {
       p.heads[blockIdx.x].last = -1;
       if (A.pool.err) atomicExch(A.pool.err, TQ_DEVERR_SMEM_PLAN);
@@ -248,6 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
   const bool whole_tmem = *slot == 0;
   const int total = pre[A.B], per = range_of(total, p.grid);
   const int begin = min(total, (int)blockIdx.x * per), end = min(total, begin + per);
+  const int b_first = entry_at(pre, A.B, begin);
 
   bool ok = whole_tmem;  // cleared by a wait that gave up: the role stops working and ends
   auto wait = [&](uint32_t b, uint32_t parity) {
@@ -301,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
       q.request(reinterpret_cast<const T*>(A.q.p) + s.b * A.q.sb + qi * A.q.st + hd * A.q.sh, asks);
       return t0 < t1;
     };
-    look(0, 0, begin);
+    look(0, b_first, begin);
     bool more = begin_stretch(0);
     while (more && ok) {
       const bool idle = !__any_sync(kFull, asks);  // (uniform over the two groups' warps of the same rows)
@@ -500,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
   } else if (warp < 12) {
     // ---- V codes to fp16, K-major [coordinate][token], 64 tokens per 128-byte row
     uint32_t n = 0;
-    for (Stretch s = stretch_from(p, pre, lens, 0, begin, end); s.t0 < s.t1 && ok; s = stretch_from(p, pre, lens, s.b, s.next, end)) {
+    for (Stretch s = stretch_from(p, pre, lens, b_first, begin, end); s.t0 < s.t1 && ok; s = stretch_from(p, pre, lens, s.b, s.next, end)) {
       for (int t = s.t0; t < s.t1; ++t, ++n) {
         const int st = n & 1, vs = n % L::VS, ss = n % L::SC;
         if (!wait(bar(VR_FULL, vs), (n / L::VS) & 1)) break;
@@ -606,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
   } else if (warp == 13) {
     // ---- MMA issue, from operands that are constants of the stage
     uint32_t n = 0, segs = 0;
-    for (Stretch s = stretch_from(p, pre, lens, 0, begin, end); s.t0 < s.t1 && ok; s = stretch_from(p, pre, lens, s.b, s.next, end)) {
+    for (Stretch s = stretch_from(p, pre, lens, b_first, begin, end); s.t0 < s.t1 && ok; s = stretch_from(p, pre, lens, s.b, s.next, end)) {
       const uint32_t tiles = (uint32_t)(s.t1 - s.t0);
       if (!wait(bar(Q_FULL, 0), segs & 1)) break;
       for (uint32_t k = 0; k < min(2u, tiles); ++k) {
@@ -714,7 +742,9 @@ cudaError_t tree_go(TcParams p, int sms, int device, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, tree_join_kernel<D, F, T>, JoinParams{p.heads, p.part, p.a.out, p.a.nq, p.a.Hq, p.G, p.rows});
 }
 
-// Rows above which the tensor cores take a call.
+// Rows above which the tensor cores take a call.  Both sides (us, 8 x 32768 tokens, 8 KV heads, bf16; split / here): d = 128
+// 8 rows 97 / 96, 16 rows 109 / 96; d = 64 16 rows 84 / 84, 8 rows 54 / 84.  At 8 rows of d = 128 the split keeps more bits of the
+// queries for the same time.
 constexpr int tree_min_rows(int d) { return d == 128 ? 8 : 16; }
 
 }  // namespace
