@@ -501,8 +501,8 @@ tq_status tq_draft_tree(int32_t batch, int32_t n, const int32_t* dev_parents, co
  * where bit j of its mask is set (dev_masks [batch][nq][(nq + 31) / 32], any bits: they need not come
  * from a tree; bits from c on count for nothing).  Where c > dev_seq_len[b] the drafts before the first token
  * do not exist.  Rows that attend to nothing, and rows i >= c, are zeros.  nq: at most TQ_MAX_DRAFTS.
- * The rest as for tq_byte_attention_paged; 16-bit queries enter as e4m3 terms at head_dim 128 for more than 8
- * rows (queries times heads per KV head), at head_dim 64 for more than 16. */
+ * The rest as for tq_byte_attention_paged; 16-bit queries of more than 8 rows (queries times heads per KV head) enter
+ * as e4m3 terms at head_dim 64 and 128. */
 size_t tq_byte_tree_attention_workspace_bytes(const tq_byte_config* cfg, int32_t batch, int32_t nq, tq_dtype dtype);
 tq_status tq_byte_tree_attention_paged(const tq_byte_config* cfg, const void* dev_pool, const tq_page_table* pages,
                                        int32_t batch, int32_t nq, tq_dtype dtype, const tq_heads* q,

@@ -366,11 +366,10 @@ bool tc_takes(const AttnArgs& a);
 size_t tc_workspace(int rows);
 cudaError_t launch_tc(const AttnArgs& a, cudaStream_t s);
 // A tree's calls on the tensor memory (tq_byte_tree.cu): whether it takes a call, its workspace (0: it never takes
-// such calls), its launch; and its kernel for more than 128 rows (tq_byte_tc.cu).
+// such calls), its launch.
 bool tree_tc_takes(const AttnArgs& a);
 size_t tree_tc_workspace(int d, int rows, tq_dtype dtype);
 cudaError_t launch_tree_tc(const AttnArgs& a, cudaStream_t s);
-cudaError_t launch_tc_tree(const AttnArgs& a, cudaStream_t s);
 
 // Length and count of sequence b as the kernels use them.
 __device__ __forceinline__ int clamped_len(const int32_t* seq_len, int b, int most, int32_t* err) {

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(32 * kKeepWarps, D == 256 ? 2 : 4) byte_keep_k
   for (int j = lane; j < cnt; j += 32) bad |= __ldg(path + j) <= (j ? __ldg(path + j - 1) : -1);
   bad = __any_sync(kFull, bad);
   if (lane == 0 && h == 0 && side == 0) {
-    if (a.seq_len) a.seq_len[b] = bad ? start : start + cnt;
+    if (a.seq_len) a.seq_len[b] = (int32_t)((uint32_t)start + (bad ? 0u : (uint32_t)cnt));
     if (bad && a.pool.err) atomicExch(a.pool.err, TQ_DEVERR_BAD_PATH);
   }
   if (bad || cnt == 0) return;

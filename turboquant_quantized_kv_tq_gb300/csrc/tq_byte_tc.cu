@@ -45,6 +45,8 @@ namespace {
 using tqd::mbar_wait;
 
 constexpr int kD = 128;
+constexpr int kGroupCost = 8;      // virtual tiles of a row group: what a range costs beside its tiles (4: 125 us for
+                                   // the last 64 positions, 8: 122, 14: 124)
 constexpr int kBlk = 32 * kD + 32;
 
 template <int NT, int NQ>
@@ -66,6 +68,13 @@ struct Plan {
 enum Bar { K_FULL = 0, K_EMPTY = 2, VR_FULL = 4, VR_EMPTY = 6, V_FULL = 8, V_EMPTY = 10, S_FULL = 12, O_DONE = 14,
            Q_FULL = 16, P_FULL = 18, SC_FULL = 22, SC_EMPTY = 26, SC_READY = 30, BAR_COUNT = 34 };
 static_assert(8 * BAR_COUNT + 4 <= 320, "barriers and the tensor-memory slot");
+
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
+      :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+}
 
 // Products of one elected lane of a converged warp, from constant operands.
 constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);  // M = N = 128, fp32 D
@@ -106,7 +115,127 @@ __device__ __forceinline__ void issue_readout(uint32_t sb, int i, int h, bool ac
   __syncwarp();
 }
 
-template <typename T, int NT, int NQ, bool TREE>
+// Tokens that the rows of group rg of an entry attend to at most, and tiles.
+__device__ __forceinline__ int group_limit(const TcParams& p, int rows_per, int rg, int len, int cnt) {
+  const int last = min((rg + 1) * rows_per, p.rows) - 1;
+  const int i = min(cnt - 1, last / p.G);
+  return i * p.G + p.G - 1 < rg * rows_per ? 0 : row_limit(i, len, cnt);
+}
+__device__ __forceinline__ int cost_of(int tiles) { return tiles > 0 ? tiles + kGroupCost : 0; }
+
+// Costs before each entry (order: entry, row group, head); written by warp 0.
+__device__ __forceinline__ void fill_plan(const TcParams& p, int rows_per, int* pre, int32_t* err) {
+  const int lane = threadIdx.x & 31, most = p.a.pool.max_blocks * 16;
+  if (threadIdx.x < 32) {
+    int run = 0;
+    for (int b0 = 0; b0 < p.a.B; b0 += 32) {
+      const int b = b0 + lane;
+      int t = 0;
+      if (b < p.a.B) {
+        const int len = clamped_len(p.a.seq_len, b, most, err), cnt = clamped_count(p.a.count, b, p.a.nq);
+        for (int rg = 0; rg < p.groups; ++rg) t += cost_of(tiles_of(group_limit(p, rows_per, rg, len, cnt)));
+        t *= p.a.Hkv;
+      }
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const int o = __shfl_up_sync(kFull, t, m);
+        if (lane >= m) t += o;
+      }
+      if (b < p.a.B) pre[b + 1] = run + t;
+      run += __shfl_sync(kFull, t, 31);
+    }
+    if (lane == 0) pre[0] = 0;
+  }
+}
+
+struct Seg {
+  int b, h, rg, len, cnt, limit;
+  int t0, t1, tiles;
+  int start, next;  // of the slab's group, of the stretch after this one
+};
+__device__ __forceinline__ Seg seg_at(const TcParams& p, int rows_per, const int* pre, int at, int end) {
+  Seg s;
+  int lo = 0, hi = p.a.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid + 1] <= at) lo = mid + 1;
+    else hi = mid;
+  }
+  s.b = lo;
+  const int most = p.a.pool.max_blocks * 16;
+  s.len = clamped_len(p.a.seq_len, s.b, most, nullptr);
+  s.cnt = clamped_count(p.a.count, s.b, p.a.nq);
+  int x = at - pre[s.b], span = 1;
+  s.rg = 0;
+  for (;; ++s.rg) {
+    s.limit = group_limit(p, rows_per, s.rg, s.len, s.cnt);
+    s.tiles = tiles_of(s.limit);
+    span = cost_of(s.tiles);
+    if (x < span * p.a.Hkv || s.rg + 1 >= p.groups) break;
+    x -= span * p.a.Hkv;
+  }
+  span = max(span, 1);
+  s.h = x / span;
+  x -= s.h * span;
+  s.start = at - x;
+  s.t0 = min(x, s.tiles);
+  s.t1 = min(s.tiles, x + (end - at));
+  s.next = min(end, at + span - x);
+  return s;
+}
+
+// One query row as NT e4m3 terms in the swizzled operand tiles at q (term t at q + 16384 t); returns
+// the factor of its scores, log2(e) |scale| 2^e (the sign of `scale` goes into the terms).
+template <typename T, int NT>
+__device__ __forceinline__ float query_row(const T* src, bool live, float scale, unsigned char* q, int r) {
+  uint4 raw[16];
+#pragma unroll
+  for (int c = 0; c < 16; ++c) raw[c] = live ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0u, 0u, 0u, 0u);
+  float amax = 0.f;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    float x[16];
+    unpack16(Raw16<T>{{raw[2 * c], raw[2 * c + 1]}}, x, src);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(x[k]));
+  }
+  const bool odd = !(amax <= 3.402823466e38f);  // an infinity: the row's result is NaN, as the formula's is
+  const unsigned u = __float_as_uint(amax);
+  int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);  // amax <= 448 2^e
+  e = min(120, max(-120, e));
+  if (amax == 0.f || odd) e = 0;
+  const float inv = scale < 0.f ? -exp2i(-e) : exp2i(-e);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    float x[16];
+    unpack16(Raw16<T>{{raw[2 * c], raw[2 * c + 1]}}, x, src);
+    const int at = r * 128 + ((c ^ (r & 7)) << 4);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] *= inv;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t two[2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          float &a = x[4 * k + 2 * m], &b = x[4 * k + 2 * m + 1];
+          two[m] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+          const uint32_t back = codes_half2(two[m]);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
+          a -= f.x;
+          b -= f.y;
+        }
+        w[k] = two[0] | (two[1] << 16);
+      }
+      *reinterpret_cast<uint4*>(q + 16384 * t + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  return odd ? __uint_as_float(0x7fc00000u) : fabsf(scale) * kLog2e * exp2i(e);
+}
+
+template <typename T, int NT, int NQ>
 __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
   using L = Plan<NT, NQ>;
   extern __shared__ __align__(1024) unsigned char sm[];
@@ -147,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
     }
     tqd::fence_mbar_init();
   }
-  fill_plan<TREE>(p, L::ROWS, pre, blockIdx.x == 0 ? A.pool.err : nullptr);
+  fill_plan(p, L::ROWS, pre, blockIdx.x == 0 ? A.pool.err : nullptr);
   tqd::tc_fence_before();
   __syncthreads();
   tqd::tc_fence_after();
@@ -177,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
       for (int s = blockIdx.x; s < slabs; s += gridDim.x) {
         const int h = s % A.Hkv, rg = s / A.Hkv % p.groups, b = s / A.Hkv / p.groups;
         const int len = clamped_len(A.seq_len, b, most, nullptr), cnt = clamped_count(A.count, b, A.nq);
-        if (group_limit<TREE>(p, L::ROWS, rg, len, cnt) > 0) continue;
+        if (group_limit(p, L::ROWS, rg, len, cnt) > 0) continue;
         const int row = rg * L::ROWS + i * 128 + r;
         if (row < p.rows) {
           T* o = out_row<kD, T>(p, b, h, row);
@@ -188,31 +317,17 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
     int at = begin;
     bool headed = false;
     while (at < end && ok) {
-      const Seg s = seg_at<TREE>(p, L::ROWS, pre, at, end);
+      const Seg s = seg_at(p, L::ROWS, pre, at, end);
       const bool first = at == begin;
       at = s.next;
       if (s.t0 == s.t1) continue;
       const int row = s.rg * L::ROWS + i * 128 + r;
       const bool live = row < p.rows;
       const int qi = live ? row / p.G : 0, hd = s.h * p.G + (live ? row - qi * p.G : 0);
-      // (a tree's rows past the count are zero queries whose sums are dropped, so that they hide nothing)
-      const bool asks = live && (!TREE || qi < s.cnt);
-      const int drafts = s.len - s.cnt;  // the first draft's position (TREE)
-      const int lim = live && !TREE ? row_limit(qi, s.len, s.cnt) : 0;
-      const int least = TREE ? 0 : __reduce_min_sync(kFull, live ? lim : 0x7fffffff);
-      const T* q_row = reinterpret_cast<const T*>(A.q.p) + s.b * A.q.sb + qi * A.q.st + hd * A.q.sh;
-      unsigned char* q_tile = sm + L::Q + i * NT * 16384;
-      float f;
-      if constexpr (TREE) {
-        QueryRow<kD> q;
-        q.request(q_row, asks);
-        f = query_terms<kD, NT, T>(q, A.scale, t_s, 0, kD / 16, [&](int t, int c, const uint32_t* w) {
-          *reinterpret_cast<uint4*>(q_tile + 16384 * t + k_chunk<kD>(r, c)) = make_uint4(w[0], w[1], w[2], w[3]);
-        });
-        tqd::tc_fence_before();
-      } else {
-        f = query_row<kD, NT, T>(q_row, live, A.scale, q_tile, r);
-      }
+      const int lim = live ? row_limit(qi, s.len, s.cnt) : 0;
+      const int least = __reduce_min_sync(kFull, live ? lim : 0x7fffffff);
+      const float f = query_row<T, NT>(reinterpret_cast<const T*>(A.q.p) + s.b * A.q.sb + qi * A.q.st + hd * A.q.sh, live,
+                                       A.scale, sm + L::Q + i * NT * 16384, r);
       tqd::tc_fence_smem();
       tqd::tc_mbar_arrive(bar(Q_FULL, i));
       float M = -INFINITY, l = 0.f;
@@ -225,7 +340,6 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
         tqd::tc_fence_after();
         const float4* sc = reinterpret_cast<const float4*>(sm + L::SCALES + 128 * ss);
         const int left = lim - kTok * t;  // tokens of this tile that the row attends to
-        if (TREE && kTok * (t + 1) > drafts) hide_scores<4>(t_s, A.tree, s.b, qi, asks, s.cnt, kTok * t - drafts);
         float v[128];
         ld32_async(t_s, v);
         ld32_async(t_s + 32, v + 32);
@@ -284,11 +398,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
         return true;
       };
       for (int t = s.t0; t < s.t1; ++t) {
-        if (!TREE && kTok * (t + 1) > least ? !tile(std::bool_constant<!TREE>{}, t) : !tile(std::false_type{}, t)) break;
+        if (kTok * (t + 1) > least ? !tile(std::true_type{}, t) : !tile(std::false_type{}, t)) break;
       }
       if (!ok || !wait(bar(O_DONE, i), (n - 1) & 1)) break;
       tqd::tc_fence_after();
-      if (TREE && !asks) l = 0.f;
       const bool whole = s.t0 == 0 && s.t1 == s.tiles;
       if (whole) {
         const float il = l > 0.f || l != l ? 1.f / l : 0.f;
@@ -299,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
           tqd::tc_ld32(t_o + 32 * c, v);
           if (live) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = !TREE || asks ? v[k] * il : 0.f;
+            for (int k = 0; k < 32; ++k) v[k] *= il;
             store16(o + 32 * c, v);
             store16(o + 32 * c + 16, v + 16);
           }
@@ -314,10 +427,6 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
         for (int c = 0; c < 4; ++c) {
           float v[32];
           tqd::tc_ld32(t_o + 32 * c, v);
-          if (TREE && !asks) {  // (they may hold NaN: what lies behind the tokens is hidden from the others only)
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = 0.f;
-          }
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             reinterpret_cast<float4*>(o + 32 * c)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
@@ -335,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
     uint32_t n = 0;
     int at = begin;
     while (at < end && ok) {
-      const Seg s = seg_at<TREE>(p, L::ROWS, pre, at, end);
+      const Seg s = seg_at(p, L::ROWS, pre, at, end);
       at = s.next;
       for (int t = s.t0; t < s.t1; ++t, ++n) {
         const int st = n & 1, ss = n % L::SC;
@@ -343,7 +452,6 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
           if (!wait(bar(SC_FULL, ss), (n / L::SC) & 1)) break;
           if (lane < 8) {
             float4* x = reinterpret_cast<float4*>(sm + L::SCALES + 128 * ss + 16 * lane);
-            if (TREE && kTok * t + 16 * lane >= s.limit) *x = make_float4(1.f, 1.f, 0.f, 0.f);  // (hidden scores stay -infinity)
             const int e = log2i(x->y);  // (of a block behind the tokens: any exponent; 2^-e stays finite)
             x->y = (float)e;
             x->z = exp2i(max(-126, min(126, -e)));
@@ -392,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
     uint32_t n = 0;
     int at = begin;
     while (at < end && ok) {
-      const Seg s = seg_at<TREE>(p, L::ROWS, pre, at, end);
+      const Seg s = seg_at(p, L::ROWS, pre, at, end);
       at = s.next;
       const int blocks = (s.limit + 15) >> 4;
       int page = 0;
@@ -435,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
     uint32_t n = 0, segs = 0;
     int at = begin;
     while (at < end && ok) {
-      const Seg s = seg_at<TREE>(p, L::ROWS, pre, at, end);
+      const Seg s = seg_at(p, L::ROWS, pre, at, end);
       at = s.next;
       if (s.t0 == s.t1) continue;
       if (!wait(bar(K_FULL, n & 1), (n >> 1) & 1)) break;
@@ -478,15 +586,15 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const TcParams p) {
   }
 }
 
-template <typename T, int NT, int NQ, bool TREE>
+template <typename T, int NT, int NQ>
 cudaError_t tc_go(TcParams p, int sms, int device, cudaStream_t s) {
   using L = Plan<NT, NQ>;
   static std::atomic<uint64_t> done{0};
   p.groups = (p.rows + L::ROWS - 1) / L::ROWS;
   p.grid = sms;
-  cudaError_t e = allow_smem((const void*)tc_kernel<T, NT, NQ, TREE>, L::SMEM, device, done);
+  cudaError_t e = allow_smem((const void*)tc_kernel<T, NT, NQ>, L::SMEM, device, done);
   if (e != cudaSuccess) return e;
-  tc_kernel<T, NT, NQ, TREE><<<p.grid, kThreads, L::SMEM, s>>>(p);
+  tc_kernel<T, NT, NQ><<<p.grid, kThreads, L::SMEM, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (p.grid == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
@@ -516,15 +624,6 @@ size_t tc_workspace(int rows) {
   return kJoinHeadBytes + (size_t)2 * kMaxSms * (rows > 128 ? Plan<2, 2>::PART : Plan<2, 1>::PART) * sizeof(float);
 }
 
-cudaError_t launch_tc(const AttnArgs& a, cudaStream_t s) {
-  TcParams p;
-  int dev;
-  const int sms = tc_params(a, &p, &dev);
-  if (a.dtype == TQ_BF16)
-    return p.rows > 128 ? tc_go<__nv_bfloat16, 2, 2, false>(p, sms, dev, s) : tc_go<__nv_bfloat16, 2, 1, false>(p, sms, dev, s);
-  return p.rows > 128 ? tc_go<__half, 3, 2, false>(p, sms, dev, s) : tc_go<__half, 3, 1, false>(p, sms, dev, s);
-}
-
 int tc_params(const AttnArgs& a, TcParams* p, int* dev) {
   p->a = a;
   p->G = a.Hq / a.Hkv;
@@ -536,11 +635,13 @@ int tc_params(const AttnArgs& a, TcParams* p, int* dev) {
   return sms > kMaxSms ? kMaxSms : sms;
 }
 
-cudaError_t launch_tc_tree(const AttnArgs& a, cudaStream_t s) {
+cudaError_t launch_tc(const AttnArgs& a, cudaStream_t s) {
   TcParams p;
   int dev;
   const int sms = tc_params(a, &p, &dev);
-  return a.dtype == TQ_BF16 ? tc_go<__nv_bfloat16, 2, 2, true>(p, sms, dev, s) : tc_go<__half, 3, 2, true>(p, sms, dev, s);
+  if (a.dtype == TQ_BF16)
+    return p.rows > 128 ? tc_go<__nv_bfloat16, 2, 2>(p, sms, dev, s) : tc_go<__nv_bfloat16, 2, 1>(p, sms, dev, s);
+  return p.rows > 128 ? tc_go<__half, 3, 2>(p, sms, dev, s) : tc_go<__half, 3, 1>(p, sms, dev, s);
 }
 
 }  // namespace tqb

@@ -15,7 +15,9 @@
 // F = 2, up to 64 rows (and head dim 64 always, in groups of 64): a row has two lanes, r and r + 64, one for each half of
 // a tile's tokens.  Each has an M and an O of its own; its P holds zeros for the other half's tokens, and the lanes
 // join as partials of a range do.  So all four warps of a group work on 64 rows, each on half as many scores.
-// More than 128 rows of head dim 128 go to tc_kernel with two row tiles, which reads the pool half as often.
+// More than 128 rows are groups of 128.  Two row tiles of 128 in turn on one token tile, as tc_kernel has them, read the pool half
+// as often, which L2 makes up for: they took 213 us for 256 rows over 8 x 32768 tokens (here 220), 116 for 512 rows over 65536
+// (116), and 35 and 24 us for 256 rows over 8 x 1024 and over 2048 (25 and 18).
 //
 // Which drafts a row sees matters only in the last tiles: there a pass over the scores puts -infinity where a mask's
 // bit is clear, from a window of 32 bits at a time, before the tile's softmax, which is the same for all tiles.
@@ -31,7 +33,6 @@
 //
 // Warps: 0-7 rows, 8-11 V to fp16, 12 K copies, 13 MMA issue, 14 V copies (15 only completes the warpgroup).
 #include <atomic>
-#include <string>
 
 #include "tq_byte_tc.cuh"
 
@@ -211,6 +212,92 @@ __device__ __forceinline__ void store4(T* p, float4 v) {
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float* v) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack2(p, v[0], v[1]), pack2(p, v[2], v[3]), pack2(p, v[4], v[5]), pack2(p, v[6], v[7]));
+}
+
+// 32 W scores from column t_s of this thread's lane to -infinity where the row (draft i of entry b) does not attend to
+// the token; j0: the draft at the first (negative: a token before the drafts).  Their factors are positive, so it hides them.
+template <int W>
+__device__ __forceinline__ void hide_scores(uint32_t t_s, const TreeMasks& M, int b, int i, bool asks, int cnt, int j0) {
+  const uint32_t* m = M.row(b, i);
+  uint32_t w[W];
+#pragma unroll
+  for (int x = 0; x < W; ++x) w[x] = asks ? tree_word(m, M.words, cnt, j0 + 32 * x) : 0u;
+#pragma unroll 1
+  for (int g = 0; g < W; ++g, t_s += 32) {
+    const uint32_t bits = w[0];
+#pragma unroll
+    for (int x = 1; x < W; ++x) w[x - 1] = w[x];
+    if (!__any_sync(kFull, bits != 0xffffffffu)) continue;
+    float v[32];
+    tqd::tc_ld32(t_s, v);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = bits >> k & 1u ? v[k] : -INFINITY;
+    tqd::tc_st32(t_s, v);
+  }
+}
+
+// A query row as NT e4m3 terms.  The code is kept small: what a block runs once a stretch waits for its instructions.
+// The row is loaded ahead (request), so that it does not wait behind the next tiles' copies; its words are then put through
+// D / 2 columns of tensor memory from t_raw on, so that a loop can take them 16 values at a time: put(t, c, w) takes codes
+// 16 c .. of term t, for chunks c in [c0, c1).  Returned: the factor of the row's scores, log2(e) |scale| 2^e (the sign of
+// `scale` goes into the terms), never so small that a scaled one of -infinity is not.
+template <int D>
+struct QueryRow {
+  uint4 raw[D / 8];
+  __device__ __forceinline__ void request(const void* src, bool live) {
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) raw[c] = live ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0u, 0u, 0u, 0u);
+  }
+};
+template <int D, int NT, typename T, typename F>
+__device__ __forceinline__ float query_terms(const QueryRow<D>& q, float scale, uint32_t t_raw, int c0, int c1, F put) {
+  float amax = 0.f;
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) {
+    float x[16];
+    unpack16(Raw16<T>{{q.raw[2 * c], q.raw[2 * c + 1]}}, x, (const T*)nullptr);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(x[k]));
+    const uint32_t w[8] = {q.raw[2 * c].x, q.raw[2 * c].y, q.raw[2 * c].z, q.raw[2 * c].w,
+                           q.raw[2 * c + 1].x, q.raw[2 * c + 1].y, q.raw[2 * c + 1].z, q.raw[2 * c + 1].w};
+    st8_async(t_raw + 8 * c, w);
+  }
+  const bool odd = !(amax <= 3.402823466e38f);  // an infinity: the row's result is NaN, as the formula's is
+  const unsigned u = __float_as_uint(amax);
+  int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);  // amax <= 448 2^e
+  e = min(120, max(-120, e));
+  if (amax == 0.f || odd) e = 0;
+  const float inv = scale < 0.f ? -exp2i(-e) : exp2i(-e);
+  asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+#pragma unroll 1
+  for (int c = c0; c < c1; ++c) {
+    Raw16<T> raw;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\ntcgen05.wait::ld.sync.aligned;\n"
+                 : "=r"(raw.v[0].x), "=r"(raw.v[0].y), "=r"(raw.v[0].z), "=r"(raw.v[0].w), "=r"(raw.v[1].x), "=r"(raw.v[1].y),
+                   "=r"(raw.v[1].z), "=r"(raw.v[1].w)
+                 : "r"(t_raw + 8 * c) : "memory");
+    float x[16];
+    unpack16(raw, x, (const T*)nullptr);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] *= inv;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float &a = x[2 * k], &b = x[2 * k + 1];
+        const uint32_t two = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t back = codes_half2(two);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
+        a -= f.x;
+        b -= f.y;
+        w[k >> 1] = k & 1 ? w[k >> 1] | (two << 16) : two;
+      }
+      put(t, c, w);
+    }
+  }
+  const float f = fabsf(scale) * kLog2e * exp2i(e);
+  return odd ? __uint_as_float(0x7fc00000u) : fmaxf(f, 8.07793567e-28f);  // 2^-90
 }
 
 template <int D, int NT, int F, typename T>
@@ -742,24 +829,23 @@ cudaError_t tree_go(TcParams p, int sms, int device, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, tree_join_kernel<D, F, T>, JoinParams{p.heads, p.part, p.a.out, p.a.nq, p.a.Hq, p.G, p.rows});
 }
 
-// Rows above which the tensor cores take a call.  Both sides (us, 8 x 32768 tokens, 8 KV heads, bf16; split / here): d = 128
-// 8 rows 97 / 96, 16 rows 109 / 96; d = 64 16 rows 84 / 84, 8 rows 54 / 84.  At 8 rows of d = 128 the split keeps more bits of the
-// queries for the same time.
-constexpr int tree_min_rows(int d) { return d == 128 ? 8 : 16; }
+// Rows above which the tensor cores take a call.  Both sides (us, 8 entries, 8 KV heads, bf16; split / here), of 32768
+// tokens: d = 128 8 rows 98 / 96, 12 rows 108 / 96; d = 64 8 rows 54 / 75, 12 rows 84 / 75.  Of 1024: d = 128 8 rows 13.5 / 15.8,
+// d = 64 12 rows 13.4 / 14.1.
+constexpr int kTreeMinRows = 8;
 
 }  // namespace
 
 bool tree_tc_takes(const AttnArgs& a) {
   const int rows = a.Hq / a.Hkv * a.nq;
-  if ((a.d != 64 && a.d != 128) || a.dtype == TQ_F32 || rows <= tree_min_rows(a.d)) return false;
+  if ((a.d != 64 && a.d != 128) || a.dtype == TQ_F32 || rows <= kTreeMinRows) return false;
   // the plan counts tiles in 32 bits
   const long long groups = (rows + 63) / 64, tiles = (a.pool.max_blocks + 7) / 8 + kTreeGroupCost;
   return (long long)a.B * a.Hkv * groups * tiles < (1ll << 31) - (1ll << 20);
 }
 
 size_t tree_tc_workspace(int d, int rows, tq_dtype dtype) {
-  if ((d != 64 && d != 128) || dtype == TQ_F32 || rows <= tree_min_rows(d)) return 0;
-  if (d == 128 && rows > 128) return tc_workspace(rows);
+  if ((d != 64 && d != 128) || dtype == TQ_F32 || rows <= kTreeMinRows) return 0;
   return kJoinHeadBytes + (size_t)2 * kMaxSms * 128 * (d + 2) * sizeof(float);
 }
 
@@ -770,7 +856,6 @@ static cudaError_t tree_type(const TcParams& p, int sms, int dev, cudaStream_t s
 }
 
 cudaError_t launch_tree_tc(const AttnArgs& a, cudaStream_t s) {
-  if (a.d == 128 && a.Hq / a.Hkv * a.nq > 128) return launch_tc_tree(a, s);
   TcParams p;
   int dev;
   const int sms = tc_params(a, &p, &dev);
