@@ -12,9 +12,10 @@
 // shared memory, and the room that they took there holds tiles in flight.  Rows that do not exist cost nothing:
 // their warps only pass the barriers.
 //
-// F = 2, up to 64 rows (and head dim 64 always, in groups of 64): a row has two lanes, r and r + 64, one for each half of
-// a tile's tokens.  Each has an M and an O of its own; its P holds zeros for the other half's tokens, and the lanes
-// join as partials of a range do.  So all four warps of a group work on 64 rows, each on half as many scores.
+// F = 2, up to 64 rows: a row has two lanes, r and r + 64, one for each half of a tile's tokens.  Each has an M and an O
+// of its own; its P holds zeros for the other half's tokens, and the lanes join as partials of a range do.  So all four
+// warps of a group work on 64 rows, each on half as many scores.  Groups of 64 for more rows were slower: 96 rows of
+// 8 x 32768 tokens 184 us instead of 116 (d = 64: 143, 106).
 // More than 128 rows are groups of 128.  Two row tiles of 128 in turn on one token tile, as tc_kernel has them, read the pool half
 // as often, which L2 makes up for: they took 213 us for 256 rows over 8 x 32768 tokens (here 220), 116 for 512 rows over 65536
 // (116), and 35 and 24 us for 256 rows over 8 x 1024 and over 2048 (25 and 18).
@@ -23,7 +24,7 @@
 // bit is clear, from a window of 32 bits at a time, before the tile's softmax, which is the same for all tiles.
 //
 // Measured (us, bf16, 32 / 8 heads, 8 x 32768 tokens; the pool partly in L2): 64 rows 99, 16 rows 96, 128 rows 118;
-// fp16 with 64 rows 106; d = 64 81 for 64 rows.  A tile's time is that of a group's chain, two tiles long: scores to
+// fp16 with 64 rows 107; d = 64 78 for 64 rows, 108 for 128.  A tile's time is that of a group's chain, two tiles long: scores to
 // registers 350 cycles, maximum to P 900, the readout's issue 430, the next scores' 360 and their 500 in the tensor
 // cores (F = 2, d = 64; 2500 in all).  At d = 128 and 64 rows that meets what HBM gives (5.4 TB/s of 6.8); at d = 64 it is
 // twice that, at 128 rows 1.3 times.  Tried and not kept: an O for each group (a second join, queries in shared
@@ -851,7 +852,7 @@ size_t tree_tc_workspace(int d, int rows, tq_dtype dtype) {
 
 template <typename T, int NT>
 static cudaError_t tree_type(const TcParams& p, int sms, int dev, cudaStream_t s) {
-  if (p.a.d == 64) return tree_go<64, NT, 2, T>(p, sms, dev, s);
+  if (p.a.d == 64) return p.rows <= 64 ? tree_go<64, NT, 2, T>(p, sms, dev, s) : tree_go<64, NT, 1, T>(p, sms, dev, s);
   return p.rows <= 64 ? tree_go<128, NT, 2, T>(p, sms, dev, s) : tree_go<128, NT, 1, T>(p, sms, dev, s);
 }
 
