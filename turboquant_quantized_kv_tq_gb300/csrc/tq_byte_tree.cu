@@ -306,6 +306,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
   using L = Plan<D>;
   constexpr int ROWS = 128 / F;     // rows of a group: each has F lanes,
   constexpr int NB = 8 / F;         // each of which takes this many blocks of a tile
+  // What a tile needs beside its scores (scales, the reference, the next keys) is waited for before them: a wait that is over
+  // takes some 200 cycles too.  At d = 128, and where a row has two lanes, it was slower: what is then held meanwhile spills, or
+  // the products wait for keys that are late (128 rows 126 us instead of 119; d = 64 with 192 rows of 16 x 16384 tokens 55, not 63).
+  constexpr bool EARLY = F == 1 && D == 64;
   extern __shared__ __align__(1024) unsigned char sm[];
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const AttnArgs& A = p.a;
@@ -434,9 +438,29 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
       // one tile; false: a wait gave up
       auto tile = [&](int t) {
         const uint32_t g_tile = n + (uint32_t)(t - t0), turn = g_tile >> 1;
-        if (!wait(bar(S_FULL, i), turn & 1)) return false;
+        float m_old = -INFINITY;
+        if (!EARLY && !wait(bar(S_FULL, i), turn & 1)) return false;
         const int ss = g_tile % L::SC;
         if (!wait(bar(SC_READY, ss), (g_tile / L::SC) & 1)) return false;
+        auto reference = [&] {
+          if (t > t0) {
+            if (!wait(bar(REF_SET, i ^ 1), ((g_tile - 1) >> 1) & 1)) return false;
+            m_old = refs[128 * (i ^ 1) + r];
+          }
+          return true;
+        };
+        const float4* sc = reinterpret_cast<const float4*>(sm + L::SCALES + 128 * ss) + NB * part;
+        float a[NB], e[NB], v[2][32];
+        auto scales = [&] {
+#pragma unroll
+          for (int g = 0; g < NB; ++g) {
+            const float2 x = *reinterpret_cast<const float2*>(sc + g);
+            a[g] = f * x.x;
+            e[g] = x.y;
+          }
+        };
+        if (EARLY) scales();
+        if (EARLY && ((!idle && !reference()) || !wait(bar(S_FULL, i), turn & 1))) return false;
         if (idle) {
           tqd::tc_mbar_arrive(bar(REF_SET, i));
           tqd::tc_mbar_arrive(bar(P_FULL, 2 * i));
@@ -445,21 +469,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
           return true;
         }
         tqd::tc_fence_after();
-        const float4* sc = reinterpret_cast<const float4*>(sm + L::SCALES + 128 * ss) + NB * part;
         const int j0 = kTok * t + 16 * NB * part - drafts;  // the draft at the lane's first score
         if (j0 + 16 * NB > 0) hide_scores<NB / 2>(t_mine, A.tree, stretch(segs)->b, qi, asks, stretch(segs)->cnt, j0);
         // A whole row's scores are read twice, 32 at a time, for the maximum and for P: held from one to the other they
         // left the warps too few registers (138 us for 8 x 32768 tokens and 64 rows).  P takes the first half of the columns:
         // block g's lie at 8 g, below the scores of block g that it comes from.
-        float a[NB], e[NB], v[2][32];
         ld32_async(t_mine, v[0]);
         if (F == 2) ld32_async(t_mine + 32, v[1]);
-#pragma unroll
-        for (int g = 0; g < NB; ++g) {
-          const float2 x = *reinterpret_cast<const float2*>(sc + g);
-          a[g] = f * x.x;
-          e[g] = x.y;
-        }
+        if (!EARLY) scales();
         float top = -INFINITY;
 #pragma unroll
         for (int c = 0; c < NB / 2; ++c) {
@@ -472,11 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
 #pragma unroll
           for (int g = 0; g < NB; ++g) st8_async(t_s + 8 * (NB * (1 - part) + g), none);
         }
-        float m_old = -INFINITY;
-        if (t > t0) {
-          if (!wait(bar(REF_SET, i ^ 1), ((g_tile - 1) >> 1) & 1)) return false;
-          m_old = refs[128 * (i ^ 1) + r];
-        }
+        if (!EARLY && !reference()) return false;
         const bool raise = top > m_old + kSlack;
         const float m_new = raise ? top - kTop : m_old;
         refs[128 * i + r] = m_new;
@@ -734,6 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
       ++segs;
       for (uint32_t k = 0; k < tiles && ok; ++k) {
         const uint32_t g = n + k;
+        if (EARLY && k + 2 < tiles && !wait(bar(K_FULL, (g + 2) % L::KS), ((g + 2) / L::KS) & 1)) break;
         if (!wait(bar(V_FULL, g & 1), (g >> 1) & 1)) break;
         if (!wait(bar(P_FULL, 2 * (g & 1)), (g >> 1) & 1)) break;
         tqd::tc_fence_after();
@@ -746,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
           else issue_readout<D, F, 0, 1>(sb, true);
         }
         if (k + 2 < tiles) {
-          if (!wait(bar(K_FULL, (g + 2) % L::KS), ((g + 2) / L::KS) & 1)) break;
+          if (!EARLY && !wait(bar(K_FULL, (g + 2) % L::KS), ((g + 2) / L::KS) & 1)) break;
           issue_scores<D, NT>(sb, g + 2);
         }
       }
