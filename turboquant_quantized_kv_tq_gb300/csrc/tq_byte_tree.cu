@@ -15,7 +15,7 @@
 // F = 2, up to 64 rows: a row has two lanes, r and r + 64, one for each half of a tile's tokens.  Each has an M and an O
 // of its own; its P holds zeros for the other half's tokens, and the lanes join as partials of a range do.  So all four
 // warps of a group work on 64 rows, each on half as many scores.  Groups of 64 for more rows were slower: 96 rows of
-// 8 x 32768 tokens 184 us instead of 116 (d = 64: 143, 106).
+// 8 x 32768 tokens 184 us instead of 116 (d = 64: 143, 94).
 // More than 128 rows are groups of 128.  Two row tiles of 128 in turn on one token tile, as tc_kernel has them, read the pool half
 // as often, which L2 makes up for: they took 213 us for 256 rows over 8 x 32768 tokens (here 220), 116 for 512 rows over 65536
 // (116), and 35 and 24 us for 256 rows over 8 x 1024 and over 2048 (25 and 18).
@@ -24,7 +24,7 @@
 // bit is clear, from a window of 32 bits at a time, before the tile's softmax, which is the same for all tiles.
 //
 // Measured (us, bf16, 32 / 8 heads, 8 x 32768 tokens; the pool partly in L2): 64 rows 99, 16 rows 96, 128 rows 118;
-// fp16 with 64 rows 107; d = 64 78 for 64 rows, 108 for 128.  A tile's time is that of a group's chain, two tiles long: scores to
+// fp16 107 and 135 for 64 and 128 rows; d = 64 78 and 94.  A tile's time is that of a group's chain, two tiles long: scores to
 // registers 350 cycles, maximum to P 900, the readout's issue 430, the next scores' 360 and their 500 in the tensor
 // cores (F = 2, d = 64; 2500 in all).  At d = 128 and 64 rows that meets what HBM gives (5.4 TB/s of 6.8); at d = 64 it is
 // twice that, at 128 rows 1.3 times.  Tried and not kept: an O for each group (a second join, queries in shared
@@ -306,10 +306,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
   using L = Plan<D>;
   constexpr int ROWS = 128 / F;     // rows of a group: each has F lanes,
   constexpr int NB = 8 / F;         // each of which takes this many blocks of a tile
-  // What a tile needs beside its scores (scales, the reference, the next keys) is waited for before them: a wait that is over
-  // takes some 200 cycles too.  At d = 128, and where a row has two lanes, it was slower: what is then held meanwhile spills, or
-  // the products wait for keys that are late (128 rows 126 us instead of 119; d = 64 with 192 rows of 16 x 16384 tokens 55, not 63).
-  constexpr bool EARLY = F == 1 && D == 64;
+  // What a tile needs beside its scores (scales, the reference) is waited for before them, and the keys of the scores behind a
+  // readout before the readout: a wait that is over takes some 200 cycles too.  At d = 128, and where a row has two lanes,
+  // it was slower (what is then held meanwhile spills, or the products wait for keys that are late) but for fp16's keys.
+  // Late / early: 192 rows of d = 64 over 16 x 16384 tokens 63 / 55 us; d = 128, 128 rows of 8 x 32768 119 / 126, fp16's keys 143 / 135.
+  constexpr bool EARLY = F == 1 && D == 64, EARLY_KEYS = F == 1 && (D == 64 || NT == 3);
   extern __shared__ __align__(1024) unsigned char sm[];
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const AttnArgs& A = p.a;
@@ -747,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
       ++segs;
       for (uint32_t k = 0; k < tiles && ok; ++k) {
         const uint32_t g = n + k;
-        if (EARLY && k + 2 < tiles && !wait(bar(K_FULL, (g + 2) % L::KS), ((g + 2) / L::KS) & 1)) break;
+        if (EARLY_KEYS && k + 2 < tiles && !wait(bar(K_FULL, (g + 2) % L::KS), ((g + 2) / L::KS) & 1)) break;
         if (!wait(bar(V_FULL, g & 1), (g >> 1) & 1)) break;
         if (!wait(bar(P_FULL, 2 * (g & 1)), (g >> 1) & 1)) break;
         tqd::tc_fence_after();
@@ -760,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
           else issue_readout<D, F, 0, 1>(sb, true);
         }
         if (k + 2 < tiles) {
-          if (!EARLY && !wait(bar(K_FULL, (g + 2) % L::KS), ((g + 2) / L::KS) & 1)) break;
+          if (!EARLY_KEYS && !wait(bar(K_FULL, (g + 2) % L::KS), ((g + 2) / L::KS) & 1)) break;
           issue_scores<D, NT>(sb, g + 2);
         }
       }
