@@ -239,6 +239,27 @@ def test_maxima_that_rise_and_fall(dtype, d, Hq, H, nq, rise):
     _check(out, want, spread, reach, max(seq), d, DT[dtype], wide, least)
 
 
+MANY = [("bf16", 64, 8, 2, 17), ("bf16", 64, 8, 2, 40), ("f16", 64, 16, 2, 24), ("f16", 128, 8, 1, 24), ("f16", 128, 7, 1, 13), ("bf16", 128, 16, 2, 33)]
+
+
+@pytest.mark.parametrize("dtype,d,Hq,H,nq", MANY)
+def test_more_than_64_rows(dtype, d, Hq, H, nq):
+    """Groups of 128 rows, the last one partly filled: long sequences beside short ones, and trees of few drafts beside those of many."""
+    _run(d, dtype, Hq, H, [9000, 33, 4097, 0, 6001, 700], [nq, nq, max(1, nq // 2), nq, 1, 0], nq, seed=5, from_tree=True)
+
+
+@pytest.mark.parametrize("dtype,d,Hq,H,nq", MANY)
+@pytest.mark.parametrize("rise", [0.13, -0.13])
+def test_maxima_of_more_than_64_rows(dtype, d, Hq, H, nq, rise):
+    test_maxima_that_rise_and_fall(dtype, d, Hq, H, nq, rise)
+
+
+@pytest.mark.parametrize("dtype,d,Hq,H,nq", ROUTES + MANY)
+def test_tables_that_end_with_the_sequence(dtype, d, Hq, H, nq):
+    """The longest sequence fills its table and its last tile; others end with a tile or a block before it."""
+    _run(d, dtype, Hq, H, [512, 384, 496, 128, 16], [nq, nq, nq, nq, min(nq, 16)], nq, seed=6)
+
+
 @pytest.mark.parametrize("dtype,d,Hq,H,nq", ROUTES)
 @pytest.mark.parametrize("scale", [0.0, -0.07, 1e-30, 3.0])
 def test_scales_of_the_scores(dtype, d, Hq, H, nq, scale):
