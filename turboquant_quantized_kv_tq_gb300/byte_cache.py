@@ -2,9 +2,9 @@
 ``tq_byte_*`` entry points of ``include/tq.h``).
 
 ``Rotary`` holds a rotation's device table, ``norm_rotate`` applies it (and the norms) to queries and
-keys, ``draft_tree`` makes the masks and positions of trees of drafted tokens, and ``PagedByteCache`` owns a pool of e4m3 codes with a scale for each 16-token block, KV head
-and side.  Tensors may be strided views (a fused projection's slices): only the head dimension has to
-be contiguous, with rows on 16-byte boundaries.  Nothing is copied or converted here; a layout that
+keys, ``draft_tree`` makes the masks and positions of trees of drafted tokens, and ``PagedByteCache`` owns a
+pool of e4m3 codes with a scale for each 16-token block, KV head and side.  Tensors may be strided views (a fused
+projection's slices): only the head dimension has to be contiguous, with rows on 16-byte boundaries.  Nothing is copied or converted here; a layout that
 the kernels do not take is refused.
 
 The calls compute no gradients: while grad mode is on, inputs that require one are refused.

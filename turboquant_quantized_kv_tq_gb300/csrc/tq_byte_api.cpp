@@ -406,7 +406,8 @@ tq_status tq_byte_read_paged(const tq_byte_config* cfg, const void* dev_pool, co
   if (!aligned(k_out, 16) || !aligned(v_out, 16)) return fail(TQ_ERR_INVALID_ARG, "outputs must be 16-byte aligned");
   const int bytes = dtype_bytes(dtype);
   const Span pool = span_of(dev_pool, tq_byte_pool_bytes(cfg, pages->num_pages));
-  const Span k = span_of(k_out, batch, n, cfg->num_kv_heads, cfg->head_dim, bytes), v = span_of(v_out, batch, n, cfg->num_kv_heads, cfg->head_dim, bytes);
+  const Span k = span_of(k_out, batch, n, cfg->num_kv_heads, cfg->head_dim, bytes);
+  const Span v = span_of(v_out, batch, n, cfg->num_kv_heads, cfg->head_dim, bytes);
   if (overlap(k, v)) return fail(TQ_ERR_INVALID_ARG, "the outputs overlap");
   const size_t list = (size_t)batch * 4;
   const Span in[4] = {pool, span_of(dev_start, list), span_of(dev_count, dev_count ? list : 0),

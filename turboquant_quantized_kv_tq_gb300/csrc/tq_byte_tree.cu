@@ -23,14 +23,16 @@
 // Which drafts a row sees matters only in the last tiles: there a pass over the scores puts -infinity where a mask's
 // bit is clear, from a window of 32 bits at a time, before the tile's softmax, which is the same for all tiles.
 //
-// Measured (us, bf16, 32 / 8 heads, 8 x 32768 tokens; the pool partly in L2): 64 rows 99, 16 rows 96, 128 rows 118;
-// fp16 107 and 135 for 64 and 128 rows; d = 64 78 and 94.  A tile's time is that of a group's chain, two tiles long: scores to
-// registers 350 cycles, maximum to P 900, the readout's issue 430, the next scores' 360 and their 500 in the tensor
-// cores (F = 2, d = 64; 2500 in all).  At d = 128 and 64 rows that meets what HBM gives (5.4 TB/s of 6.8); at d = 64 it is
-// twice that, at 128 rows 1.3 times.  Tried and not kept: an O for each group (a second join, queries in shared
-// memory: 157), P in columns of its own so that scores run ahead of the readout (146 instead of 116 for 128 rows, 121
-// instead of 86 at d = 64, also with the readout issued by another warp), a row's 128 scores held in registers (124
-// instead of 117), copies of keys, values and scales by one warp (172), partials by row (6000 cycles a stretch).
+// Measured (us, bf16, 32 / 8 heads, 8 x 32768 tokens, pools out of L2): 16 rows 96, 64 rows 101, 128 rows 119; fp16 107 and 135
+// for 64 and 128 rows; d = 64 78 and 94.  A tile's time is that of a group's chain, two tiles long: scores to registers
+// 350 cycles, maximum to P 900, the readout's issue 430, the next scores' 360 and their 500 in the tensor cores (F = 2,
+// d = 64; 2500 in all).  At d = 128 and 64 rows that meets what HBM gives (5.3 TB/s of 6.8); at d = 64 it is twice that, at
+// 128 rows 1.3 times.  Tried and not kept: an O for each group (a second join, queries in shared memory: 157), P in columns
+// of its own so that scores run ahead of the readout (146 instead of 116 for 128 rows, 121 instead of 86 at d = 64, also with
+// the readout issued by another warp), a row's 128 scores held in registers (124 instead of 117), sixteen row warps of 96
+// registers, two to a row, above 64 rows (d = 64 51 instead of 55, d = 128 115 to 125; the code for up to 64 rows beside it 110
+// instead of 101), a part of the exponentials on the FMA pipe (130 to 145 instead of 118), copies of keys, values and scales
+// by one warp (172), partials by row (6000 cycles a stretch).
 //
 // Warps: 0-7 rows, 8-11 V to fp16, 12 K copies, 13 MMA issue, 14 V copies (15 only completes the warpgroup).
 #include <atomic>
