@@ -1,0 +1,67 @@
+"""What a tree's masks hide reaches nothing, whatever lies there: against the definition on the visible tokens alone.
+
+Tolerances: as in test_gpu_tree.py, whose comments derive them."""
+
+import numpy as np
+import pytest
+import torch
+
+import byte_reference as ref
+import tree_reference as tree
+from test_gpu_byte_cache import DT, _api, _i32, _np, _table
+from test_gpu_tree import _check, _terms
+
+pytestmark = pytest.mark.gpu
+
+# up to 8 rows, 9 to 64 and more at head dims 64 and 128, the other kernel's types and head dim
+ROUTES = [("bf16", 128, 4, 2, 2), ("bf16", 128, 4, 2, 20), ("f16", 128, 8, 2, 40), ("bf16", 64, 4, 2, 20), ("f16", 64, 8, 2, 40),
+          ("f32", 128, 4, 2, 20), ("bf16", 256, 4, 2, 20)]
+
+
+def _prompt(d, Hq, H, seq, blocks, dtype, zeroed=True):
+    """A cache whose first seq[b] tokens were appended, into a pool that was zeroed, or held anything, before."""
+    B = len(seq)
+    pages = B * blocks + 1
+    c = _api().PagedByteCache(d, Hq, H, pages, blocks)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(d + Hq)
+    if not zeroed:
+        c.pool.copy_(torch.randint(0, 256, c.pool.shape, generator=g, device="cuda", dtype=torch.uint8))
+    table = _table(B, blocks, pages, seed=d)
+    k, v = (torch.randn(B, H, max(seq), d, generator=g, device="cuda").to(DT[dtype]) for _ in range(2))
+    c.append(k, v, _i32([0] * B), _i32(table), count=_i32(seq))
+    assert c.device_error() == 0
+    return c, table, g
+
+
+def _visible(c, table, q, seq, H, d, dtype, sees):
+    """Bounds and values by the definition, where the tokens from seq[b] on are never visible; the pool's bytes there
+    are put to zeros for the reference, which multiplies what it hides by nothing but reads it."""
+    n = q.shape[1]
+    pool = ref.Pool(c.pool.cpu().numpy(), H, d)
+    for b, s in enumerate(seq):
+        for t in range(s, s + n):
+            for h in range(H):
+                for side in (0, 1):
+                    blk = pool.blocks[table[b][t // 16], h]
+                    blk[pool.at[side, t % 16]] = 0
+                    if t % 16 == 0:
+                        pool.set_scale(table[b][t // 16], h, side, 0)
+    lens, cnt = [s + n for s in seq], [n] * len(seq)
+    Hq = q.shape[2]
+    want, spread, reach, least = tree.attention(_np(q), pool, lens, cnt, table, d ** -0.5, sees, 2.0 ** -31)
+    wide = _terms(_np(q), pool, lens, cnt, table, d ** -0.5, dtype != "f32" and d != 256 and Hq // H * n > 8)
+    return want, spread, reach, least, wide
+
+
+@pytest.mark.parametrize("dtype,d,Hq,H,nq", ROUTES)
+@pytest.mark.parametrize("seq", [[96, 128, 37], [256, 16, 1]])
+def test_hidden_drafts_that_were_never_appended(dtype, d, Hq, H, nq, seq):
+    """The drafts' blocks are as a zeroed pool has them, scales of 0 among them."""
+    blocks = (max(seq) + nq + 15) // 16
+    c, table, g = _prompt(d, Hq, H, seq, blocks, dtype)
+    q = torch.randn(len(seq), nq, Hq, d, generator=g, device="cuda").to(DT[dtype])
+    sees = np.zeros((len(seq), nq, nq), dtype=bool)
+    out = c.attention(q, _i32([s + nq for s in seq]), _i32(table), tree=_i32(tree.pack(sees)))
+    want, spread, reach, least, wide = _visible(c, table, q, seq, H, d, dtype, sees)
+    _check(out, want, spread, reach, max(seq) + nq, d, DT[dtype], wide, least)

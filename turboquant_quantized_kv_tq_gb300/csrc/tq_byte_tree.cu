@@ -218,7 +218,8 @@ __device__ __forceinline__ void store8(T* p, const float* v) {
 }
 
 // 32 W scores from column t_s of this thread's lane to -infinity where the row (draft i of entry b) does not attend to
-// the token; j0: the draft at the first (negative: a token before the drafts).  Their factors are positive, so it hides them.
+// the token; j0: the draft at the first (negative: a token before the drafts).  Their factors, a row's (2^-90 at least) times
+// a block's scale (2^-30 at least), are positive normal numbers, so it hides them.
 template <int W>
 __device__ __forceinline__ void hide_scores(uint32_t t_s, const TreeMasks& M, int b, int i, bool asks, int cnt, int j0) {
   const uint32_t* m = M.row(b, i);
@@ -640,7 +641,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
           if (n >= L::SC && !wait(bar(SC_EMPTY, ss), (n / L::SC - 1) & 1)) break;
           if (lane < 8) {
             float2 x = *reinterpret_cast<const float2*>(sm + L::VR + (vs * 8 + lane) * L::VB + 16 * D);
-            if (kTok * t + 16 * lane >= s.len) x = make_float2(1.f, 1.f);  // (a block behind the tokens: hidden scores stay -infinity)
+            // Within an append's range, 2^-30 to 2^30, whatever stands there: a block behind the tokens, or of hidden drafts that were
+            // never appended, may hold anything (in a zeroed pool 0, and 0 times a hidden score of -infinity is NaN).
+            x.x = fminf(fmaxf(x.x, 9.31322575e-10f), 1073741824.f);
+            x.y = fminf(fmaxf(x.y, 9.31322575e-10f), 1073741824.f);
             const int e = log2i(x.y);
             *reinterpret_cast<float4*>(sm + L::SCALES + 128 * ss + 16 * lane) =
                 make_float4(x.x, (float)e, exp2i(max(-126, min(126, -e))), 0.f);
