@@ -65,3 +65,26 @@ def test_hidden_drafts_that_were_never_appended(dtype, d, Hq, H, nq, seq):
     out = c.attention(q, _i32([s + nq for s in seq]), _i32(table), tree=_i32(tree.pack(sees)))
     want, spread, reach, least, wide = _visible(c, table, q, seq, H, d, dtype, sees)
     _check(out, want, spread, reach, max(seq) + nq, d, DT[dtype], wide, least)
+
+
+@pytest.mark.parametrize("dtype,d,Hq,H,nq", ROUTES)
+@pytest.mark.parametrize("odd", [float("inf"), -float("inf"), float("nan")])
+def test_odd_queries_of_rows_that_see_nothing(dtype, d, Hq, H, nq, odd):
+    """Rows that attend to nothing are zeros whatever their queries hold; the same queries are NaN where they attend to a
+    token, and no other row minds."""
+    seq = [nq, 200 + nq, 130]
+    c, table, g = _prompt(d, Hq, H, seq, 17, dtype)
+    q = torch.randn(3, nq, Hq, d, generator=g, device="cuda").to(DT[dtype])
+    sees = np.zeros((3, nq, nq), dtype=bool)
+    sees[0, nq // 2:, 0] = True   # the first entry has no tokens before its drafts
+    args = _i32(seq), _i32(table)
+    clean = c.attention(q, *args, tree=_i32(tree.pack(sees)))
+    hit = torch.zeros(3, nq, Hq, dtype=torch.bool, device="cuda")
+    hit[:, 0, 1] = hit[:, nq - 1, Hq - 1] = True
+    q[..., 3] = torch.where(hit, torch.full_like(q[..., 3], odd), q[..., 3])
+    out = c.attention(q, *args, tree=_i32(tree.pack(sees)))
+    blind = torch.zeros_like(hit)
+    blind[0, :nq // 2] = True
+    assert not out[blind].any()
+    assert torch.isnan(out[hit & ~blind]).all()
+    assert torch.equal(out[~hit], clean[~hit]) and torch.isfinite(clean.float()).all()

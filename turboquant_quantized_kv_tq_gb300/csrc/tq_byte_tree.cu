@@ -244,7 +244,8 @@ __device__ __forceinline__ void hide_scores(uint32_t t_s, const TreeMasks& M, in
 // The row is loaded ahead (request), so that it does not wait behind the next tiles' copies; its words are then put through
 // D / 2 columns of tensor memory from t_raw on, so that a loop can take them 16 values at a time: put(t, c, w) takes codes
 // 16 c .. of term t, for chunks c in [c0, c1).  Returned: the factor of the row's scores, log2(e) |scale| 2^e (the sign of
-// `scale` goes into the terms), never so small that a scaled one of -infinity is not.
+// `scale` goes into the terms), never so small that a scaled one of -infinity is not.  A row with an infinity is all NaN
+// codes (a NaN is one by itself): what the row attends to makes it NaN, as the formula does, and where that is nothing it is zeros.
 template <int D>
 struct QueryRow {
   uint4 raw[D / 8];
@@ -266,12 +267,12 @@ __device__ __forceinline__ float query_terms(const QueryRow<D>& q, float scale, 
                            q.raw[2 * c + 1].x, q.raw[2 * c + 1].y, q.raw[2 * c + 1].z, q.raw[2 * c + 1].w};
     st8_async(t_raw + 8 * c, w);
   }
-  const bool odd = !(amax <= 3.402823466e38f);  // an infinity: the row's result is NaN, as the formula's is
+  const bool odd = !(amax <= 3.402823466e38f);  // an infinity
   const unsigned u = __float_as_uint(amax);
   int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);  // amax <= 448 2^e
   e = min(120, max(-120, e));
   if (amax == 0.f || odd) e = 0;
-  const float inv = scale < 0.f ? -exp2i(-e) : exp2i(-e);
+  const float inv = odd ? __uint_as_float(0x7fc00000u) : scale < 0.f ? -exp2i(-e) : exp2i(-e);
   asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 #pragma unroll 1
   for (int c = c0; c < c1; ++c) {
@@ -300,8 +301,7 @@ __device__ __forceinline__ float query_terms(const QueryRow<D>& q, float scale, 
       put(t, c, w);
     }
   }
-  const float f = fabsf(scale) * kLog2e * exp2i(e);
-  return odd ? __uint_as_float(0x7fc00000u) : fmaxf(f, 8.07793567e-28f);  // 2^-90
+  return fmaxf(fabsf(scale) * kLog2e * exp2i(e), 8.07793567e-28f);  // 2^-90
 }
 
 template <int D, int NT, int F, typename T>
