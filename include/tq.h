@@ -499,7 +499,8 @@ tq_status tq_draft_tree(int32_t batch, int32_t n, const int32_t* dev_parents, co
 /* tq_byte_attention_paged for a tree: entry b's c = min(dev_count[b], nq) drafts are the last c of its
  * dev_seq_len[b] tokens.  Draft i < c attends to the first dev_seq_len[b] - c tokens, and to draft j < c
  * where bit j of its mask is set (dev_masks [batch][nq][(nq + 31) / 32], any bits: they need not come
- * from a tree; bits from c on count for nothing).  Where c > dev_seq_len[b] the drafts before the first token
+ * from a tree; bits from c on count for nothing).  What the pool holds for drafts that no row attends to is never
+ * used: they need not be appended.  Where c > dev_seq_len[b] the drafts before the first token
  * do not exist.  Rows that attend to nothing, and rows i >= c, are zeros.  nq: at most TQ_MAX_DRAFTS.
  * The rest as for tq_byte_attention_paged; 16-bit queries of more than 8 rows (queries times heads per KV head) enter
  * as e4m3 terms at head_dim 64 and 128. */

@@ -34,21 +34,19 @@ def _prompt(d, Hq, H, seq, blocks, dtype, zeroed=True):
     return c, table, g
 
 
-def _visible(c, table, q, seq, H, d, dtype, sees):
-    """Bounds and values by the definition, where the tokens from seq[b] on are never visible; the pool's bytes there
-    are put to zeros for the reference, which multiplies what it hides by nothing but reads it."""
-    n = q.shape[1]
+def _by_definition(c, table, q, seq, there, H, d, dtype, sees):
+    """Values and bounds by the definition; the first there[b] tokens were appended and what lies behind them is hidden (put
+    to zeros here: the reference reads it and gives it no weight)."""
+    n, Hq = q.shape[1:3]
     pool = ref.Pool(c.pool.cpu().numpy(), H, d)
-    for b, s in enumerate(seq):
-        for t in range(s, s + n):
+    lens, cnt = [s + n for s in seq], [n] * len(seq)
+    for b, s in enumerate(there):
+        for t in range(s, lens[b]):
             for h in range(H):
                 for side in (0, 1):
-                    blk = pool.blocks[table[b][t // 16], h]
-                    blk[pool.at[side, t % 16]] = 0
+                    pool.blocks[table[b][t // 16], h][pool.at[side, t % 16]] = 0
                     if t % 16 == 0:
                         pool.set_scale(table[b][t // 16], h, side, 0)
-    lens, cnt = [s + n for s in seq], [n] * len(seq)
-    Hq = q.shape[2]
     want, spread, reach, least = tree.attention(_np(q), pool, lens, cnt, table, d ** -0.5, sees, 2.0 ** -31)
     wide = _terms(_np(q), pool, lens, cnt, table, d ** -0.5, dtype != "f32" and d != 256 and Hq // H * n > 8)
     return want, spread, reach, least, wide
@@ -63,7 +61,7 @@ def test_hidden_drafts_that_were_never_appended(dtype, d, Hq, H, nq, seq):
     q = torch.randn(len(seq), nq, Hq, d, generator=g, device="cuda").to(DT[dtype])
     sees = np.zeros((len(seq), nq, nq), dtype=bool)
     out = c.attention(q, _i32([s + nq for s in seq]), _i32(table), tree=_i32(tree.pack(sees)))
-    want, spread, reach, least, wide = _visible(c, table, q, seq, H, d, dtype, sees)
+    want, spread, reach, least, wide = _by_definition(c, table, q, seq, seq, H, d, dtype, sees)
     _check(out, want, spread, reach, max(seq) + nq, d, DT[dtype], wide, least)
 
 
@@ -88,3 +86,20 @@ def test_odd_queries_of_rows_that_see_nothing(dtype, d, Hq, H, nq, odd):
     assert not out[blind].any()
     assert torch.isnan(out[hit & ~blind]).all()
     assert torch.equal(out[~hit], clean[~hit]) and torch.isfinite(clean.float()).all()
+
+
+@pytest.mark.parametrize("dtype,d,Hq,H,nq", ROUTES)
+@pytest.mark.parametrize("seq", [[96, 128, 37], [256, 15, 1]])
+def test_hidden_drafts_of_a_pool_that_held_anything(dtype, d, Hq, H, nq, seq):
+    """The same where the pool held NaN codes and senseless scales before; a draft that was appended is visible among them."""
+    blocks = (max(seq) + nq + 15) // 16
+    c, table, g = _prompt(d, Hq, H, seq, blocks, dtype, zeroed=False)
+    B = len(seq)
+    k, v = (torch.randn(B, H, 1, d, generator=g, device="cuda").to(DT[dtype]) for _ in range(2))
+    c.append(k, v, _i32(seq), _i32(table))
+    q = torch.randn(B, nq, Hq, d, generator=g, device="cuda").to(DT[dtype])
+    sees = np.zeros((B, nq, nq), dtype=bool)
+    sees[:, ::2, 0] = True
+    out = c.attention(q, _i32([s + nq for s in seq]), _i32(table), tree=_i32(tree.pack(sees)))
+    want, spread, reach, least, wide = _by_definition(c, table, q, seq, [s + 1 for s in seq], H, d, dtype, sees)
+    _check(out, want, spread, reach, max(seq) + nq, d, DT[dtype], wide, least)

@@ -84,6 +84,11 @@ __device__ __forceinline__ void codes_half4(uint32_t four, uint32_t& a, uint32_t
       : "=r"(a), "=r"(b)
       : "r"(four));
 }
+// Four codes with zeros for NaNs.
+__device__ __forceinline__ uint32_t without_nans(uint32_t four) {
+  const uint32_t nan = ((four & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // a NaN is 0x7f or 0xff
+  return four & ~((nan >> 7) * 0xffu);
+}
 __device__ __forceinline__ float decode1(unsigned char c) {
   const uint32_t h = codes_half2(c);
   return __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));

@@ -198,11 +198,13 @@ __device__ __forceinline__ uint32_t tree_word(const uint32_t* m, int words, int 
 // Which tokens rows 2u + k of group r do not attend to: those from the row's limit on.
 template <int NR>
 struct Limits {
+  static constexpr bool kTree = false;
   const int (&lim)[NR][2];
   __device__ __forceinline__ bool operator()(int r, int k, int tok) const { return tok >= lim[r][k]; }
 };
 // The same of a tree: drafts whose bit is clear, and every draft for rows past the count.
 struct TreeLimits {
+  static constexpr bool kTree = true;
   const TreeMasks& M;
   int b, row0, G, drafts, cnt;  // row0: of the thread's row (0, 0); drafts: the first draft's position
   __device__ __forceinline__ bool operator()(int r, int k, int tok) const {
@@ -301,7 +303,8 @@ __device__ __forceinline__ void tile_step_edge(const unsigned char* blk, const Q
       }
     }
   }
-  // codes behind the sequence's end may be NaN: zero them (their probabilities are zero already)
+  // codes behind the sequence's end, and of hidden drafts that were never appended, may be NaN: zero them (their
+  // probabilities are zero already)
   uint32_t keep = 0xffffffffu;
   if (EDGE && tok0 + 16 > len) {
     const int t = len - tok0;
@@ -315,6 +318,10 @@ __device__ __forceinline__ void tile_step_edge(const unsigned char* blk, const Q
     if (EDGE) {
       w0 &= keep;
       w1 &= keep;
+      if constexpr (H::kTree) {
+        w0 = without_nans(w0);
+        w1 = without_nans(w1);
+      }
     }
     uint32_t a0, a1, a2, a3;
     codes_half4(w0, a0, a2);

@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
 #pragma unroll
           for (int m = 0; m < D / 32; ++m)
             raw[k][m] = *reinterpret_cast<const uint4*>(sm + L::VR + (vs * 8 + (warp - 8) + 4 * k) * L::VB + 16 * (lane + 32 * m));
-        if (kTok * (t + 1) > s.len) {  // tokens behind the last become zeros
+        if (kTok * (t + 1) > s.len - s.cnt) {  // tokens behind the last become zeros, and NaN codes (of hidden drafts never appended)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int have = s.len - kTok * t - 16 * ((warp - 8) + 4 * k);
@@ -670,10 +670,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
                         (2 * u + 9 < have ? 0xff000000u : 0u);
 #pragma unroll
             for (int m = 0; m < D / 32; ++m) {
-              raw[k][m].x &= keep[0];
-              raw[k][m].y &= keep[1];
-              raw[k][m].z &= keep[2];
-              raw[k][m].w &= keep[3];
+              raw[k][m].x = without_nans(raw[k][m].x & keep[0]);
+              raw[k][m].y = without_nans(raw[k][m].y & keep[1]);
+              raw[k][m].z = without_nans(raw[k][m].z & keep[2]);
+              raw[k][m].w = without_nans(raw[k][m].w & keep[3]);
             }
           }
         }
