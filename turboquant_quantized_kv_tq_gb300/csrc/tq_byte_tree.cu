@@ -74,7 +74,8 @@ struct Plan {
   static constexpr int T_O = 256, T_Q = 384;                      // columns of O and of the queries' terms (S_i at 128 i)
   static constexpr int SMEM = PRE + (TQ_MAX_BATCH + 1) * 4;
   static_assert(SMEM <= 227 * 1024, "shared memory");
-  static constexpr int PART = 128 * (D + 2);                      // floats of a partial
+  static constexpr int PART = 128 * (D + 2);                      // floats of a partial: M[128], l[128], O[D / 4][128][4]
+  static constexpr int CARRY = 2 * 256;                           // and of a block's (M, l) between the stretches of a slab, by row thread
 };
 // (P_FULL: part h of group i at 2 i + h)
 enum Bar { K_FULL = 0, K_EMPTY = 8, VR_FULL = 16, VR_EMPTY = 24, V_FULL = 32, V_EMPTY = 34, S_FULL = 36, O_DONE = 38, REF_SET = 40,
@@ -117,6 +118,13 @@ __device__ __forceinline__ void fill_tree_plan(const TcParams& p, int* pre, int2
 }
 
 // A stretch of a slab's tiles [t0, t1), the first from cost `at` (< end) on that has a tile; t0 = t1: there is none.
+// The tensor cores' sum O truncates at every product (16 tokens) that it takes in: over 100000 tokens of values with mean 1 it
+// came out 4.1e-4 low (F = 2, where half of a lane's products are of zeros: 1.9e-4), twice fp16's rounding.  So a block's part
+// of a slab is cut into stretches of at most kMostTiles, which join in fp32 in its place for a partial.  1024 products lose
+// 2^-14 of an evenly growing sum at most; measured 4.1e-5 and 1.9e-5.  A cut costs the block a stretch's start and end (64 / 128 /
+// 256 / none: 152 slabs of 49152 tokens, 64 rows 340 / 320 / 315 / 306 us, 128 rows 388 / 366 / 370 / 359; 8 x 32768 tokens with
+// 64 rows, 108 tiles a block, 105 / 99 / 99 / 98).
+constexpr int kMostTiles = 128;
 struct Stretch {
   int b, h, rg, len, cnt;
   int t0, t1, tiles;
@@ -141,8 +149,13 @@ __device__ __forceinline__ Stretch stretch_from(const TcParams& p, const int* pr
     const int2 n = len[b];
     const int tiles = tiles_of(n.x), span = tree_cost(tiles), x = at - pre[b], k = x / span, y = x - k * span;
     if (y < tiles) {
-      const int rg = k / p.a.Hkv;
-      return Stretch{b, k - rg * p.a.Hkv, rg, n.x, n.y, y, min(tiles, y + (end - at)), tiles, at - y, min(end, at + span - y)};
+      const int rg = k / p.a.Hkv, left = min(tiles - y, end - at);
+      int take = left, next = min(end, at + span - y);
+      if (left > kMostTiles) {
+        take = left < 2 * kMostTiles ? (left + 1) >> 1 : kMostTiles;
+        next = at + take;
+      }
+      return Stretch{b, k - rg * p.a.Hkv, rg, n.x, n.y, y, y + take, tiles, at - y, next};
     }
     at += span - y;
   }
@@ -588,12 +601,40 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
         mine = ex2(top - ref);
         sum = fmaf(sum, mine, (sums[r ^ 64] + sums[128 + (r ^ 64)]) * ex2(other - ref));
       }
-      const bool whole = now.t0 == 0 && now.t1 == now.tiles;
-      if (whole) mine *= sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-      T* out = out_row<D, T>(p, now.b, now.h, was_live ? now.rg * ROWS + rr : 0);
-      float* partial = p.part + (2ll * blockIdx.x + (now.t0 + now.start == begin ? 0 : 1)) * L::PART;
+      // the block's part of the slab: tiles [max(0, begin - start), stop)
+      const int stop = min(now.tiles, end - now.start);
+      const bool inside = now.start >= begin && stop == now.tiles, done = now.t1 == stop, whole = inside && done;
+      // (a slab that lies inside the range uses the place of the last one, which comes after it)
+      float* partial = p.part + (2ll * blockIdx.x + (now.start <= begin ? 0 : 1)) * L::PART;
+      float2* carry = reinterpret_cast<float2*>(p.part + 2ll * p.grid * L::PART + (long long)blockIdx.x * L::CARRY) + threadIdx.x;
       // [4 coordinates][row]: a warp writes 512 bytes in a row (as rows of their own they took 6000 cycles)
       float4* to = reinterpret_cast<float4*>(partial + 256) + rr;
+      if (now.t0 > max(0, begin - now.start) && !idle) {  // the sums of the stretches before
+        const float2 x = *carry;
+        const float all = fmaxf(most, x.x), ref = all == -INFINITY ? 0.f : all, w = ex2(most - ref), before = ex2(x.x - ref);
+        sum = fmaf(sum, w, x.y * before);
+        most = all;
+        mine *= w;
+#pragma unroll 1
+        for (int c = i * (D / 8); c < (i + 1) * (D / 8); c += 4) {
+          float o[16];
+          uint32_t y[16];
+          tqd::tc_ld16(t_o + 4 * c, o);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 z = part == 0 ? to[(c + k) * 128] : make_float4(0.f, 0.f, 0.f, 0.f);
+            y[4 * k] = __float_as_uint(fmaf(z.x, before, o[4 * k] * mine));
+            y[4 * k + 1] = __float_as_uint(fmaf(z.y, before, o[4 * k + 1] * mine));
+            y[4 * k + 2] = __float_as_uint(fmaf(z.z, before, o[4 * k + 2] * mine));
+            y[4 * k + 3] = __float_as_uint(fmaf(z.w, before, o[4 * k + 3] * mine));
+          }
+          tqd::tc_st16(t_o + 4 * c, y);
+        }
+        mine = 1.f;
+      }
+      if (!done) *carry = make_float2(most, sum);
+      if (whole) mine *= sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+      T* out = out_row<D, T>(p, now.b, now.h, was_live ? now.rg * ROWS + rr : 0);
       if (!whole && i == 0 && part == 0) {
         partial[rr] = most;
         partial[128 + rr] = sum;
@@ -637,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
       }
       tqd::tc_fence_before();
       tqd::tc_mbar_arrive(bar(OUT_READ, 0));  // (the next stretch's first products overwrite the sums)
-      if (threadIdx.x == 0 && now.t0 == 0 && now.t1 < now.tiles) {  // this range's last stretch begins a group that goes on
+      if (threadIdx.x == 0 && done && !inside && now.start >= begin) {  // this range's last slab goes on past it
         p.heads[blockIdx.x] = JoinHead{(now.start + now.tiles - 1) / per, now.start == begin ? 0 : 1, now.b, now.h, now.rg};
         headed = true;
       }
@@ -881,7 +922,7 @@ bool tree_tc_takes(const AttnArgs& a) {
 
 size_t tree_tc_workspace(int d, int rows, tq_dtype dtype) {
   if ((d != 64 && d != 128) || dtype == TQ_F32 || rows <= kTreeMinRows) return 0;
-  return kJoinHeadBytes + (size_t)2 * kMaxSms * 128 * (d + 2) * sizeof(float);
+  return kJoinHeadBytes + (size_t)kMaxSms * (2 * 128 * (d + 2) + 2 * 256) * sizeof(float);
 }
 
 template <typename T, int NT>
