@@ -502,6 +502,7 @@ tq_status tq_draft_tree(int32_t batch, int32_t n, const int32_t* dev_parents, co
  * from a tree; bits from c on count for nothing).  What the pool holds for drafts that no row attends to is never
  * used: they need not be appended.  Where c > dev_seq_len[b] the drafts before the first token
  * do not exist.  Rows that attend to nothing, and rows i >= c, are zeros.  nq: at most TQ_MAX_DRAFTS.
+ * out and ws overlap no other argument.
  * The rest as for tq_byte_attention_paged; 16-bit queries of more than 8 rows (queries times heads per KV head) enter
  * as e4m3 terms at head_dim 64 and 128. */
 size_t tq_byte_tree_attention_workspace_bytes(const tq_byte_config* cfg, int32_t batch, int32_t nq, tq_dtype dtype);

@@ -333,9 +333,15 @@ tq_status tq_byte_tree_attention_paged(const tq_byte_config* cfg, const void* de
   s = attention_args(cfg, dev_pool, pages, batch, nq, dtype, q, dev_seq_len, dev_count, scale, out, ws, ws_bytes, need, dev_error, &a);
   if (s != TQ_OK) return s;
   a.tree = TreeMasks{(const uint32_t*)dev_masks, nq, (nq + 31) / 32};
-  const Span m = span_of(dev_masks, (size_t)batch * nq * a.tree.words * 4);
-  if (overlap(m, span_of(ws, need)) || overlap(m, span_of(out, batch, nq, cfg->num_q_heads, cfg->head_dim, dtype_bytes(dtype))))
-    return fail(TQ_ERR_INVALID_ARG, "ws and out must not overlap the masks");
+  // (blocks begin at unlike times: one's outputs would change what another reads)
+  const size_t list = (size_t)batch * 4;
+  const Span w = span_of(ws, need), o = span_of(out, batch, nq, cfg->num_q_heads, cfg->head_dim, dtype_bytes(dtype));
+  const Span in[5] = {span_of(dev_masks, (size_t)batch * nq * a.tree.words * 4), span_of(dev_seq_len, list),
+                      span_of(dev_count, dev_count ? list : 0), span_of(pages->block_table, list * pages->max_blocks_per_seq),
+                      span_of(dev_error, dev_error ? 4 : 0)};
+  for (const Span& i : in)
+    if (overlap(w, i) || overlap(o, i))
+      return fail(TQ_ERR_INVALID_ARG, "ws and out must not overlap the masks, lengths, counts, table or error word");
   return launch_tree_attention(a, stream);
 }
 
@@ -374,10 +380,10 @@ tq_status tq_byte_keep_paged(const tq_byte_config* cfg, void* dev_pool, const tq
   const Span path = span_of(dev_path, (size_t)n * list), start = span_of(dev_start, list);
   const Span count = span_of(dev_count, dev_count ? list : 0), len = span_of(dev_seq_len, dev_seq_len ? list : 0);
   const Span pool = span_of(dev_pool, tq_byte_pool_bytes(cfg, pages->num_pages));
-  const Span table = span_of(pages->block_table, list * pages->max_blocks_per_seq);
+  const Span table = span_of(pages->block_table, list * pages->max_blocks_per_seq), err = span_of(dev_error, dev_error ? 4 : 0);
   // (other entries' starts and counts are read while an entry's length is written)
-  if (overlap(len, path) || overlap(len, start) || overlap(len, count) || overlap(len, table))
-    return fail(TQ_ERR_INVALID_ARG, "seq_len must not overlap an input");
+  if (overlap(len, path) || overlap(len, start) || overlap(len, count) || overlap(len, table) || overlap(len, err))
+    return fail(TQ_ERR_INVALID_ARG, "seq_len must not overlap an input or the error word");
   if (overlap(pool, path) || overlap(pool, start) || overlap(pool, count) || overlap(pool, len))
     return fail(TQ_ERR_INVALID_ARG, "path, start, count and seq_len must not overlap the pool");
   a.d = cfg->head_dim;
@@ -410,10 +416,10 @@ tq_status tq_byte_read_paged(const tq_byte_config* cfg, const void* dev_pool, co
   const Span v = span_of(v_out, batch, n, cfg->num_kv_heads, cfg->head_dim, bytes);
   if (overlap(k, v)) return fail(TQ_ERR_INVALID_ARG, "the outputs overlap");
   const size_t list = (size_t)batch * 4;
-  const Span in[4] = {pool, span_of(dev_start, list), span_of(dev_count, dev_count ? list : 0),
-                      span_of(pages->block_table, list * pages->max_blocks_per_seq)};
+  const Span in[5] = {pool, span_of(dev_start, list), span_of(dev_count, dev_count ? list : 0),
+                      span_of(pages->block_table, list * pages->max_blocks_per_seq), span_of(dev_error, dev_error ? 4 : 0)};
   for (const Span& i : in)
-    if (overlap(k, i) || overlap(v, i)) return fail(TQ_ERR_INVALID_ARG, "the outputs must not overlap the pool or an input");
+    if (overlap(k, i) || overlap(v, i)) return fail(TQ_ERR_INVALID_ARG, "the outputs must not overlap the pool, an input or the error word");
   a.d = cfg->head_dim;
   a.B = batch;
   a.n = n;
