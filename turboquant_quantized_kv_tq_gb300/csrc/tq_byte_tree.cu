@@ -335,11 +335,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
   using L = Plan<D>;
   constexpr int ROWS = 128 / F;     // rows of a group: each has F lanes,
   constexpr int NB = 8 / F;         // each of which takes this many blocks of a tile
-  // What a tile needs beside its scores (scales, the reference) is waited for before them, and the keys of the scores behind a
-  // readout before the readout: a wait that is over takes some 200 cycles too.  At d = 128, and where a row has two lanes,
-  // it was slower (what is then held meanwhile spills, or the products wait for keys that are late) but for fp16's keys.
-  // Late / early: 192 rows of d = 64 over 16 x 16384 tokens 63 / 55 us; d = 128, 128 rows of 8 x 32768 119 / 126, fp16's keys 143 / 135.
-  constexpr bool EARLY = F == 1 && D == 64, EARLY_KEYS = F == 1 && (D == 64 || NT == 3);
   extern __shared__ __align__(1024) unsigned char sm[];
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const AttnArgs& A = p.a;
@@ -469,28 +464,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
       auto tile = [&](int t) {
         const uint32_t g_tile = n + (uint32_t)(t - t0), turn = g_tile >> 1;
         float m_old = -INFINITY;
-        if (!EARLY && !wait(bar(S_FULL, i), turn & 1)) return false;
         const int ss = g_tile % L::SC;
+        // (scales and the reference are waited for before the scores, and below the next keys before the readout: a wait that is
+        // over takes time too.  Behind / before: 8 x 32768 tokens, 128 rows 110 / 103 us, fp16 121 / 122, 64 rows 97 / 97; d = 64 84 / 72.)
         if (!wait(bar(SC_READY, ss), (g_tile / L::SC) & 1)) return false;
-        auto reference = [&] {
-          if (t > t0) {
-            if (!wait(bar(REF_SET, i ^ 1), ((g_tile - 1) >> 1) & 1)) return false;
-            m_old = refs[128 * (i ^ 1) + r];
-          }
-          return true;
-        };
         const float4* sc = reinterpret_cast<const float4*>(sm + L::SCALES + 128 * ss) + NB * part;
         float a[NB], e[NB], v[2][32];
-        auto scales = [&] {
 #pragma unroll
-          for (int g = 0; g < NB; ++g) {
-            const float2 x = *reinterpret_cast<const float2*>(sc + g);
-            a[g] = f * x.x;
-            e[g] = x.y;
-          }
-        };
-        if (EARLY) scales();
-        if (EARLY && ((!idle && !reference()) || !wait(bar(S_FULL, i), turn & 1))) return false;
+        for (int g = 0; g < NB; ++g) {
+          const float2 x = *reinterpret_cast<const float2*>(sc + g);
+          a[g] = f * x.x;
+          e[g] = x.y;
+        }
+        if (t > t0 && !idle) {
+          if (!wait(bar(REF_SET, i ^ 1), ((g_tile - 1) >> 1) & 1)) return false;
+          m_old = refs[128 * (i ^ 1) + r];
+        }
+        if (!wait(bar(S_FULL, i), turn & 1)) return false;
         if (idle) {
           tqd::tc_mbar_arrive(bar(REF_SET, i));
           tqd::tc_mbar_arrive(bar(P_FULL, 2 * i));
@@ -506,7 +496,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
         // block g's lie at 8 g, below the scores of block g that it comes from.
         ld32_async(t_mine, v[0]);
         if (F == 2) ld32_async(t_mine + 32, v[1]);
-        if (!EARLY) scales();
         float top = -INFINITY;
 #pragma unroll
         for (int c = 0; c < NB / 2; ++c) {
@@ -519,7 +508,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
 #pragma unroll
           for (int g = 0; g < NB; ++g) st8_async(t_s + 8 * (NB * (1 - part) + g), none);
         }
-        if (!EARLY && !reference()) return false;
         const bool raise = top > m_old + kSlack;
         const float m_new = raise ? top - kTop : m_old;
         refs[128 * i + r] = m_new;
@@ -808,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
       ++segs;
       for (uint32_t k = 0; k < tiles && ok; ++k) {
         const uint32_t g = n + k;
-        if (EARLY_KEYS && k + 2 < tiles && !wait(bar(K_FULL, (g + 2) % L::KS), ((g + 2) / L::KS) & 1)) break;
+        if (k + 2 < tiles && !wait(bar(K_FULL, (g + 2) % L::KS), ((g + 2) / L::KS) & 1)) break;
         if (!wait(bar(V_FULL, g & 1), (g >> 1) & 1)) break;
         if (!wait(bar(P_FULL, 2 * (g & 1)), (g >> 1) & 1)) break;
         tqd::tc_fence_after();
@@ -820,10 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
           if (g & 1) issue_readout<D, F, 1, 1>(sb, true);
           else issue_readout<D, F, 0, 1>(sb, true);
         }
-        if (k + 2 < tiles) {
-          if (!EARLY_KEYS && !wait(bar(K_FULL, (g + 2) % L::KS), ((g + 2) / L::KS) & 1)) break;
-          issue_scores<D, NT>(sb, g + 2);
-        }
+        if (k + 2 < tiles) issue_scores<D, NT>(sb, g + 2);
       }
       n += tiles;
     }
