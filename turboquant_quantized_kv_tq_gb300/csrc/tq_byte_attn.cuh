@@ -407,7 +407,7 @@ static_assert(kJoinHeadBytes >= kMaxRanges * sizeof(JoinHead), "heads");
 
 struct JoinParams {
   const JoinHead* heads;
-  const float* part;  // [range][2](M[ROWS], l[ROWS], O[ROWS][D])
+  const float* part;  // [range][2](M[ROWS], l[ROWS], O[ROWS][D]); of tree_join_kernel as tree_kernel's Plan says
   void* out;
   int nq, Hq, G, rows;
 };

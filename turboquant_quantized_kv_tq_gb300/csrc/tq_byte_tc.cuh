@@ -17,7 +17,7 @@ struct TcParams {
   AttnArgs a;
   int G, rows, groups;  // groups: row groups of a slab
   JoinHead* heads;  // [grid]
-  float* part;      // [grid][first stretch, last](M[ROWS], l[ROWS], O[ROWS][D])
+  float* part;      // [grid][first stretch, last](M[ROWS], l[ROWS], O[ROWS][D]); tree_kernel's: see its Plan
   int grid;
 };
 // Fills p (but for the groups and the grid); the device's SMs, and its index.

@@ -14,25 +14,23 @@
 //
 // F = 2, up to 64 rows: a row has two lanes, r and r + 64, one for each half of a tile's tokens.  Each has an M and an O
 // of its own; its P holds zeros for the other half's tokens, and the lanes join as partials of a range do.  So all four
-// warps of a group work on 64 rows, each on half as many scores.  Groups of 64 for more rows were slower: 96 rows of
-// 8 x 32768 tokens 184 us instead of 116 (d = 64: 143, 94).
-// More than 128 rows are groups of 128.  Two row tiles of 128 in turn on one token tile, as tc_kernel has them, read the pool half
-// as often, which L2 makes up for: they took 213 us for 256 rows over 8 x 32768 tokens (here 220), 116 for 512 rows over 65536
-// (116), and 35 and 24 us for 256 rows over 8 x 1024 and over 2048 (25 and 18).
+// warps of a group work on 64 rows, each on half as many scores.  8 x 32768 tokens, two lanes / one: d = 64, 64 rows 73 / 78 us, 72
+// rows (two groups of 64) 132 / 80; d = 128, 32 rows 94 / 94, 64 rows 97 / 95, 96 rows 185 / 99.  More than 128 rows are groups of 128,
+// and the pool is read once for each: 256 rows of 8 x 1024 tokens 25 us, of 8 x 32768 215.
 //
 // Which drafts a row sees matters only in the last tiles: there a pass over the scores puts -infinity where a mask's
 // bit is clear, from a window of 32 bits at a time, before the tile's softmax, which is the same for all tiles.
 //
-// Measured (us, bf16, 32 / 8 heads, 8 x 32768 tokens, pools out of L2): 16 rows 96, 64 rows 101, 128 rows 119; fp16 107 and 135
-// for 64 and 128 rows; d = 64 78 and 94.  A tile's time is that of a group's chain, two tiles long: scores to registers
-// 350 cycles, maximum to P 900, the readout's issue 430, the next scores' 360 and their 500 in the tensor cores (F = 2,
-// d = 64; 2500 in all).  At d = 128 and 64 rows that meets what HBM gives (5.3 TB/s of 6.8); at d = 64 it is twice that, at
-// 128 rows 1.3 times.  Tried and not kept: an O for each group (a second join, queries in shared memory: 157), P in columns
-// of its own so that scores run ahead of the readout (146 instead of 116 for 128 rows, 121 instead of 86 at d = 64, also with
-// the readout issued by another warp), a row's 128 scores held in registers (124 instead of 117), sixteen row warps of 96
-// registers, two to a row, above 64 rows (d = 64 51 instead of 55, d = 128 115 to 125; the code for up to 64 rows beside it 110
-// instead of 101), a part of the exponentials on the FMA pipe (130 to 145 instead of 118), copies of keys, values and scales
-// by one warp (172), partials by row (6000 cycles a stretch).
+// Bits: a query is exact but for what lies below 2^-18 of its row's largest value (the split kernel, up to 8 rows: 2^-39): the
+// price of scores on the codes as they are stored, which the tensor cores take at twice fp16's rate and nothing has to unpack.
+// A weight is one fp16 number.  Its rounding is what moves a bf16 result from the fp32 form's, by 8e-4 in the 2-norm (bf16's own
+// rounding: 1.7e-3); a second term would double the readout's products.  M, l and the joins are fp32, O the tensor cores' fp32
+// for up to kMostTiles tiles.
+//
+// Measured (us, bf16, 32 / 8 heads, 8 x 32768 tokens, pools out of L2): 16 rows 94, 64 rows 97, 128 rows 103; fp16 106 and 121
+// for 64 and 128 rows; d = 64 71 and 80.  At d = 128 and up to 64 rows that meets what HBM gives (5.5 TB/s of 6.8).  Otherwise no
+// pipe is near its limit (tensor 36 to 42 %, issue 30 to 46 %): the time is the chain of a tile -- scores to registers, maximum,
+// P, readout, next scores -- on two row groups.  The code has to stay well below 128 KB (poll, below).
 //
 // Warps: 0-7 rows, 8-11 V to fp16, 12 K copies, 13 MMA issue, 14 V copies (15 only completes the warpgroup).
 #include <atomic>
@@ -43,8 +41,9 @@ namespace tqb {
 namespace {
 
 // tqd::mbar_wait as a loop that stays one: unrolled four times at each of its places it made up 50 of the kernel's 126 KB of
-// code, as much as the SM's instruction cache holds.  Before / after: 64 unlike lengths, 91 rows 45 / 35 us; d = 64, 192 rows of
-// 16 x 16384 tokens 55 / 47; d = 128, 64 and 128 rows of 8 x 32768 101 / 98 and 119 / 112.  (8 KB more of unrolled code: 147.)
+// code, and from 128 KB on every form slowed down, as from an instruction cache of that size.  Unrolled / here: 64 unlike
+// lengths, 91 rows 45 / 35 us; d = 64, 192 rows of 16 x 16384 tokens 55 / 47; 64 and 128 rows of 8 x 32768 tokens 101 / 98 and 119 /
+// 112 (135 KB of code: 102, 147).
 __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
 #pragma unroll 1
   for (uint32_t i = 0; i < kWaitLimit; ++i) {
@@ -83,7 +82,7 @@ enum Bar { K_FULL = 0, K_EMPTY = 8, VR_FULL = 16, VR_EMPTY = 24, V_FULL = 32, V_
 static_assert(8 * BAR_COUNT + 4 <= 496, "barriers and the tensor-memory slot");
 
 // Virtual tiles of a row group: what a range costs beside its tiles (4 / 6 / 8 / 12: a batch of 64 unlike lengths, 91 rows
-// 43 / 45 / 47 / 49 us; of 32, 64 rows 42 / 39 / 39 / 43; 8 x 32768 tokens 100 / 100 / 99 / 99).
+// 36 / 35 / 36 / 40 us; of 32, 64 rows 39 / 36 / 36 / 36; 8 x 32768 tokens 98 / 97 / 97 / 97).
 constexpr int kTreeGroupCost = 6;
 __device__ __forceinline__ int tree_cost(int tiles) { return tiles > 0 ? tiles + kTreeGroupCost : 0; }
 
@@ -122,8 +121,8 @@ __device__ __forceinline__ void fill_tree_plan(const TcParams& p, int* pre, int2
 // came out 4.1e-4 low (F = 2, where half of a lane's products are of zeros: 1.9e-4), twice fp16's rounding.  So a block's part
 // of a slab is cut into stretches of at most kMostTiles, which join in fp32 in its place for a partial.  1024 products lose
 // 2^-14 of an evenly growing sum at most; measured 4.1e-5 and 1.9e-5.  A cut costs the block a stretch's start and end (64 / 128 /
-// 256 / none: 152 slabs of 49152 tokens, 64 rows 340 / 320 / 315 / 306 us, 128 rows 388 / 366 / 370 / 359; 8 x 32768 tokens with
-// 64 rows, 108 tiles a block, 105 / 99 / 99 / 98).
+// 256 / none: 152 slabs of 49152 tokens, 64 rows 332 / 308 / 304 / 295 us, 128 rows 352 / 334 / 331 / 324; 8 x 32768 tokens with
+// 64 rows, 108 tiles a block, 103 / 97 / 97 / 97).
 constexpr int kMostTiles = 128;
 struct Stretch {
   int b, h, rg, len, cnt;
@@ -466,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const TcParams p) {
         float m_old = -INFINITY;
         const int ss = g_tile % L::SC;
         // (scales and the reference are waited for before the scores, and below the next keys before the readout: a wait that is
-        // over takes time too.  Behind / before: 8 x 32768 tokens, 128 rows 110 / 103 us, fp16 121 / 122, 64 rows 97 / 97; d = 64 84 / 72.)
+        // over takes time too.  Behind / before: 8 x 32768 tokens, 128 rows 110 / 103 us, fp16 123 / 121, 64 rows 97 / 97; d = 64, 64 rows 78 / 71.)
         if (!wait(bar(SC_READY, ss), (g_tile / L::SC) & 1)) return false;
         const float4* sc = reinterpret_cast<const float4*>(sm + L::SCALES + 128 * ss) + NB * part;
         float a[NB], e[NB], v[2][32];
@@ -891,8 +890,8 @@ cudaError_t tree_go(TcParams p, int sms, int device, cudaStream_t s) {
 }
 
 // Rows above which the tensor cores take a call.  Both sides (us, 8 entries, 8 KV heads, bf16; split / here), of 32768
-// tokens: d = 128 8 rows 98 / 96, 12 rows 108 / 96; d = 64 8 rows 54 / 75, 12 rows 84 / 75.  Of 1024: d = 128 8 rows 13.5 / 15.8,
-// d = 64 12 rows 13.4 / 14.1.
+// tokens: d = 128 8 rows 99 / 94, 12 rows 109 / 94; d = 64 8 rows 54 / 69, 12 rows 84 / 69.  Of 1024: d = 128 8 rows 14.9 / 14.9, 12
+// rows 17.0 / 14.9; d = 64 8 rows 11.3 / 12.7, 12 rows 13.4 / 12.8.
 constexpr int kTreeMinRows = 8;
 
 }  // namespace
