@@ -103,3 +103,17 @@ def test_hidden_drafts_of_a_pool_that_held_anything(dtype, d, Hq, H, nq, seq):
     out = c.attention(q, _i32([s + nq for s in seq]), _i32(table), tree=_i32(tree.pack(sees)))
     want, spread, reach, least, wide = _by_definition(c, table, q, seq, [s + 1 for s in seq], H, d, dtype, sees)
     _check(out, want, spread, reach, max(seq) + nq, d, DT[dtype], wide, least)
+
+
+@pytest.mark.parametrize("dtype,d,Hq,H,nq", ROUTES + [("f32", 64, 4, 1, 40), ("f16", 256, 8, 1, 30), ("bf16", 128, 8, 1, 60), ("f16", 64, 8, 1, 60)])
+def test_rows_past_the_count_beside_drafts_that_were_never_appended(dtype, d, Hq, H, nq):
+    """Groups of rows of which none asks, in sequences that are shared out and joined: zeros, whatever the drafts' places hold."""
+    seq, cnt = [4010, 3001, 5005], [max(1, nq // 2), nq, max(1, nq // 3)]  # (drafts on both sides of a block's end)
+    blocks = (max(seq) + nq + 15) // 16
+    c, table, g = _prompt(d, Hq, H, seq, blocks, dtype, zeroed=False)
+    q = torch.randn(3, nq, Hq, d, generator=g, device="cuda").to(DT[dtype])
+    none = torch.zeros(3, nq, (nq + 31) // 32, dtype=torch.int32, device="cuda")
+    out = c.attention(q, _i32([s + k for s, k in zip(seq, cnt)]), _i32(table), count=_i32(cnt), tree=none)
+    for b in range(3):
+        assert not out[b, cnt[b]:].any()
+        assert torch.isfinite(out[b, :cnt[b]].float()).all() and out[b, :cnt[b]].any()

@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, TERMS>::NW * 32, (Cfg<D, NR, TERMS>
         least = min(least, row < asks ? lim[r][k] : 0x7fffffff);
       }
     least = __reduce_min_sync(kFull, least);
-    least = min(least, len);
+    least = min(least, TREE ? max(0, drafts) : len);  // (a tree's drafts are hidden from a group without a row that asks, too)
     auto hide = [&] {
       if constexpr (TREE) return TreeLimits{A.tree, s.b, row0 + 2 * u, p.G, drafts, cnt};
       else return Limits<NR>{lim};
